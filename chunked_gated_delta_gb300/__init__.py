@@ -24,10 +24,12 @@ from .binding import (  # noqa: F401
     load_library,
     make_dims,
     new_workspace,
+    rms_norm,
     selftest_wait_timeout,
     state_map,
     status,
     status_string,
+    step,
     workspace_layout,
     workspace_size,
 )

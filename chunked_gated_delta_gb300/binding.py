@@ -7,6 +7,7 @@ is no CPU fallback: if the library cannot be loaded, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -19,6 +20,7 @@ KDA_OK = 0
 STATUS_NAMES = {
     0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "KDA_ERR_ALIGNMENT",
     4: "KDA_ERR_WORKSPACE", 5: "KDA_ERR_CUDA", 6: "KDA_ERR_TIMEOUT", 7: "KDA_ERR_BAD_SEQLENS",
+    8: "KDA_ERR_BAD_SLOTS",
 }
 
 # Every symbol the header declares (checked by the CPU test suite).
@@ -26,7 +28,7 @@ EXPORTS = ("kda_fwd_workspace_size", "kda_fwd", "kda_fwd_intra", "kda_fwd_scan",
            "kda_status_string", "kda_chunk_table", "kda_workspace_layout", "kda_fwd_host_arena_size",
            "kda_fwd_host", "kda_fwd_noalloc", "kda_selftest_wait_timeout", "kda_bwd_dh",
            "kda_fwd_ex", "kda_fwd_intra_ex", "kda_fwd_scan_ex", "kda_bwd_dh_ex", "kda_fwd_state_map",
-           "kda_chain_states")
+           "kda_chain_states", "kda_step", "kda_rms_norm")
 
 
 class KdaError(RuntimeError):
@@ -45,6 +47,22 @@ class FwdOpts(ctypes.Structure):
     """kda_fwd_opts: interface variants of the forward (all zero = kda_fwd)."""
     _fields_ = [("io_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
                 ("beta_logits", ctypes.c_int32), ("qk_heads", ctypes.c_int32), ("plan", ctypes.c_int32)]
+
+
+class StepOpts(ctypes.Structure):
+    """kda_step_opts: element types, cache size and token strides of kda_step."""
+    _fields_ = [("io_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("beta_logits", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
+                ("num_slots", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64)]
+
+
+class NormOpts(ctypes.Structure):
+    """kda_norm_opts: element types, eps and row strides of kda_rms_norm."""
+    _fields_ = [("io_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("weight_f32", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64)]
 
 
 IO_BF16, IO_F16 = 0, 1
@@ -101,6 +119,9 @@ def load_library(build_if_missing: bool = True):
             "kda_bwd_dh_ex": (ctypes.c_int, [F32, P, P, P, P, P, P, D, O, P, SZ, P]),
             "kda_fwd_state_map": (ctypes.c_int, [P, P, P, P, P, P, P, D, P, SZ, P]),
             "kda_chain_states": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, P]),
+            "kda_step": (ctypes.c_int, [P, P, P, P, P, F32, P, P, P, P, D, ctypes.POINTER(StepOpts), P, P]),
+            "kda_rms_norm": (ctypes.c_int, [P, P, P, P, P, P, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.POINTER(NormOpts), P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -380,3 +401,177 @@ def bwd_dh(scale, do, dv_in, dht, dims: Dims, workspace, want_dhck=True, want_dh
                                       workspace.numel(), _stream_handle(stream))
     _check(rc, "kda_bwd_dh_ex")
     return dhck, dv2, dh0
+
+
+# ----------------------------------------------------------------- the served layer's operators
+# A decode step calls these once per layer and token, at a few microseconds of
+# kernel time each, so the marshalling below keeps to plain attribute reads:
+# the argument structs are made once per set of sizes, and the stream handle is
+# read without building a stream object.
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=4096)
+def _struct(cls, *fields):
+    return ctypes.byref(cls(*fields))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _token_stride(name, t):
+    """Elements between consecutive token rows of [B, T, ...] (0: contiguous)."""
+    if t.is_contiguous():
+        return 0
+    B, T = t.shape[:2]
+    inner = 1
+    for size, step in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if size != 1 and step != inner:
+            raise TypeError(f"{name}: the heads of a token must be contiguous")
+        inner *= size
+    if B * T <= 1:
+        return 0
+    step = t.stride(1) if T > 1 else t.stride(0)
+    if step < inner or (B > 1 and t.stride(0) != T * step):
+        raise TypeError(f"{name}: token rows must be equally spaced over [B, T] and not overlap")
+    return step
+
+
+def step(q, k, v, g, beta, state, slots=None, scale=None, cu_seqlens=None, out=None, status=None, stream=None,
+         beta_logits=False):
+    """Decode step (kda_step): the gated delta rule over the few new tokens of
+    each sequence, on a cache of states updated in place.  Returns o [B,T,H,V].
+
+    q, k: [B,T,Hqk,K]; v: [B,T,H,V]; beta: [B,T,H], all bf16 or all fp16; g:
+    fp32 [B,T,H,K]; the rows of consecutive tokens may lie apart (views of a
+    wider projection).  cu_seqlens: int32 [N+1] on the device (B must be 1,
+    lengths of zero allowed) or None for B sequences of T tokens.  state:
+    [num_slots,H,K,V] fp32 or bf16 (what fwd's ht holds); slots: int32 [N] on
+    the device, the state of each sequence (negative: padding, o is zero), or
+    None for slot n.  ``status``: an int32 CUDA tensor that starts at zero and
+    takes the errors found in slots and cu_seqlens; ``binding.status`` reads it.
+    """
+    import torch
+    io = q.dtype
+    f16 = io == torch.float16
+    if not f16 and io != torch.bfloat16:
+        raise TypeError("q must be bf16 or fp16")
+    if q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[:2] != q.shape[:2]:
+        raise TypeError("q and k are [B,T,Hqk,K], v is [B,T,H,V]")
+    B, T, Hqk, K = q.shape
+    H, V = v.shape[2], v.shape[3]
+    if k.dtype != io or v.dtype != io or beta.dtype != io or g.dtype != torch.float32:
+        raise TypeError("k, v and beta have q's dtype, g is float32")
+    if g.shape != (B, T, H, K) or beta.shape != (B, T, H):
+        raise TypeError("g is [B,T,H,K], beta is [B,T,H]")
+    s16 = state.dtype == torch.bfloat16
+    if (not s16 and state.dtype != torch.float32) or not state.is_contiguous() or state.dim() != 4 \
+            or state.shape[1:] != (H, K, V):
+        raise TypeError("state must be a contiguous float32 or bfloat16 tensor [num_slots,H,K,V]")
+    N = 0
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous() or N < 1:
+            raise TypeError("cu_seqlens must be a contiguous CUDA int32 tensor [N+1]")
+    if slots is not None and (slots.dtype != torch.int32 or not slots.is_cuda or not slots.is_contiguous()
+                              or slots.numel() != (N or B)):
+        raise TypeError("slots must be a contiguous CUDA int32 tensor, one per sequence")
+    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1):
+        raise TypeError("status must be a CUDA int32 tensor")
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and g.is_cuda and beta.is_cuda and state.is_cuda):
+        raise TypeError("step takes CUDA tensors")
+    if out is None:
+        out = torch.empty((B, T, H, V), dtype=io, device=q.device)
+    elif out.dtype != io or out.shape != v.shape or not out.is_cuda or not out.is_contiguous():
+        raise TypeError("out must be a contiguous CUDA tensor of v's shape and dtype")
+    opts = _struct(StepOpts, f16, s16, 1 if beta_logits else 0, Hqk if Hqk != H else 0, state.shape[0], 0,
+                   _token_stride("q", q), _token_stride("k", k), _token_stride("v", v), _token_stride("g", g),
+                   _token_stride("beta", beta))
+    rc = load_library().kda_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                 K ** -0.5 if scale is None else scale, state.data_ptr(), _addr(slots),
+                                 _addr(cu_seqlens), out.data_ptr(), _struct(Dims, B, T, H, K, V, N), opts,
+                                 _addr(status), _raw_stream(stream, q.device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_step")
+    return out
+
+
+def _dtype_codes():
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+
+
+_dtype_codes = functools.lru_cache(maxsize=1)(_dtype_codes)
+
+
+def _row_stride(name, t, dim):
+    """Elements between consecutive rows of [..., dim] (0: contiguous)."""
+    if t.is_contiguous():
+        return 0
+    if dim != 1 and t.stride(-1) != 1:
+        raise TypeError(f"{name}: the elements of a row must be contiguous")
+    step, rows = None, 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size != 1:
+            if step is None:
+                step = st
+            elif st != step * rows:
+                raise TypeError(f"{name}: rows must be equally spaced")
+            rows *= size
+    if step is not None and step < dim:
+        raise TypeError(f"{name}: rows must not overlap")
+    return 0 if step is None else step
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, residual_out=None, stream=None):
+    """Root-mean-square norm over the last dimension (kda_rms_norm):
+    s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight, in fp32.
+    Returns (y, y_scale, s).
+
+    x: [..., dim] bf16, fp16 or fp32, rows equally spaced; residual: the same
+    shape and dtype, or None; weight: [dim] of x's dtype or fp32, or None.
+    out_dtype: x's (default), float32 or float8_e4m3fn; the last stores codes
+    with one fp32 scale per row, y ~ codes * y_scale[..., None] (y_scale is None
+    otherwise).  s, in x's dtype, is returned when there is a residual (else
+    None); ``residual_out`` takes it and may be ``residual`` itself.
+    """
+    import torch
+    codes = _dtype_codes()
+    io = x.dtype
+    out_dtype = io if out_dtype is None else out_dtype
+    if io not in codes or io == torch.float8_e4m3fn or x.dim() < 1 or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor of bf16, fp16 or fp32")
+    if out_dtype not in (io, torch.float32, torch.float8_e4m3fn):
+        raise TypeError("out_dtype must be x's dtype, float32 or float8_e4m3fn")
+    shape, dim = x.shape, x.shape[-1]
+    if residual is not None and (residual.dtype != io or residual.shape != shape or not residual.is_cuda):
+        raise TypeError("residual must be a CUDA tensor of x's shape and dtype")
+    if weight is not None and (weight.dtype not in (io, torch.float32) or weight.shape != (dim,)
+                               or not weight.is_cuda or not weight.is_contiguous()):
+        raise TypeError("weight must be a contiguous CUDA tensor [dim] of x's dtype or float32")
+    if residual_out is not None and (residual_out.dtype != io or residual_out.shape != shape
+                                     or not residual_out.is_cuda):
+        raise TypeError("residual_out must be a CUDA tensor of x's shape and dtype")
+    device = x.device
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=io, device=device)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    elif out.dtype != out_dtype or out.shape != shape or not out.is_cuda or not out.is_contiguous():
+        raise TypeError("out must be a contiguous CUDA tensor of x's shape and out_dtype")
+    scale = torch.empty(shape[:-1], dtype=torch.float32, device=device) if out_dtype == torch.float8_e4m3fn else None
+    opts = _struct(NormOpts, codes[io], codes[out_dtype],
+                   1 if weight is not None and weight.dtype == torch.float32 else 0, eps,
+                   _row_stride("x", x, dim), 0 if residual is None else _row_stride("residual", residual, dim),
+                   0 if residual_out is None else _row_stride("residual_out", residual_out, dim))
+    rc = load_library().kda_rms_norm(x.data_ptr(), _addr(residual), _addr(weight), out.data_ptr(), _addr(scale),
+                                     _addr(residual_out), x.numel() // dim if dim else 0, dim, opts,
+                                     _raw_stream(stream, device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_rms_norm")
+    return out, scale, residual_out

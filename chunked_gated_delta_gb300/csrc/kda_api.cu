@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "layer_ops.cuh"
 #include "tensormap.h"
 
 namespace kda {
@@ -926,6 +927,7 @@ kda_status kda_fwd_status(const void* workspace, void* stream) {
         return KDA_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return KDA_ERR_CUDA;
     if (word & kStatusBadSeqlens) return KDA_ERR_BAD_SEQLENS;
+    if (word & kStatusBadSlots) return KDA_ERR_BAD_SLOTS;
     if (word & kStatusTimeout) return KDA_ERR_TIMEOUT;
     return KDA_OK;
 }
@@ -940,6 +942,7 @@ const char* kda_status_string(kda_status s) {
     case KDA_ERR_CUDA: return "CUDA launch or driver error";
     case KDA_ERR_TIMEOUT: return "a kernel pipeline wait timed out";
     case KDA_ERR_BAD_SEQLENS: return "cu_seqlens must satisfy 0 = c0 <= c1 <= ... <= cN = T";
+    case KDA_ERR_BAD_SLOTS: return "a state slot is outside the cache or given twice";
     }
     return "unknown status";
 }

@@ -1,0 +1,254 @@
+// norm.cu -- kda_rms_norm: root-mean-square norm of rows, with the residual's
+// addition before it and an output in 16, 32 or 8 bits (e4m3 with one scale a
+// row).
+//
+//     s = x + r;   y = s * (1 / sqrt(mean(s^2) + eps)) * w
+//     8 bits: a = max(max |y|, 1e-30), code = e4m3(y * (448 / a)), scale = a / 448
+//
+// Bound: HBM; every element is read once and written once.  A row stays in the
+// registers of its threads between the load and the store, so the two
+// statistics (the sum of squares, then the largest |y|) cost exchanges but no
+// second read.  A row is taken by a team: 8 to 32 lanes of a warp for short
+// rows (head norms), so that its sums are shuffles and several rows share a
+// CTA, or a whole CTA for long ones, with one barrier per statistic.
+#include "layer_ops.cuh"
+
+namespace kda {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 1e-30f;  // keeps 448 / a finite for a row of zeros
+
+struct NormArgs {
+    const void *x, *r, *w;
+    void *y, *sum;
+    float* y_scale;
+    int64_t rows, x_stride, r_stride, sum_stride;
+    int dim, out, w_f32;
+    float eps, inv_dim;
+};
+
+// VEC elements of type IO (a KDA_DTYPE) as fp32: one 16-byte load (two for
+// fp32) where VEC is 8, else one element.
+template <int IO, int VEC>
+__device__ __forceinline__ void load_vec(const void* p, int64_t at, float* f) {
+    if constexpr (VEC == 8 && IO == KDA_DTYPE_F32) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        const float4 a = q[0], b = q[1];
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else if constexpr (VEC == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = from_b16x2<IO == KDA_DTYPE_F16>(w[i]);
+            f[2 * i] = v.x, f[2 * i + 1] = v.y;
+        }
+    } else if constexpr (IO == KDA_DTYPE_F32) {
+        f[0] = static_cast<const float*>(p)[at];
+    } else {
+        f[0] = from_b16<IO == KDA_DTYPE_F16>(static_cast<const uint16_t*>(p)[at]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(void* p, int64_t at, const float* f, int dtype) {
+    if constexpr (VEC == 8) {
+        if (dtype == KDA_DTYPE_F32) {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+            q[0] = make_float4(f[0], f[1], f[2], f[3]);
+            q[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else if (dtype == KDA_DTYPE_E4M3) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + at) =
+                make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+        } else {
+            const bool h = dtype == KDA_DTYPE_F16;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+                make_uint4(pack_b16x2(f[0], f[1], h), pack_b16x2(f[2], f[3], h), pack_b16x2(f[4], f[5], h),
+                           pack_b16x2(f[6], f[7], h));
+        }
+    } else {
+        if (dtype == KDA_DTYPE_F32) static_cast<float*>(p)[at] = f[0];
+        else if (dtype == KDA_DTYPE_E4M3) static_cast<uint8_t*>(p)[at] = (uint8_t)pack_e4m3x2(f[0], 0.f);
+        else static_cast<uint16_t*>(p)[at] = to_b16(f[0], dtype == KDA_DTYPE_F16);
+    }
+}
+
+// Reduces v over the team: lanes of a warp (TEAM <= 32), or the whole CTA
+// (TEAM = 0) through s[32].
+template <int TEAM, bool MAX>
+__device__ __forceinline__ float team_reduce(float v, float* s) {
+    auto join = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
+    constexpr int kLanes = TEAM ? TEAM : 32;
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) v = join(v, __shfl_xor_sync(~0u, v, off));
+    if constexpr (TEAM == 0) {
+        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) s[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = lane < warps ? s[lane] : 0.f;  // 0 is neutral for both (|y| >= 0)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = join(v, __shfl_xor_sync(~0u, v, off));
+    }
+    return v;
+}
+
+template <int IO, int VEC, int NV, int TEAM>
+__global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormArgs a) {
+    __shared__ float s_red[2][32];
+    const int per = TEAM ? (int)(blockDim.x / TEAM) : 1;  // rows a CTA takes
+    const int lane = TEAM ? (int)(threadIdx.x % TEAM) : (int)threadIdx.x;
+    const int width = TEAM ? TEAM : (int)blockDim.x;
+    const int64_t row = (int64_t)blockIdx.x * per + (TEAM ? (int)(threadIdx.x / TEAM) : 0);
+    const bool live = row < a.rows;  // (teams past the last row still take part in the shuffles)
+    float s[NV][VEC];
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * width) * VEC;
+        if (live && c < a.dim) {
+            load_vec<IO, VEC>(a.x, row * a.x_stride + c, s[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[i][j] = 0.f;
+        }
+    }
+    if (a.r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * width) * VEC;
+            if (live && c < a.dim) {
+                float r[VEC];
+                load_vec<IO, VEC>(a.r, row * a.r_stride + c, r);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[i][j] += r[j];
+                if (a.sum) store_vec<VEC>(a.sum, row * a.sum_stride + c, s[i], IO);
+            }
+        }
+    } else if (a.sum) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * width) * VEC;
+            if (live && c < a.dim) store_vec<VEC>(a.sum, row * a.sum_stride + c, s[i], IO);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sq += s[i][j] * s[i][j];
+    sq = team_reduce<TEAM, false>(sq, s_red[0]);
+    const float rstd = 1.f / sqrtf(sq * a.inv_dim + a.eps);
+    float amax = kAmaxFloor;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * width) * VEC;
+        float w[VEC];
+        if (a.w && c < a.dim) {
+            if (a.w_f32) load_vec<KDA_DTYPE_F32, VEC>(a.w, c, w);
+            else load_vec<IO, VEC>(a.w, c, w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[j] = 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            s[i][j] = s[i][j] * rstd * w[j];
+            if (c < a.dim) amax = max_nan(amax, fabsf(s[i][j]));
+        }
+    }
+    float inv = 1.f;
+    if (a.out == KDA_DTYPE_E4M3) {
+        amax = team_reduce<TEAM, true>(amax, s_red[1]);
+        inv = kE4m3Max / amax;
+        if (live && lane == 0) a.y_scale[row] = amax / kE4m3Max;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * width) * VEC;
+        if (live && c < a.dim) {
+            if (a.out == KDA_DTYPE_E4M3) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[i][j] *= inv;
+            }
+            store_vec<VEC>(a.y, row * a.dim + c, s[i], a.out);
+        }
+    }
+}
+
+template <int IO, int VEC, int NV, int TEAM>
+cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
+    const int64_t per = TEAM ? threads / TEAM : 1;
+    kda_norm_kernel<IO, VEC, NV, TEAM><<<(unsigned)((a.rows + per - 1) / per), threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// The team for a row of `vecs` vectors.
+template <int IO, int VEC>
+cudaError_t pick(const NormArgs& a, cudaStream_t s) {
+    const int vecs = (a.dim + VEC - 1) / VEC;
+    if (vecs <= 8) return launch<IO, VEC, 1, 8>(a, 256, s);
+    if (vecs <= 16) return launch<IO, VEC, 1, 16>(a, 256, s);
+    if (vecs <= 32) return launch<IO, VEC, 1, 32>(a, 256, s);
+    if (vecs <= 64) return launch<IO, VEC, 2, 32>(a, 256, s);
+    if (vecs <= 128) return launch<IO, VEC, 4, 32>(a, 256, s);
+    const int threads = (vecs + 31) / 32 * 32;
+    if (threads <= 512) return launch<IO, VEC, 1, 0>(a, threads, s);
+    if (vecs <= 2048) return launch<IO, VEC, 2, 0>(a, (threads / 2 + 31) / 32 * 32, s);
+    if (vecs <= 4096) return launch<IO, VEC, 4, 0>(a, 1024, s);
+    if constexpr (VEC == 1) {
+        if (vecs <= 8192) return launch<IO, VEC, 8, 0>(a, 1024, s);
+        if (vecs <= 16384) return launch<IO, VEC, 16, 0>(a, 1024, s);
+        return launch<IO, VEC, 32, 0>(a, 1024, s);
+    }
+    return cudaErrorInvalidValue;  // not reached: dim <= 32768
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_rms_norm(const void* x, const void* residual, const void* weight, void* y, float* y_scale,
+                                   void* sum, int64_t rows, int64_t dim, const kda_norm_opts* opts, void* stream) {
+    if (!opts || rows < 0 || dim < 1) return KDA_ERR_INVALID_ARG;
+    const kda_norm_opts& p = *opts;
+    if (p.io_dtype != KDA_DTYPE_BF16 && p.io_dtype != KDA_DTYPE_F16 && p.io_dtype != KDA_DTYPE_F32)
+        return KDA_ERR_INVALID_ARG;
+    if (p.out_dtype != p.io_dtype && p.out_dtype != KDA_DTYPE_F32 && p.out_dtype != KDA_DTYPE_E4M3)
+        return KDA_ERR_INVALID_ARG;
+    if ((p.weight_f32 != 0 && p.weight_f32 != 1) || !(p.eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if ((p.out_dtype == KDA_DTYPE_E4M3) != (y_scale != nullptr)) return KDA_ERR_INVALID_ARG;
+    if (dim > 32768) return KDA_ERR_UNSUPPORTED;
+    NormArgs a{};
+    a.x_stride = p.x_stride ? p.x_stride : dim;
+    a.r_stride = p.residual_stride ? p.residual_stride : dim;
+    a.sum_stride = p.sum_stride ? p.sum_stride : dim;
+    if (a.x_stride < dim || a.r_stride < dim || a.sum_stride < dim) return KDA_ERR_INVALID_ARG;
+    if (rows == 0) return KDA_OK;
+    if (rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (!x || !y) return KDA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(p.io_dtype), wes = p.weight_f32 ? 4 : es, oes = dtype_bytes(p.out_dtype);
+    if (!is_aligned(x, es) || !is_aligned(residual, es) || !is_aligned(sum, es) || !is_aligned(weight, wes) ||
+        !is_aligned(y, oes) || !is_aligned(y_scale, 4))
+        return KDA_ERR_ALIGNMENT;
+    a.x = x;
+    a.r = residual;
+    a.w = weight;
+    a.y = y;
+    a.sum = sum;
+    a.y_scale = y_scale;
+    a.rows = rows;
+    a.dim = (int)dim;
+    a.out = p.out_dtype;
+    a.w_f32 = p.weight_f32;
+    a.eps = p.eps;
+    a.inv_dim = 1.f / (float)dim;
+    const bool wide = dim % 8 == 0 && is_aligned(x, 16) && is_aligned(residual, 16) && is_aligned(sum, 16) &&
+                      is_aligned(weight, 16) && is_aligned(y, 8 * oes < 16 ? 8 : 16) && a.x_stride * es % 16 == 0 &&
+                      (!residual || a.r_stride * es % 16 == 0) && (!sum || a.sum_stride * es % 16 == 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (p.io_dtype == KDA_DTYPE_BF16) e = wide ? pick<KDA_DTYPE_BF16, 8>(a, s) : pick<KDA_DTYPE_BF16, 1>(a, s);
+    else if (p.io_dtype == KDA_DTYPE_F16) e = wide ? pick<KDA_DTYPE_F16, 8>(a, s) : pick<KDA_DTYPE_F16, 1>(a, s);
+    else e = wide ? pick<KDA_DTYPE_F32, 8>(a, s) : pick<KDA_DTYPE_F32, 1>(a, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}

@@ -46,7 +46,8 @@ typedef enum kda_status {
     KDA_ERR_WORKSPACE = 4,    /* workspace NULL, misaligned or smaller than required    */
     KDA_ERR_CUDA = 5,         /* a CUDA launch / driver call failed                     */
     KDA_ERR_TIMEOUT = 6,      /* a kernel pipeline wait ran out of time (kda_fwd_status) */
-    KDA_ERR_BAD_SEQLENS = 7   /* cu_seqlens not 0 = c0 <= c1 <= ... <= cN = T          */
+    KDA_ERR_BAD_SEQLENS = 7,  /* cu_seqlens not 0 = c0 <= c1 <= ... <= cN = T          */
+    KDA_ERR_BAD_SLOTS = 8     /* a state slot outside the cache, or given twice (kda_step) */
 } kda_status;
 
 /*
@@ -357,6 +358,85 @@ kda_status kda_fwd_status(const void* workspace, void* stream);
  * The context stays usable afterwards (no trap, no fault).
  */
 kda_status kda_selftest_wait_timeout(void* status_word, unsigned long long limit_ns, void* stream);
+
+/*
+ * Decode step: the gated delta rule over the few new tokens of each sequence,
+ * on a cache of recurrent states that is updated in place,
+ *     S_t = (I - beta_t k_t k_t^T) Diag(exp g_t) S_{t-1} + beta_t k_t v_t^T,
+ *     o_t = scale * S_t^T q_t,
+ * token by token with S on chip in fp32 (one launch; no workspace, no chunks).
+ * It continues what kda_fwd's ht holds.  The dims and the tensors q, k, v, g,
+ * beta, o have kda_fwd_ex's meanings: N = B sequences of T tokens each, or
+ * packed sequences with cu_seqlens (lengths of zero are fine: that state is
+ * not touched).  Meant for T of one to a few tokens; any T is correct.
+ *   state     [num_slots, H, K, V] fp32 or bf16 (state_dtype), read and written
+ *             in place; other slots than those named are not touched.  With
+ *             bf16 it is rounded once per call, after the last token.
+ *   slots     device int32 [N]: the slot of each sequence, or NULL for slot n
+ *             (N <= num_slots then).  A negative slot marks padding: its tokens
+ *             get o = 0 and no state.  A slot >= num_slots, or one that an
+ *             earlier sequence of the same call has, is an error: o = 0 for it,
+ *             its state untouched, KDA_ERR_BAD_SLOTS in the status word.  (A
+ *             sequence without tokens is not looked at, but its slot is taken.)
+ *   status_word  device int32 (4-byte aligned) or NULL.  Errors in the contents
+ *             of slots and cu_seqlens are or-ed into it; the caller sets it to
+ *             zero once, and kda_fwd_status(status_word, stream) reads it.  A
+ *             sequence whose cu_seqlens are out of order is skipped.
+ *   opts      io_dtype, state_dtype, beta_logits, qk_heads as in kda_fwd_opts;
+ *             num_slots (> 0); *_stride: elements between the rows of
+ *             consecutive tokens of q, k, v, g, beta (0: contiguous), so that
+ *             they may be parts of wider projections' outputs.  o is contiguous.
+ * o and state are 16-byte aligned, the other tensors to their own elements
+ * (KDA_ERR_ALIGNMENT).  Asynchronous on `stream`.
+ */
+typedef struct kda_step_opts {
+    int32_t io_dtype;
+    int32_t state_dtype;
+    int32_t beta_logits;
+    int32_t qk_heads;
+    int32_t num_slots;
+    int32_t reserved;  /* 0 */
+    int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
+} kda_step_opts;
+kda_status kda_step(const void* q, const void* k, const void* v, const float* g, const void* beta, float scale,
+                    void* state, const int32_t* slots, const int32_t* cu_seqlens, void* o, const kda_dims* dims,
+                    const kda_step_opts* opts, int32_t* status_word, void* stream);
+
+/* Element types of kda_rms_norm and kda_linear. */
+#define KDA_DTYPE_BF16 0
+#define KDA_DTYPE_F16 1
+#define KDA_DTYPE_F32 2
+#define KDA_DTYPE_E4M3 3
+
+/*
+ * Root-mean-square norm of each row, with the residual's addition before it:
+ *     s = x + residual;  y = s / sqrt(mean(s^2) + eps) * weight
+ * in fp32, each output rounded once.  With out_dtype KDA_DTYPE_E4M3, y is
+ * stored in 8 bits with one scale per row:
+ *     a = max(max |y|, 1e-30);  y_scale = a / 448;  code = e4m3(y * (448 / a)).
+ * A row that holds a NaN or an infinity gets the NaN that the formulas give.
+ *   x         [rows, dim] bf16, fp16 or fp32 (io_dtype)
+ *   residual  [rows, dim] of the same type, or NULL
+ *   weight    [dim] of io_dtype, or fp32 with weight_f32, or NULL (ones)
+ *   y         [rows, dim] out_dtype: io_dtype, KDA_DTYPE_F32 or KDA_DTYPE_E4M3
+ *   y_scale   fp32 [rows], with KDA_DTYPE_E4M3 only (else NULL)
+ *   sum       [rows, dim] of io_dtype: s, or NULL; it may be `residual` or `x`
+ *             itself with the same stride (each element is read before it is
+ *             written), and may not overlap them in another way
+ *   *_stride  elements between rows (0: contiguous); y is contiguous
+ * rows >= 0; dim in 1 .. 32768 (KDA_ERR_UNSUPPORTED above).  Any alignment of
+ * the elements' own size is accepted; rows that all start on 16 bytes with
+ * dim a multiple of 8 take 16-byte loads and stores.
+ */
+typedef struct kda_norm_opts {
+    int32_t io_dtype;
+    int32_t out_dtype;
+    int32_t weight_f32;
+    float eps;
+    int64_t x_stride, residual_stride, sum_stride;
+} kda_norm_opts;
+kda_status kda_rms_norm(const void* x, const void* residual, const void* weight, void* y, float* y_scale, void* sum,
+                        int64_t rows, int64_t dim, const kda_norm_opts* opts, void* stream);
 
 /* Static description of a status code.  Never NULL. */
 const char* kda_status_string(kda_status s);
