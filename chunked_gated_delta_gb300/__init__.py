@@ -21,6 +21,7 @@ from .binding import (  # noqa: F401
     host_arena_size,
     fwd_scan,
     library_path,
+    linear,
     load_library,
     make_dims,
     new_workspace,

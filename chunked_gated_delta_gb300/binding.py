@@ -28,7 +28,7 @@ EXPORTS = ("kda_fwd_workspace_size", "kda_fwd", "kda_fwd_intra", "kda_fwd_scan",
            "kda_status_string", "kda_chunk_table", "kda_workspace_layout", "kda_fwd_host_arena_size",
            "kda_fwd_host", "kda_fwd_noalloc", "kda_selftest_wait_timeout", "kda_bwd_dh",
            "kda_fwd_ex", "kda_fwd_intra_ex", "kda_fwd_scan_ex", "kda_bwd_dh_ex", "kda_fwd_state_map",
-           "kda_chain_states", "kda_step", "kda_rms_norm")
+           "kda_chain_states", "kda_step", "kda_rms_norm", "kda_linear")
 
 
 class KdaError(RuntimeError):
@@ -65,6 +65,15 @@ class NormOpts(ctypes.Structure):
                 ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64)]
 
 
+class LinearOpts(ctypes.Structure):
+    """kda_linear_opts: element types, activation and row strides of kda_linear."""
+    _fields_ = [("io_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "sigmoid": 3, "logsigmoid": 4}
 IO_BF16, IO_F16 = 0, 1
 STATE_F32, STATE_BF16 = 0, 1
 PLAN_AUTO, PLAN_TWO_STAGE, PLAN_FUSED = 0, 1, 2
@@ -122,6 +131,8 @@ def load_library(build_if_missing: bool = True):
             "kda_step": (ctypes.c_int, [P, P, P, P, P, F32, P, P, P, P, D, ctypes.POINTER(StepOpts), P, P]),
             "kda_rms_norm": (ctypes.c_int, [P, P, P, P, P, P, ctypes.c_int64, ctypes.c_int64,
                                             ctypes.POINTER(NormOpts), P]),
+            "kda_linear": (ctypes.c_int, [P, P, P, P, P, P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.POINTER(LinearOpts), P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -575,3 +586,61 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, 
     if rc != KDA_OK:
         raise KdaError(rc, "kda_rms_norm")
     return out, scale, residual_out
+
+
+def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None, out_dtype=None, out=None,
+           status=None, stream=None):
+    """Projection (kda_linear): act(x @ w^T * x_scale * w_scale + bias) + residual,
+    computed in fp32 and rounded once to out_dtype.  Returns y [..., N].
+
+    x: [..., K], w: [N, K], both bf16, fp16 or float8_e4m3fn, rows equally
+    spaced and starting on 16 bytes; x_scale: fp32 [...] (one per row of x) and
+    w_scale: fp32 [N], with float8 only; bias: fp32 [N]; residual: [..., N] of
+    out_dtype.  out_dtype: bf16, fp16 or float32; defaults to x's dtype, bf16
+    for float8.  act: None, "silu", "gelu", "sigmoid" or "logsigmoid".  ``out``
+    may be ``residual`` itself.  ``status``: as in step.
+    """
+    import torch
+    codes = _dtype_codes()
+    io, f8 = x.dtype, x.dtype == torch.float8_e4m3fn
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if f8 else io
+    if io not in codes or io == torch.float32 or w.dtype != io or not x.is_cuda or not w.is_cuda:
+        raise TypeError("x and w must be CUDA tensors of one dtype: bf16, fp16 or float8_e4m3fn")
+    if out_dtype not in codes or out_dtype == torch.float8_e4m3fn:
+        raise TypeError("out_dtype must be bf16, fp16 or float32")
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(k for k in ACTS if k)}")
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise TypeError("x is [..., K], w is [N, K]")
+    N, K = w.shape
+    lead = x.shape[:-1]
+    M = x.numel() // K if K else 0
+    if f8:
+        if x_scale is None or w_scale is None or x_scale.shape != lead or w_scale.shape != (N,) \
+                or x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 or not x_scale.is_cuda \
+                or not w_scale.is_cuda or not x_scale.is_contiguous() or not w_scale.is_contiguous():
+            raise TypeError("float8 operands take contiguous CUDA float32 x_scale [...] and w_scale [N]")
+    elif x_scale is not None or w_scale is not None:
+        raise TypeError("x_scale and w_scale go with float8 operands only")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_cuda
+                             or not bias.is_contiguous()):
+        raise TypeError("bias must be a contiguous CUDA float32 tensor [N]")
+    y_shape = (*lead, N)
+    if residual is not None and (residual.dtype != out_dtype or residual.shape != y_shape or not residual.is_cuda):
+        raise TypeError("residual must be a CUDA tensor [..., N] of out_dtype")
+    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1):
+        raise TypeError("status must be a CUDA int32 tensor")
+    if out is None:
+        out = torch.empty(y_shape, dtype=out_dtype, device=x.device)
+    elif out.dtype != out_dtype or out.shape != y_shape or not out.is_cuda:
+        raise TypeError("out must be a CUDA tensor [..., N] of out_dtype")
+    opts = _struct(LinearOpts, codes[io], codes[out_dtype], ACTS[act], 0, _row_stride("x", x, K),
+                   _row_stride("w", w, K), 0 if residual is None else _row_stride("residual", residual, N),
+                   _row_stride("out", out, N))
+    rc = load_library().kda_linear(x.data_ptr(), w.data_ptr(), _addr(bias), _addr(residual), _addr(x_scale),
+                                   _addr(w_scale), out.data_ptr(), M, N, K, opts, _addr(status),
+                                   _raw_stream(stream, x.device))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_linear")
+    return out

@@ -438,6 +438,45 @@ typedef struct kda_norm_opts {
 kda_status kda_rms_norm(const void* x, const void* residual, const void* weight, void* y, float* y_scale, void* sum,
                         int64_t rows, int64_t dim, const kda_norm_opts* opts, void* stream);
 
+/*
+ * Projection: a product with scales, bias, activation and residual in its
+ * epilogue, in fp32 from the accumulators and rounded once:
+ *     y[m, n] = act(x_scale[m] w_scale[n] sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+ *   x         [M, K], w [N, K] (a linear layer's weight): bf16, fp16 or e4m3 (io_dtype)
+ *   x_scale   fp32 [M], w_scale fp32 [N]: with e4m3 only (else NULL); x and x_scale
+ *             are kda_rms_norm's 8-bit output
+ *   bias      fp32 [N] or NULL
+ *   residual  [M, N] of out_dtype, or NULL
+ *   y         [M, N] bf16, fp16 or fp32 (out_dtype); it may be `residual` itself
+ *             with the same stride
+ *   act       KDA_ACT_*: SILU v sigmoid(v); GELU v Phi(v) (the error function's
+ *             form); SIGMOID (beta); LOGSIGMOID log(sigmoid(v)) (the decay g, in fp32)
+ *   *_stride  elements between rows (0: contiguous)
+ *   status_word  device int32 or NULL, as in kda_step: KDA_ERR_TIMEOUT if a
+ *             pipeline wait ran out (y is then incomplete)
+ * M >= 0; N, K >= 1, any of them odd.  x and w are 16-byte aligned with row
+ * strides of a multiple of 16 bytes where they have more than one row
+ * (KDA_ERR_ALIGNMENT), which is what a TMA load of their rows needs; y and residual to their own elements.  No
+ * workspace.  Results do not depend on timing (no atomics); they may differ in
+ * the last bits between different M, whose sums are cut differently.
+ * Asynchronous on `stream`.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SILU 1
+#define KDA_ACT_GELU 2
+#define KDA_ACT_SIGMOID 3
+#define KDA_ACT_LOGSIGMOID 4
+typedef struct kda_linear_opts {
+    int32_t io_dtype;
+    int32_t out_dtype;
+    int32_t act;
+    int32_t reserved;  /* 0 */
+    int64_t x_stride, w_stride, residual_stride, y_stride;
+} kda_linear_opts;
+kda_status kda_linear(const void* x, const void* w, const float* bias, const void* residual, const float* x_scale,
+                      const float* w_scale, void* y, int64_t M, int64_t N, int64_t K, const kda_linear_opts* opts,
+                      int32_t* status_word, void* stream);
+
 /* Static description of a status code.  Never NULL. */
 const char* kda_status_string(kda_status s);
 

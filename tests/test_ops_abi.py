@@ -64,5 +64,28 @@ def test_norm_refusals(lib):
     assert call_norm(lib, rows=0, x=0, y=0) == 0                              # nothing to do
 
 
+def call_linear(lib, M=4, N=128, K=64, x=FAKE, w=FAKE, b=None, r=None, xs=None, ws=None, y=FAKE, word=None, opts=None,
+                **kw):
+    o = binding.LinearOpts(**kw) if opts is None else opts
+    return lib.kda_linear(P(x), P(w), P(b), P(r), P(xs), P(ws), P(y), M, N, K, ctypes.byref(o) if o else None, P(word),
+                          None)
+
+
+def test_linear_refusals(lib):
+    assert call_linear(lib, opts=False) == 1
+    assert call_linear(lib, M=-1) == 1 and call_linear(lib, N=0) == 1 and call_linear(lib, K=0) == 1
+    for kw in (dict(io_dtype=2), dict(io_dtype=4), dict(out_dtype=3), dict(act=5), dict(act=-1), dict(reserved=1),
+               dict(io_dtype=3), dict(io_dtype=3, xs=FAKE), dict(xs=FAKE), dict(ws=FAKE), dict(x_stride=63),
+               dict(w_stride=8), dict(residual_stride=127), dict(y_stride=-128)):
+        assert call_linear(lib, **kw) == 1, kw
+    assert call_linear(lib, x=0) == 1 and call_linear(lib, w=0) == 1 and call_linear(lib, y=0) == 1
+    assert call_linear(lib, x=FAKE + 8) == 3 and call_linear(lib, w=FAKE + 2) == 3 and call_linear(lib, K=63) == 3
+    assert call_linear(lib, x_stride=68) == 3 and call_linear(lib, w_stride=65) == 3
+    assert call_linear(lib, y=FAKE + 1) == 3 and call_linear(lib, r=FAKE + 1) == 3 and call_linear(lib, b=FAKE + 2) == 3
+    assert call_linear(lib, word=FAKE + 2) == 3
+    assert call_linear(lib, M=1 << 31) == 2 and call_linear(lib, N=1 << 31) == 2
+    assert call_linear(lib, M=0, x=0, y=0) == 0                               # nothing to do
+
+
 def test_bad_slots_has_a_name():
     assert "slot" in kda.status_string(8) and binding.STATUS_NAMES[8] == "KDA_ERR_BAD_SLOTS"
