@@ -15,82 +15,14 @@
 // tiles, a cluster of CTAs shares one tile: each takes a slice of k, and they
 // join their fp32 sums through distributed shared memory, in rank order, each
 // CTA finishing a part of the tokens.
-#include <cuda.h>
-
-#include "internal.h"
-#include "layer_ops.cuh"
-#include "ptx.cuh"
-#include "tensormap.h"
+#include "linear.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kLinThreads = 128;
 constexpr int kFeatures = 128;      // rows of w per tile
-constexpr int kRowBytes = 128;      // bytes of k per stage: 64 16-bit or 128 8-bit elements
-constexpr int kSmemMax = 227 * 1024;
 constexpr int kMaxStages = 12;
-
-struct LinArgs {
-    CUtensorMap tm_w, tm_x;  // 2-D {k, rows}
-    const float* bias;       // or null
-    const void* residual;    // out type, or null
-    const float *x_scale, *w_scale;  // e4m3 only
-    void* y;
-    int32_t* status;         // or null
-    int64_t ldr, ldy;        // elements between rows
-    int M, N, kblocks;
-    uint32_t idesc;
-    int out, act;
-};
-
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], "
-        "%1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Instruction descriptor with e4m3 A and B (format 0), fp32 D, both K-major.
-constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-    case KDA_ACT_SILU: return v / (1.f + expf(-v));
-    case KDA_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case KDA_ACT_SIGMOID: return 1.f / (1.f + expf(-v));
-    case KDA_ACT_LOGSIGMOID: return fminf(v, 0.f) - log1pf(expf(-fabsf(v)));
-    default: return v;
-    }
-}
-__device__ __forceinline__ float load_out(const void* p, int64_t at, int dtype) {
-    if (dtype == KDA_DTYPE_F32) return static_cast<const float*>(p)[at];
-    const uint16_t w = static_cast<const uint16_t*>(p)[at];
-    return dtype == KDA_DTYPE_F16 ? from_b16<true>(w) : from_b16<false>(w);
-}
-__device__ __forceinline__ void store_out(void* p, int64_t at, float v, int dtype) {
-    if (dtype == KDA_DTYPE_F32) static_cast<float*>(p)[at] = v;
-    else static_cast<uint16_t*>(p)[at] = to_b16(v, dtype == KDA_DTYPE_F16);
-}
 
 template <int NT>
 struct LinShape {
@@ -194,7 +126,8 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     const int tokens = min(NT, a.M - m0);
     auto finish = [&](float v, int m) {
         if (F8) v *= a.x_scale[m] * ws;
-        v = activate(v + bias, a.act);
+        v += bias;
+        activate_all<1>(&v, a.act);
         if (a.residual) v += load_out(a.residual, (int64_t)m * a.ldr + n, a.out);
         store_out(a.y, (int64_t)m * a.ldy + n, v, a.out);
     };
@@ -272,17 +205,6 @@ cudaError_t launch(const LinArgs& a, bool f8, int log_split, cudaStream_t s) {
     return f8 ? launch<NT, true>(a, log_split, s) : launch<NT, false>(a, log_split, s);
 }
 
-bool rows_map(CUtensorMap* m, int io, const void* base, int64_t rows, int64_t k, int64_t ld, int box_rows) {
-    const int es = dtype_bytes(io);
-    const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows};
-    const uint64_t strides[1] = {(uint64_t)ld * es};
-    const uint32_t box[2] = {(uint32_t)(kRowBytes / es), (uint32_t)box_rows};
-    const CUtensorMapDataType dt = io == KDA_DTYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : io == KDA_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return make_tensormap(m, dt, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 }  // namespace
 }  // namespace kda
 
@@ -315,18 +237,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
         return KDA_ERR_ALIGNMENT;
 
     const int kblocks = (int)((K * es + kRowBytes - 1) / kRowBytes);
-    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    const int64_t tiles_m = (M + nt - 1) / nt, tiles_n = (N + kFeatures - 1) / kFeatures;
-    if (tiles_m > 65535) return KDA_ERR_UNSUPPORTED;
-    // As many slices of k as fill the SMs with one CTA each, at least four stages of k in each.
-    int log_split = 0;
-    while (log_split < 3 && (tiles_m * tiles_n << (log_split + 1)) <= device_sm_count() &&
-           kblocks >> (log_split + 1) >= 4)
-        ++log_split;
-
     LinArgs a{};
-    if (!rows_map(&a.tm_w, p.io_dtype, w, N, K, ldw, kFeatures) || !rows_map(&a.tm_x, p.io_dtype, x, M, K, ldx, nt))
-        return KDA_ERR_CUDA;
     a.bias = bias;
     a.residual = residual;
     a.x_scale = x_scale;
@@ -338,12 +249,28 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     a.M = (int)M;
     a.N = (int)N;
     a.kblocks = kblocks;
+    a.out = p.out_dtype;
+    a.act = p.act;
+    a.io = p.io_dtype;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool rows_on_16 = is_aligned(y, 16) && ldy * oes % 16 == 0 &&
+                            (!residual || (is_aligned(residual, 16) && ldr * oes % 16 == 0));
+    if (rows_on_16 && ((M + 255) / 256) * ((N + 255) / 256) >= 64)
+        return launch_linear_wide(a, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    const int64_t tiles_m = (M + nt - 1) / nt, tiles_n = (N + kFeatures - 1) / kFeatures;
+    if (tiles_m > 65535) return KDA_ERR_UNSUPPORTED;
+    // As many slices of k as fill the SMs with one CTA each, at least four stages of k in each.
+    int log_split = 0;
+    while (log_split < 3 && (tiles_m * tiles_n << (log_split + 1)) <= device_sm_count() &&
+           kblocks >> (log_split + 1) >= 4)
+        ++log_split;
+
+    if (!rows_map(&a.tm_w, p.io_dtype, w, N, K, ldw, kFeatures) || !rows_map(&a.tm_x, p.io_dtype, x, M, K, ldx, nt))
+        return KDA_ERR_CUDA;
     a.idesc = f8                             ? idesc_e4m3_f32(kFeatures, nt)
               : p.io_dtype == KDA_DTYPE_BF16 ? ptx::idesc_bf16_f32(kFeatures, nt, 0, 0)
                                              : ptx::idesc_f16_f32(kFeatures, nt, 0, 0);
-    a.out = p.out_dtype;
-    a.act = p.act;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (nt) {
     case 16: e = launch<16>(a, f8, log_split, s); break;

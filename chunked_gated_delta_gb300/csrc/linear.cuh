@@ -1,0 +1,111 @@
+// linear.cuh -- what the two kernels of kda_linear share (linear.cu: few
+// tokens, or rows of y off 16 bytes; linear_wide.cu: many tokens): arguments,
+// cluster and tcgen05 wrappers, the activations.
+#pragma once
+#include <cuda.h>
+
+#include "internal.h"
+#include "layer_ops.cuh"
+#include "ptx.cuh"
+#include "tensormap.h"
+
+namespace kda {
+
+constexpr int kRowBytes = 128;  // bytes of k per stage: 64 16-bit or 128 8-bit elements
+constexpr int kSmemMax = 227 * 1024;
+
+struct LinArgs {
+    CUtensorMap tm_w, tm_x;  // 2-D {k, rows}
+    const float* bias;       // or null
+    const void* residual;    // out type, or null
+    const float *x_scale, *w_scale;  // e4m3 only
+    void* y;
+    int32_t* status;         // or null
+    int64_t ldr, ldy;        // elements between rows
+    int M, N, kblocks;
+    uint32_t idesc;
+    int out, act, io;
+};
+
+// The kernel for many tokens (linear_wide.cu).  Takes the arguments with tm_w,
+// tm_x and idesc unset; x, w are the operands and ldx, ldw their row strides.
+cudaError_t launch_linear_wide(LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldx, int64_t ldw,
+                               cudaStream_t s);
+
+namespace {
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], "
+        "%1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor with e4m3 A and B (format 0), fp32 D, both K-major.
+constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <int ACT>
+__device__ __forceinline__ float activated(float v) {
+    if constexpr (ACT == KDA_ACT_SILU) return v / (1.f + expf(-v));
+    if constexpr (ACT == KDA_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    if constexpr (ACT == KDA_ACT_SIGMOID) return 1.f / (1.f + expf(-v));
+    if constexpr (ACT == KDA_ACT_LOGSIGMOID) return fminf(v, 0.f) - log1pf(expf(-fabsf(v)));
+    return v;
+}
+template <int ACT, int COUNT>
+__device__ __forceinline__ void activated_all(float* v) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) v[i] = activated<ACT>(v[i]);
+}
+// One branch for all of a thread's values.
+template <int COUNT>
+__device__ __forceinline__ void activate_all(float* v, int act) {
+    switch (act) {
+    case KDA_ACT_SILU: activated_all<KDA_ACT_SILU, COUNT>(v); break;
+    case KDA_ACT_GELU: activated_all<KDA_ACT_GELU, COUNT>(v); break;
+    case KDA_ACT_SIGMOID: activated_all<KDA_ACT_SIGMOID, COUNT>(v); break;
+    case KDA_ACT_LOGSIGMOID: activated_all<KDA_ACT_LOGSIGMOID, COUNT>(v); break;
+    }
+}
+__device__ __forceinline__ float load_out(const void* p, int64_t at, int dtype) {
+    if (dtype == KDA_DTYPE_F32) return static_cast<const float*>(p)[at];
+    const uint16_t w = static_cast<const uint16_t*>(p)[at];
+    return dtype == KDA_DTYPE_F16 ? from_b16<true>(w) : from_b16<false>(w);
+}
+__device__ __forceinline__ void store_out(void* p, int64_t at, float v, int dtype) {
+    if (dtype == KDA_DTYPE_F32) static_cast<float*>(p)[at] = v;
+    else static_cast<uint16_t*>(p)[at] = to_b16(v, dtype == KDA_DTYPE_F16);
+}
+
+inline bool rows_map(CUtensorMap* m, int io, const void* base, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+    const int es = dtype_bytes(io);
+    const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)ld * es};
+    const uint32_t box[2] = {(uint32_t)(kRowBytes / es), (uint32_t)box_rows};
+    const CUtensorMapDataType dt = io == KDA_DTYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : io == KDA_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return make_tensormap(m, dt, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+}  // namespace kda

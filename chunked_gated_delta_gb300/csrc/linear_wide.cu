@@ -1,0 +1,366 @@
+// linear_wide.cu -- the kernel of kda_linear for many tokens.
+//
+// A pair of CTAs (a cluster of two, on two SMs that share a tensor-core pair)
+// makes 256 tokens x 256 features at a time with cta_group::2 MMAs: each CTA
+// loads 128 rows of x and 128 rows of w, its tensor core reads both CTAs' w,
+// and it accumulates its own 128 tokens x 256 features in TMEM.  That halves
+// the shared-memory and L2 reads of w per flop against a CTA by itself.  The
+// pairs are persistent; each has two accumulators (all 512 columns of TMEM),
+// so the epilogue of a tile runs beside the MMAs of the next.
+//
+// Roles per CTA: warp 0 loads (TMA, a ring of kStages stages), warp 1 of the
+// first CTA issues the MMAs of both, warps 2-9 are the epilogue: warp w has
+// the 32 tokens of TMEM lane quarter w % 4 and one half of the features.  A
+// thread has a token's row; 128-byte row pieces go through a swizzled staging
+// box per warp, which TMA loads the residual into and stores y from, so
+// global memory sees whole lines and ragged edges are clipped by the copy.
+#include "linear.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kTileM = 256, kTileN = 256;  // per pair
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 128 * kRowBytes;         // one CTA's part of x or of w in a stage
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpilogueWarps = 8;
+constexpr int kBoxBytes = 32 * 128;                    // 32 tokens x 128 bytes
+constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kSmemBytes = kStages * kStageBytes + kEpilogueWarps * kBoxBytes + 1024;
+constexpr int kGroup = 8;                              // token tiles that share a sweep over the features
+
+struct WideArgs {
+    LinArgs a;
+    CUtensorMap tm_y, tm_r;  // boxes of 128 bytes x 32 rows
+    int tiles_m, tiles_n;
+};
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(m), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+template <bool F8>
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    if constexpr (F8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f8f6f4 [%0], "
+            "%1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], "
+            "%1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+            "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(ptx::smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+// Tile t of the sweep: groups of kGroup token tiles, the features outside, the group's tokens inside.
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int* tm, int* tn) {
+    const int per = kGroup * tiles_n;
+    const int g = t / per, first = g * kGroup, rows = min(kGroup, tiles_m - first);
+    const int in = t - g * per;
+    *tn = in / rows;
+    *tm = first + in - *tn * rows;
+}
+
+// OUT16: y is bf16 or fp16 (64 columns a box), else fp32 (32 columns a box).
+template <bool F8, bool OUT16>
+__global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __grid_constant__ WideArgs p) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], res[kEpilogueWarps];
+    __shared__ uint32_t tmem_base;
+    __shared__ int s_fail;
+    uint8_t* ring = ptx::align_smem_1024(raw);
+    const LinArgs& a = p.a;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int tiles = p.tiles_m * p.tiles_n;
+
+    if (tid == 0) {
+        ptx::prefetch_tmap(&a.tm_w);
+        ptx::prefetch_tmap(&a.tm_x);
+        ptx::prefetch_tmap(&p.tm_y);
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&acc_full[b], 1);
+            ptx::mbar_init(&acc_empty[b], 2 * kEpilogueWarps);
+        }
+        for (int w = 0; w < kEpilogueWarps; ++w) ptx::mbar_init(&res[w], 1);
+        ptx::fence_mbar_init();
+        s_fail = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         ptx::smem_u32(&tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are set before either signals the other's
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;  // stages issued
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int tm, tn;
+                tile_at(t, p.tiles_m, p.tiles_n, &tm, &tn);
+                const int m = tm * kTileM + (int)rank * 128, n = tn * kTileN + (int)rank * 128;
+                for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                    const int s = it % kStages, round = it / kStages;
+                    if (round > 0 && !(ok = ptx::mbar_wait(&empty[s], (round - 1) & 1, kWaitLimitNs))) break;
+                    uint8_t* x = ring + s * kStageBytes;
+                    const int k = kb * (F8 ? kRowBytes : kRowBytes / 2);
+                    // the first CTA's barrier counts the bytes of both
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                    const uint32_t bar = peer_smem(ptx::smem_u32(&full[s]), 0);
+                    tma_load_pair(x, &a.tm_x, bar, k, m);
+                    tma_load_pair(x + kOperandBytes, &a.tm_w, bar, k, n);
+                }
+            }
+            if (!ok) {  // let the copies in flight land (the first CTA sees both CTAs' bytes)
+                s_fail = 1;
+                if (rank == 0)
+                    for (int i = max(0, it - kStages); i < it; ++i)
+                        ptx::mbar_wait(&full[i % kStages], (i / kStages) & 1, kWaitLimitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int it = 0, n_acc = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs, ++n_acc) {
+                const int b = n_acc & 1;
+                if (n_acc >= 2 && !(ok = wait_cluster(&acc_empty[b], ((n_acc >> 1) - 1) & 1, kWaitLimitNs))) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(b * kTileN);
+                for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!(ok = ptx::mbar_wait(&full[s], (it / kStages) & 1, kWaitLimitNs))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t x = ptx::smem_u32(ring + s * kStageBytes);
+                    const uint64_t da = ptx::smem_desc(x, 0, 1024), db = ptx::smem_desc(x + kOperandBytes, 0, 1024);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // 32 bytes of k each
+                        mma_pair<F8>(d, da + 2 * j, db + 2 * j, a.idesc, kb > 0 || j > 0);
+                    commit_pair(&empty[s]);
+                }
+                if (ok) commit_pair(&acc_full[b]);
+            }
+            if (!ok) s_fail = 1;
+        }
+    } else {
+        constexpr int kBoxCols = OUT16 ? 64 : 32;
+        constexpr int kBoxes = 128 / kBoxCols;
+        const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+        uint8_t* box = ring + kStages * kStageBytes + e * kBoxBytes;
+        uint8_t* row = box + lane * 128;
+        const bool f16 = a.out == KDA_DTYPE_F16;
+        int n_acc = 0;
+        uint32_t loads = 0, asked = 0;  // residual boxes that arrived, and that were asked for (lane 0)
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs, ++n_acc) {
+            int tm, tn;
+            tile_at(t, p.tiles_m, p.tiles_n, &tm, &tn);
+            const int b = n_acc & 1;
+            const int m0 = tm * kTileM + (int)rank * 128 + quarter * 32, n0 = tn * kTileN + half * 128;
+            float bias[4], scale[4];  // of features n0 + 32 i + lane, handed round by shuffles
+            float xs = 1.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = n0 + 32 * i + lane;
+                bias[i] = a.bias && n < a.N ? a.bias[n] : 0.f;
+                scale[i] = F8 && n < a.N ? a.w_scale[n] : 1.f;
+            }
+            if (F8 && m0 + lane < a.M) xs = a.x_scale[m0 + lane];
+            const bool rows = m0 < a.M;
+            auto load_residual = [&](int n) {
+                if (lane == 0) {
+                    ptx::bulk_wait_read0();  // the box's last store has read it
+                    ptx::mbar_arrive_expect_tx(&res[e], kBoxBytes);
+                    ptx::tma_load_2d(box, &p.tm_r, &res[e], n, m0);
+                    ++asked;
+                }
+            };
+            if (a.residual && rows && n0 < a.N) load_residual(n0);
+            ok = __all_sync(~0u, ptx::mbar_wait(&acc_full[b], (n_acc >> 1) & 1, 2 * kWaitLimitNs));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * kTileN + half * 128);
+#pragma unroll
+            for (int q = 0; q < kBoxes; ++q) {
+                const int n = n0 + q * kBoxCols;
+                const bool live = rows && n < a.N;
+                float v[kBoxCols];
+#pragma unroll
+                for (int c = 0; c < kBoxCols; c += 16) ptx::tmem_ld16(acc + q * kBoxCols + c, v + c);
+                ptx::tmem_ld_wait();
+                if (q == kBoxes - 1) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(peer_smem(ptx::smem_u32(&acc_empty[b]), 0));
+                }
+                if (!live) continue;
+#pragma unroll
+                for (int c = 0; c < kBoxCols; ++c) {
+                    const int i = (q * kBoxCols + c) >> 5, from = (q * kBoxCols + c) & 31;
+                    if (F8) v[c] *= xs * __shfl_sync(~0u, scale[i], from);
+                    v[c] += __shfl_sync(~0u, bias[i], from);
+                }
+                activate_all<kBoxCols>(v, a.act);
+                if (a.residual) {
+                    ok = __all_sync(~0u, ptx::mbar_wait(&res[e], loads & 1, kWaitLimitNs));
+                    if (!ok) break;
+                    ++loads;
+                } else {
+                    if (lane == 0) ptx::bulk_wait_read0();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // 16-byte pieces of the row, swizzled
+                    uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
+                    if constexpr (OUT16) {
+                        float* f = v + 8 * j;
+                        if (a.residual) {
+                            const uint4 u = *at;
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 r = f16 ? from_b16x2<true>(w[i]) : from_b16x2<false>(w[i]);
+                                f[2 * i] += r.x;
+                                f[2 * i + 1] += r.y;
+                            }
+                        }
+                        *at = make_uint4(pack_b16x2(f[0], f[1], f16), pack_b16x2(f[2], f[3], f16),
+                                         pack_b16x2(f[4], f[5], f16), pack_b16x2(f[6], f[7], f16));
+                    } else {
+                        float4 f = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        if (a.residual) {
+                            const float4 r = *reinterpret_cast<float4*>(at);
+                            f.x += r.x;
+                            f.y += r.y;
+                            f.z += r.z;
+                            f.w += r.w;
+                        }
+                        *reinterpret_cast<float4*>(at) = f;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::tma_store_2d(&p.tm_y, box, n, m0);
+                    ptx::bulk_commit();
+                }
+                if (a.residual && q + 1 < kBoxes && n + kBoxCols < a.N) load_residual(n + kBoxCols);
+            }
+        }
+        if (!ok) s_fail = 1;
+        if (lane == 0) {
+            if (asked != loads) ptx::mbar_wait(&res[e], loads & 1, kWaitLimitNs);
+            ptx::bulk_wait0();
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the other may still signal or read it
+    ptx::tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (s_fail && tid == 0 && a.status) atomicOr(a.status, kStatusTimeout);
+}
+
+bool box_map(CUtensorMap* m, int dtype, const void* base, int64_t M, int64_t N, int64_t ld) {
+    const int es = dtype_bytes(dtype);
+    const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M};
+    const uint64_t strides[1] = {(uint64_t)ld * es};
+    const uint32_t box[2] = {(uint32_t)(128 / es), 32};
+    const CUtensorMapDataType dt = dtype == KDA_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == KDA_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return make_tensormap(m, dt, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool F8, bool OUT16>
+cudaError_t launch(const WideArgs& p, cudaStream_t s) {
+    auto kern = kda_linear_wide_kernel<F8, OUT16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = device_sm_count() / 2;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_wide(LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldx, int64_t ldw,
+                               cudaStream_t s) {
+    WideArgs p{};
+    if (!rows_map(&a.tm_x, a.io, x, a.M, K, ldx, 128) || !rows_map(&a.tm_w, a.io, w, a.N, K, ldw, 128) ||
+        !box_map(&p.tm_y, a.out, a.y, a.M, a.N, a.ldy) ||
+        (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr)))
+        return cudaErrorInvalidValue;
+    const bool f8 = a.io == KDA_DTYPE_E4M3;
+    a.idesc = f8                        ? idesc_e4m3_f32(kTileM, kTileN)
+              : a.io == KDA_DTYPE_BF16 ? ptx::idesc_bf16_f32(kTileM, kTileN, 0, 0)
+                                       : ptx::idesc_f16_f32(kTileM, kTileN, 0, 0);
+    if ((((int64_t)a.M + kTileM - 1) / kTileM) * (((int64_t)a.N + kTileN - 1) / kTileN) > INT32_MAX)
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.tiles_m = (a.M + kTileM - 1) / kTileM;
+    p.tiles_n = (a.N + kTileN - 1) / kTileN;
+    const bool out16 = a.out != KDA_DTYPE_F32;
+    if (f8) return out16 ? launch<true, true>(p, s) : launch<true, false>(p, s);
+    return out16 ? launch<false, true>(p, s) : launch<false, false>(p, s);
+}
+
+}  // namespace kda
