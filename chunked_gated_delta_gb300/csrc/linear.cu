@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     __shared__ int s_fail;
     uint8_t* ring = ptx::align_smem_1024(raw);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
     const int split = 1 << log_split;
     const int rank = log_split ? (int)cluster_rank() : 0;
     const int n0 = (int)(blockIdx.x >> log_split) * kFeatures;
@@ -73,12 +73,12 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         int issued = 0;
         bool ok = true;
         for (; issued < count; ++issued) {
             const int s = issued % kStages, round = issued / kStages;
-            if (round > 0 && !ptx::mbar_wait(&empty[s], (round - 1) & 1, kWaitLimitNs)) {
+            if (round > 0 && !wait_for(&empty[s], (round - 1) & 1)) {
                 ok = false;
                 break;
             }
@@ -91,13 +91,13 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
         if (!ok) {  // let the copies in flight land before the CTA unwinds
             s_fail = 1;
             for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                ptx::mbar_wait(&full[i % kStages], (i / kStages) & 1, kWaitLimitNs);
+                wait_for(&full[i % kStages], (i / kStages) & 1);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         bool ok = true;
         for (int i = 0; i < count && ok; ++i) {
             const int s = i % kStages;
-            ok = ptx::mbar_wait(&full[s], (i / kStages) & 1, kWaitLimitNs);
+            ok = wait_for(&full[s], (i / kStages) & 1);
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t w = ptx::smem_u32(ring + s * Shape::kStageBytes);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
         else s_fail = 1;
     }
     __syncwarp();
-    if (!ptx::mbar_wait(&done, 0, 2 * kWaitLimitNs)) s_fail = 1;
+    if (!wait_for(&done, 0, 2 * kWaitLimitNs)) s_fail = 1;
     ptx::tc_fence_after();
     __syncthreads();
     bool fail = s_fail != 0;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     auto finish = [&](float v, int m) {
         if (F8) v *= a.x_scale[m] * ws;
         v += bias;
-        activate_all<1>(&v, a.act);
+        activate_all<1, false>(&v, a.act);
         if (a.residual) v += load_out(a.residual, (int64_t)m * a.ldr + n, a.out);
         store_out(a.y, (int64_t)m * a.ldy + n, v, a.out);
     };
@@ -256,7 +256,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     const bool rows_on_16 = is_aligned(y, 16) && ldy * oes % 16 == 0 &&
                             (!residual || (is_aligned(residual, 16) && ldr * oes % 16 == 0));
     if (rows_on_16 && ((M + 255) / 256) * ((N + 255) / 256) >= 64)
-        return launch_linear_wide(a, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        return launch_linear_wide(a, 256, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
     const int64_t tiles_m = (M + nt - 1) / nt, tiles_n = (N + kFeatures - 1) / kFeatures;
     if (tiles_m > 65535) return KDA_ERR_UNSUPPORTED;

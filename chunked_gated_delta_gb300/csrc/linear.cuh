@@ -27,10 +27,11 @@ struct LinArgs {
     int out, act, io;
 };
 
-// The kernel for many tokens (linear_wide.cu).  Takes the arguments with tm_w,
-// tm_x and idesc unset; x, w are the operands and ldx, ldw their row strides.
-cudaError_t launch_linear_wide(LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldx, int64_t ldw,
-                               cudaStream_t s);
+// The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile; an
+// fp32 y takes 128.  tm_w, tm_x and idesc are set there; x, w are the operands and
+// ldx, ldw their row strides.
+cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
+                               int64_t ldw, cudaStream_t s);
 
 namespace {
 
@@ -45,6 +46,43 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
 // Instruction descriptor with e4m3 A and B (format 0), fp32 D, both K-major.
 constexpr uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Waits for the phase with this parity, for kWaitLimitNs at most.  The clock is
+// read only after a thousand tries: a read costs more than a stage's wait.
+// CLUSTER: the arrivals may come from the other CTA of a pair.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+            "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(ptx::smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        ok = ptx::mbar_try_wait(bar, parity);
+    return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 1024; ++i)
+            if (try_wait<CLUSTER>(bar, parity)) return true;
+        const uint64_t t = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
+}
+// One lane of a converged warp.  Unlike a test of the lane number it tells the
+// compiler that a single thread runs what follows, so that TMA and tcgen05
+// instructions take their operands from uniform registers without a loop.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -63,27 +101,42 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int ACT>
+// FAST: y has 16 bits, whose rounding (2^-9 or 2^-12) hides the few 2^-23 of the
+// approximate exponential and quotient; else they are within an ulp or two.
+template <int ACT, bool FAST>
 __device__ __forceinline__ float activated(float v) {
-    if constexpr (ACT == KDA_ACT_SILU) return v / (1.f + expf(-v));
+    if constexpr (ACT == KDA_ACT_SILU) return FAST ? __fdividef(v, 1.f + __expf(-v)) : v / (1.f + expf(-v));
     if constexpr (ACT == KDA_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if constexpr (ACT == KDA_ACT_SIGMOID) return 1.f / (1.f + expf(-v));
-    if constexpr (ACT == KDA_ACT_LOGSIGMOID) return fminf(v, 0.f) - log1pf(expf(-fabsf(v)));
+    if constexpr (ACT == KDA_ACT_SIGMOID) return FAST ? __fdividef(1.f, 1.f + __expf(-v)) : 1.f / (1.f + expf(-v));
+    if constexpr (ACT == KDA_ACT_LOGSIGMOID) {
+        // min(v, 0) - log(1 + e), e = exp(-|v|) in [0, 1]: log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3,
+        // by artanh's series s + s^3/3 + ... + s^15/15 (the rest is below 2^-27 of it)
+        const float e = FAST ? __expf(-fabsf(v)) : expf(-fabsf(v));
+        const float s = __fdividef(e, 2.f + e), z = s * s;
+        float r = 1.f / 15.f;
+        r = fmaf(r, z, 1.f / 13.f);
+        r = fmaf(r, z, 1.f / 11.f);
+        r = fmaf(r, z, 1.f / 9.f);
+        r = fmaf(r, z, 1.f / 7.f);
+        r = fmaf(r, z, 1.f / 5.f);
+        r = fmaf(r, z, 1.f / 3.f);
+        return fminf(v, 0.f) - 2.f * fmaf(s * z, r, s);
+    }
     return v;
 }
-template <int ACT, int COUNT>
+template <int ACT, int COUNT, bool FAST>
 __device__ __forceinline__ void activated_all(float* v) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] = activated<ACT>(v[i]);
+    for (int i = 0; i < COUNT; ++i) v[i] = activated<ACT, FAST>(v[i]);
 }
 // One branch for all of a thread's values.
-template <int COUNT>
+template <int COUNT, bool FAST>
 __device__ __forceinline__ void activate_all(float* v, int act) {
     switch (act) {
-    case KDA_ACT_SILU: activated_all<KDA_ACT_SILU, COUNT>(v); break;
-    case KDA_ACT_GELU: activated_all<KDA_ACT_GELU, COUNT>(v); break;
-    case KDA_ACT_SIGMOID: activated_all<KDA_ACT_SIGMOID, COUNT>(v); break;
-    case KDA_ACT_LOGSIGMOID: activated_all<KDA_ACT_LOGSIGMOID, COUNT>(v); break;
+    case KDA_ACT_SILU: activated_all<KDA_ACT_SILU, COUNT, FAST>(v); break;
+    case KDA_ACT_GELU: activated_all<KDA_ACT_GELU, COUNT, FAST>(v); break;
+    case KDA_ACT_SIGMOID: activated_all<KDA_ACT_SIGMOID, COUNT, FAST>(v); break;
+    case KDA_ACT_LOGSIGMOID: activated_all<KDA_ACT_LOGSIGMOID, COUNT, FAST>(v); break;
     }
 }
 __device__ __forceinline__ float load_out(const void* p, int64_t at, int dtype) {

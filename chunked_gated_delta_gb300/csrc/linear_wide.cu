@@ -19,15 +19,22 @@
 namespace kda {
 namespace {
 
-constexpr int kTileM = 256, kTileN = 256;  // per pair
-constexpr int kStages = 6;
-constexpr int kOperandBytes = 128 * kRowBytes;         // one CTA's part of x or of w in a stage
-constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kTileM = 256;                            // tokens per pair
 constexpr int kEpilogueWarps = 8;
 constexpr int kBoxBytes = 32 * 128;                    // 32 tokens x 128 bytes
 constexpr int kThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kSmemBytes = kStages * kStageBytes + kEpilogueWarps * kBoxBytes + 1024;
 constexpr int kGroup = 8;                              // token tiles that share a sweep over the features
+constexpr int kSegment = 16;                           // stages of k per accumulator where y is fp32
+
+// TN: features per pair, 256 or 128.
+template <int TN>
+struct WideShape {
+    static constexpr int kXBytes = 128 * kRowBytes;                  // one CTA's part of x in a stage
+    static constexpr int kStageBytes = kXBytes + TN / 2 * kRowBytes;  // and of w
+    static constexpr int kStages = TN == 256 ? 6 : 8;
+    static constexpr int kAccs = 512 / TN;                            // accumulators in TMEM
+    static constexpr int kSmem = kStages * kStageBytes + kEpilogueWarps * kBoxBytes + 1024;
+};
 
 struct WideArgs {
     LinArgs a;
@@ -69,19 +76,11 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
-            "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(ptx::smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (ptx::globaltimer_ns() - t0 > limit_ns) return false;
-    }
+// A warp has read its part of an accumulator: the first CTA may fill it again.
+__device__ __forceinline__ void release(uint64_t* acc_empty, int lane) {
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_remote(peer_smem(ptx::smem_u32(acc_empty), 0));
 }
 
 // Tile t of the sweep: groups of kGroup token tiles, the features outside, the group's tokens inside.
@@ -93,17 +92,24 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int* tm
     *tm = first + in - *tn * rows;
 }
 
-// OUT16: y is bf16 or fp16 (64 columns a box), else fp32 (32 columns a box).
-template <bool F8, bool OUT16>
+// OUT16: y is bf16 or fp16 (64 columns a box), else fp32 (32 columns a box).  An
+// fp32 y gets more of the sum's accuracy: the tensor cores' own additions drop
+// bits below the running sum, so k is cut into segments of kSegment stages,
+// each in an accumulator of its own, that the epilogue adds in registers.
+template <int TN, bool F8, bool OUT16>
 __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __grid_constant__ WideArgs p) {
+    using Shape = WideShape<TN>;
+    constexpr int kStages = Shape::kStages, kStageBytes = Shape::kStageBytes, kAccs = Shape::kAccs;
+    constexpr bool kSegments = !OUT16;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], res[kEpilogueWarps];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], acc_full[kAccs], acc_empty[kAccs];
+    __shared__ __align__(8) uint64_t res[kEpilogueWarps];
     __shared__ uint32_t tmem_base;
     __shared__ int s_fail;
     uint8_t* ring = ptx::align_smem_1024(raw);
     const LinArgs& a = p.a;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     const int tiles = p.tiles_m * p.tiles_n;
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kAccs; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
             ptx::mbar_init(&acc_empty[b], 2 * kEpilogueWarps);
         }
@@ -138,75 +144,81 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
     const uint32_t tmem = tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int it = 0;  // stages issued
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 int tm, tn;
                 tile_at(t, p.tiles_m, p.tiles_n, &tm, &tn);
-                const int m = tm * kTileM + (int)rank * 128, n = tn * kTileN + (int)rank * 128;
+                const int m = tm * kTileM + (int)rank * 128, n = tn * TN + (int)rank * (TN / 2);
                 for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
                     const int s = it % kStages, round = it / kStages;
-                    if (round > 0 && !(ok = ptx::mbar_wait(&empty[s], (round - 1) & 1, kWaitLimitNs))) break;
+                    if (round > 0 && !(ok = wait_for(&empty[s], (round - 1) & 1))) break;
                     uint8_t* x = ring + s * kStageBytes;
                     const int k = kb * (F8 ? kRowBytes : kRowBytes / 2);
                     // the first CTA's barrier counts the bytes of both
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
                     const uint32_t bar = peer_smem(ptx::smem_u32(&full[s]), 0);
                     tma_load_pair(x, &a.tm_x, bar, k, m);
-                    tma_load_pair(x + kOperandBytes, &a.tm_w, bar, k, n);
+                    tma_load_pair(x + Shape::kXBytes, &a.tm_w, bar, k, n);
                 }
             }
             if (!ok) {  // let the copies in flight land (the first CTA sees both CTAs' bytes)
                 s_fail = 1;
                 if (rank == 0)
                     for (int i = max(0, it - kStages); i < it; ++i)
-                        ptx::mbar_wait(&full[i % kStages], (i / kStages) & 1, kWaitLimitNs);
+                        wait_for(&full[i % kStages], (i / kStages) & 1);
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && elect_one()) {
             int it = 0, n_acc = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++n_acc) {
-                const int b = n_acc & 1;
-                if (n_acc >= 2 && !(ok = wait_cluster(&acc_empty[b], ((n_acc >> 1) - 1) & 1, kWaitLimitNs))) break;
-                ptx::tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(b * kTileN);
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
+                    const bool opens = kSegments ? kb % kSegment == 0 : kb == 0;
+                    const int b = n_acc % kAccs, round = n_acc / kAccs;
+                    if (opens) {
+                        if (round > 0 && !(ok = wait_for<true>(&acc_empty[b], (round - 1) & 1))) break;
+                        ptx::tc_fence_after();
+                    }
                     const int s = it % kStages;
-                    if (!(ok = ptx::mbar_wait(&full[s], (it / kStages) & 1, kWaitLimitNs))) break;
+                    if (!(ok = wait_for(&full[s], (it / kStages) & 1))) break;
                     ptx::tc_fence_after();
                     const uint32_t x = ptx::smem_u32(ring + s * kStageBytes);
-                    const uint64_t da = ptx::smem_desc(x, 0, 1024), db = ptx::smem_desc(x + kOperandBytes, 0, 1024);
+                    const uint64_t da = ptx::smem_desc(x, 0, 1024), db = ptx::smem_desc(x + Shape::kXBytes, 0, 1024);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // 32 bytes of k each
-                        mma_pair<F8>(d, da + 2 * j, db + 2 * j, a.idesc, kb > 0 || j > 0);
+                        mma_pair<F8>(tmem + (uint32_t)(b * TN), da + 2 * j, db + 2 * j, a.idesc, !opens || j > 0);
                     commit_pair(&empty[s]);
+                    if (kb + 1 == a.kblocks || (kSegments && (kb + 1) % kSegment == 0)) {
+                        commit_pair(&acc_full[b]);
+                        ++n_acc;
+                    }
                 }
-                if (ok) commit_pair(&acc_full[b]);
             }
             if (!ok) s_fail = 1;
         }
     } else {
+        constexpr int kCols = TN / 2;  // features of a warp
         constexpr int kBoxCols = OUT16 ? 64 : 32;
-        constexpr int kBoxes = 128 / kBoxCols;
+        constexpr int kBoxes = kCols / kBoxCols;
         const int e = warp - 2, quarter = warp & 3, half = e >> 2;
         uint8_t* box = ring + kStages * kStageBytes + e * kBoxBytes;
         uint8_t* row = box + lane * 128;
         const bool f16 = a.out == KDA_DTYPE_F16;
+        const int segments = kSegments ? (a.kblocks + kSegment - 1) / kSegment : 1;
         int n_acc = 0;
         uint32_t loads = 0, asked = 0;  // residual boxes that arrived, and that were asked for (lane 0)
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, ++n_acc) {
+        for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             tile_at(t, p.tiles_m, p.tiles_n, &tm, &tn);
-            const int b = n_acc & 1;
-            const int m0 = tm * kTileM + (int)rank * 128 + quarter * 32, n0 = tn * kTileN + half * 128;
-            float bias[4], scale[4];  // of features n0 + 32 i + lane, handed round by shuffles
+            const int m0 = tm * kTileM + (int)rank * 128 + quarter * 32, n0 = tn * TN + half * kCols;
+            float bias[kCols / 32], scale[kCols / 32];  // of features n0 + 32 i + lane, handed round by shuffles
             float xs = 1.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kCols / 32; ++i) {
                 const int n = n0 + 32 * i + lane;
                 bias[i] = a.bias && n < a.N ? a.bias[n] : 0.f;
                 scale[i] = F8 && n < a.N ? a.w_scale[n] : 1.f;
@@ -222,22 +234,40 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                 }
             };
             if (a.residual && rows && n0 < a.N) load_residual(n0);
-            ok = __all_sync(~0u, ptx::mbar_wait(&acc_full[b], (n_acc >> 1) & 1, 2 * kWaitLimitNs));
+            float sum[kSegments ? kCols : 1];
+            uint32_t acc = 0;
+            for (int g = 0; g < segments; ++g, ++n_acc) {
+                const int b = n_acc % kAccs;
+                ok = __all_sync(~0u, wait_for(&acc_full[b], (n_acc / kAccs) & 1, 2 * kWaitLimitNs));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * TN + half * kCols);
+                if constexpr (kSegments) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 16) {
+                        float v[16];
+                        ptx::tmem_ld16(acc + c, v);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[c + j] = g ? sum[c + j] + v[j] : v[j];
+                    }
+                    release(&acc_empty[b], lane);
+                }
+            }
             if (!ok) break;
-            ptx::tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * kTileN + half * 128);
 #pragma unroll
             for (int q = 0; q < kBoxes; ++q) {
                 const int n = n0 + q * kBoxCols;
                 const bool live = rows && n < a.N;
                 float v[kBoxCols];
+                if constexpr (kSegments) {
 #pragma unroll
-                for (int c = 0; c < kBoxCols; c += 16) ptx::tmem_ld16(acc + q * kBoxCols + c, v + c);
-                ptx::tmem_ld_wait();
-                if (q == kBoxes - 1) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_remote(peer_smem(ptx::smem_u32(&acc_empty[b]), 0));
+                    for (int c = 0; c < kBoxCols; ++c) v[c] = sum[q * kBoxCols + c];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kBoxCols; c += 16) ptx::tmem_ld16(acc + q * kBoxCols + c, v + c);
+                    ptx::tmem_ld_wait();
+                    if (q == kBoxes - 1) release(&acc_empty[(n_acc - 1) % kAccs], lane);
                 }
                 if (!live) continue;
 #pragma unroll
@@ -246,9 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                     if (F8) v[c] *= xs * __shfl_sync(~0u, scale[i], from);
                     v[c] += __shfl_sync(~0u, bias[i], from);
                 }
-                activate_all<kBoxCols>(v, a.act);
+                activate_all<kBoxCols, OUT16>(v, a.act);
                 if (a.residual) {
-                    ok = __all_sync(~0u, ptx::mbar_wait(&res[e], loads & 1, kWaitLimitNs));
+                    ok = __all_sync(~0u, wait_for(&res[e], loads & 1));
                     if (!ok) break;
                     ++loads;
                 } else {
@@ -295,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
         }
         if (!ok) s_fail = 1;
         if (lane == 0) {
-            if (asked != loads) ptx::mbar_wait(&res[e], loads & 1, kWaitLimitNs);
+            if (asked != loads) wait_for(&res[e], loads & 1);
             ptx::bulk_wait0();
         }
     }
@@ -320,12 +350,19 @@ bool box_map(CUtensorMap* m, int dtype, const void* base, int64_t M, int64_t N, 
     return make_tensormap(m, dt, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool F8, bool OUT16>
-cudaError_t launch(const WideArgs& p, cudaStream_t s) {
-    auto kern = kda_linear_wide_kernel<F8, OUT16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
+template <int TN, bool F8, bool OUT16>
+cudaError_t launch(WideArgs& p, const void* w, int64_t K, int64_t ldw, cudaStream_t s) {
+    LinArgs& a = p.a;
+    if (!rows_map(&a.tm_w, a.io, w, a.N, K, ldw, TN / 2)) return cudaErrorInvalidValue;
+    a.idesc = F8                        ? idesc_e4m3_f32(kTileM, TN)
+              : a.io == KDA_DTYPE_BF16 ? ptx::idesc_bf16_f32(kTileM, TN, 0, 0)
+                                       : ptx::idesc_f16_f32(kTileM, TN, 0, 0);
+    p.tiles_n = (a.N + TN - 1) / TN;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = device_sm_count() / 2;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    auto kern = kda_linear_wide_kernel<TN, F8, OUT16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WideShape<TN>::kSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -333,7 +370,7 @@ cudaError_t launch(const WideArgs& p, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = WideShape<TN>::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -342,25 +379,19 @@ cudaError_t launch(const WideArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear_wide(LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldx, int64_t ldw,
-                               cudaStream_t s) {
+cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
+                               int64_t ldw, cudaStream_t s) {
     WideArgs p{};
-    if (!rows_map(&a.tm_x, a.io, x, a.M, K, ldx, 128) || !rows_map(&a.tm_w, a.io, w, a.N, K, ldw, 128) ||
-        !box_map(&p.tm_y, a.out, a.y, a.M, a.N, a.ldy) ||
+    p.a = a;
+    p.tiles_m = (a.M + kTileM - 1) / kTileM;
+    if (!rows_map(&p.a.tm_x, a.io, x, a.M, K, ldx, 128) || !box_map(&p.tm_y, a.out, a.y, a.M, a.N, a.ldy) ||
         (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr)))
         return cudaErrorInvalidValue;
     const bool f8 = a.io == KDA_DTYPE_E4M3;
-    a.idesc = f8                        ? idesc_e4m3_f32(kTileM, kTileN)
-              : a.io == KDA_DTYPE_BF16 ? ptx::idesc_bf16_f32(kTileM, kTileN, 0, 0)
-                                       : ptx::idesc_f16_f32(kTileM, kTileN, 0, 0);
-    if ((((int64_t)a.M + kTileM - 1) / kTileM) * (((int64_t)a.N + kTileN - 1) / kTileN) > INT32_MAX)
-        return cudaErrorInvalidValue;
-    p.a = a;
-    p.tiles_m = (a.M + kTileM - 1) / kTileM;
-    p.tiles_n = (a.N + kTileN - 1) / kTileN;
-    const bool out16 = a.out != KDA_DTYPE_F32;
-    if (f8) return out16 ? launch<true, true>(p, s) : launch<true, false>(p, s);
-    return out16 ? launch<false, true>(p, s) : launch<false, false>(p, s);
+    if (a.out == KDA_DTYPE_F32)
+        return f8 ? launch<128, true, false>(p, w, K, ldw, s) : launch<128, false, false>(p, w, K, ldw, s);
+    if (tn == 128) return f8 ? launch<128, true, true>(p, w, K, ldw, s) : launch<128, false, true>(p, w, K, ldw, s);
+    return f8 ? launch<256, true, true>(p, w, K, ldw, s) : launch<256, false, true>(p, w, K, ldw, s);
 }
 
 }  // namespace kda
