@@ -15,12 +15,15 @@
 // tiles, a cluster of CTAs shares one tile: each takes a slice of k, and they
 // join their fp32 sums through distributed shared memory, in rank order, each
 // CTA finishing a part of the tokens.
+#include <cmath>
+
 #include "linear.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kLinThreads = 128;
+constexpr int kLinThreads = 256;
+constexpr int kLinWarps = kLinThreads / 32;
 constexpr int kFeatures = 128;      // rows of w per tile
 constexpr int kMaxStages = 12;
 
@@ -30,7 +33,8 @@ struct LinShape {
     static constexpr int kFit = (kSmemMax - 2048) / kStageBytes;
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
     static constexpr int kSmem = kStages * kStageBytes + 1024;
-    static constexpr int kCols = NT < 32 ? 32 : NT;  // TMEM columns (a power of two, at least 32)
+    // accumulators that an fp32 y sums its stages of k in turn in (see linear_wide.cu on its segments)
+    static constexpr int kAccs = NT <= 64 ? 8 : 512 / NT;
     static_assert(kStages * kStageBytes >= kFeatures * NT * 4, "the ring holds the tile's partial sums");
 };
 
@@ -52,6 +56,8 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     const int m0 = (int)blockIdx.y * NT;
     const int kb0 = (int)((int64_t)a.kblocks * rank >> log_split);
     const int count = (int)((int64_t)a.kblocks * (rank + 1) >> log_split) - kb0;
+    const int accs = a.out == KDA_DTYPE_F32 ? min(Shape::kAccs, count) : 1;
+    const uint32_t cols = a.out == KDA_DTYPE_F32 ? NT * Shape::kAccs : NT < 32 ? 32 : NT;  // a power of two >= 32
 
     if (tid == 0) {
         ptx::prefetch_tmap(&a.tm_w);
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
         s_fail = 0;
     }
     if (warp == 2) {
-        ptx::tmem_alloc(&tmem_base, Shape::kCols);
+        ptx::tmem_alloc(&tmem_base, cols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -102,10 +108,11 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
             ptx::tc_fence_after();
             const uint32_t w = ptx::smem_u32(ring + s * Shape::kStageBytes);
             const uint64_t da = ptx::smem_desc(w, 0, 1024), db = ptx::smem_desc(w + kFeatures * kRowBytes, 0, 1024);
+            const uint32_t d = tmem + (uint32_t)(i % accs * NT);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {  // 32 bytes of k each
-                if constexpr (F8) mma_f8(tmem, da + 2 * j, db + 2 * j, a.idesc, i > 0 || j > 0);
-                else ptx::mma_bf16(tmem, da + 2 * j, db + 2 * j, a.idesc, i > 0 || j > 0);
+                if constexpr (F8) mma_f8(d, da + 2 * j, db + 2 * j, a.idesc, i >= accs || j > 0);
+                else ptx::mma_bf16(d, da + 2 * j, db + 2 * j, a.idesc, i >= accs || j > 0);
             }
             ptx::mma_commit(&empty[s]);
         }
@@ -118,65 +125,107 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     __syncthreads();
     bool fail = s_fail != 0;
 
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const int n = n0 + tid;  // a thread's feature
-    const bool n_ok = n < a.N;
-    const float bias = a.bias && n_ok ? a.bias[n] : 0.f;
-    const float ws = F8 && n_ok ? a.w_scale[n] : 1.f;
+    // The tile's sums go to shared memory as [token][feature] in fp32, in the
+    // ring, which is free once the MMAs (of every CTA of the cluster) are done;
+    // with split > 1 each CTA finishes NT / split tokens, and gets their sums
+    // over every slice of k.  From there a warp takes a token, a lane four
+    // features, so y and the residual move in 256-byte rows.
+    const int log_part = (31 - __clz(NT)) - log_split, part = 1 << log_part;
     const int tokens = min(NT, a.M - m0);
-    auto finish = [&](float v, int m) {
-        if (F8) v *= a.x_scale[m] * ws;
-        v += bias;
-        activate_all<1, false>(&v, a.act);
-        if (a.residual) v += load_out(a.residual, (int64_t)m * a.ldr + n, a.out);
-        store_out(a.y, (int64_t)m * a.ldy + n, v, a.out);
-    };
-
-    if (log_split == 0) {
-        for (int c = 0; c < tokens && !fail; c += 16) {
+    const int lane = tid & 31, quarter = warp & 3;
+    if (log_split) cluster_sync_all();
+    if (!fail) {
+        constexpr int kWarpCols = NT < 32 ? 16 : NT / 2;  // tokens of a warp's lane quarter
+        const uint32_t mine = ptx::smem_u32(ring) + (uint32_t)(quarter * 32 + lane) * 4u;
+        const int c0 = (warp >> 2) * kWarpCols;
+        for (int c = c0; c < min(c0 + kWarpCols, tokens); c += 16) {
             float v[16];
-            ptx::tmem_ld16(lanes + c, v);
+            const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c;
+            ptx::tmem_ld16(at, v);
             ptx::tmem_ld_wait();
-            if (n_ok) {
+            for (int g = 1; g < accs; ++g) {
+                float u[16];
+                ptx::tmem_ld16(at + (uint32_t)(g * NT), u);
+                ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < tokens) finish(v[j], m0 + c + j);
+                for (int j = 0; j < 16; ++j) v[j] += u[j];
             }
-        }
-    } else {
-        // Each CTA of the cluster finishes NT / split tokens.  Their partial
-        // sums from every slice of k are gathered in its ring, which is free
-        // once all the cluster's MMAs are done.
-        const int log_part = (31 - __clz(NT)) - log_split, part = 1 << log_part;
-        cluster_sync_all();
-        const uint32_t mine = ptx::smem_u32(ring) + (uint32_t)tid * 4u;
-        for (int c = 0; c < tokens && !fail; c += 16) {
-            float v[16];
-            ptx::tmem_ld16(lanes + c, v);
-            ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                if (c + j < tokens) {
-                    const int to = (c + j) >> log_part;
-                    const uint32_t row = (uint32_t)((rank << log_part) + ((c + j) & (part - 1)));
-                    st_cluster_f32(peer_smem(mine + row * (kFeatures * 4u), (uint32_t)to), v[j]);
-                }
+                const uint32_t to = (uint32_t)(c + j) >> log_part;
+                const uint32_t row = (uint32_t)((rank << log_part) + ((c + j) & (part - 1)));
+                const uint32_t addr = mine + row * (kFeatures * 4u);
+                if (log_split == 0)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v[j]) : "memory");
+                else if (c + j < tokens)
+                    st_cluster_f32(peer_smem(addr, to), v[j]);
             }
         }
-        cluster_sync_all();
-        const float* sums = reinterpret_cast<const float*>(ring) + tid;
-        for (int c = 0; c < part && !fail; ++c) {
+    }
+    if (log_split) cluster_sync_all();
+    else __syncthreads();
+    const int n = n0 + lane * 4;
+    if (!fail && n < a.N) {
+        const int live = min(4, a.N - n);
+        float bias[4], ws[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bias[i] = a.bias && i < live ? a.bias[n + i] : 0.f;
+            ws[i] = F8 && i < live ? a.w_scale[n + i] : 1.f;
+        }
+        const float4* sums = reinterpret_cast<const float4*>(ring) + lane;
+        const bool wide = a.wide && live == 4;
+        for (int c = warp; c < part; c += kLinWarps) {
             const int t = (rank << log_part) + c;
-            if (t < tokens && n_ok) {
-                float v = 0.f;
-                for (int r = 0; r < split; ++r) v += sums[((r << log_part) + c) * kFeatures];
-                finish(v, m0 + t);
+            if (t >= tokens) break;
+            float4 f = sums[c * (kFeatures / 4)];
+            for (int r = 1; r < split; ++r) {
+                const float4 u = sums[((r << log_part) + c) * (kFeatures / 4)];
+                f.x += u.x;
+                f.y += u.y;
+                f.z += u.z;
+                f.w += u.w;
+            }
+            float v[4] = {f.x, f.y, f.z, f.w};
+            const float xs = F8 ? a.x_scale[m0 + t] : 1.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = (F8 ? v[i] * (xs * ws[i]) : v[i]) + bias[i];
+            if (a.out == KDA_DTYPE_F32) activate_all<4, false>(v, a.act);
+            else activate_all<4, true>(v, a.act);
+            const int64_t at = (int64_t)(m0 + t) * a.ldy + n, rat = (int64_t)(m0 + t) * a.ldr + n;
+            if (wide) {
+                if (a.out == KDA_DTYPE_F32) {
+                    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (a.residual) r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + rat);
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) =
+                        make_float4(v[0] + r.x, v[1] + r.y, v[2] + r.z, v[3] + r.w);
+                } else {
+                    const bool f16 = a.out == KDA_DTYPE_F16;
+                    if (a.residual) {
+                        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + rat);
+                        const float2 lo = f16 ? from_b16x2<true>(u.x) : from_b16x2<false>(u.x);
+                        const float2 hi = f16 ? from_b16x2<true>(u.y) : from_b16x2<false>(u.y);
+                        v[0] += lo.x;
+                        v[1] += lo.y;
+                        v[2] += hi.x;
+                        v[3] += hi.y;
+                    }
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                        make_uint2(pack_b16x2(v[0], v[1], f16), pack_b16x2(v[2], v[3], f16));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < live) {
+                        if (a.residual) v[i] += load_out(a.residual, rat + i, a.out);
+                        store_out(a.y, at + i, v[i], a.out);
+                    }
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 2) ptx::tmem_dealloc(tmem, Shape::kCols);
+    if (warp == 2) ptx::tmem_dealloc(tmem, cols);
     if (fail && tid == 0 && a.status) atomicOr(a.status, kStatusTimeout);
 }
 
@@ -203,6 +252,51 @@ cudaError_t launch(const LinArgs& a, int log_split, cudaStream_t s) {
 template <int NT>
 cudaError_t launch(const LinArgs& a, bool f8, int log_split, cudaStream_t s) {
     return f8 ? launch<NT, true>(a, log_split, s) : launch<NT, false>(a, log_split, s);
+}
+
+// Which kernel takes a call, and how it cuts it: the least of the modelled
+// times.  The constants (us) were measured on GB300 at K = 2048 and 4096, M = 1
+// to 4096, N = 32 to 8192: what a call costs beside its stages, a stage of k,
+// and the end of a tile.  E.g. at N = K = 4096, 16 bits: M = 64 in tiles of 64
+// tokens takes 18.2, 13.9, 12.0, 23.0 us for 1, 2, 4, 8 slices of k; M = 256
+// takes 25.3 us in tiles of 64 and two slices, 17.6 in tiles of 128 and two,
+// 18.9 in the wide kernel with 128 features, 26.5 with 256; M = 2048 takes 56.7
+// in the wide kernel with 128, 46.0 with 256.
+struct Plan {
+    bool wide;
+    int tokens;     // per tile; of the wide kernel: features per tile
+    int log_split;  // 2^log_split slices of k
+};
+Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16, bool out16) {
+    const int sms = device_sm_count();
+    const double stream = (double)bytes / 6.6e6;  // x and w once from HBM
+    auto cost = [&](int64_t units, int64_t slots, double stages, double per_stage, double end, double call) {
+        const double waves = (double)((units + slots - 1) / slots);
+        return call + fmax(waves * stages * per_stage, stream) + waves * end;
+    };
+    Plan best{false, 16, 0};
+    double least = 1e30;
+    auto offer = [&](Plan p, double c) {
+        if (c < least) least = c, best = p;
+    };
+    constexpr struct { int tokens; double stage, end; } kNarrow[] = {
+        {16, 0.186, 0.3}, {32, 0.19, 0.5}, {64, 0.205, 1.0}, {128, 0.245, 2.9}};
+    for (const auto& t : kNarrow) {
+        if (t.tokens < 64 && t.tokens < M) continue;      // a second token tile would read w again
+        const int64_t tiles = (M + t.tokens - 1) / t.tokens * ((N + kFeatures - 1) / kFeatures);
+        for (int ls = 0; ls <= 3 && (ls == 0 || kblocks >> ls >= 4); ++ls) {
+            const int slots = ls < 3 ? sms : 96;          // clusters of 8 leave SMs of a GPC over
+            offer({false, t.tokens, ls}, cost(tiles << ls, slots, (double)((kblocks + (1 << ls) - 1) >> ls), t.stage,
+                                              t.end / (1 << ls), ls ? 4.5 : 3.3));
+        }
+        if (t.tokens >= M) break;
+    }
+    if (rows_on_16 && M > 64) {
+        const int64_t tm = (M + 255) / 256;
+        offer({true, 128, 0}, cost(tm * ((N + 127) / 128), sms / 2, kblocks, 0.215, 0.7, 4.3));
+        if (out16) offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5));
+    }
+    return best;
 }
 
 }  // namespace
@@ -255,17 +349,13 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool rows_on_16 = is_aligned(y, 16) && ldy * oes % 16 == 0 &&
                             (!residual || (is_aligned(residual, 16) && ldr * oes % 16 == 0));
-    if (rows_on_16 && ((M + 255) / 256) * ((N + 255) / 256) >= 64)
-        return launch_linear_wide(a, 256, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    const int64_t tiles_m = (M + nt - 1) / nt, tiles_n = (N + kFeatures - 1) / kFeatures;
-    if (tiles_m > 65535) return KDA_ERR_UNSUPPORTED;
-    // As many slices of k as fill the SMs with one CTA each, at least four stages of k in each.
-    int log_split = 0;
-    while (log_split < 3 && (tiles_m * tiles_n << (log_split + 1)) <= device_sm_count() &&
-           kblocks >> (log_split + 1) >= 4)
-        ++log_split;
-
+    const int four = 4 * oes;  // bytes of a lane's features
+    a.wide = is_aligned(y, four) && ldy % 4 == 0 && (!residual || (is_aligned(residual, four) && ldr % 4 == 0));
+    const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16, oes == 2);
+    if (plan.wide)
+        return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const int nt = plan.tokens, log_split = plan.log_split;
+    if ((M + nt - 1) / nt > 65535) return KDA_ERR_UNSUPPORTED;
     if (!rows_map(&a.tm_w, p.io_dtype, w, N, K, ldw, kFeatures) || !rows_map(&a.tm_x, p.io_dtype, x, M, K, ldx, nt))
         return KDA_ERR_CUDA;
     a.idesc = f8                             ? idesc_e4m3_f32(kFeatures, nt)
@@ -276,8 +366,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     case 16: e = launch<16>(a, f8, log_split, s); break;
     case 32: e = launch<32>(a, f8, log_split, s); break;
     case 64: e = launch<64>(a, f8, log_split, s); break;
-    case 128: e = launch<128>(a, f8, log_split, s); break;
-    default: e = launch<256>(a, f8, log_split, s); break;
+    default: e = launch<128>(a, f8, log_split, s); break;
     }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -25,11 +25,13 @@ struct LinArgs {
     int M, N, kblocks;
     uint32_t idesc;
     int out, act, io;
+    int wide;  // rows of y and residual take loads and stores of four elements
 };
 
-// The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile; an
-// fp32 y takes 128.  tm_w, tm_x and idesc are set there; x, w are the operands and
-// ldx, ldw their row strides.
+// The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile;
+// an fp32 y takes 128.
+// tm_w, tm_x and idesc are set there; x, w are the operands and ldx, ldw their
+// row strides.
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
                                int64_t ldw, cudaStream_t s);
 

@@ -388,6 +388,7 @@ cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const vo
         (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr)))
         return cudaErrorInvalidValue;
     const bool f8 = a.io == KDA_DTYPE_E4M3;
+    // (at 256 features the segments' running sums would not fit in an epilogue thread's registers)
     if (a.out == KDA_DTYPE_F32)
         return f8 ? launch<128, true, false>(p, w, K, ldw, s) : launch<128, false, false>(p, w, K, ldw, s);
     if (tn == 128) return f8 ? launch<128, true, true>(p, w, K, ldw, s) : launch<128, false, true>(p, w, K, ldw, s);
