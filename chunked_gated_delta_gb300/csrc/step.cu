@@ -14,12 +14,15 @@
 // of one (sequence, head): the columns are independent given q, k, g, beta.  It
 // holds its K x VT part in registers as float4 (a warp's load covers whole
 // 128-byte lines), in fp32 whatever the cache's type, across all the tokens.
+#include "internal.h"
 #include "layer_ops.cuh"
+#include "waits.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kStepThreads = 256;
+constexpr int kTokens = 4;  // tokens whose inputs are loaded together (even: the exchange buffers alternate)
 
 struct StepArgs {
     const uint16_t *q, *k, *v, *beta;  // bf16 or fp16 bits
@@ -32,10 +35,114 @@ struct StepArgs {
     int64_t q_stride, k_stride, v_stride, g_stride, beta_stride;
     float scale;
     int N, T, H, V, group, num_slots, logits;
+    int vec;  // q, k, v and g rows take loads of four elements
 };
 
 __device__ __forceinline__ void report(int32_t* status, int bit) {
     if (status) atomicOr(status, bit);
+}
+
+// Whether sequence n's offsets are not those of 0 = c0 <= c1 <= ... <= cN = T.
+__device__ __forceinline__ bool bad_offsets(const StepArgs& a, int n, int bos, int eos) {
+    return bos < 0 || eos < bos || eos > a.T || (n == 0 && bos != 0) || (n == a.N - 1 && eos != a.T);
+}
+// Bulk copies of whole states: 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// One token on the K x COLS part of a state that THREADS threads hold, each kRows
+// rows (THREADS / (COLS / 4) apart) of four columns.  kqe: per row k, q, exp(g);
+// sum, kq: where the warps exchange, not those of the token before (a thread may
+// still read them); sync: a barrier of these threads, false to give up.  o
+// points at the thread's columns of the token's output.
+template <int K, int COLS, bool F16, int kRows, int THREADS, typename Sync>
+__device__ __forceinline__ bool step_token(float4 (&S)[kRows], const float4* kqe, const float* v_in, float beta,
+                                           float4 (*sum)[THREADS / 32][COLS / 4], float* kq_sum, float scale,
+                                           uint16_t* o, int tid, Sync sync) {
+    constexpr int kColGroups = COLS / 4, kRowLanes = THREADS / kColGroups, kWarps = THREADS / 32;
+    const int cg = tid % kColGroups, rl = tid / kColGroups, warp = tid >> 5, lane = tid & 31;
+    float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+    float kq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const float4 r = kqe[rl + i * kRowLanes];
+        S[i].x *= r.z;
+        S[i].y *= r.z;
+        S[i].z *= r.z;
+        S[i].w *= r.z;
+        pk.x += r.x * S[i].x;
+        pk.y += r.x * S[i].y;
+        pk.z += r.x * S[i].z;
+        pk.w += r.x * S[i].w;
+        pq.x += r.y * S[i].x;
+        pq.y += r.y * S[i].y;
+        pq.z += r.y * S[i].z;
+        pq.w += r.y * S[i].w;
+        kq += r.x * r.y;
+    }
+#pragma unroll
+    for (int off = kColGroups; off < 32; off <<= 1) {  // row lanes of the same columns in this warp
+        pk.x += __shfl_xor_sync(~0u, pk.x, off);
+        pk.y += __shfl_xor_sync(~0u, pk.y, off);
+        pk.z += __shfl_xor_sync(~0u, pk.z, off);
+        pk.w += __shfl_xor_sync(~0u, pk.w, off);
+        pq.x += __shfl_xor_sync(~0u, pq.x, off);
+        pq.y += __shfl_xor_sync(~0u, pq.y, off);
+        pq.z += __shfl_xor_sync(~0u, pq.z, off);
+        pq.w += __shfl_xor_sync(~0u, pq.w, off);
+        kq += __shfl_xor_sync(~0u, kq, off);
+    }
+    if (lane < kColGroups) {
+        sum[0][warp][cg] = pk;
+        sum[1][warp][cg] = pq;
+    }
+    if (lane == 0) kq_sum[warp] = kq;
+    if (!sync()) return false;
+    float4 d = sum[0][0][cg];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        const float4 x = sum[0][w][cg];
+        d.x += x.x;
+        d.y += x.y;
+        d.z += x.z;
+        d.w += x.w;
+    }
+    const float4 v = *reinterpret_cast<const float4*>(v_in + cg * 4);
+    d = make_float4(beta * (v.x - d.x), beta * (v.y - d.y), beta * (v.z - d.z), beta * (v.w - d.w));
+    if (rl == 0) {
+        float4 y = sum[1][0][cg];
+        float c = kq_sum[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 x = sum[1][w][cg];
+            y.x += x.x;
+            y.y += x.y;
+            y.z += x.z;
+            y.w += x.w;
+            c += kq_sum[w];
+        }
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_b16x2(scale * (y.x + c * d.x), scale * (y.y + c * d.y), F16),
+                                                  pack_b16x2(scale * (y.z + c * d.z), scale * (y.w + c * d.w), F16));
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const float kk = kqe[rl + i * kRowLanes].x;
+        S[i].x += kk * d.x;
+        S[i].y += kk * d.y;
+        S[i].z += kk * d.z;
+        S[i].w += kk * d.w;
+    }
+    return true;
 }
 
 template <int K, int VT, bool F16, bool STATE16>
@@ -45,13 +152,13 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     constexpr int kRows = K / kRowLanes;                    // rows a thread holds
     constexpr int kWarps = kStepThreads / 32;
     static_assert(kRows >= 1 && kRows * kRowLanes == K, "the threads tile the K rows");
-    __shared__ float4 s_kqe[2][K];   // per row: k, q, exp(g)
-    __shared__ float s_v[2][VT];
-    __shared__ float s_beta[2];
-    __shared__ float4 s_sum[2][kWarps][kColGroups];  // per warp: S^T k, S^T q
-    __shared__ float s_kq[kWarps];
+    __shared__ float4 s_kqe[kTokens][K];   // per row: k, q, exp(g)
+    __shared__ float s_v[kTokens][VT];
+    __shared__ float s_beta[kTokens];
+    __shared__ float4 s_sum[2][2][kWarps][kColGroups];  // per warp: S^T k, S^T q
+    __shared__ float s_kq[2][kWarps];
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int tiles = a.V / VT;
     const int tile = blockIdx.x % tiles;
     const int h = (blockIdx.x / tiles) % a.H;
@@ -62,8 +169,7 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     int len = a.T;
     if (a.cu) {
         const int bos = a.cu[n], eos = a.cu[n + 1];
-        const bool bad = bos < 0 || eos < bos || eos > a.T || (n == 0 && bos != 0) || (n == a.N - 1 && eos != a.T);
-        if (bad) {
+        if (bad_offsets(a, n, bos, eos)) {
             if (first) report(a.status, kStatusBadSeqlens);
             return;
         }
@@ -91,36 +197,45 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         }
     }
 
-    // A token's inputs: k and g rows by the first K threads, q by the next 128,
-    // v by the first VT; loaded one token ahead of their use.
+    // Inputs of kTokens tokens at a time, whose loads are in flight together: k
+    // and g rows by the first K threads, q by the next 128, v by the first VT.
     const int hq = h / a.group;
     const int kr = tid & 127;
-    float in_k = 0.f, in_g = 0.f, in_q = 0.f, in_v = 0.f, in_b = 0.f;
-    auto load_token = [&](int64_t row) {
-        if (tid < K) {
-            in_k = from_b16<F16>(a.k[row * a.k_stride + (int64_t)hq * K + tid]);
-            in_g = a.g[row * a.g_stride + (int64_t)h * K + tid];
+    float in_k[kTokens], in_g[kTokens], in_q[kTokens], in_v[kTokens], in_b[kTokens];
+    auto load_tokens = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            if (t0 + j >= len) break;
+            const int64_t row = row0 + t0 + j;
+            if (tid < K) {
+                in_k[j] = from_b16<F16>(a.k[row * a.k_stride + (int64_t)hq * K + tid]);
+                in_g[j] = a.g[row * a.g_stride + (int64_t)h * K + tid];
+            }
+            if (tid >= 128 && kr < K) in_q[j] = from_b16<F16>(a.q[row * a.q_stride + (int64_t)hq * K + kr]);
+            if (tid < VT) in_v[j] = from_b16<F16>(a.v[row * a.v_stride + (int64_t)h * a.V + tile * VT + tid]);
+            if (tid == 0) in_b[j] = from_b16<F16>(a.beta[row * a.beta_stride + h]);
         }
-        if (tid >= 128 && kr < K) in_q = from_b16<F16>(a.q[row * a.q_stride + (int64_t)hq * K + kr]);
-        if (tid < VT) in_v = from_b16<F16>(a.v[row * a.v_stride + (int64_t)h * a.V + tile * VT + tid]);
-        if (tid == 0) in_b = from_b16<F16>(a.beta[row * a.beta_stride + h]);
     };
-    auto stage_token = [&](int b) {
-        if (tid < K) {
-            s_kqe[b][tid].x = in_k;
-            s_kqe[b][tid].z = expf(in_g);
+    auto stage_tokens = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            if (t0 + j >= len) break;
+            if (tid < K) {
+                s_kqe[j][tid].x = in_k[j];
+                s_kqe[j][tid].z = expf(in_g[j]);
+            }
+            if (tid >= 128 && kr < K) s_kqe[j][kr].y = in_q[j];
+            if (tid < VT) s_v[j][tid] = in_v[j];
+            if (tid == 0) s_beta[j] = a.logits ? 1.f / (1.f + expf(-in_b[j])) : in_b[j];
         }
-        if (tid >= 128 && kr < K) s_kqe[b][kr].y = in_q;
-        if (tid < VT) s_v[b][tid] = in_v;
-        if (tid == 0) s_beta[b] = a.logits ? 1.f / (1.f + expf(-in_b)) : in_b;
     };
-    load_token(row0);
+    load_tokens(0);
 
     // The same slot twice would race: the first sequence that names it has it.
     bool taken = false;
     if (in_cache && a.slots)
         for (int j = tid; j < n; j += kStepThreads) taken |= a.slots[j] == slot;
-    stage_token(0);
+    stage_tokens(0);
     taken = __syncthreads_or(taken);
 
     uint16_t* o = a.o + (row0 * a.H + h) * a.V + tile * VT + cg * 4;
@@ -131,86 +246,19 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         return;
     }
 
-    for (int t = 0; t < len; ++t) {
-        const int b = t & 1;
-        if (t + 1 < len) load_token(row0 + t + 1);
-        float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
-        float kq = 0.f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const float4 r = s_kqe[b][rl + i * kRowLanes];
-            S[i].x *= r.z;
-            S[i].y *= r.z;
-            S[i].z *= r.z;
-            S[i].w *= r.z;
-            pk.x += r.x * S[i].x;
-            pk.y += r.x * S[i].y;
-            pk.z += r.x * S[i].z;
-            pk.w += r.x * S[i].w;
-            pq.x += r.y * S[i].x;
-            pq.y += r.y * S[i].y;
-            pq.z += r.y * S[i].z;
-            pq.w += r.y * S[i].w;
-            kq += r.x * r.y;
-        }
-#pragma unroll
-        for (int off = kColGroups; off < 32; off <<= 1) {  // row lanes of the same columns in this warp
-            pk.x += __shfl_xor_sync(~0u, pk.x, off);
-            pk.y += __shfl_xor_sync(~0u, pk.y, off);
-            pk.z += __shfl_xor_sync(~0u, pk.z, off);
-            pk.w += __shfl_xor_sync(~0u, pk.w, off);
-            pq.x += __shfl_xor_sync(~0u, pq.x, off);
-            pq.y += __shfl_xor_sync(~0u, pq.y, off);
-            pq.z += __shfl_xor_sync(~0u, pq.z, off);
-            pq.w += __shfl_xor_sync(~0u, pq.w, off);
-            kq += __shfl_xor_sync(~0u, kq, off);
-        }
-        if (lane < kColGroups) {
-            s_sum[0][warp][cg] = pk;
-            s_sum[1][warp][cg] = pq;
-        }
-        if (lane == 0) s_kq[warp] = kq;
-        __syncthreads();
-        float4 d = s_sum[0][0][cg];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 x = s_sum[0][w][cg];
-            d.x += x.x;
-            d.y += x.y;
-            d.z += x.z;
-            d.w += x.w;
-        }
-        const float beta = s_beta[b];
-        const float4 v = *reinterpret_cast<const float4*>(&s_v[b][cg * 4]);
-        d = make_float4(beta * (v.x - d.x), beta * (v.y - d.y), beta * (v.z - d.z), beta * (v.w - d.w));
-        if (rl == 0) {
-            float4 y = s_sum[1][0][cg];
-            float c = s_kq[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 x = s_sum[1][w][cg];
-                y.x += x.x;
-                y.y += x.y;
-                y.z += x.z;
-                y.w += x.w;
-                c += s_kq[w];
-            }
-            *reinterpret_cast<uint2*>(o + t * o_step) =
-                make_uint2(pack_b16x2(a.scale * (y.x + c * d.x), a.scale * (y.y + c * d.y), F16),
-                           pack_b16x2(a.scale * (y.z + c * d.z), a.scale * (y.w + c * d.w), F16));
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const float kk = s_kqe[b][rl + i * kRowLanes].x;
-            S[i].x += kk * d.x;
-            S[i].y += kk * d.y;
-            S[i].z += kk * d.z;
-            S[i].w += kk * d.w;
-        }
-        if (t + 1 < len) {
-            stage_token(b ^ 1);  // last read before the barrier above, in token t - 1's update
+    for (int t0 = 0; t0 < len; t0 += kTokens) {
+        if (t0 > 0) {
+            __syncthreads();  // the tokens before have been read
+            stage_tokens(t0);
             __syncthreads();
         }
+        if (t0 + kTokens < len) load_tokens(t0 + kTokens);
+        for (int j = 0; j < min(kTokens, len - t0); ++j)
+            step_token<K, VT, F16, kRows, kStepThreads>(S, s_kqe[j], s_v[j], s_beta[j], s_sum[j & 1], s_kq[j & 1],
+                                                        a.scale, o + (t0 + j) * o_step, tid, [] {
+                                                            __syncthreads();
+                                                            return true;
+                                                        });
     }
 
 #pragma unroll
@@ -222,6 +270,363 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         else
             *reinterpret_cast<float4*>(static_cast<float*>(a.state) + off) = S[i];
     }
+}
+
+// ------------------------------------------------------------------ many sequences
+// With states enough to fill the GPU the call is a stream through them, and the
+// kernel above spends its time between a CTA's load, its sums and its store.
+// Here CTAs are persistent: a warp loads whole states (K V elements are
+// contiguous) into a ring in shared memory with bulk copies, two groups of 256
+// threads take them in turn, and a warp stores them back from the ring, so
+// loads, sums and stores of different states overlap on every SM.
+//
+// The tokens' inputs (k, q, g, v, beta) of a group come through a small ring of
+// their own, filled by a warp that has several tokens' loads in flight: one
+// token's inputs are a kilobyte that nothing else has touched, and waiting for
+// them token by token cost about 2 us each.  The units (a sequence and head)
+// are published ahead of the loads so that it can run ahead.
+constexpr int kGroupThreads = 256;
+constexpr int kGroups = 2;
+constexpr int kLoadWarp = kGroups * kGroupThreads / 32, kStoreWarp = kLoadWarp + 1, kInputWarp = kLoadWarp + 2;
+constexpr int kStreamThreads = (kInputWarp + kGroups) * 32;
+constexpr int kUnits = 64;  // published units kept
+// Barriers of the loads, one per unit in turn, more of them than slots of the
+// ring: copies land in any order, so a group can wait for its next unit while
+// the other group's unit in the same slot is still on its way.  With a barrier
+// per slot that wait would be two phases early, which its parity cannot tell
+// from a phase that is over.  Units up to kRing + 2 before one that is waited
+// for are done, so kFull barriers are never more than one phase behind.
+constexpr int kFull = 16;
+constexpr int kDepth = 3;   // tokens an input warp has in flight
+// Units published before a load is waited for.  An input warp may look kDepth + 1
+// of its group's units ahead of the one that holds the ring up.
+constexpr int kAhead = kGroups * (kDepth + 1) + 2;
+
+struct Unit {
+    int64_t row0, state;  // first token row; first element of the state
+    int len, head;        // tokens; < 0: no more units
+};
+
+template <int K, int V, bool STATE16>
+struct StreamShape {
+    static constexpr int kBytes = K * V * (STATE16 ? 2 : 4);
+    static constexpr bool kLarge = kBytes > 32768;
+    static constexpr int kRing = kLarge ? 3 : kBytes == 32768 ? 5 : 8;
+    static constexpr int kSlots = kLarge ? 3 : 6;   // tokens in a group's input ring
+    static constexpr int kSums = kLarge ? 1 : 2;    // exchange buffers: with one, a second barrier per token
+    struct Token {
+        float4 kqe[K];
+        float v[V];
+        float beta, pad[3];
+    };
+    struct Group {
+        float4 sum[kSums][2][kGroupThreads / 32][V / 4];
+        float kq[kSums][kGroupThreads / 32];
+        Token token[kSlots];
+        uint64_t token_full[kSlots], token_empty[kSlots];
+    };
+    struct Shared {
+        uint8_t ring[kRing][kBytes];
+        Group group[kGroups];
+        Unit unit[kUnits];
+        uint64_t known[kUnits], full[kFull], done[kRing], empty[kRing];
+    };
+    static constexpr int kSmem = (int)sizeof(Shared) + 128;
+    static_assert(kSmem <= 227 * 1024, "fits an SM");
+    static_assert(kRing >= kGroups + 1 && kFull >= kRing + kGroups && kUnits >= kRing + kAhead + 32 + kGroups, "published units outlive their use");
+};
+
+// Named barrier of one group; true if `ok` holds for all its threads.
+__device__ __forceinline__ bool group_sync(int group, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(group + 1), "n"(kGroupThreads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
+// COUNT (2 or 4) consecutive 16-bit or fp32 elements as fp32; vec: they are aligned to their size together.
+template <bool F16, int COUNT>
+__device__ __forceinline__ void load_some(const uint16_t* p, bool vec, uint16_t (&w)[COUNT]) {
+    if (vec) {
+        uint32_t u[COUNT / 2];
+        if constexpr (COUNT == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            u[0] = x.x, u[1] = x.y;
+        } else {
+            u[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) w[i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) w[i] = p[i];
+    }
+}
+template <int COUNT>
+__device__ __forceinline__ void load_some(const float* p, bool vec, float (&w)[COUNT]) {
+    if (vec) {
+        if constexpr (COUNT == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(p);
+            w[0] = x.x, w[1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) w[i] = p[i];
+    }
+}
+
+template <int K, int V, bool F16, bool STATE16>
+__global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(const StepArgs a) {
+    using Shape = StreamShape<K, V, STATE16>;
+    constexpr int kRing = Shape::kRing, kSlots = Shape::kSlots;
+    constexpr int kColGroups = V / 4;
+    constexpr int kRowLanes = kGroupThreads / kColGroups;
+    constexpr int kRows = K / kRowLanes;
+    constexpr int kWarps = kGroupThreads / 32;
+    extern __shared__ uint8_t raw[];
+    auto& sm = *reinterpret_cast<typename Shape::Shared*>(raw + ((128u - (ptx::smem_u32(raw) & 127u)) & 127u));
+
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kUnits; ++i) ptx::mbar_init(&sm.known[i], 1);
+        for (int i = 0; i < kFull; ++i) ptx::mbar_init(&sm.full[i], 1);
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(&sm.done[i], kWarps);
+            ptx::mbar_init(&sm.empty[i], 1);
+        }
+        for (int g = 0; g < kGroups; ++g)
+            for (int i = 0; i < kSlots; ++i) {
+                ptx::mbar_init(&sm.group[g].token_full[i], 32);
+                ptx::mbar_init(&sm.group[g].token_empty[i], kWarps);
+            }
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+
+    if (warp == kLoadWarp) {
+        const int total = a.N * a.H;
+        int u = blockIdx.x, published = 0, issued = 0, batch = kAhead + 1;
+        bool end = false, ok = true;
+        while (ok) {
+            if (!end && published <= issued + kAhead) {
+                // A batch of units, one per lane, so that their offsets and slots, and the
+                // look through the earlier sequences' slots, are waited for once.  (The
+                // first batch is small: the first loads wait for it.)
+                const int64_t mine = u + (int64_t)lane * gridDim.x;
+                const bool here = lane < batch && mine < total;
+                const int n = here ? (int)mine / a.H : 0, h = here ? (int)mine - n * a.H : 0;
+                Unit unit{(int64_t)n * a.T, 0, here ? a.T : 0, h};
+                if (here && a.cu) {
+                    const int bos = a.cu[n], eos = a.cu[n + 1];
+                    const bool bad = bad_offsets(a, n, bos, eos);
+                    if (bad && h == 0) report(a.status, kStatusBadSeqlens);
+                    unit.row0 = bos;
+                    unit.len = bad ? 0 : eos - bos;
+                }
+                const int slot = here && a.slots ? a.slots[n] : n;
+                bool taken = false;
+                if (a.slots) {
+                    const int most = __reduce_max_sync(~0u, unit.len > 0 && slot >= 0 ? n : 0);
+#pragma unroll 8
+                    for (int j = 0; j < most; ++j) taken |= a.slots[j] == slot && j < n;
+                }
+                const bool refused = unit.len > 0 && (slot < 0 || slot >= a.num_slots || taken);
+                if (refused) {
+                    if (h == 0 && slot >= 0) report(a.status, kStatusBadSlots);
+                    uint16_t* o = a.o + (unit.row0 * a.H + h) * V;
+                    for (int t = 0; t < unit.len; ++t, o += (int64_t)a.H * V)
+                        for (int c = 0; c < V; c += 8) *reinterpret_cast<uint4*>(o + c) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                unit.state = ((int64_t)slot * a.H + h) * (K * V);
+                const uint32_t live = __ballot_sync(~0u, unit.len > 0 && !refused);
+                if ((live >> lane) & 1u) {
+                    const int i = (published + __popc(live & ((1u << lane) - 1u))) % kUnits;
+                    sm.unit[i] = unit;
+                    ptx::mbar_arrive(&sm.known[i]);
+                }
+                published += __popc(live);
+                u = (int)min((int64_t)total, u + (int64_t)batch * gridDim.x);
+                batch = 32;
+                if (u >= total) {
+                    end = true;
+                    if (lane < kGroups) {  // the end, once for each group
+                        const int i = (published + lane) % kUnits;
+                        sm.unit[i].len = -1;
+                        ptx::mbar_arrive(&sm.known[i]);
+                    }
+                }
+                __syncwarp();
+            } else if (issued < published) {
+                const int s = issued % kRing, round = issued / kRing;
+                if (round > 0) ok = __all_sync(~0u, wait_for(&sm.empty[s], (round - 1) & 1));
+                if (!ok) break;
+                if (elect_one()) {
+                    uint64_t* full = &sm.full[issued % kFull];
+                    ptx::mbar_arrive_expect_tx(full, Shape::kBytes);
+                    bulk_load(sm.ring[s],
+                              static_cast<const uint8_t*>(a.state) + sm.unit[issued % kUnits].state * (STATE16 ? 2 : 4),
+                              Shape::kBytes, full);
+                }
+                __syncwarp();
+                ++issued;
+            } else {
+                break;
+            }
+        }
+        if (!ok && lane == 0) report(a.status, kStatusTimeout);
+        for (int i = max(0, issued - kRing); i < issued; ++i) wait_for(&sm.full[i % kFull], (i / kFull) & 1);
+    } else if (warp == kStoreWarp) {
+        if (elect_one()) {
+            for (int i = 0;; ++i) {
+                const int s = i % kRing;
+                if (!wait_for(&sm.known[i % kUnits], (i / kUnits) & 1)) break;
+                const Unit unit = sm.unit[i % kUnits];
+                if (unit.len < 0 || !wait_for(&sm.done[s], (i / kRing) & 1)) break;
+                bulk_store(static_cast<uint8_t*>(a.state) + unit.state * (STATE16 ? 2 : 4), sm.ring[s],
+                           Shape::kBytes);
+                ptx::bulk_commit();
+                ptx::bulk_wait_read0();
+                ptx::mbar_arrive(&sm.empty[s]);
+            }
+            ptx::bulk_wait0();
+        }
+    } else if (warp >= kInputWarp) {
+        auto& gr = sm.group[warp - kInputWarp];
+        constexpr int kk = K / 32, vv = V / 32;  // elements of a lane
+        uint16_t rk[kDepth][kk], rq[kDepth][kk], rv[kDepth][vv], rb[kDepth];
+        float rg[kDepth][kk];
+        bool has[kDepth];
+        int i = warp - kInputWarp, t = 0;  // the next token to ask for
+        bool ok = wait_for(&sm.known[i], 0);
+        Unit unit = sm.unit[i];
+        auto ask = [&](int d) {
+            has[d] = ok && unit.len > 0;
+            if (!has[d]) return;
+            const int64_t row = unit.row0 + t;
+            const int h = unit.head, hq = h / a.group;
+            load_some<F16, kk>(a.k + row * a.k_stride + (int64_t)hq * K + lane * kk, a.vec, rk[d]);
+            load_some<F16, kk>(a.q + row * a.q_stride + (int64_t)hq * K + lane * kk, a.vec, rq[d]);
+            load_some<kk>(a.g + row * a.g_stride + (int64_t)h * K + lane * kk, a.vec, rg[d]);
+            load_some<F16, vv>(a.v + row * a.v_stride + (int64_t)h * V + lane * vv, a.vec, rv[d]);
+            rb[d] = a.beta[row * a.beta_stride + h];
+            if (++t == unit.len) {
+                t = 0;
+                i += kGroups;
+                ok = wait_for(&sm.known[i % kUnits], (i / kUnits) & 1);
+                unit = sm.unit[i % kUnits];
+            }
+        };
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) ask(d);
+        bool more = true;
+        for (int c = 0; more;) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                more = more && has[d];
+                if (!more) break;
+                const int s = c % kSlots, round = c / kSlots;
+                if (round > 0 && !wait_for(&gr.token_empty[s], (round - 1) & 1)) {
+                    more = false;
+                    break;
+                }
+                auto& to = gr.token[s];
+#pragma unroll
+                for (int e = 0; e < kk; ++e)
+                    to.kqe[lane * kk + e] =
+                        make_float4(from_b16<F16>(rk[d][e]), from_b16<F16>(rq[d][e]), expf(rg[d][e]), 0.f);
+#pragma unroll
+                for (int e = 0; e < vv; ++e) to.v[lane * vv + e] = from_b16<F16>(rv[d][e]);
+                if (lane == 0) {
+                    const float x = from_b16<F16>(rb[d]);
+                    to.beta = a.logits ? 1.f / (1.f + expf(-x)) : x;
+                }
+                ptx::mbar_arrive(&gr.token_full[s]);
+                ++c;
+                ask(d);
+            }
+        }
+    } else {
+        const int group = warp / kWarps, gt = tid - group * kGroupThreads;
+        const int cg = gt % kColGroups, rl = gt / kColGroups;
+        auto& gr = sm.group[group];
+        bool ok = true;
+        int c = 0;  // tokens done
+        for (int i = group;; i += kGroups) {
+            ok = wait_for(&sm.known[i % kUnits], (i / kUnits) & 1);
+            const Unit unit = sm.unit[i % kUnits];
+            if (ok && unit.len < 0) {  // (a thread that gave up waits for the others once)
+                ok = group_sync(group, true);
+                break;
+            }
+            const int s = i % kRing;
+            float4* tile = reinterpret_cast<float4*>(sm.ring[s]);
+            uint2* tile16 = reinterpret_cast<uint2*>(sm.ring[s]);
+            ok = ok && wait_for(&sm.full[i % kFull], (i / kFull) & 1);
+            float4 S[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int at = (rl + r * kRowLanes) * kColGroups + cg;
+                if constexpr (STATE16) {
+                    const uint2 w = tile16[at];
+                    const float2 lo = from_b16x2<false>(w.x), hi = from_b16x2<false>(w.y);
+                    S[r] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                } else {
+                    S[r] = tile[at];
+                }
+            }
+            uint16_t* o = a.o + (unit.row0 * a.H + unit.head) * V + cg * 4;
+            int t = 0;
+            do {  // (once with ok false, to give up together)
+                const int ts = c % kSlots, b = c % Shape::kSums;
+                ok = ok && wait_for(&gr.token_full[ts], (c / kSlots) & 1);
+                const auto& token = gr.token[ts];
+                if (Shape::kSums == 1 && c > 0 && !(ok = group_sync(group, ok))) break;  // the sums before have been read
+                ok = step_token<K, V, F16, kRows, kGroupThreads>(S, token.kqe, token.v, token.beta, gr.sum[b], gr.kq[b],
+                                                                 a.scale, o, gt, [&] { return group_sync(group, ok); });
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&gr.token_empty[ts]);
+                ++c;
+                o += (int64_t)a.H * V;
+            } while (++t < unit.len);
+            if (!ok) break;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int at = (rl + r * kRowLanes) * kColGroups + cg;
+                if constexpr (STATE16)
+                    tile16[at] = make_uint2(pack_b16x2(S[r].x, S[r].y, false), pack_b16x2(S[r].z, S[r].w, false));
+                else
+                    tile[at] = S[r];
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.done[s]);
+        }
+        if (!ok && gt == 0) report(a.status, kStatusTimeout);
+    }
+}
+
+template <int K, int V, bool F16, bool STATE16>
+cudaError_t launch_stream(const StepArgs& a, int sms, cudaStream_t s) {
+    auto kern = kda_step_stream_kernel<K, V, F16, STATE16>;
+    constexpr int kSmem = StreamShape<K, V, STATE16>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)min((int64_t)sms, (int64_t)a.N * a.H), kStreamThreads, kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int K, int V>
+cudaError_t launch_stream(const StepArgs& a, bool f16, bool state16, int sms, cudaStream_t s) {
+    if (f16) return state16 ? launch_stream<K, V, true, true>(a, sms, s) : launch_stream<K, V, true, false>(a, sms, s);
+    return state16 ? launch_stream<K, V, false, true>(a, sms, s) : launch_stream<K, V, false, false>(a, sms, s);
 }
 
 template <int K, int VT>
@@ -299,8 +704,19 @@ extern "C" kda_status kda_step(const void* q, const void* k, const void* v, cons
     a.group = d.H / hq;
     a.num_slots = p.num_slots;
     a.logits = p.beta_logits;
+    a.vec = is_aligned(q, 8) && is_aligned(k, 8) && is_aligned(v, 8) && is_aligned(g, 16) && a.q_stride % 4 == 0 &&
+            a.k_stride % 4 == 0 && a.v_stride % 4 == 0 && a.g_stride % 4 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f16 = p.io_dtype == KDA_IO_F16, s16 = p.state_dtype == KDA_STATE_BF16;
-    const cudaError_t e = d.K == 128 ? launch<128, 64>(a, f16, s16, s) : launch<64, 64>(a, f16, s16, s);
+    const int sms = device_sm_count();
+    cudaError_t e;
+    if ((int64_t)N * d.H >= 2 * sms) {
+        if (d.K == 128)
+            e = d.V == 128 ? launch_stream<128, 128>(a, f16, s16, sms, s) : launch_stream<128, 64>(a, f16, s16, sms, s);
+        else
+            e = d.V == 128 ? launch_stream<64, 128>(a, f16, s16, sms, s) : launch_stream<64, 64>(a, f16, s16, sms, s);
+    } else {
+        e = d.K == 128 ? launch<128, 64>(a, f16, s16, s) : launch<64, 64>(a, f16, s16, s);
+    }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -85,6 +85,23 @@ def test_many_sequences_every_rule():
         check(inputs(B, 1, 2, 64, 64, seed=B), cache(B, 2, 64, 64), None, [(i, i + 1) for i in range(B)])
 
 
+@pytest.mark.parametrize("B,H,K,V,st", [(420, 32, 128, 128, torch.float32), (1400, 8, 64, 64, torch.float32),
+                                        (900, 16, 128, 64, torch.bfloat16)])
+def test_long_streams_repeat(B, H, K, V, st):
+    """More states per SM than any ring or table of the kernel holds, again and again: every call gives what the
+    same call gives on small parts of the batch (which take the other kernel), to a rounding."""
+    x = inputs(B, 1, H, K, V, seed=B)
+    state = cache(B, H, K, V, st)
+    parts = state.clone()
+    o_parts = torch.cat([kda.step(*(x[n][i:i + 2] for n in ("q", "k", "v", "g", "beta")), parts[i:i + 2])
+                         for i in range(0, B, 2)])
+    for _ in range(12):
+        got = state.clone()
+        o = kda.step(x["q"], x["k"], x["v"], x["g"], x["beta"], got)
+        assert_close(o, o_parts.double(), 2 * HALF_ULP[torch.bfloat16], 1e-3)
+        assert_close(got, parts.double(), 2 * HALF_ULP[st], 1e-3)
+
+
 @pytest.mark.parametrize("lens", [[0], [1], [5], [0, 1, 5, 0, 2, 9, 0], [0, 0, 0], [70, 1, 3]])
 def test_packed_lengths(lens):
     cu = [0]
