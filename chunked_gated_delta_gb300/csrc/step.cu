@@ -60,89 +60,110 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
                  : "memory");
 }
 
-// One token on the K x COLS part of a state that THREADS threads hold, each kRows
-// rows (THREADS / (COLS / 4) apart) of four columns.  kqe: per row k, q, exp(g);
-// sum, kq: where the warps exchange, not those of the token before (a thread may
-// still read them); sync: a barrier of these threads, false to give up.  o
-// points at the thread's columns of the token's output.
+// A token's inputs in shared memory.
+template <int K, int COLS>
+struct Token {
+    float4 kqe[K];  // per row: k, q, exp(g)
+    float v[COLS];
+    float beta, unused[3];
+};
+
+// What the warps of THREADS threads exchange of a token: S^T k and S^T q of their rows.
+template <int COLS, int THREADS>
+struct Sums {
+    float4 k[THREADS / 32][COLS / 4], q[THREADS / 32][COLS / 4];
+};
+
+__device__ __forceinline__ void add4(float4& a, const float4 b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+__device__ __forceinline__ void fma4(float4& a, float k, const float4 b) {
+    a.x = fmaf(k, b.x, a.x);
+    a.y = fmaf(k, b.y, a.y);
+    a.z = fmaf(k, b.z, a.z);
+    a.w = fmaf(k, b.w, a.w);
+}
+__device__ __forceinline__ float4 shuffle4(const float4 a, int off) {
+    return make_float4(__shfl_xor_sync(~0u, a.x, off), __shfl_xor_sync(~0u, a.y, off), __shfl_xor_sync(~0u, a.z, off),
+                       __shfl_xor_sync(~0u, a.w, off));
+}
+
+// One token on the K x COLS part of a state that THREADS threads hold, each
+// kRows rows (THREADS / (COLS / 4) apart) of four columns.  sums: not those of
+// the token before (a thread may still read them); sync: a barrier of these
+// threads, false to give up.  o points at the thread's columns of the token's
+// output.
 template <int K, int COLS, bool F16, int kRows, int THREADS, typename Sync>
-__device__ __forceinline__ bool step_token(float4 (&S)[kRows], const float4* kqe, const float* v_in, float beta,
-                                           float4 (*sum)[THREADS / 32][COLS / 4], float* kq_sum, float scale,
-                                           uint16_t* o, int tid, Sync sync) {
+__device__ __forceinline__ bool step_token(float4 (&S)[kRows], const Token<K, COLS>& in, Sums<COLS, THREADS>& sums,
+                                           float scale, uint16_t* o, int tid, Sync sync) {
     constexpr int kColGroups = COLS / 4, kRowLanes = THREADS / kColGroups, kWarps = THREADS / 32;
     const int cg = tid % kColGroups, rl = tid / kColGroups, warp = tid >> 5, lane = tid & 31;
     float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
-    float kq = 0.f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const float4 r = kqe[rl + i * kRowLanes];
+        const float4 r = in.kqe[rl + i * kRowLanes];
         S[i].x *= r.z;
         S[i].y *= r.z;
         S[i].z *= r.z;
         S[i].w *= r.z;
-        pk.x += r.x * S[i].x;
-        pk.y += r.x * S[i].y;
-        pk.z += r.x * S[i].z;
-        pk.w += r.x * S[i].w;
-        pq.x += r.y * S[i].x;
-        pq.y += r.y * S[i].y;
-        pq.z += r.y * S[i].z;
-        pq.w += r.y * S[i].w;
-        kq += r.x * r.y;
+        fma4(pk, r.x, S[i]);
+        fma4(pq, r.y, S[i]);
     }
 #pragma unroll
     for (int off = kColGroups; off < 32; off <<= 1) {  // row lanes of the same columns in this warp
-        pk.x += __shfl_xor_sync(~0u, pk.x, off);
-        pk.y += __shfl_xor_sync(~0u, pk.y, off);
-        pk.z += __shfl_xor_sync(~0u, pk.z, off);
-        pk.w += __shfl_xor_sync(~0u, pk.w, off);
-        pq.x += __shfl_xor_sync(~0u, pq.x, off);
-        pq.y += __shfl_xor_sync(~0u, pq.y, off);
-        pq.z += __shfl_xor_sync(~0u, pq.z, off);
-        pq.w += __shfl_xor_sync(~0u, pq.w, off);
-        kq += __shfl_xor_sync(~0u, kq, off);
+        add4(pk, shuffle4(pk, off));
+        add4(pq, shuffle4(pq, off));
     }
     if (lane < kColGroups) {
-        sum[0][warp][cg] = pk;
-        sum[1][warp][cg] = pq;
+        sums.k[warp][cg] = pk;
+        sums.q[warp][cg] = pq;
     }
-    if (lane == 0) kq_sum[warp] = kq;
-    if (!sync()) return false;
-    float4 d = sum[0][0][cg];
+    float kq = 0.f;  // k . q, for the warp that writes o
+    if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        const float4 x = sum[0][w][cg];
-        d.x += x.x;
-        d.y += x.y;
-        d.z += x.z;
-        d.w += x.w;
+        for (int r = 0; r < K; r += 32) kq += in.kqe[r + lane].x * in.kqe[r + lane].y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) kq += __shfl_xor_sync(~0u, kq, off);
     }
-    const float4 v = *reinterpret_cast<const float4*>(v_in + cg * 4);
+    if (!sync()) return false;
+    float4 d = sums.k[0][cg];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) add4(d, sums.k[w][cg]);
+    const float beta = in.beta;
+    const float4 v = *reinterpret_cast<const float4*>(in.v + cg * 4);
     d = make_float4(beta * (v.x - d.x), beta * (v.y - d.y), beta * (v.z - d.z), beta * (v.w - d.w));
     if (rl == 0) {
-        float4 y = sum[1][0][cg];
-        float c = kq_sum[0];
+        float4 y = sums.q[0][cg];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 x = sum[1][w][cg];
-            y.x += x.x;
-            y.y += x.y;
-            y.z += x.z;
-            y.w += x.w;
-            c += kq_sum[w];
-        }
-        *reinterpret_cast<uint2*>(o) = make_uint2(pack_b16x2(scale * (y.x + c * d.x), scale * (y.y + c * d.y), F16),
-                                                  pack_b16x2(scale * (y.z + c * d.z), scale * (y.w + c * d.w), F16));
+        for (int w = 1; w < kWarps; ++w) add4(y, sums.q[w][cg]);
+        fma4(y, kq, d);
+        *reinterpret_cast<uint2*>(o) =
+            make_uint2(pack_b16x2(scale * y.x, scale * y.y, F16), pack_b16x2(scale * y.z, scale * y.w, F16));
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const float kk = kqe[rl + i * kRowLanes].x;
-        S[i].x += kk * d.x;
-        S[i].y += kk * d.y;
-        S[i].z += kk * d.z;
-        S[i].w += kk * d.w;
-    }
+    for (int i = 0; i < kRows; ++i) fma4(S[i], in.kqe[rl + i * kRowLanes].x, d);
     return true;
+}
+// Four elements of a state, in fp32 or bf16, at p[index of 4].
+template <bool STATE16>
+__device__ __forceinline__ float4 load_state(const void* p, int64_t four) {
+    if constexpr (STATE16) {
+        const uint2 w = static_cast<const uint2*>(p)[four];
+        const float2 lo = from_b16x2<false>(w.x), hi = from_b16x2<false>(w.y);
+        return make_float4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+        return static_cast<const float4*>(p)[four];
+    }
+}
+template <bool STATE16>
+__device__ __forceinline__ void store_state(void* p, int64_t four, float4 s) {
+    if constexpr (STATE16)
+        static_cast<uint2*>(p)[four] = make_uint2(pack_b16x2(s.x, s.y, false), pack_b16x2(s.z, s.w, false));
+    else
+        static_cast<float4*>(p)[four] = s;
 }
 
 template <int K, int VT, bool F16, bool STATE16>
@@ -150,13 +171,9 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     constexpr int kColGroups = VT / 4;                      // threads across a row, 4 columns each
     constexpr int kRowLanes = kStepThreads / kColGroups;    // rows in flight per step of i
     constexpr int kRows = K / kRowLanes;                    // rows a thread holds
-    constexpr int kWarps = kStepThreads / 32;
     static_assert(kRows >= 1 && kRows * kRowLanes == K, "the threads tile the K rows");
-    __shared__ float4 s_kqe[kTokens][K];   // per row: k, q, exp(g)
-    __shared__ float s_v[kTokens][VT];
-    __shared__ float s_beta[kTokens];
-    __shared__ float4 s_sum[2][2][kWarps][kColGroups];  // per warp: S^T k, S^T q
-    __shared__ float s_kq[2][kWarps];
+    __shared__ Token<K, VT> s_token[kTokens];
+    __shared__ Sums<VT, kStepThreads> s_sums[2];
 
     const int tid = threadIdx.x;
     const int tiles = a.V / VT;
@@ -181,20 +198,13 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     const bool in_cache = slot >= 0 && slot < a.num_slots;
 
     const int cg = tid % kColGroups, rl = tid / kColGroups;
-    const int64_t at = in_cache ? (((int64_t)slot * a.H + h) * K + rl) * a.V + tile * VT + cg * 4 : 0;
+    // (a state's elements in fours)
+    const int64_t at = in_cache ? ((((int64_t)slot * a.H + h) * K + rl) * a.V + tile * VT) / 4 + cg : 0;
+    const int64_t row_step = (int64_t)kRowLanes * a.V / 4;
     float4 S[kRows];
     if (in_cache) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int64_t off = at + (int64_t)i * kRowLanes * a.V;
-            if constexpr (STATE16) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.state) + off);
-                const float2 lo = from_b16x2<false>(w.x), hi = from_b16x2<false>(w.y);
-                S[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
-            } else {
-                S[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.state) + off);
-            }
-        }
+        for (int i = 0; i < kRows; ++i) S[i] = load_state<STATE16>(a.state, at + i * row_step);
     }
 
     // Inputs of kTokens tokens at a time, whose loads are in flight together: k
@@ -221,12 +231,12 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         for (int j = 0; j < kTokens; ++j) {
             if (t0 + j >= len) break;
             if (tid < K) {
-                s_kqe[j][tid].x = in_k[j];
-                s_kqe[j][tid].z = expf(in_g[j]);
+                s_token[j].kqe[tid].x = in_k[j];
+                s_token[j].kqe[tid].z = expf(in_g[j]);
             }
-            if (tid >= 128 && kr < K) s_kqe[j][kr].y = in_q[j];
-            if (tid < VT) s_v[j][tid] = in_v[j];
-            if (tid == 0) s_beta[j] = a.logits ? 1.f / (1.f + expf(-in_b[j])) : in_b[j];
+            if (tid >= 128 && kr < K) s_token[j].kqe[kr].y = in_q[j];
+            if (tid < VT) s_token[j].v[tid] = in_v[j];
+            if (tid == 0) s_token[j].beta = a.logits ? 1.f / (1.f + expf(-in_b[j])) : in_b[j];
         }
     };
     load_tokens(0);
@@ -254,41 +264,34 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         }
         if (t0 + kTokens < len) load_tokens(t0 + kTokens);
         for (int j = 0; j < min(kTokens, len - t0); ++j)
-            step_token<K, VT, F16, kRows, kStepThreads>(S, s_kqe[j], s_v[j], s_beta[j], s_sum[j & 1], s_kq[j & 1],
-                                                        a.scale, o + (t0 + j) * o_step, tid, [] {
+            step_token<K, VT, F16, kRows, kStepThreads>(S, s_token[j], s_sums[j & 1], a.scale, o + (t0 + j) * o_step, tid,
+                                                        [] {
                                                             __syncthreads();
                                                             return true;
                                                         });
     }
 
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t off = at + (int64_t)i * kRowLanes * a.V;
-        if constexpr (STATE16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.state) + off) =
-                make_uint2(pack_b16x2(S[i].x, S[i].y, false), pack_b16x2(S[i].z, S[i].w, false));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.state) + off) = S[i];
-    }
+    for (int i = 0; i < kRows; ++i) store_state<STATE16>(a.state, at + i * row_step, S[i]);
 }
 
 // ------------------------------------------------------------------ many sequences
 // With states enough to fill the GPU the call is a stream through them, and the
 // kernel above spends its time between a CTA's load, its sums and its store.
 // Here CTAs are persistent: a warp loads whole states (K V elements are
-// contiguous) into a ring in shared memory with bulk copies, two groups of 256
-// threads take them in turn, and a warp stores them back from the ring, so
+// contiguous) into a ring in shared memory with bulk copies, groups of threads
+// (two of 256, or four of 128 where V is 64: 16 or 8 rows a thread for K = 128
+// or 64 either way) take them in turn, and a warp stores them back from the ring, so
 // loads, sums and stores of different states overlap on every SM.
 //
-// The tokens' inputs (k, q, g, v, beta) of a group come through a small ring of
-// their own, filled by a warp that has several tokens' loads in flight: one
+// The tokens' inputs (k, q, g, v, beta) come through a small ring for each group,
+// filled by one of two warps that have several tokens' loads in flight: one
 // token's inputs are a kilobyte that nothing else has touched, and waiting for
 // them token by token cost about 2 us each.  The units (a sequence and head)
 // are published ahead of the loads so that it can run ahead.
-constexpr int kGroupThreads = 256;
-constexpr int kGroups = 2;
-constexpr int kLoadWarp = kGroups * kGroupThreads / 32, kStoreWarp = kLoadWarp + 1, kInputWarp = kLoadWarp + 2;
-constexpr int kStreamThreads = (kInputWarp + kGroups) * 32;
+constexpr int kComputeWarps = 16, kInputWarps = 2;
+constexpr int kLoadWarp = kComputeWarps, kStoreWarp = kLoadWarp + 1, kFirstInputWarp = kLoadWarp + 2;
+constexpr int kStreamThreads = (kFirstInputWarp + kInputWarps) * 32;
 constexpr int kUnits = 64;  // published units kept
 // Barriers of the loads, one per unit in turn, more of them than slots of the
 // ring: copies land in any order, so a group can wait for its next unit while
@@ -298,9 +301,9 @@ constexpr int kUnits = 64;  // published units kept
 // for are done, so kFull barriers are never more than one phase behind.
 constexpr int kFull = 16;
 constexpr int kDepth = 3;   // tokens an input warp has in flight
-// Units published before a load is waited for.  An input warp may look kDepth + 1
-// of its group's units ahead of the one that holds the ring up.
-constexpr int kAhead = kGroups * (kDepth + 1) + 2;
+// Units published before a load is waited for.  An input warp takes every second
+// unit, and may look kDepth of them ahead of the one that holds the ring up.
+constexpr int kAhead = kInputWarps * (kDepth + 1) + 2;
 
 struct Unit {
     int64_t row0, state;  // first token row; first element of the state
@@ -309,20 +312,17 @@ struct Unit {
 
 template <int K, int V, bool STATE16>
 struct StreamShape {
+    static constexpr int kThreads = 2 * V;                       // of a group
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kGroups = kComputeWarps / kWarps;
     static constexpr int kBytes = K * V * (STATE16 ? 2 : 4);
     static constexpr bool kLarge = kBytes > 32768;
     static constexpr int kRing = kLarge ? 3 : kBytes == 32768 ? 5 : 8;
-    static constexpr int kSlots = kLarge ? 3 : 6;   // tokens in a group's input ring
+    static constexpr int kSlots = kLarge ? 3 : 4;   // tokens in a group's input ring
     static constexpr int kSums = kLarge ? 1 : 2;    // exchange buffers: with one, a second barrier per token
-    struct Token {
-        float4 kqe[K];
-        float v[V];
-        float beta, pad[3];
-    };
     struct Group {
-        float4 sum[kSums][2][kGroupThreads / 32][V / 4];
-        float kq[kSums][kGroupThreads / 32];
-        Token token[kSlots];
+        Sums<V, kThreads> sums[kSums];
+        Token<K, V> token[kSlots];
         uint64_t token_full[kSlots], token_empty[kSlots];
     };
     struct Shared {
@@ -333,17 +333,20 @@ struct StreamShape {
     };
     static constexpr int kSmem = (int)sizeof(Shared) + 128;
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    static_assert(kRing >= kGroups + 1 && kFull >= kRing + kGroups && kUnits >= kRing + kAhead + 32 + kGroups, "published units outlive their use");
+    static_assert(kRing >= kGroups + 1 && kFull >= kRing + kGroups && kUnits >= kRing + kAhead + 32 + kGroups,
+                  "barriers and published units outlive their use");
+    static_assert(kGroups % kInputWarps == 0, "a group's tokens come from one warp");
 };
 
 // Named barrier of one group; true if `ok` holds for all its threads.
+template <int THREADS>
 __device__ __forceinline__ bool group_sync(int group, bool ok) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
-        : "r"(group + 1), "n"(kGroupThreads), "r"((uint32_t)ok)
+        : "r"(group + 1), "n"(THREADS), "r"((uint32_t)ok)
         : "memory");
     return all != 0;
 }
@@ -385,11 +388,11 @@ __device__ __forceinline__ void load_some(const float* p, bool vec, float (&w)[C
 template <int K, int V, bool F16, bool STATE16>
 __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(const StepArgs a) {
     using Shape = StreamShape<K, V, STATE16>;
-    constexpr int kRing = Shape::kRing, kSlots = Shape::kSlots;
+    constexpr int kRing = Shape::kRing, kSlots = Shape::kSlots, kGroups = Shape::kGroups;
+    constexpr int kThreads = Shape::kThreads, kWarps = Shape::kWarps;
     constexpr int kColGroups = V / 4;
-    constexpr int kRowLanes = kGroupThreads / kColGroups;
+    constexpr int kRowLanes = kThreads / kColGroups;
     constexpr int kRows = K / kRowLanes;
-    constexpr int kWarps = kGroupThreads / 32;
     extern __shared__ uint8_t raw[];
     auto& sm = *reinterpret_cast<typename Shape::Shared*>(raw + ((128u - (ptx::smem_u32(raw) & 127u)) & 127u));
 
@@ -497,40 +500,62 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             }
             ptx::bulk_wait0();
         }
-    } else if (warp >= kInputWarp) {
-        auto& gr = sm.group[warp - kInputWarp];
+    } else if (warp >= kFirstInputWarp) {
         constexpr int kk = K / 32, vv = V / 32;  // elements of a lane
         uint16_t rk[kDepth][kk], rq[kDepth][kk], rv[kDepth][vv], rb[kDepth];
         float rg[kDepth][kk];
         bool has[kDepth];
-        int i = warp - kInputWarp, t = 0;  // the next token to ask for
+        int i = warp - kFirstInputWarp, t = 0;  // the next token to ask for
+        int to_group[kDepth], sent[kGroups / kInputWarps] = {};  // tokens sent to each of its groups
         bool ok = wait_for(&sm.known[i], 0);
         Unit unit = sm.unit[i];
+        const uint16_t *pk = nullptr, *pq = nullptr, *pv = nullptr, *pb = nullptr;  // this lane's part of the next token
+        const float* pg = nullptr;
+        auto open = [&] {
+            if (!ok || unit.len <= 0) return;
+            const int hq = unit.head / a.group;
+            pk = a.k + unit.row0 * a.k_stride + hq * K + lane * kk;
+            pq = a.q + unit.row0 * a.q_stride + hq * K + lane * kk;
+            pg = a.g + unit.row0 * a.g_stride + unit.head * K + lane * kk;
+            pv = a.v + unit.row0 * a.v_stride + unit.head * V + lane * vv;
+            pb = a.beta + unit.row0 * a.beta_stride + unit.head;
+        };
+        open();
         auto ask = [&](int d) {
             has[d] = ok && unit.len > 0;
             if (!has[d]) return;
-            const int64_t row = unit.row0 + t;
-            const int h = unit.head, hq = h / a.group;
-            load_some<F16, kk>(a.k + row * a.k_stride + (int64_t)hq * K + lane * kk, a.vec, rk[d]);
-            load_some<F16, kk>(a.q + row * a.q_stride + (int64_t)hq * K + lane * kk, a.vec, rq[d]);
-            load_some<kk>(a.g + row * a.g_stride + (int64_t)h * K + lane * kk, a.vec, rg[d]);
-            load_some<F16, vv>(a.v + row * a.v_stride + (int64_t)h * V + lane * vv, a.vec, rv[d]);
-            rb[d] = a.beta[row * a.beta_stride + h];
+            to_group[d] = i % kGroups;
+            load_some<F16, kk>(pk, a.vec, rk[d]);
+            load_some<F16, kk>(pq, a.vec, rq[d]);
+            load_some<kk>(pg, a.vec, rg[d]);
+            load_some<F16, vv>(pv, a.vec, rv[d]);
+            rb[d] = *pb;
+            pk += a.k_stride;
+            pq += a.q_stride;
+            pg += a.g_stride;
+            pv += a.v_stride;
+            pb += a.beta_stride;
             if (++t == unit.len) {
                 t = 0;
-                i += kGroups;
+                i += kInputWarps;
                 ok = wait_for(&sm.known[i % kUnits], (i / kUnits) & 1);
                 unit = sm.unit[i % kUnits];
+                open();
             }
         };
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) ask(d);
         bool more = true;
-        for (int c = 0; more;) {
+        while (more) {
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
                 more = more && has[d];
                 if (!more) break;
+                auto& gr = sm.group[to_group[d]];
+                int c = 0;  // the token's number in its group (the array stays in registers)
+#pragma unroll
+                for (int x = 0; x < kGroups / kInputWarps; ++x)
+                    if (to_group[d] / kInputWarps == x) c = sent[x]++;
                 const int s = c % kSlots, round = c / kSlots;
                 if (round > 0 && !wait_for(&gr.token_empty[s], (round - 1) & 1)) {
                     more = false;
@@ -538,22 +563,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                 }
                 auto& to = gr.token[s];
 #pragma unroll
-                for (int e = 0; e < kk; ++e)
-                    to.kqe[lane * kk + e] =
-                        make_float4(from_b16<F16>(rk[d][e]), from_b16<F16>(rq[d][e]), expf(rg[d][e]), 0.f);
+                for (int x = 0; x < kk; ++x) {
+                    to.kqe[lane * kk + x] =
+                        make_float4(from_b16<F16>(rk[d][x]), from_b16<F16>(rq[d][x]), expf(rg[d][x]), 0.f);
+                }
 #pragma unroll
-                for (int e = 0; e < vv; ++e) to.v[lane * vv + e] = from_b16<F16>(rv[d][e]);
+                for (int x = 0; x < vv; ++x) to.v[lane * vv + x] = from_b16<F16>(rv[d][x]);
                 if (lane == 0) {
                     const float x = from_b16<F16>(rb[d]);
                     to.beta = a.logits ? 1.f / (1.f + expf(-x)) : x;
                 }
                 ptx::mbar_arrive(&gr.token_full[s]);
-                ++c;
                 ask(d);
             }
         }
     } else {
-        const int group = warp / kWarps, gt = tid - group * kGroupThreads;
+        const int group = warp / kWarps, gt = tid - group * kThreads;
         const int cg = gt % kColGroups, rl = gt / kColGroups;
         auto& gr = sm.group[group];
         bool ok = true;
@@ -562,34 +587,24 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             ok = wait_for(&sm.known[i % kUnits], (i / kUnits) & 1);
             const Unit unit = sm.unit[i % kUnits];
             if (ok && unit.len < 0) {  // (a thread that gave up waits for the others once)
-                ok = group_sync(group, true);
+                ok = group_sync<kThreads>(group, true);
                 break;
             }
             const int s = i % kRing;
-            float4* tile = reinterpret_cast<float4*>(sm.ring[s]);
-            uint2* tile16 = reinterpret_cast<uint2*>(sm.ring[s]);
+            void* tile = sm.ring[s];
             ok = ok && wait_for(&sm.full[i % kFull], (i / kFull) & 1);
             float4 S[kRows];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int at = (rl + r * kRowLanes) * kColGroups + cg;
-                if constexpr (STATE16) {
-                    const uint2 w = tile16[at];
-                    const float2 lo = from_b16x2<false>(w.x), hi = from_b16x2<false>(w.y);
-                    S[r] = make_float4(lo.x, lo.y, hi.x, hi.y);
-                } else {
-                    S[r] = tile[at];
-                }
-            }
+            for (int r = 0; r < kRows; ++r) S[r] = load_state<STATE16>(tile, (rl + r * kRowLanes) * kColGroups + cg);
             uint16_t* o = a.o + (unit.row0 * a.H + unit.head) * V + cg * 4;
             int t = 0;
             do {  // (once with ok false, to give up together)
                 const int ts = c % kSlots, b = c % Shape::kSums;
                 ok = ok && wait_for(&gr.token_full[ts], (c / kSlots) & 1);
-                const auto& token = gr.token[ts];
-                if (Shape::kSums == 1 && c > 0 && !(ok = group_sync(group, ok))) break;  // the sums before have been read
-                ok = step_token<K, V, F16, kRows, kGroupThreads>(S, token.kqe, token.v, token.beta, gr.sum[b], gr.kq[b],
-                                                                 a.scale, o, gt, [&] { return group_sync(group, ok); });
+                // with one exchange buffer: the sums before have been read
+                if (Shape::kSums == 1 && c > 0 && !(ok = group_sync<kThreads>(group, ok))) break;
+                ok = step_token<K, V, F16, kRows, kThreads>(S, gr.token[ts], gr.sums[b], a.scale, o, gt,
+                                                            [&] { return group_sync<kThreads>(group, ok); });
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&gr.token_empty[ts]);
@@ -598,13 +613,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             } while (++t < unit.len);
             if (!ok) break;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int at = (rl + r * kRowLanes) * kColGroups + cg;
-                if constexpr (STATE16)
-                    tile16[at] = make_uint2(pack_b16x2(S[r].x, S[r].y, false), pack_b16x2(S[r].z, S[r].w, false));
-                else
-                    tile[at] = S[r];
-            }
+            for (int r = 0; r < kRows; ++r) store_state<STATE16>(tile, (rl + r * kRowLanes) * kColGroups + cg, S[r]);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sm.done[s]);
