@@ -1,4 +1,5 @@
-"""ctypes binding of ``libkda.so`` (the C ABI in ``include/kda.h``).
+"""ctypes binding of ``libkda.so`` (the C ABI in ``include/kda.h``); the served
+layer's operators (step, rms_norm, linear) go through a compiled extension.
 
 Argument marshalling only: every step of the forward runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There
@@ -7,7 +8,6 @@ is no CPU fallback: if the library cannot be loaded, the calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -73,7 +73,6 @@ class LinearOpts(ctypes.Structure):
                 ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
 
 
-ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "sigmoid": 3, "logsigmoid": 4}
 IO_BF16, IO_F16 = 0, 1
 STATE_F32, STATE_BF16 = 0, 1
 PLAN_AUTO, PLAN_TWO_STAGE, PLAN_FUSED = 0, 1, 2
@@ -416,41 +415,26 @@ def bwd_dh(scale, do, dv_in, dht, dims: Dims, workspace, want_dhck=True, want_dh
 
 # ----------------------------------------------------------------- the served layer's operators
 # A decode step calls these once per layer and token, at a few microseconds of
-# kernel time each, so the marshalling below keeps to plain attribute reads:
-# the argument structs are made once per set of sizes, and the stream handle is
-# read without building a stream object.
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+# kernel time each: their checks and marshalling are in the compiled extension
+# (csrc_torch/layer_calls.cpp).
+_calls = None
 
 
-@functools.lru_cache(maxsize=4096)
-def _struct(cls, *fields):
-    return ctypes.byref(cls(*fields))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _token_stride(name, t):
-    """Elements between consecutive token rows of [B, T, ...] (0: contiguous)."""
-    if t.is_contiguous():
-        return 0
-    B, T = t.shape[:2]
-    inner = 1
-    for size, step in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        if size != 1 and step != inner:
-            raise TypeError(f"{name}: the heads of a token must be contiguous")
-        inner *= size
-    if B * T <= 1:
-        return 0
-    step = t.stride(1) if T > 1 else t.stride(0)
-    if step < inner or (B > 1 and t.stride(0) != T * step):
-        raise TypeError(f"{name}: token rows must be equally spaced over [B, T] and not overlap")
-    return step
+def _layer_calls():
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
+        load_library()
+        path = _build.EXTENSION
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing; run chunked_gated_delta_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_layer_calls", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_layer_calls", loader))
+        loader.exec_module(module)
+        module.set_error(KdaError)
+        _calls = module
+    return _calls
 
 
 def step(q, k, v, g, beta, state, slots=None, scale=None, cu_seqlens=None, out=None, status=None, stream=None,
@@ -467,76 +451,8 @@ def step(q, k, v, g, beta, state, slots=None, scale=None, cu_seqlens=None, out=N
     None for slot n.  ``status``: an int32 CUDA tensor that starts at zero and
     takes the errors found in slots and cu_seqlens; ``binding.status`` reads it.
     """
-    import torch
-    io = q.dtype
-    f16 = io == torch.float16
-    if not f16 and io != torch.bfloat16:
-        raise TypeError("q must be bf16 or fp16")
-    if q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[:2] != q.shape[:2]:
-        raise TypeError("q and k are [B,T,Hqk,K], v is [B,T,H,V]")
-    B, T, Hqk, K = q.shape
-    H, V = v.shape[2], v.shape[3]
-    if k.dtype != io or v.dtype != io or beta.dtype != io or g.dtype != torch.float32:
-        raise TypeError("k, v and beta have q's dtype, g is float32")
-    if g.shape != (B, T, H, K) or beta.shape != (B, T, H):
-        raise TypeError("g is [B,T,H,K], beta is [B,T,H]")
-    s16 = state.dtype == torch.bfloat16
-    if (not s16 and state.dtype != torch.float32) or not state.is_contiguous() or state.dim() != 4 \
-            or state.shape[1:] != (H, K, V):
-        raise TypeError("state must be a contiguous float32 or bfloat16 tensor [num_slots,H,K,V]")
-    N = 0
-    if cu_seqlens is not None:
-        N = cu_seqlens.numel() - 1
-        if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous() or N < 1:
-            raise TypeError("cu_seqlens must be a contiguous CUDA int32 tensor [N+1]")
-    if slots is not None and (slots.dtype != torch.int32 or not slots.is_cuda or not slots.is_contiguous()
-                              or slots.numel() != (N or B)):
-        raise TypeError("slots must be a contiguous CUDA int32 tensor, one per sequence")
-    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1):
-        raise TypeError("status must be a CUDA int32 tensor")
-    if not (q.is_cuda and k.is_cuda and v.is_cuda and g.is_cuda and beta.is_cuda and state.is_cuda):
-        raise TypeError("step takes CUDA tensors")
-    if out is None:
-        out = torch.empty((B, T, H, V), dtype=io, device=q.device)
-    elif out.dtype != io or out.shape != v.shape or not out.is_cuda or not out.is_contiguous():
-        raise TypeError("out must be a contiguous CUDA tensor of v's shape and dtype")
-    opts = _struct(StepOpts, f16, s16, 1 if beta_logits else 0, Hqk if Hqk != H else 0, state.shape[0], 0,
-                   _token_stride("q", q), _token_stride("k", k), _token_stride("v", v), _token_stride("g", g),
-                   _token_stride("beta", beta))
-    rc = load_library().kda_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                 K ** -0.5 if scale is None else scale, state.data_ptr(), _addr(slots),
-                                 _addr(cu_seqlens), out.data_ptr(), _struct(Dims, B, T, H, K, V, N), opts,
-                                 _addr(status), _raw_stream(stream, q.device))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_step")
-    return out
-
-
-def _dtype_codes():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
-
-
-_dtype_codes = functools.lru_cache(maxsize=1)(_dtype_codes)
-
-
-def _row_stride(name, t, dim):
-    """Elements between consecutive rows of [..., dim] (0: contiguous)."""
-    if t.is_contiguous():
-        return 0
-    if dim != 1 and t.stride(-1) != 1:
-        raise TypeError(f"{name}: the elements of a row must be contiguous")
-    step, rows = None, 1
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size != 1:
-            if step is None:
-                step = st
-            elif st != step * rows:
-                raise TypeError(f"{name}: rows must be equally spaced")
-            rows *= size
-    if step is not None and step < dim:
-        raise TypeError(f"{name}: rows must not overlap")
-    return 0 if step is None else step
+    return (_calls or _layer_calls()).step(q, k, v, g, beta, state, slots, scale,
+                                           cu_seqlens, out, status, stream, beta_logits)
 
 
 def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, residual_out=None, stream=None):
@@ -551,41 +467,7 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, 
     otherwise).  s, in x's dtype, is returned when there is a residual (else
     None); ``residual_out`` takes it and may be ``residual`` itself.
     """
-    import torch
-    codes = _dtype_codes()
-    io = x.dtype
-    out_dtype = io if out_dtype is None else out_dtype
-    if io not in codes or io == torch.float8_e4m3fn or x.dim() < 1 or not x.is_cuda:
-        raise TypeError("x must be a CUDA tensor of bf16, fp16 or fp32")
-    if out_dtype not in (io, torch.float32, torch.float8_e4m3fn):
-        raise TypeError("out_dtype must be x's dtype, float32 or float8_e4m3fn")
-    shape, dim = x.shape, x.shape[-1]
-    if residual is not None and (residual.dtype != io or residual.shape != shape or not residual.is_cuda):
-        raise TypeError("residual must be a CUDA tensor of x's shape and dtype")
-    if weight is not None and (weight.dtype not in (io, torch.float32) or weight.shape != (dim,)
-                               or not weight.is_cuda or not weight.is_contiguous()):
-        raise TypeError("weight must be a contiguous CUDA tensor [dim] of x's dtype or float32")
-    if residual_out is not None and (residual_out.dtype != io or residual_out.shape != shape
-                                     or not residual_out.is_cuda):
-        raise TypeError("residual_out must be a CUDA tensor of x's shape and dtype")
-    device = x.device
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=io, device=device)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=device)
-    elif out.dtype != out_dtype or out.shape != shape or not out.is_cuda or not out.is_contiguous():
-        raise TypeError("out must be a contiguous CUDA tensor of x's shape and out_dtype")
-    scale = torch.empty(shape[:-1], dtype=torch.float32, device=device) if out_dtype == torch.float8_e4m3fn else None
-    opts = _struct(NormOpts, codes[io], codes[out_dtype],
-                   1 if weight is not None and weight.dtype == torch.float32 else 0, eps,
-                   _row_stride("x", x, dim), 0 if residual is None else _row_stride("residual", residual, dim),
-                   0 if residual_out is None else _row_stride("residual_out", residual_out, dim))
-    rc = load_library().kda_rms_norm(x.data_ptr(), _addr(residual), _addr(weight), out.data_ptr(), _addr(scale),
-                                     _addr(residual_out), x.numel() // dim if dim else 0, dim, opts,
-                                     _raw_stream(stream, device))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_rms_norm")
-    return out, scale, residual_out
+    return (_calls or _layer_calls()).rms_norm(x, weight, residual, eps, out_dtype, out, residual_out, stream)
 
 
 def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None, out_dtype=None, out=None,
@@ -600,47 +482,5 @@ def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None,
     for float8.  act: None, "silu", "gelu", "sigmoid" or "logsigmoid".  ``out``
     may be ``residual`` itself.  ``status``: as in step.
     """
-    import torch
-    codes = _dtype_codes()
-    io, f8 = x.dtype, x.dtype == torch.float8_e4m3fn
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if f8 else io
-    if io not in codes or io == torch.float32 or w.dtype != io or not x.is_cuda or not w.is_cuda:
-        raise TypeError("x and w must be CUDA tensors of one dtype: bf16, fp16 or float8_e4m3fn")
-    if out_dtype not in codes or out_dtype == torch.float8_e4m3fn:
-        raise TypeError("out_dtype must be bf16, fp16 or float32")
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(k for k in ACTS if k)}")
-    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
-        raise TypeError("x is [..., K], w is [N, K]")
-    N, K = w.shape
-    lead = x.shape[:-1]
-    M = x.numel() // K if K else 0
-    if f8:
-        if x_scale is None or w_scale is None or x_scale.shape != lead or w_scale.shape != (N,) \
-                or x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 or not x_scale.is_cuda \
-                or not w_scale.is_cuda or not x_scale.is_contiguous() or not w_scale.is_contiguous():
-            raise TypeError("float8 operands take contiguous CUDA float32 x_scale [...] and w_scale [N]")
-    elif x_scale is not None or w_scale is not None:
-        raise TypeError("x_scale and w_scale go with float8 operands only")
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_cuda
-                             or not bias.is_contiguous()):
-        raise TypeError("bias must be a contiguous CUDA float32 tensor [N]")
-    y_shape = (*lead, N)
-    if residual is not None and (residual.dtype != out_dtype or residual.shape != y_shape or not residual.is_cuda):
-        raise TypeError("residual must be a CUDA tensor [..., N] of out_dtype")
-    if status is not None and (status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1):
-        raise TypeError("status must be a CUDA int32 tensor")
-    if out is None:
-        out = torch.empty(y_shape, dtype=out_dtype, device=x.device)
-    elif out.dtype != out_dtype or out.shape != y_shape or not out.is_cuda:
-        raise TypeError("out must be a CUDA tensor [..., N] of out_dtype")
-    opts = _struct(LinearOpts, codes[io], codes[out_dtype], ACTS[act], 0, _row_stride("x", x, K),
-                   _row_stride("w", w, K), 0 if residual is None else _row_stride("residual", residual, N),
-                   _row_stride("out", out, N))
-    rc = load_library().kda_linear(x.data_ptr(), w.data_ptr(), _addr(bias), _addr(residual), _addr(x_scale),
-                                   _addr(w_scale), out.data_ptr(), M, N, K, opts, _addr(status),
-                                   _raw_stream(stream, x.device))
-    if rc != KDA_OK:
-        raise KdaError(rc, "kda_linear")
-    return out
+    return (_calls or _layer_calls()).linear(x, w, bias, act, residual,
+                                             x_scale, w_scale, out_dtype, out, status, stream)

@@ -1,9 +1,13 @@
-"""In-tree build of ``libkda.so`` (sm_103a) with plain nvcc.
+"""In-tree build of ``libkda.so`` (sm_103a) with plain nvcc, and of the Python
+extension ``_layer_calls.so`` with the host compiler.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel to an object
 (``-gencode arch=compute_103a,code=sm_103a -lineinfo -O3``), then the objects
-are linked into ``chunked_gated_delta_gb300/libkda.so``.  The build is skipped
-when the library is newer than every source and header.
+are linked into ``chunked_gated_delta_gb300/libkda.so``.  The extension
+(``csrc_torch/layer_calls.cpp``: the Python calls of the served layer's
+operators, on torch's tensors) is compiled beside them against torch's headers
+and linked to the library.  The build is skipped when both are newer than every
+source and header.
 """
 from __future__ import annotations
 
@@ -11,13 +15,16 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
+CSRC_TORCH = os.path.join(PKG, "csrc_torch", "layer_calls.cpp")
 LIB = os.path.join(PKG, "libkda.so")
+EXTENSION = os.path.join(PKG, "_layer_calls.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,18 +45,55 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [CSRC_TORCH, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXTENSION):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXTENSION))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _host_compiler() -> str:
+    for cand in (os.environ.get("CXX"), "g++", "c++"):
+        if cand and shutil.which(cand):
+            return cand
+    raise RuntimeError("no C++ compiler found: the Python extension cannot be built")
+
+
+def _compile_extension() -> str:
+    """csrc_torch/layer_calls.cpp to an object, against this interpreter's torch."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(OBJDIR, "layer_calls.cpp.o")
+    _run([_host_compiler(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + sysconfig.get_paths()["include"],
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+          "-c", CSRC_TORCH, "-o", obj], "compiling layer_calls.cpp")
+    return obj
+
+
+def _link_extension(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXTENSION + f".tmp{os.getpid()}"
+    _run([_host_compiler(), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + lib,
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib],
+         "linking the Python extension")
+    os.replace(tmp, EXTENSION)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libkda.so; returns its path."""
+    """Compile and link libkda.so and the Python extension; returns the library's path."""
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
@@ -66,14 +110,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        extension = ex.submit(_compile_extension)
         objs = list(ex.map(compile_one, srcs))
+        extension = extension.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of libkda.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_extension(extension)
     return LIB
 
 
