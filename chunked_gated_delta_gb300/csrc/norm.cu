@@ -6,11 +6,13 @@
 //     8 bits: a = max(max |y|, 1e-30), code = e4m3(y * (448 / a)), scale = a / 448
 //
 // Bound: HBM; every element is read once and written once.  A row stays in the
-// registers of its threads between the load and the store, so the two
-// statistics (the sum of squares, then the largest |y|) cost exchanges but no
-// second read.  A row is taken by a team: 8 to 32 lanes of a warp for short
-// rows (head norms), so that its sums are shuffles and several rows share a
-// CTA, or a whole CTA for long ones, with one barrier per statistic.
+// registers of its threads between the load and the store, so the statistics
+// cost exchanges but no second read: the sum of squares and, for 8 bits, the
+// largest |s w|, which times 1 / sqrt(...) is the largest |y| (to a rounding),
+// so that both are joined at once.  A row is taken by a team: 2 to 32 lanes of a
+// warp for short rows (head norms), so that its sums are shuffles and many rows
+// share a CTA, or a whole CTA for long ones, with one barrier.
+#include "internal.h"
 #include "layer_ops.cuh"
 
 namespace kda {
@@ -73,35 +75,38 @@ __device__ __forceinline__ void store_vec(void* p, int64_t at, const float* f, i
     }
 }
 
-// Reduces v over the team: lanes of a warp (TEAM <= 32), or the whole CTA
-// (TEAM = 0) through s[32].
-template <int TEAM, bool MAX>
-__device__ __forceinline__ float team_reduce(float v, float* s) {
-    auto join = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
+// Joins the sum and the largest over the team: lanes of a warp (TEAM <= 32), or
+// the whole CTA (TEAM = 0) through s[32].
+template <int TEAM>
+__device__ __forceinline__ float2 team_join(float2 v, float2* s, bool with_max) {
+    auto join = [&](int off) {
+        v.x += __shfl_xor_sync(~0u, v.x, off);
+        if (with_max) v.y = max_nan(v.y, __shfl_xor_sync(~0u, v.y, off));
+    };
     constexpr int kLanes = TEAM ? TEAM : 32;
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) v = join(v, __shfl_xor_sync(~0u, v, off));
+    for (int off = kLanes / 2; off > 0; off >>= 1) join(off);
     if constexpr (TEAM == 0) {
         const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) s[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = lane < warps ? s[lane] : 0.f;  // 0 is neutral for both (|y| >= 0)
+        v = lane < warps ? s[lane] : make_float2(0.f, 0.f);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v = join(v, __shfl_xor_sync(~0u, v, off));
+        for (int off = 16; off > 0; off >>= 1) join(off);
     }
     return v;
 }
 
 template <int IO, int VEC, int NV, int TEAM>
 __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormArgs a) {
-    __shared__ float s_red[2][32];
+    __shared__ float2 s_join[32];
     const int per = TEAM ? (int)(blockDim.x / TEAM) : 1;  // rows a CTA takes
     const int lane = TEAM ? (int)(threadIdx.x % TEAM) : (int)threadIdx.x;
     const int width = TEAM ? TEAM : (int)blockDim.x;
     const int64_t row = (int64_t)blockIdx.x * per + (TEAM ? (int)(threadIdx.x / TEAM) : 0);
     const bool live = row < a.rows;  // (teams past the last row still take part in the shuffles)
+    const bool f8 = a.out == KDA_DTYPE_E4M3;
     float s[NV][VEC];
-    float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * width) * VEC;
@@ -121,43 +126,40 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
                 load_vec<IO, VEC>(a.r, row * a.r_stride + c, r);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) s[i][j] += r[j];
-                if (a.sum) store_vec<VEC>(a.sum, row * a.sum_stride + c, s[i], IO);
             }
         }
-    } else if (a.sum) {
+    }
+    if (a.sum) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + i * width) * VEC;
             if (live && c < a.dim) store_vec<VEC>(a.sum, row * a.sum_stride + c, s[i], IO);
         }
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sq += s[i][j] * s[i][j];
-    sq = team_reduce<TEAM, false>(sq, s_red[0]);
-    const float rstd = 1.f / sqrtf(sq * a.inv_dim + a.eps);
-    float amax = kAmaxFloor;
+    // s becomes s w; the scale of a row follows its statistics
+    float2 stat = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * width) * VEC;
-        float w[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) stat.x += s[i][j] * s[i][j];
         if (a.w && c < a.dim) {
+            float w[VEC];
             if (a.w_f32) load_vec<KDA_DTYPE_F32, VEC>(a.w, c, w);
             else load_vec<IO, VEC>(a.w, c, w);
-        } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) w[j] = 1.f;
+            for (int j = 0; j < VEC; ++j) s[i][j] *= w[j];
         }
+        if (f8) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            s[i][j] = s[i][j] * rstd * w[j];
-            if (c < a.dim) amax = max_nan(amax, fabsf(s[i][j]));
+            for (int j = 0; j < VEC; ++j) stat.y = max_nan(stat.y, fabsf(s[i][j]));
         }
     }
+    stat = team_join<TEAM>(stat, s_join, f8);
+    const float rstd = 1.f / sqrtf(stat.x * a.inv_dim + a.eps);
     float inv = 1.f;
-    if (a.out == KDA_DTYPE_E4M3) {
-        amax = team_reduce<TEAM, true>(amax, s_red[1]);
+    if (f8) {
+        const float amax = max_nan(kAmaxFloor, stat.y * rstd);
         inv = kE4m3Max / amax;
         if (live && lane == 0) a.y_scale[row] = amax / kE4m3Max;
     }
@@ -165,10 +167,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
     for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * width) * VEC;
         if (live && c < a.dim) {
-            if (a.out == KDA_DTYPE_E4M3) {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) s[i][j] *= inv;
-            }
+            for (int j = 0; j < VEC; ++j) s[i][j] = s[i][j] * rstd * inv;
             store_vec<VEC>(a.y, row * a.dim + c, s[i], a.out);
         }
     }
@@ -181,25 +181,42 @@ cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// The team for a row of `vecs` vectors.
+// The team for a row of `vecs` vectors.  Four 16-byte loads a thread, whatever
+// the row (two vectors of x and two of the residual, or four of x), are in flight
+// together and keep the sums short.  Measured, of the 6.67 TB/s that a copy
+// reaches: 1.07 M rows of 128 with one vector a thread 5.3 TB/s, with four 6.6;
+// 260000 rows of 512 with residual, e4m3, two vectors 6.1, four 5.4; 32768 rows
+// of 4096 without residual one vector 4.4, two 5.3, four 6.4, eight 4.8.  Few
+// rows leave most SMs idle and take the shortest path instead: one vector a
+// thread (one row of 4096: 2.6 us against 3.9).
 template <int IO, int VEC>
 cudaError_t pick(const NormArgs& a, cudaStream_t s) {
     const int vecs = (a.dim + VEC - 1) / VEC;
-    if (vecs <= 8) return launch<IO, VEC, 1, 8>(a, 256, s);
-    if (vecs <= 16) return launch<IO, VEC, 1, 16>(a, 256, s);
-    if (vecs <= 32) return launch<IO, VEC, 1, 32>(a, 256, s);
-    if (vecs <= 64) return launch<IO, VEC, 2, 32>(a, 256, s);
-    if (vecs <= 128) return launch<IO, VEC, 4, 32>(a, 256, s);
-    const int threads = (vecs + 31) / 32 * 32;
-    if (threads <= 512) return launch<IO, VEC, 1, 0>(a, threads, s);
-    if (vecs <= 2048) return launch<IO, VEC, 2, 0>(a, (threads / 2 + 31) / 32 * 32, s);
-    if (vecs <= 4096) return launch<IO, VEC, 4, 0>(a, 1024, s);
-    if constexpr (VEC == 1) {
-        if (vecs <= 8192) return launch<IO, VEC, 8, 0>(a, 1024, s);
-        if (vecs <= 16384) return launch<IO, VEC, 16, 0>(a, 1024, s);
-        return launch<IO, VEC, 32, 0>(a, 1024, s);
+    auto threads = [&](int nv) { return (vecs + nv * 32 - 1) / (nv * 32) * 32; };
+    if constexpr (VEC == 8) {
+        if (vecs > 32 && vecs <= 1024 && a.rows <= 2 * device_sm_count())
+            return launch<IO, VEC, 1, 0>(a, threads(1), s);
+        if (a.r) {
+            if (vecs <= 4) return launch<IO, VEC, 2, 2>(a, 256, s);
+            if (vecs <= 8) return launch<IO, VEC, 2, 4>(a, 256, s);
+            if (vecs <= 16) return launch<IO, VEC, 2, 8>(a, 256, s);
+            if (vecs <= 32) return launch<IO, VEC, 2, 16>(a, 256, s);
+            if (vecs <= 64) return launch<IO, VEC, 2, 32>(a, 256, s);
+        } else {
+            if (vecs <= 8) return launch<IO, VEC, 4, 2>(a, 256, s);
+            if (vecs <= 16) return launch<IO, VEC, 4, 4>(a, 256, s);
+            if (vecs <= 32) return launch<IO, VEC, 4, 8>(a, 256, s);
+            if (vecs <= 64) return launch<IO, VEC, 4, 16>(a, 256, s);
+        }
+        if (vecs <= 128) return launch<IO, VEC, 4, 32>(a, 256, s);
+        return launch<IO, VEC, 4, 0>(a, threads(4), s);
+    } else {
+        if (vecs <= 32) return launch<IO, VEC, 4, 8>(a, 256, s);
+        if (vecs <= 128) return launch<IO, VEC, 4, 32>(a, 256, s);
+        if (vecs <= 512) return launch<IO, VEC, 16, 32>(a, 256, s);
+        if (vecs <= 16384) return launch<IO, VEC, 16, 0>(a, threads(16), s);
+        return launch<IO, VEC, 32, 0>(a, threads(32), s);
     }
-    return cudaErrorInvalidValue;  // not reached: dim <= 32768
 }
 
 }  // namespace
