@@ -75,9 +75,11 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
+    ptx::grid_dep_launch();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
+    ptx::grid_dep_wait();
 
     if (warp == 0 && elect_one()) {
         int issued = 0;
@@ -235,18 +237,8 @@ cudaError_t launch(const LinArgs& a, int log_split, cudaStream_t s) {
     auto kern = kda_linear_kernel<NT, F8>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1u << log_split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.N + kFeatures - 1) / kFeatures) << log_split, (unsigned)((a.M + NT - 1) / NT));
-    cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = Shape::kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, log_split);
+    const dim3 grid((unsigned)((a.N + kFeatures - 1) / kFeatures) << log_split, (unsigned)((a.M + NT - 1) / NT));
+    return launch_cluster(kern, grid, dim3(kLinThreads), Shape::kSmem, 1u << log_split, s, a, log_split);
 }
 
 template <int NT>
@@ -351,6 +343,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
                             (!residual || (is_aligned(residual, 16) && ldr * oes % 16 == 0));
     const int four = 4 * oes;  // bytes of a lane's features
     a.wide = is_aligned(y, four) && ldy % 4 == 0 && (!residual || (is_aligned(residual, four) && ldr % 4 == 0));
+    if (M == 1) return launch_linear_one(a, x, w, K, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16, oes == 2);
     if (plan.wide)
         return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -1,5 +1,5 @@
-// linear.cuh -- what the two kernels of kda_linear share (linear.cu: few
-// tokens, or rows of y off 16 bytes; linear_wide.cu: many tokens): arguments,
+// linear.cuh -- what the kernels of kda_linear share (linear_one.cu: one token;
+// linear.cu: few tokens, or rows of y off 16 bytes; linear_wide.cu: many): arguments,
 // cluster and tcgen05 wrappers, the activations.
 #pragma once
 #include <cuda.h>
@@ -29,12 +29,34 @@ struct LinArgs {
     int wide;  // rows of y and residual take loads and stores of four elements
 };
 
+// The kernel for one token (linear_one.cu).
+cudaError_t launch_linear_one(const LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldw, cudaStream_t s);
 // The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile;
 // an fp32 y takes 128.
 // tm_w, tm_x and idesc are set there; x, w are the operands and ldx, ldw their
 // row strides.
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
                                int64_t ldw, cudaStream_t s);
+
+// launch_dependent (internal.h) with a cluster of `size` CTAs along x.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned size,
+                                  cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 namespace {
 

@@ -138,10 +138,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     ptx::tc_fence_before();
+    ptx::grid_dep_launch();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are set before either signals the other's
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base;
+    ptx::grid_dep_wait();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -363,18 +365,8 @@ cudaError_t launch(WideArgs& p, const void* w, int64_t K, int64_t ldw, cudaStrea
     auto kern = kda_linear_wide_kernel<TN, F8, OUT16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WideShape<TN>::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = WideShape<TN>::kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return launch_cluster(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kThreads),
+                          WideShape<TN>::kSmem, 2, s, p);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@
 // share a CTA, or a whole CTA for long ones, with one barrier.
 #include "internal.h"
 #include "layer_ops.cuh"
+#include "ptx.cuh"
 
 namespace kda {
 namespace {
@@ -100,6 +101,8 @@ __device__ __forceinline__ float2 team_join(float2 v, float2* s, bool with_max) 
 template <int IO, int VEC, int NV, int TEAM>
 __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormArgs a) {
     __shared__ float2 s_join[32];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const int per = TEAM ? (int)(blockDim.x / TEAM) : 1;  // rows a CTA takes
     const int lane = TEAM ? (int)(threadIdx.x % TEAM) : (int)threadIdx.x;
     const int width = TEAM ? TEAM : (int)blockDim.x;
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
 template <int IO, int VEC, int NV, int TEAM>
 cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
     const int64_t per = TEAM ? threads / TEAM : 1;
-    kda_norm_kernel<IO, VEC, NV, TEAM><<<(unsigned)((a.rows + per - 1) / per), threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kda_norm_kernel<IO, VEC, NV, TEAM>, dim3((unsigned)((a.rows + per - 1) / per)),
+                            dim3((unsigned)threads), 0, s, a);
 }
 
 // The team for a row of `vecs` vectors.  Four 16-byte loads a thread, whatever

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     __shared__ Sums<VT, kStepThreads> s_sums[2];
 
     const int tid = threadIdx.x;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
     const int tiles = a.V / VT;
     const int tile = blockIdx.x % tiles;
     const int h = (blockIdx.x / tiles) % a.H;
@@ -411,7 +413,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             }
         ptx::fence_mbar_init();
     }
+    ptx::grid_dep_launch();
     __syncthreads();
+    ptx::grid_dep_wait();
 
     if (warp == kLoadWarp) {
         const int total = a.N * a.H;
@@ -628,8 +632,8 @@ cudaError_t launch_stream(const StepArgs& a, int sms, cudaStream_t s) {
     constexpr int kSmem = StreamShape<K, V, STATE16>::kSmem;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)min((int64_t)sms, (int64_t)a.N * a.H), kStreamThreads, kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3((unsigned)min((int64_t)sms, (int64_t)a.N * a.H)), dim3(kStreamThreads), kSmem, s,
+                            a);
 }
 
 template <int K, int V>
@@ -641,14 +645,9 @@ cudaError_t launch_stream(const StepArgs& a, bool f16, bool state16, int sms, cu
 template <int K, int VT>
 cudaError_t launch(const StepArgs& a, bool f16, bool state16, cudaStream_t s) {
     const unsigned grid = (unsigned)((int64_t)a.N * a.H * (a.V / VT));
-    if (f16) {
-        if (state16) kda_step_kernel<K, VT, true, true><<<grid, kStepThreads, 0, s>>>(a);
-        else kda_step_kernel<K, VT, true, false><<<grid, kStepThreads, 0, s>>>(a);
-    } else {
-        if (state16) kda_step_kernel<K, VT, false, true><<<grid, kStepThreads, 0, s>>>(a);
-        else kda_step_kernel<K, VT, false, false><<<grid, kStepThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    auto kern = f16 ? (state16 ? kda_step_kernel<K, VT, true, true> : kda_step_kernel<K, VT, true, false>)
+                    : (state16 ? kda_step_kernel<K, VT, false, true> : kda_step_kernel<K, VT, false, false>);
+    return launch_dependent(kern, dim3(grid), dim3(kStepThreads), 0, s, a);
 }
 
 }  // namespace
