@@ -259,7 +259,7 @@ struct Plan {
     int tokens;     // per tile; of the wide kernel: features per tile
     int log_split;  // 2^log_split slices of k
 };
-Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16, bool out16) {
+Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16) {
     const int sms = device_sm_count();
     const double stream = (double)bytes / 6.6e6;  // x and w once from HBM
     auto cost = [&](int64_t units, int64_t slots, double stages, double per_stage, double end, double call) {
@@ -286,7 +286,7 @@ Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16, b
     if (rows_on_16 && M > 64) {
         const int64_t tm = (M + 255) / 256;
         offer({true, 128, 0}, cost(tm * ((N + 127) / 128), sms / 2, kblocks, 0.215, 0.7, 4.3));
-        if (out16) offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5));
+        offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5));
     }
     return best;
 }
@@ -344,7 +344,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     const int four = 4 * oes;  // bytes of a lane's features
     a.wide = is_aligned(y, four) && ldy % 4 == 0 && (!residual || (is_aligned(residual, four) && ldr % 4 == 0));
     if (M == 1) return launch_linear_one(a, x, w, K, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16, oes == 2);
+    const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16);
     if (plan.wide)
         return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     const int nt = plan.tokens, log_split = plan.log_split;

@@ -31,8 +31,7 @@ struct LinArgs {
 
 // The kernel for one token (linear_one.cu).
 cudaError_t launch_linear_one(const LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldw, cudaStream_t s);
-// The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile;
-// an fp32 y takes 128.
+// The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile.
 // tm_w, tm_x and idesc are set there; x, w are the operands and ldx, ldw their
 // row strides.
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
@@ -89,26 +88,41 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// FAST: y has 16 bits, whose rounding (2^-9 or 2^-12) hides the few 2^-23 of the
-// approximate exponential and quotient; else they are within an ulp or two.
+// exp(-|v|) to about 2^-22: 2^t with t = -|v| log2 e in fp32, times one plus what
+// that product lost (its rounding and the rest of log2 e) times ln 2.  Below
+// exp(-104) it is zero.
+__device__ __forceinline__ float exp_minus_abs(float v) {
+    constexpr float kLog2e = 1.44269504f, kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.693147181f;
+    const float x = fmaxf(-fabsf(v), -104.f), t = x * kLog2e;
+    const float lost = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e * kLn2, lost, e);
+}
+// FAST: y has 16 bits, whose rounding (2^-9 or 2^-12) hides the approximate
+// exponential's error, which grows with |v|; else the results are within about
+// 2^-21 (all the epilogue's threads do this for every element, so the library's
+// exact forms would hold up the tiles behind).
 template <int ACT, bool FAST>
 __device__ __forceinline__ float activated(float v) {
-    if constexpr (ACT == KDA_ACT_SILU) return FAST ? __fdividef(v, 1.f + __expf(-v)) : v / (1.f + expf(-v));
     if constexpr (ACT == KDA_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if constexpr (ACT == KDA_ACT_SIGMOID) return FAST ? __fdividef(1.f, 1.f + __expf(-v)) : 1.f / (1.f + expf(-v));
+    if constexpr (ACT == KDA_ACT_SILU || ACT == KDA_ACT_SIGMOID) {
+        const float one = ACT == KDA_ACT_SILU ? v : 1.f;
+        if constexpr (FAST) return __fdividef(one, 1.f + __expf(-v));
+        const float e = exp_minus_abs(v);
+        const float y = __fdividef(v < 0.f ? one * e : one, 1.f + e);
+        return v == v ? y : v;
+    }
     if constexpr (ACT == KDA_ACT_LOGSIGMOID) {
-        // min(v, 0) - log(1 + e), e = exp(-|v|) in [0, 1]: log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3,
-        // by artanh's series s + s^3/3 + ... + s^15/15 (the rest is below 2^-27 of it)
-        const float e = FAST ? __expf(-fabsf(v)) : expf(-fabsf(v));
+        // min(v, 0) - log(1 + e), e = exp(-|v|): log(1 + e) = 2 artanh(s) with s = e / (2 + e) <= 1/3, and
+        // artanh(s) = s (1 + z p(z)), z = s^2, with p fitted to sum z^k / (2 k + 3) on [0, 1/9] (to 5e-9 of z p)
+        const float e = FAST ? __expf(-fabsf(v)) : exp_minus_abs(v);
         const float s = __fdividef(e, 2.f + e), z = s * s;
-        float r = 1.f / 15.f;
-        r = fmaf(r, z, 1.f / 13.f);
-        r = fmaf(r, z, 1.f / 11.f);
-        r = fmaf(r, z, 1.f / 9.f);
-        r = fmaf(r, z, 1.f / 7.f);
-        r = fmaf(r, z, 1.f / 5.f);
-        r = fmaf(r, z, 1.f / 3.f);
-        return fminf(v, 0.f) - 2.f * fmaf(s * z, r, s);
+        float p = 0.14012229f;
+        p = fmaf(p, z, 0.13999571f);
+        p = fmaf(p, z, 0.2001085f);
+        p = fmaf(p, z, 0.33333207f);
+        return (v > 0.f ? 0.f : v) - 2.f * fmaf(s * z, p, s);
     }
     return v;
 }

@@ -9,8 +9,10 @@
 // so the epilogue of a tile runs beside the MMAs of the next.
 //
 // Roles per CTA: warp 0 loads (TMA, a ring of kStages stages), warp 1 of the
-// first CTA issues the MMAs of both, warps 2-9 are the epilogue: warp w has
-// the 32 tokens of TMEM lane quarter w % 4 and one half of the features.  A
+// first CTA issues the MMAs of both, warps 4-11 are the epilogue: warp w has
+// the 32 tokens of TMEM lane quarter w % 4 and one half of the features.  The
+// first four warps hand their registers to the epilogue's (an fp32 y keeps 128
+// running sums a thread).  A
 // thread has a token's row; 128-byte row pieces go through a swizzled staging
 // box per warp, which TMA loads the residual into and stores y from, so
 // global memory sees whole lines and ragged edges are clipped by the copy.
@@ -22,7 +24,10 @@ namespace {
 constexpr int kTileM = 256;                            // tokens per pair
 constexpr int kEpilogueWarps = 8;
 constexpr int kBoxBytes = 32 * 128;                    // 32 tokens x 128 bytes
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kFirstEpilogue = 4;                      // warp
+constexpr int kThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
+// registers: 128 x 40 + 256 x 224 of the 384 x 168 that a block is launched with
+constexpr int kFewRegs = 40, kManyRegs = 224;
 constexpr int kGroup = 8;                              // token tiles that share a sweep over the features
 constexpr int kSegment = 16;                           // stages of k per accumulator where y is fp32
 
@@ -81,6 +86,33 @@ __device__ __forceinline__ void release(uint64_t* acc_empty, int lane) {
     ptx::tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_remote(peer_smem(ptx::smem_u32(acc_empty), 0));
+}
+
+// The 32 fp32 values of a lane's row in a box, two swizzled pieces at a time.
+template <int ACT>
+__device__ __forceinline__ void activated_row(uint8_t* row, int lane) {
+#pragma unroll 1
+    for (int j = 0; j < 8; j += 2) {
+        float4* p[2] = {reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4)),
+                        reinterpret_cast<float4*>(row + (((j + 1) ^ (lane & 7)) << 4))};
+        float4 f[2] = {*p[0], *p[1]};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[i].x = activated<ACT, false>(f[i].x);
+            f[i].y = activated<ACT, false>(f[i].y);
+            f[i].z = activated<ACT, false>(f[i].z);
+            f[i].w = activated<ACT, false>(f[i].w);
+            *p[i] = f[i];
+        }
+    }
+}
+__device__ __forceinline__ void activate_row(uint8_t* row, int lane, int act) {
+    switch (act) {
+    case KDA_ACT_SILU: activated_row<KDA_ACT_SILU>(row, lane); break;
+    case KDA_ACT_GELU: activated_row<KDA_ACT_GELU>(row, lane); break;
+    case KDA_ACT_SIGMOID: activated_row<KDA_ACT_SIGMOID>(row, lane); break;
+    case KDA_ACT_LOGSIGMOID: activated_row<KDA_ACT_LOGSIGMOID>(row, lane); break;
+    }
 }
 
 // Tile t of the sweep: groups of kGroup token tiles, the features outside, the group's tokens inside.
@@ -145,8 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
     const uint32_t tmem = tmem_base;
     ptx::grid_dep_wait();
 
-    if (warp == 0) {
-        if (elect_one()) {
+    if (warp < kFirstEpilogue) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 0 && elect_one()) {
             int it = 0;  // stages issued
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
@@ -172,8 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                         wait_for(&full[i % kStages], (i / kStages) & 1);
             }
         }
-    } else if (warp == 1) {
-        if (rank == 0 && elect_one()) {
+        if (warp == 1 && rank == 0 && elect_one()) {
             int it = 0, n_acc = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
@@ -202,10 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
             if (!ok) s_fail = 1;
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         constexpr int kCols = TN / 2;  // features of a warp
         constexpr int kBoxCols = OUT16 ? 64 : 32;
         constexpr int kBoxes = kCols / kBoxCols;
-        const int e = warp - 2, quarter = warp & 3, half = e >> 2;
+        const int e = warp - kFirstEpilogue, quarter = warp & 3, half = e >> 2;
         uint8_t* box = ring + kStages * kStageBytes + e * kBoxBytes;
         uint8_t* row = box + lane * 128;
         const bool f16 = a.out == KDA_DTYPE_F16;
@@ -257,15 +290,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                 }
             }
             if (!ok) break;
-#pragma unroll
+            // One box of the row piece after another.  (Running sums are in registers, so
+            // their boxes are unrolled; from TMEM it is a loop, whose code is shorter.)
+#pragma unroll(kSegments ? kBoxes : 1)
             for (int q = 0; q < kBoxes; ++q) {
                 const int n = n0 + q * kBoxCols;
                 const bool live = rows && n < a.N;
-                float v[kBoxCols];
-                if constexpr (kSegments) {
-#pragma unroll
-                    for (int c = 0; c < kBoxCols; ++c) v[c] = sum[q * kBoxCols + c];
-                } else {
+                float fresh[kSegments ? 1 : kBoxCols];
+                float* v = kSegments ? sum + q * kBoxCols : fresh;  // (registers: every index is known)
+                if constexpr (!kSegments) {
 #pragma unroll
                     for (int c = 0; c < kBoxCols; c += 16) ptx::tmem_ld16(acc + q * kBoxCols + c, v + c);
                     ptx::tmem_ld_wait();
@@ -273,12 +306,17 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                 }
                 if (!live) continue;
 #pragma unroll
-                for (int c = 0; c < kBoxCols; ++c) {
-                    const int i = (q * kBoxCols + c) >> 5, from = (q * kBoxCols + c) & 31;
-                    if (F8) v[c] *= xs * __shfl_sync(~0u, scale[i], from);
-                    v[c] += __shfl_sync(~0u, bias[i], from);
+                for (int h = 0; h < kBoxCols / 32; ++h) {
+                    float box_bias = bias[h], box_scale = scale[h];
+#pragma unroll
+                    for (int i = 1; i < kBoxes; ++i)
+                        if (q == i) box_bias = bias[i * (kBoxCols / 32) + h], box_scale = scale[i * (kBoxCols / 32) + h];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (F8) v[32 * h + c] *= xs * __shfl_sync(~0u, box_scale, c);
+                        v[32 * h + c] += __shfl_sync(~0u, box_bias, c);
+                    }
                 }
-                activate_all<kBoxCols, OUT16>(v, a.act);
                 if (a.residual) {
                     ok = __all_sync(~0u, wait_for(&res[e], loads & 1));
                     if (!ok) break;
@@ -287,10 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                     if (lane == 0) ptx::bulk_wait_read0();
                     __syncwarp();
                 }
+                if constexpr (OUT16) {
+                    activate_all<kBoxCols, true>(v, a.act);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {  // 16-byte pieces of the row, swizzled
-                    uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
-                    if constexpr (OUT16) {
+                    for (int j = 0; j < 8; ++j) {  // 16-byte pieces of the row, swizzled
+                        uint4* at = reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4));
                         float* f = v + 8 * j;
                         if (a.residual) {
                             const uint4 u = *at;
@@ -304,16 +343,32 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                         }
                         *at = make_uint4(pack_b16x2(f[0], f[1], f16), pack_b16x2(f[2], f[3], f16),
                                          pack_b16x2(f[4], f[5], f16), pack_b16x2(f[6], f[7], f16));
-                    } else {
+                    }
+                } else {
+                    // The activation runs over the row in the box, in a loop: unrolled over the
+                    // registers its code alone, once per tile, took longer than its arithmetic
+                    // (4096 x 2048 x 2048 with log-sigmoid 40 us, without it 30).
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float4* at = reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4));
+                        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (a.residual) r = *at;
                         float4 f = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        if (a.act == KDA_ACT_NONE) f = make_float4(f.x + r.x, f.y + r.y, f.z + r.z, f.w + r.w);
+                        *at = f;
+                        v[4 * j] = r.x, v[4 * j + 1] = r.y, v[4 * j + 2] = r.z, v[4 * j + 3] = r.w;
+                    }
+                    if (a.act != KDA_ACT_NONE) {
+                        activate_row(row, lane, a.act);
                         if (a.residual) {
-                            const float4 r = *reinterpret_cast<float4*>(at);
-                            f.x += r.x;
-                            f.y += r.y;
-                            f.z += r.z;
-                            f.w += r.w;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float4* at = reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4));
+                                const float4 f = *at;
+                                *at = make_float4(f.x + v[4 * j], f.y + v[4 * j + 1], f.z + v[4 * j + 2],
+                                                  f.w + v[4 * j + 3]);
+                            }
                         }
-                        *reinterpret_cast<float4*>(at) = f;
                     }
                 }
                 ptx::fence_proxy_async_smem();
@@ -369,6 +424,11 @@ cudaError_t launch(WideArgs& p, const void* w, int64_t K, int64_t ldw, cudaStrea
                           WideShape<TN>::kSmem, 2, s, p);
 }
 
+template <int TN, bool F8>
+cudaError_t launch(WideArgs& p, bool out16, const void* w, int64_t K, int64_t ldw, cudaStream_t s) {
+    return out16 ? launch<TN, F8, true>(p, w, K, ldw, s) : launch<TN, F8, false>(p, w, K, ldw, s);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
@@ -380,11 +440,9 @@ cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const vo
         (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr)))
         return cudaErrorInvalidValue;
     const bool f8 = a.io == KDA_DTYPE_E4M3;
-    // (at 256 features the segments' running sums would not fit in an epilogue thread's registers)
-    if (a.out == KDA_DTYPE_F32)
-        return f8 ? launch<128, true, false>(p, w, K, ldw, s) : launch<128, false, false>(p, w, K, ldw, s);
-    if (tn == 128) return f8 ? launch<128, true, true>(p, w, K, ldw, s) : launch<128, false, true>(p, w, K, ldw, s);
-    return f8 ? launch<256, true, true>(p, w, K, ldw, s) : launch<256, false, true>(p, w, K, ldw, s);
+    const bool out16 = a.out != KDA_DTYPE_F32;
+    if (tn == 128) return f8 ? launch<128, true>(p, out16, w, K, ldw, s) : launch<128, false>(p, out16, w, K, ldw, s);
+    return f8 ? launch<256, true>(p, out16, w, K, ldw, s) : launch<256, false>(p, out16, w, K, ldw, s);
 }
 
 }  // namespace kda

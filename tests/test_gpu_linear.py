@@ -151,6 +151,23 @@ def test_bad_rows_stay_by_themselves():
         assert torch.equal(y[rows][:, cols], ref[rows][:, cols])
 
 
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_activations_of_extreme_values(act, out):
+    """Through the bias: NaN stays NaN, infinities and large values give the functions' limits."""
+    vals = [float("nan"), float("inf"), 1e30, 200.0, 89.0, 20.0, 1e-6, 0.0, -1e-6, -20.0, -89.0, -104.0, -200.0, -1e30]
+    b = torch.tensor(vals * 20, device="cuda")
+    want = ACTS[act](b.double())
+    for M in (1, 20, 300, 4096):
+        x, w = torch.zeros((M, 64), device="cuda").to(BF16), torch.zeros((280, 64), device="cuda").to(BF16)
+        y = kda.linear(x, w, bias=b, act=act, out_dtype=out).double()
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(y), nan.expand(M, -1))
+        ok = ~nan & torch.isfinite(want.to(out))
+        assert torch.equal(y[:, ~nan & ~ok], want[~nan & ~ok].expand(M, -1))
+        assert_close(y[:, ok], want[ok].expand(M, -1), HALF_ULP[out] + 2.0 ** -20, 1e-30)
+
+
 def test_output_beyond_32_bits():
     M, N, K = 70000, 32768, 64
     x, w, _, _ = operands(M, N, K, BF16)
