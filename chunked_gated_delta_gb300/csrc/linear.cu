@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kLinThreads = 256;
 constexpr int kLinWarps = kLinThreads / 32;
+constexpr int kEarly = 2;           // tokens of a warp whose residual is loaded before the sums are there
 constexpr int kFeatures = 128;      // rows of w per tile
 constexpr int kMaxStages = 12;
 
@@ -81,6 +82,30 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     const uint32_t tmem = tmem_base;
     ptx::grid_dep_wait();
 
+    // What the end of the tile needs besides the sums is asked for now: a warp's
+    // features' bias and scales, and the residual and scale of its first tokens.
+    const int log_part = (31 - __clz(NT)) - log_split, part = 1 << log_part;
+    const int tokens = min(NT, a.M - m0);
+    const int lane = tid & 31, n = n0 + lane * 4, live = min(4, a.N - n);
+    const bool wide = a.wide && live == 4;
+    float bias[4], ws[4], xs[kEarly];
+    uint4 early[kEarly];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bias[i] = a.bias && i < live ? a.bias[n + i] : 0.f;
+        ws[i] = F8 && i < live ? a.w_scale[n + i] : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i) {
+        const int c = warp + i * kLinWarps, t = (rank << log_part) + c;
+        xs[i] = 1.f;
+        early[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < part && t < tokens) {
+            if (F8) xs[i] = a.x_scale[m0 + t];
+            if (a.residual && wide) early[i] = load_four(a.residual, (int64_t)(m0 + t) * a.ldr + n, a.out);
+        }
+    }
+
     if (warp == 0 && elect_one()) {
         int issued = 0;
         bool ok = true;
@@ -132,9 +157,7 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     // with split > 1 each CTA finishes NT / split tokens, and gets their sums
     // over every slice of k.  From there a warp takes a token, a lane four
     // features, so y and the residual move in 256-byte rows.
-    const int log_part = (31 - __clz(NT)) - log_split, part = 1 << log_part;
-    const int tokens = min(NT, a.M - m0);
-    const int lane = tid & 31, quarter = warp & 3;
+    const int quarter = warp & 3;
     if (log_split) cluster_sync_all();
     if (!fail) {
         constexpr int kWarpCols = NT < 32 ? 16 : NT / 2;  // tokens of a warp's lane quarter
@@ -166,54 +189,37 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
     }
     if (log_split) cluster_sync_all();
     else __syncthreads();
-    const int n = n0 + lane * 4;
-    if (!fail && n < a.N) {
-        const int live = min(4, a.N - n);
-        float bias[4], ws[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bias[i] = a.bias && i < live ? a.bias[n + i] : 0.f;
-            ws[i] = F8 && i < live ? a.w_scale[n + i] : 1.f;
-        }
+    if (!fail && live > 0) {
         const float4* sums = reinterpret_cast<const float4*>(ring) + lane;
-        const bool wide = a.wide && live == 4;
-        for (int c = warp; c < part; c += kLinWarps) {
+        auto finish = [&](int c, float x_scale, uint4 r, bool have_r) {
             const int t = (rank << log_part) + c;
-            if (t >= tokens) break;
+            if (c >= part || t >= tokens) return;
             float4 f = sums[c * (kFeatures / 4)];
-            for (int r = 1; r < split; ++r) {
-                const float4 u = sums[((r << log_part) + c) * (kFeatures / 4)];
+            for (int k = 1; k < split; ++k) {
+                const float4 u = sums[((k << log_part) + c) * (kFeatures / 4)];
                 f.x += u.x;
                 f.y += u.y;
                 f.z += u.z;
                 f.w += u.w;
             }
             float v[4] = {f.x, f.y, f.z, f.w};
-            const float xs = F8 ? a.x_scale[m0 + t] : 1.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (F8 ? v[i] * (xs * ws[i]) : v[i]) + bias[i];
+            for (int i = 0; i < 4; ++i) v[i] = (F8 ? v[i] * (x_scale * ws[i]) : v[i]) + bias[i];
             if (a.out == KDA_DTYPE_F32) activate_all<4, false>(v, a.act);
             else activate_all<4, true>(v, a.act);
             const int64_t at = (int64_t)(m0 + t) * a.ldy + n, rat = (int64_t)(m0 + t) * a.ldr + n;
             if (wide) {
+                if (a.residual && !have_r) r = load_four(a.residual, rat, a.out);
                 if (a.out == KDA_DTYPE_F32) {
-                    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (a.residual) r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + rat);
                     *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) =
-                        make_float4(v[0] + r.x, v[1] + r.y, v[2] + r.z, v[3] + r.w);
+                        make_float4(v[0] + __uint_as_float(r.x), v[1] + __uint_as_float(r.y),
+                                    v[2] + __uint_as_float(r.z), v[3] + __uint_as_float(r.w));
                 } else {
                     const bool f16 = a.out == KDA_DTYPE_F16;
-                    if (a.residual) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + rat);
-                        const float2 lo = f16 ? from_b16x2<true>(u.x) : from_b16x2<false>(u.x);
-                        const float2 hi = f16 ? from_b16x2<true>(u.y) : from_b16x2<false>(u.y);
-                        v[0] += lo.x;
-                        v[1] += lo.y;
-                        v[2] += hi.x;
-                        v[3] += hi.y;
-                    }
+                    const float2 lo = f16 ? from_b16x2<true>(r.x) : from_b16x2<false>(r.x);
+                    const float2 hi = f16 ? from_b16x2<true>(r.y) : from_b16x2<false>(r.y);
                     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                        make_uint2(pack_b16x2(v[0], v[1], f16), pack_b16x2(v[2], v[3], f16));
+                        make_uint2(pack_b16x2(v[0] + lo.x, v[1] + lo.y, f16), pack_b16x2(v[2] + hi.x, v[3] + hi.y, f16));
                 }
             } else {
 #pragma unroll
@@ -223,7 +229,12 @@ __global__ void __launch_bounds__(kLinThreads) kda_linear_kernel(const __grid_co
                         store_out(a.y, at + i, v[i], a.out);
                     }
             }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i) finish(warp + i * kLinWarps, xs[i], early[i], true);
+        for (int c = warp + kEarly * kLinWarps; c < part; c += kLinWarps)
+            finish(c, F8 && m0 + (rank << log_part) + c < a.M ? a.x_scale[m0 + (rank << log_part) + c] : 1.f,
+                   make_uint4(0u, 0u, 0u, 0u), false);
     }
     ptx::tc_fence_before();
     __syncthreads();

@@ -146,6 +146,12 @@ __device__ __forceinline__ float load_out(const void* p, int64_t at, int dtype) 
     const uint16_t w = static_cast<const uint16_t*>(p)[at];
     return dtype == KDA_DTYPE_F16 ? from_b16<true>(w) : from_b16<false>(w);
 }
+// Four elements as they lie in memory (16-bit ones in x and y).
+__device__ __forceinline__ uint4 load_four(const void* p, int64_t at, int dtype) {
+    if (dtype == KDA_DTYPE_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    return make_uint4(u.x, u.y, 0u, 0u);
+}
 __device__ __forceinline__ void store_out(void* p, int64_t at, float v, int dtype) {
     if (dtype == KDA_DTYPE_F32) static_cast<float*>(p)[at] = v;
     else static_cast<uint16_t*>(p)[at] = to_b16(v, dtype == KDA_DTYPE_F16);
