@@ -399,20 +399,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
     auto& sm = *reinterpret_cast<typename Shape::Shared*>(raw + ((128u - (ptx::smem_u32(raw) & 127u)) & 127u));
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < kUnits; ++i) ptx::mbar_init(&sm.known[i], 1);
-        for (int i = 0; i < kFull; ++i) ptx::mbar_init(&sm.full[i], 1);
-        for (int i = 0; i < kRing; ++i) {
-            ptx::mbar_init(&sm.done[i], kWarps);
-            ptx::mbar_init(&sm.empty[i], 1);
-        }
-        for (int g = 0; g < kGroups; ++g)
-            for (int i = 0; i < kSlots; ++i) {
-                ptx::mbar_init(&sm.group[g].token_full[i], 32);
-                ptx::mbar_init(&sm.group[g].token_empty[i], kWarps);
-            }
-        ptx::fence_mbar_init();
+    if (tid < kUnits) ptx::mbar_init(&sm.known[tid], 1);
+    if (tid < kFull) ptx::mbar_init(&sm.full[tid], 1);
+    if (tid < kRing) {
+        ptx::mbar_init(&sm.done[tid], kWarps);
+        ptx::mbar_init(&sm.empty[tid], 1);
     }
+    if (tid < kGroups * kSlots) {
+        ptx::mbar_init(&sm.group[tid / kSlots].token_full[tid % kSlots], 32);
+        ptx::mbar_init(&sm.group[tid / kSlots].token_empty[tid % kSlots], kWarps);
+    }
+    ptx::fence_mbar_init();
     ptx::grid_dep_launch();
     __syncthreads();
     ptx::grid_dep_wait();
