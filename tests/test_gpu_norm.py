@@ -86,6 +86,26 @@ def test_strides_and_alignment(out):
     check(wide[:, :600].unflatten(0, (11, 1)), None, None, out)
 
 
+@pytest.mark.parametrize("dim", [31, 33, 127, 250, 513, 1001, 4095, 5003, 16383, 32761])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16, torch.float32])
+def test_rows_off_16_bytes(dim, io):
+    """Every distance of a row's start from 16 bytes; x, residual and sum alike or not; nothing outside is written."""
+    flat = randn(40 * dim + 64, seed=dim, dtype=io)
+    for lead in (0, 1, 3, 7):
+        x = flat[lead:lead + 17 * dim].view(17, dim)
+        for rlead in (lead, lead + 1):
+            r = flat.flip(0)[rlead:rlead + 17 * dim].view(17, dim)
+            for out in (io, F8, torch.float32):
+                check(x, 1 + 0.3 * randn(dim, seed=2).to(io), r, out)
+                check(x, None, None, out)
+        raw = torch.full((17 * dim + 32,), 7.0, dtype=io, device="cuda")
+        part = raw[lead:lead + 17 * dim].view(17, dim)
+        y, _, s = kda.rms_norm(x, None, residual=x, residual_out=part)
+        torch.cuda.synchronize()
+        assert torch.equal(part, (x.float() + x.float()).to(io))
+        assert (raw[:lead] == 7).all() and (raw[lead + 17 * dim:] == 7).all()
+
+
 def test_sum_in_place():
     for dim in (128, 4096, 5003):
         x, r = randn(13, dim, dtype=torch.bfloat16), randn(13, dim, seed=1, dtype=torch.bfloat16)
