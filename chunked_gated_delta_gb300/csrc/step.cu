@@ -298,7 +298,7 @@ constexpr int kUnits = 64;  // published units kept
 // Packed sequences are taken longest first, up to this many: the CTAs and groups
 // take units in turn, so neighbours in that order share out evenly (96 sequences
 // of 0 to 5 tokens in their own order: 45.6 us, the last group 1.7 times the
-// mean; sorted: SORTED_US).  More sequences even out by their number.
+// mean; sorted: 40.7).  More sequences even out by their number.
 constexpr int kMostSorted = 512;
 // Barriers of the loads, one per unit in turn, more of them than slots of the
 // ring: copies land in any order, so a group can wait for its next unit while
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
         ptx::mbar_init(&sm.empty[tid], 1);
     }
     if (tid < kGroups * kSlots) {
-        ptx::mbar_init(&sm.group[tid / kSlots].token_full[tid % kSlots], 32);
+        ptx::mbar_init(&sm.group[tid / kSlots].token_full[tid % kSlots], 1);
         ptx::mbar_init(&sm.group[tid / kSlots].token_empty[tid % kSlots], kWarps);
     }
     ptx::fence_mbar_init();
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
         bool has[kDepth];
         int i = warp - kFirstInputWarp, t = 0;  // the next token to ask for
         int to_group[kDepth], sent[kGroups / kInputWarps] = {};  // tokens sent to each of its groups
-        bool ok = wait_for(&sm.known[i], 0);
+        bool ok = __all_sync(~0u, wait_for(&sm.known[i], 0));
         Unit unit = sm.unit[i];
         const uint16_t *pk = nullptr, *pq = nullptr, *pv = nullptr, *pb = nullptr;  // this lane's part of the next token
         const float* pg = nullptr;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             if (++t == unit.len) {
                 t = 0;
                 i += kInputWarps;
-                ok = wait_for(&sm.known[i % kUnits], (i / kUnits) & 1);
+                ok = __all_sync(~0u, wait_for(&sm.known[i % kUnits], (i / kUnits) & 1));
                 unit = sm.unit[i % kUnits];
                 open();
             }
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                 for (int x = 0; x < kGroups / kInputWarps; ++x)
                     if (to_group[d] / kInputWarps == x) c = sent[x]++;
                 const int s = c % kSlots, round = c / kSlots;
-                if (round > 0 && !wait_for(&gr.token_empty[s], (round - 1) & 1)) {
+                if (round > 0 && !__all_sync(~0u, wait_for(&gr.token_empty[s], (round - 1) & 1))) {
                     more = false;
                     break;
                 }
@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                     const float x = from_b16<F16>(rb[d]);
                     to.beta = a.logits ? 1.f / (1.f + expf(-x)) : x;
                 }
-                ptx::mbar_arrive(&gr.token_full[s]);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&gr.token_full[s]);  // (32 arrivals would queue up at the barrier)
                 ask(d);
             }
         }
