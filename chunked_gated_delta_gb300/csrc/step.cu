@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
 constexpr int kComputeWarps = 16, kInputWarps = 2;
 constexpr int kLoadWarp = kComputeWarps, kStoreWarp = kLoadWarp + 1, kFirstInputWarp = kLoadWarp + 2;
 constexpr int kStreamThreads = (kFirstInputWarp + kInputWarps) * 32;
-constexpr int kUnits = 64;  // published units kept
+constexpr int kUnits = 60;  // published units kept
 // Packed sequences are taken longest first, up to this many: the CTAs and groups
 // take units in turn, so neighbours in that order share out evenly (96 sequences
 // of 0 to 5 tokens in their own order: 45.6 us, the last group 1.7 times the
@@ -313,8 +313,8 @@ constexpr int kDepth = 3;   // tokens an input warp has in flight
 constexpr int kAhead = kInputWarps * (kDepth + 1) + 2;
 
 struct Unit {
-    int64_t row0, state;  // first token row; first element of the state
-    int len, head;        // tokens; < 0: no more units
+    int64_t row0, state;           // first token row; first element of the state
+    int len, head, qk_head, unused;  // tokens; < 0: no more units
 };
 
 template <int K, int V, bool STATE16>
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                 const bool here = lane < batch && mine < total;
                 const int at = here ? (int)mine / a.H : 0, h = here ? (int)mine - at * a.H : 0;
                 const int n = sorted ? sm.order[at] : at;
-                Unit unit{(int64_t)n * a.T, 0, here ? a.T : 0, h};
+                Unit unit{(int64_t)n * a.T, 0, here ? a.T : 0, h, h / a.group, 0};
                 if (here && a.cu) {
                     const int bos = a.cu[n], eos = a.cu[n + 1];
                     const bool bad = bad_offsets(a, n, bos, eos);
@@ -547,14 +547,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
         Unit unit = sm.unit[i];
         const uint16_t *pk = nullptr, *pq = nullptr, *pv = nullptr, *pb = nullptr;  // this lane's part of the next token
         const float* pg = nullptr;
+        // Where a unit's five inputs start: one lane computes each, and hands it round.
+        const int64_t my_stride = lane == 0 ? a.k_stride : lane == 1 ? a.q_stride : lane == 2 ? a.g_stride
+                                                       : lane == 3 ? a.v_stride : a.beta_stride;
+        const int my_dim = lane < 3 ? K : lane == 3 ? V : 1;
         auto open = [&] {
-            if (!ok || unit.len <= 0) return;
-            const int hq = unit.head / a.group;
-            pk = a.k + unit.row0 * a.k_stride + hq * K + lane * kk;
-            pq = a.q + unit.row0 * a.q_stride + hq * K + lane * kk;
-            pg = a.g + unit.row0 * a.g_stride + unit.head * K + lane * kk;
-            pv = a.v + unit.row0 * a.v_stride + unit.head * V + lane * vv;
-            pb = a.beta + unit.row0 * a.beta_stride + unit.head;
+            const int64_t at = unit.row0 * my_stride + (int64_t)(lane < 2 ? unit.qk_head : unit.head) * my_dim;
+            pk = a.k + __shfl_sync(~0u, at, 0) + lane * kk;
+            pq = a.q + __shfl_sync(~0u, at, 1) + lane * kk;
+            pg = a.g + __shfl_sync(~0u, at, 2) + lane * kk;
+            pv = a.v + __shfl_sync(~0u, at, 3) + lane * vv;
+            pb = a.beta + __shfl_sync(~0u, at, 4);
         };
         open();
         auto ask = [&](int d) {
