@@ -10,6 +10,10 @@
 // The 16 warps of a CTA are 1, 2 or 4 groups of rows times 16, 8 or 4 shares of
 // k (fewer rows where N is small, to have CTAs for every SM); the shares are
 // joined through shared memory in order.
+//
+// Measured (bf16; the tensor-core kernel in brackets): 4096 x 4096 7.3 us (9.1),
+// 4.6 TB/s; 2048 x 2048 2.8 (4.8); 32 x 4096 2.3 (4.3).  For two tokens the same
+// scheme took 10.8 us against 9.1, so it ends at one.
 #include "linear.cuh"
 
 namespace kda {

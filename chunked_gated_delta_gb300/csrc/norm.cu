@@ -11,7 +11,10 @@
 // largest |s w|, which times 1 / sqrt(...) is the largest |y| (to a rounding),
 // so that both are joined at once.  A row is taken by a team: 2 to 32 lanes of a
 // warp for short rows (head norms), so that its sums are shuffles and many rows
-// share a CTA, or a whole CTA for long ones, with one barrier.
+// share a CTA, or a whole CTA for long ones, with one barrier.  Measured: 1.07 M
+// rows of 128 82 us (6.7 TB/s, what a copy reaches), with residual to e4m3 6.9;
+// 32768 rows of 4096 with residual to e4m3 170 us (5.5: the four warps of a row
+// wait for each other at the barrier).
 #include <type_traits>
 
 #include "internal.h"

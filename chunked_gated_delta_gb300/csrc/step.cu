@@ -10,10 +10,17 @@
 // instead of two dependent ones.
 //
 // Bound: each state is read and written once per call, 2 K V 4 bytes (128 KB at
-// K = V = 128 in fp32) against ~7 K V flops, so HBM.  One CTA takes VT columns
-// of one (sequence, head): the columns are independent given q, k, g, beta.  It
+// K = V = 128 in fp32) against ~7 K V flops, so HBM for a token or two; a few
+// tokens per state of 128 x 64 are bound by the issue of their arithmetic.
+//
+// Two kernels.  This one, for few (sequence, head) pairs: one CTA takes VT
+// columns of one pair (the columns are independent given q, k, g, beta).  It
 // holds its K x VT part in registers as float4 (a warp's load covers whole
 // 128-byte lines), in fp32 whatever the cache's type, across all the tokens.
+// From two pairs per SM on the streaming kernel below takes over.  Measured at
+// K = V = 128 in fp32, this kernel against that one: 32 pairs 3.4 us, 5.0;
+// 128 pairs 4.6, 5.4; 256 pairs 10.7, 10.5; 512 pairs 18, 16; 16384 pairs 490,
+// 350 (6.1 TB/s, 92% of what a copy reaches).
 #include "internal.h"
 #include "layer_ops.cuh"
 #include "waits.cuh"
@@ -282,9 +289,10 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
 // kernel above spends its time between a CTA's load, its sums and its store.
 // Here CTAs are persistent: a warp loads whole states (K V elements are
 // contiguous) into a ring in shared memory with bulk copies, groups of threads
-// (two of 256, or four of 128 where V is 64: 16 or 8 rows a thread for K = 128
-// or 64 either way) take them in turn, and a warp stores them back from the ring, so
-// loads, sums and stores of different states overlap on every SM.
+// (two of 256, or four of 128 where V is 64, so that a thread has 16 rows for K =
+// 128 and 8 for 64; three groups of 256 with half the rows measured 11% slower)
+// take them in turn, and a warp stores them back from the ring, so loads, sums
+// and stores of different states overlap on every SM.
 //
 // The tokens' inputs (k, q, g, v, beta) come through a small ring for each group,
 // filled by one of two warps that have several tokens' loads in flight: one
@@ -300,6 +308,9 @@ constexpr int kUnits = 60;  // published units kept
 // of 0 to 5 tokens in their own order: 45.6 us, the last group 1.7 times the
 // mean; sorted: 40.7).  More sequences even out by their number.
 constexpr int kMostSorted = 512;
+// Tokens of a sequence (of all, where packed) that the streaming kernel takes: a
+// few tenths of a second at most, well under what its waits allow.
+constexpr int kMostStreamed = 1 << 16;
 // Barriers of the loads, one per unit in turn, more of them than slots of the
 // ring: copies land in any order, so a group can wait for its next unit while
 // the other group's unit in the same slot is still on its way.  With a barrier
@@ -754,7 +765,8 @@ extern "C" kda_status kda_step(const void* q, const void* k, const void* v, cons
     const bool f16 = p.io_dtype == KDA_IO_F16, s16 = p.state_dtype == KDA_STATE_BF16;
     const int sms = device_sm_count();
     cudaError_t e;
-    if ((int64_t)N * d.H >= 2 * sms) {
+    // (Tokens of one sequence follow one another: its waits must not run out over a very long one.)
+    if ((int64_t)N * d.H >= 2 * sms && d.T <= kMostStreamed) {
         if (d.K == 128)
             e = d.V == 128 ? launch_stream<128, 128>(a, f16, s16, sms, s) : launch_stream<128, 64>(a, f16, s16, sms, s);
         else

@@ -1,5 +1,5 @@
-// waits.cuh -- bounded waits on mbarriers that cost little while the barrier is
-// nearly there, and the election of one thread of a warp (decode step, projection).
+// waits.cuh -- bounded waits on mbarriers and the election of one thread of a
+// warp (decode step, projection).
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -7,8 +7,9 @@
 namespace kda {
 namespace {
 
-// Waits for the phase with this parity, for kWaitLimitNs at most.  The clock is
-// read only after a thousand tries: a read costs more than a stage's wait.
+// Waits for the phase with this parity, for kWaitLimitNs at most (the clock is
+// read after each thousand tries).  The phase before it must be over, and the
+// one after it not: parity tells no more.
 // CLUSTER: the arrivals may come from the other CTA of a pair.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {

@@ -27,6 +27,10 @@
  *  - Supported shapes: K in {64, 128}, V in {64, 128}, H >= 1, T >= 0.
  *    Other K/V return KDA_ERR_UNSUPPORTED.
  *  - Every tensor base pointer must be 16-byte aligned (KDA_ERR_ALIGNMENT).
+ * The operators around the recurrence in a served layer (kda_step,
+ * kda_rms_norm, kda_linear) state their own shapes, strides and alignments.
+ * They read and write nothing before the work ahead of them on `stream` is
+ * done, although their launch may overlap its end.
  */
 #ifndef KDA_H_
 #define KDA_H_
@@ -379,9 +383,10 @@ kda_status kda_selftest_wait_timeout(void* status_word, unsigned long long limit
  *             its state untouched, KDA_ERR_BAD_SLOTS in the status word.  (A
  *             sequence without tokens is not looked at, but its slot is taken.)
  *   status_word  device int32 (4-byte aligned) or NULL.  Errors in the contents
- *             of slots and cu_seqlens are or-ed into it; the caller sets it to
- *             zero once, and kda_fwd_status(status_word, stream) reads it.  A
- *             sequence whose cu_seqlens are out of order is skipped.
+ *             of slots and cu_seqlens (and a pipeline wait that ran out) are
+ *             or-ed into it; the caller sets it to zero once, and
+ *             kda_fwd_status(status_word, stream) reads it.  A sequence whose
+ *             cu_seqlens are out of order is skipped.
  *   opts      io_dtype, state_dtype, beta_logits, qk_heads as in kda_fwd_opts;
  *             num_slots (> 0); *_stride: elements between the rows of
  *             consecutive tokens of q, k, v, g, beta (0: contiguous), so that
@@ -454,7 +459,9 @@ kda_status kda_rms_norm(const void* x, const void* residual, const void* weight,
  *   *_stride  elements between rows (0: contiguous)
  *   status_word  device int32 or NULL, as in kda_step: KDA_ERR_TIMEOUT if a
  *             pipeline wait ran out (y is then incomplete)
- * M >= 0; N, K >= 1, any of them odd.  x and w are 16-byte aligned with row
+ * M >= 0; N, K >= 1, any of them odd (KDA_ERR_UNSUPPORTED beyond 2^30 of
+ * either, or beyond 8 million rows of x where y's or the residual's rows do not
+ * all start on 16 bytes).  x and w are 16-byte aligned with row
  * strides of a multiple of 16 bytes where they have more than one row
  * (KDA_ERR_ALIGNMENT), which is what a TMA load of their rows needs; y and residual to their own elements.  No
  * workspace.  Results do not depend on timing (no atomics); they may differ in
