@@ -87,7 +87,7 @@ def _link_extension(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = EXTENSION + f".tmp{os.getpid()}"
     _run([_host_compiler(), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + lib,
-          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib],
+          "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib],
          "linking the Python extension")
     os.replace(tmp, EXTENSION)
 

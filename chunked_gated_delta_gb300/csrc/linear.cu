@@ -291,6 +291,7 @@ Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16) {
         {16, 0.186, 0.3}, {32, 0.19, 0.5}, {64, 0.205, 1.0}, {128, 0.245, 2.9}};
     for (const auto& t : kNarrow) {
         if (t.tokens < 64 && t.tokens < M) continue;      // a second token tile would read w again
+        if ((M + t.tokens - 1) / t.tokens > 65535) continue;  // (rows of the grid)
         const int64_t tiles = (M + t.tokens - 1) / t.tokens * ((N + kFeatures - 1) / kFeatures);
         for (int ls = 0; ls <= 3 && (ls == 0 || kblocks >> ls >= 4); ++ls) {
             const int slots = ls < 3 ? sms : 96;          // clusters of 8 leave SMs of a GPC over
