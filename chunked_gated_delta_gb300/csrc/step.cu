@@ -370,26 +370,32 @@ __device__ __forceinline__ bool group_sync(int group, bool ok) {
     return all != 0;
 }
 
-// COUNT (2 or 4) consecutive 16-bit or fp32 elements as fp32; vec: they are aligned to their size together.
-template <bool F16, int COUNT>
-__device__ __forceinline__ void load_some(const uint16_t* p, bool vec, uint16_t (&w)[COUNT]) {
-    if (vec) {
-        uint32_t u[COUNT / 2];
-        if constexpr (COUNT == 4) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            u[0] = x.x, u[1] = x.y;
-        } else {
-            u[0] = *reinterpret_cast<const uint32_t*>(p);
-        }
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i) w[i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
-    } else {
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i) w[i] = p[i];
-    }
-}
+// COUNT (2 or 4) consecutive 16-bit elements as they come from memory: two in a
+// word where vec says that they are aligned together, else one.  Taken apart only
+// when they are used: a load's first use is where its latency is waited for.
 template <int COUNT>
-__device__ __forceinline__ void load_some(const float* p, bool vec, float (&w)[COUNT]) {
+struct Raw16 {
+    uint32_t w[COUNT];
+    __device__ __forceinline__ void load(const uint16_t* p, bool vec) {
+        if (vec) {
+            if constexpr (COUNT == 4) {
+                const uint2 x = *reinterpret_cast<const uint2*>(p);
+                w[0] = x.x, w[1] = x.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t*>(p);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) w[i] = p[i];
+        }
+    }
+    template <bool F16>
+    __device__ __forceinline__ float at(int i, bool vec) const {
+        return from_b16<F16>((uint16_t)(vec ? w[i / 2] >> (16 * (i & 1)) : w[i]));
+    }
+};
+template <int COUNT>
+__device__ __forceinline__ void load_f32(const float* p, bool vec, float (&w)[COUNT]) {
     if (vec) {
         if constexpr (COUNT == 4) {
             const float4 x = *reinterpret_cast<const float4*>(p);
@@ -549,7 +555,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
         }
     } else if (warp >= kFirstInputWarp) {
         constexpr int kk = K / 32, vv = V / 32;  // elements of a lane
-        uint16_t rk[kDepth][kk], rq[kDepth][kk], rv[kDepth][vv], rb[kDepth];
+        Raw16<kk> rk[kDepth], rq[kDepth];
+        Raw16<vv> rv[kDepth];
+        uint16_t rb[kDepth];
         float rg[kDepth][kk];
         bool has[kDepth];
         int i = warp - kFirstInputWarp, t = 0;  // the next token to ask for
@@ -575,10 +583,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
             has[d] = ok && unit.len > 0;
             if (!has[d]) return;
             to_group[d] = i % kGroups;
-            load_some<F16, kk>(pk, a.vec, rk[d]);
-            load_some<F16, kk>(pq, a.vec, rq[d]);
-            load_some<kk>(pg, a.vec, rg[d]);
-            load_some<F16, vv>(pv, a.vec, rv[d]);
+            rk[d].load(pk, a.vec);
+            rq[d].load(pq, a.vec);
+            load_f32<kk>(pg, a.vec, rg[d]);
+            rv[d].load(pv, a.vec);
             rb[d] = *pb;
             pk += a.k_stride;
             pq += a.q_stride;
@@ -615,10 +623,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
 #pragma unroll
                 for (int x = 0; x < kk; ++x) {
                     to.kqe[lane * kk + x] =
-                        make_float4(from_b16<F16>(rk[d][x]), from_b16<F16>(rq[d][x]), expf(rg[d][x]), 0.f);
+                        make_float4(rk[d].template at<F16>(x, a.vec), rq[d].template at<F16>(x, a.vec), expf(rg[d][x]), 0.f);
                 }
 #pragma unroll
-                for (int x = 0; x < vv; ++x) to.v[lane * vv + x] = from_b16<F16>(rv[d][x]);
+                for (int x = 0; x < vv; ++x) to.v[lane * vv + x] = rv[d].template at<F16>(x, a.vec);
                 if (lane == 0) {
                     const float x = from_b16<F16>(rb[d]);
                     to.beta = a.logits ? 1.f / (1.f + expf(-x)) : x;
