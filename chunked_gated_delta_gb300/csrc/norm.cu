@@ -11,15 +11,15 @@
 // largest |s w|, which times 1 / sqrt(...) is the largest |y| (to a rounding),
 // so that both are joined at once.  A row is taken by a team: 2 to 32 lanes of a
 // warp for short rows (head norms), so that its sums are shuffles and many rows
-// share a CTA, or a whole CTA for long ones, with one barrier.  Measured: 1.07 M
-// rows of 128 82 us (6.7 TB/s, what a copy reaches), with residual to e4m3 6.9;
-// 32768 rows of 4096 with residual to e4m3 170 us (5.5: the four warps of a row
-// wait for each other at the barrier).
+// share a CTA, or a whole CTA for long ones, with one barrier; long rows with a
+// residual go through a ring in shared memory instead (below).  Measured: 1.07 M
+// rows of 128 82 us (6.7 TB/s, what a copy reaches), with residual to e4m3 6.9
+// TB/s; 32768 rows of 4096 84 us (6.4), with residual to e4m3 152 (6.2).
 #include <type_traits>
 
 #include "internal.h"
 #include "layer_ops.cuh"
-#include "ptx.cuh"
+#include "waits.cuh"
 
 namespace kda {
 namespace {
@@ -235,6 +235,154 @@ cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
                             dim3((unsigned)threads), 0, s, a);
 }
 
+// ------------------------------------------------------------------ long rows with a residual
+// Two rows to load, two to store, and a barrier between: with a CTA per row (the
+// kernel above) an SM's loads stop while its rows wait for their sums.  Here CTAs
+// are persistent: a warp loads rows of x and the residual into a ring in shared
+// memory with bulk copies, and groups of 128 threads take them in turn, so the
+// loads never stop.  Measured, to e4m3: 32768 rows of 4096 170 -> 152 us (6.2 TB/s,
+// 93% of a copy), 16384 of 8192 175 -> 158; rows of 2048 gain nothing (163, 167).
+constexpr int kRingThreads = 128;  // of a group
+constexpr int kRingGroups = 4;
+constexpr int kRingAll = kRingGroups * kRingThreads + 32;
+constexpr int kMostSlots = 24;
+constexpr int kRingBytes = 200 * 1024;
+
+// Slots of the ring: a multiple of the groups, so that a slot's barriers belong
+// to one group (a group that waits a phase ahead of another's would misread
+// their parity).
+inline int ring_slots(int slot_bytes) {
+    const int n = kRingBytes / slot_bytes / kRingGroups * kRingGroups;
+    return n < kMostSlots ? n : kMostSlots;
+}
+
+template <int IO, int NV>
+__global__ void __launch_bounds__(kRingAll, 1) kda_norm_ring_kernel(const NormArgs a, int slots) {
+    constexpr int kSize = IO == KDA_DTYPE_F32 ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[kMostSlots], empty[kMostSlots];
+    __shared__ float2 s_join[kRingGroups][2][kRingThreads / 32];
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+    const int row_bytes = a.dim * kSize, slot_bytes = 2 * row_bytes;
+    if (tid < slots) {
+        ptx::mbar_init(&full[tid], 1);
+        ptx::mbar_init(&empty[tid], kRingThreads / 32);
+    }
+    ptx::fence_mbar_init();
+    ptx::grid_dep_launch();
+    __syncthreads();
+    ptx::grid_dep_wait();
+
+    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // rows of this CTA
+    if (warp == kRingGroups * (kRingThreads / 32)) {
+        if (elect_one()) {
+            int i = 0;
+            for (; i < count; ++i) {
+                const int s = i % slots, round = i / slots;
+                if (round > 0 && !wait_for(&empty[s], (round - 1) & 1)) break;
+                const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+                uint8_t* to = ring + s * slot_bytes;
+                ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)slot_bytes);
+                bulk_load(to, static_cast<const uint8_t*>(a.x) + row * a.x_stride * kSize, (uint32_t)row_bytes, &full[s]);
+                bulk_load(to + row_bytes, static_cast<const uint8_t*>(a.r) + row * a.r_stride * kSize,
+                          (uint32_t)row_bytes, &full[s]);
+            }
+            // (every copy is waited for by the group that takes its row, or here if that gave up)
+            for (int j = max(0, i - slots); j < i; ++j) wait_for(&full[j % slots], (j / slots) & 1);
+        }
+        return;
+    }
+    const int group = warp / (kRingThreads / 32), gt = tid - group * kRingThreads;
+    const bool f8 = a.out == KDA_DTYPE_E4M3;
+    bool ok = true;
+    for (int i = group, k = 0; i < count; i += kRingGroups, ++k) {
+        const int slot = i % slots;
+        const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
+        const uint8_t* x = ring + slot * slot_bytes;
+        ok = ok && wait_for(&full[slot], (i / slots) & 1);
+        float s[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (gt + v * kRingThreads) * 8;
+            if (c < a.dim) {
+                float r[8];
+                load_vec<IO, 8>(x, c, s[v]);
+                load_vec<IO, 8>(x + row_bytes, c, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[v][j] += r[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[v][j] = 0.f;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[slot]);
+        float2 stat = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (gt + v * kRingThreads) * 8;
+            if (c < a.dim && a.sum && ok) store_vec<8>(a.sum, row * a.sum_stride + c, s[v], IO);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) stat.x += s[v][j] * s[v][j];
+            if (c < a.dim && a.w) {
+                float w[8];
+                if (a.w_f32) load_vec<KDA_DTYPE_F32, 8>(a.w, c, w);
+                else load_vec<IO, 8>(a.w, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[v][j] *= w[j];
+            }
+            if (f8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) stat.y = max_nan(stat.y, fabsf(s[v][j]));
+            }
+        }
+        stat = team_join<32>(stat, nullptr, f8);
+        if (lane == 0) s_join[group][k & 1][gt >> 5] = stat;
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(group + 1), "n"(kRingThreads) : "memory");
+        stat = s_join[group][k & 1][0];
+#pragma unroll
+        for (int w = 1; w < kRingThreads / 32; ++w) {
+            const float2 o = s_join[group][k & 1][w];
+            stat.x += o.x;
+            stat.y = max_nan(stat.y, o.y);
+        }
+        const float rstd = 1.f / sqrtf(stat.x * a.inv_dim + a.eps);
+        float inv = 1.f;
+        if (f8) {
+            const float amax = max_nan(kAmaxFloor, stat.y * rstd);
+            inv = kE4m3Max / amax;
+            if (gt == 0 && ok) a.y_scale[row] = amax / kE4m3Max;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (gt + v * kRingThreads) * 8;
+            if (c < a.dim && ok) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[v][j] = s[v][j] * rstd * inv;
+                store_vec<8>(a.y, row * a.dim + c, s[v], a.out);
+            }
+        }
+    }
+}
+
+template <int IO, int NV>
+cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
+    const int slot_bytes = 2 * a.dim * (IO == KDA_DTYPE_F32 ? 4 : 2), slots = ring_slots(slot_bytes);
+    auto kern = kda_norm_ring_kernel<IO, NV>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3((unsigned)device_sm_count()), dim3(kRingAll), (size_t)(slots * slot_bytes), s, a,
+                            slots);
+}
+
+// Whether a call takes the ring: 16-byte rows long enough for a group of threads
+// and many enough for every SM's ring.
+template <int IO>
+bool ring_fits(const NormArgs& a) {
+    return a.r && a.dim > 2048 && a.dim <= 8192 && ring_slots(2 * a.dim * (IO == KDA_DTYPE_F32 ? 4 : 2)) >= kRingGroups &&
+           a.rows >= 16 * (int64_t)device_sm_count();
+}
+
 // The team for a row of `vecs` vectors.  Four 16-byte loads a thread, whatever
 // the row (two vectors of x and two of the residual, or four of x), are in flight
 // together and keep the sums short.  Measured, of the 6.67 TB/s that a copy
@@ -248,6 +396,10 @@ cudaError_t pick(const NormArgs& a, cudaStream_t s) {
     const int vecs = (a.dim + VEC - 1) / VEC;
     auto threads = [&](int nv) { return (vecs + nv * 32 - 1) / (nv * 32) * 32; };
     if constexpr (VEC == 8) {
+        if (ring_fits<IO>(a)) {
+            if (a.dim <= 4096) return launch_ring<IO, 4>(a, s);
+            return launch_ring<IO, 8>(a, s);
+        }
         if (vecs > 32 && vecs <= 1024 && a.rows <= 2 * device_sm_count())
             return launch<IO, VEC, 1, 0>(a, threads(1), s);
         if (a.r) {

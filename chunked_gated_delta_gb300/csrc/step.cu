@@ -53,14 +53,6 @@ __device__ __forceinline__ void report(int32_t* status, int bit) {
 __device__ __forceinline__ bool bad_offsets(const StepArgs& a, int n, int bos, int eos) {
     return bos < 0 || eos < bos || eos > a.T || (n == 0 && bos != 0) || (n == a.N - 1 && eos != a.T);
 }
-// Bulk copies of whole states: 16-byte aligned, a multiple of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            ptx::smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)),
                  "r"(bytes)

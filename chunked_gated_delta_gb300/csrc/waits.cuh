@@ -1,5 +1,5 @@
-// waits.cuh -- bounded waits on mbarriers and the election of one thread of a
-// warp (decode step, projection).
+// waits.cuh -- bounded waits on mbarriers, the election of one thread of a warp
+// and the untiled bulk load (decode step, norm, projection).
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -44,6 +44,15 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// Bulk copy: 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+        : "memory");
 }
 
 }  // namespace

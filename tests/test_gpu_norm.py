@@ -106,6 +106,28 @@ def test_rows_off_16_bytes(dim, io):
         assert (raw[:lead] == 7).all() and (raw[lead + 17 * dim:] == 7).all()
 
 
+@pytest.mark.parametrize("dim", [1032, 2048, 2056, 4096, 5000, 8192])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16, torch.float32])
+def test_many_long_rows_with_residual(dim, io):
+    """Enough rows for the kernel that streams them, contiguous and apart, in place, and rows with NaN."""
+    for rows in (2432, 2500, 7001):
+        wide = 2 * randn(rows, dim + 16, seed=rows, dtype=io)
+        for x, r in ((randn(rows, dim, seed=dim, dtype=io), wide[:, :dim].contiguous()),
+                     (wide[:, 8:dim + 8], wide.flip(0)[:, :dim])):
+            for out in (io, F8, torch.float32):
+                check(x, (1 + 0.3 * randn(dim, seed=2)).to(io), r, out)
+        x, r, w = randn(rows, dim, seed=1, dtype=io), randn(rows, dim, seed=2, dtype=io), 1 + randn(dim, seed=3)
+        x[17, 5], x[rows - 1, dim - 1] = float("nan"), float("nan")
+        y0, q0, s0 = kda.rms_norm(x, w, residual=r, out_dtype=F8)
+        y, q, s = kda.rms_norm(x, w, residual=r, out_dtype=F8, residual_out=r)
+        torch.cuda.synchronize()
+        assert s is r
+        for a, b in ((y0, y), (q0, q), (s0, s)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        bad = torch.isnan(q)
+        assert bad[[17, rows - 1]].all() and int(bad.sum()) == 2 and torch.isnan(y.float()[bad]).all()
+
+
 def test_sum_in_place():
     for dim in (128, 4096, 5003):
         x, r = randn(13, dim, dtype=torch.bfloat16), randn(13, dim, seed=1, dtype=torch.bfloat16)
