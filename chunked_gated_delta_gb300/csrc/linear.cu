@@ -269,7 +269,9 @@ cudaError_t launch(const LinArgs& a, bool f8, int log_split, cudaStream_t s) {
 // tokens takes 18.2, 13.9, 12.0, 23.0 us for 1, 2, 4, 8 slices of k; M = 256
 // takes 25.3 us in tiles of 64 and two slices, 17.6 in tiles of 128 and two,
 // 18.9 in the wide kernel with 128 features, 26.5 with 256; M = 2048 takes 56.7
-// in the wide kernel with 128, 46.0 with 256.
+// in the wide kernel with 128, 46.0 with 256.  Rows of y off 16 bytes: 8192 x 4095
+// x 4096 takes 338 us in tiles of 128 tokens, 148 in the wide kernel; 130 x 77 x
+// 4096 6.5 in tiles of 64 and eight slices, 17.2 in the wide kernel.
 struct Plan {
     bool wide;
     int tokens;     // per tile; of the wide kernel: features per tile
@@ -282,6 +284,9 @@ Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16) {
         const double waves = (double)((units + slots - 1) / slots);
         return call + fmax(waves * stages * per_stage, stream) + waves * end;
     };
+    // Rows off 16 bytes go element by element: after every tile of the narrow kernel,
+    // after the last one of the wide kernel, which stores while the next is summed.
+    const double odd = rows_on_16 ? 0.0 : 1.0;
     Plan best{false, 16, 0};
     double least = 1e30;
     auto offer = [&](Plan p, double c) {
@@ -296,14 +301,14 @@ Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16) {
         for (int ls = 0; ls <= 3 && (ls == 0 || kblocks >> ls >= 4); ++ls) {
             const int slots = ls < 3 ? sms : 96;          // clusters of 8 leave SMs of a GPC over
             offer({false, t.tokens, ls}, cost(tiles << ls, slots, (double)((kblocks + (1 << ls) - 1) >> ls), t.stage,
-                                              t.end / (1 << ls), ls ? 4.5 : 3.3));
+                                              (t.end + odd * t.tokens / 32) / (1 << ls), ls ? 4.5 : 3.3));
         }
         if (t.tokens >= M) break;
     }
-    if (rows_on_16 && M > 64) {
+    if (M > 64) {
         const int64_t tm = (M + 255) / 256;
-        offer({true, 128, 0}, cost(tm * ((N + 127) / 128), sms / 2, kblocks, 0.215, 0.7, 4.3));
-        offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5));
+        offer({true, 128, 0}, cost(tm * ((N + 127) / 128), sms / 2, kblocks, 0.215, 0.7, 4.3 + odd));
+        offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5 + 2 * odd));
     }
     return best;
 }
@@ -363,9 +368,9 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     if (M == 1) return launch_linear_one(a, x, w, K, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16);
     if (plan.wide)
-        return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, rows_on_16, s) == cudaSuccess ? KDA_OK
+                                                                                                  : KDA_ERR_CUDA;
     const int nt = plan.tokens, log_split = plan.log_split;
-    if ((M + nt - 1) / nt > 65535) return KDA_ERR_UNSUPPORTED;
     if (!rows_map(&a.tm_w, p.io_dtype, w, N, K, ldw, kFeatures) || !rows_map(&a.tm_x, p.io_dtype, x, M, K, ldx, nt))
         return KDA_ERR_CUDA;
     a.idesc = f8                             ? idesc_e4m3_f32(kFeatures, nt)

@@ -1,5 +1,5 @@
 // linear.cuh -- what the kernels of kda_linear share (linear_one.cu: one token;
-// linear.cu: few tokens, or rows of y off 16 bytes; linear_wide.cu: many): arguments,
+// linear.cu: few tokens; linear_wide.cu: many): arguments,
 // cluster and tcgen05 wrappers, the activations.
 #pragma once
 #include <cuda.h>
@@ -33,9 +33,9 @@ struct LinArgs {
 cudaError_t launch_linear_one(const LinArgs& a, const void* x, const void* w, int64_t K, int64_t ldw, cudaStream_t s);
 // The kernel for many tokens (linear_wide.cu), tn features (128 or 256) a tile.
 // tm_w, tm_x and idesc are set there; x, w are the operands and ldx, ldw their
-// row strides.
+// row strides; rows_on_16: all rows of y and the residual start on 16 bytes.
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
-                               int64_t ldw, cudaStream_t s);
+                               int64_t ldw, bool rows_on_16, cudaStream_t s);
 
 // launch_dependent (internal.h) with a cluster of `size` CTAs along x.
 template <typename... KArgs, typename... Args>

@@ -15,7 +15,10 @@
 // running sums a thread).  A thread has a token's row; 128-byte row pieces go
 // through a swizzled staging box per warp, which TMA loads the residual into
 // and stores y from, so global memory sees whole lines and ragged edges are
-// clipped by the copy.
+// clipped by the copy.  Rows that do not start on 16 bytes, which TMA cannot
+// move, go between box and memory by the warp's own loads and stores, lanes along
+// a row, still beside the next tile's MMAs: 8192 x 4095 x 4096 in bf16 148 us (338
+// in the kernel for few tokens, whose rows of threads store four elements each).
 //
 // Bound: the tensor cores (and, seconds long, the power limit).  A stage of 64
 // 16-bit k takes 0.316 us a pair, 2.0 PFLOP/s over 76 pairs: 32768 x 4096 x 4096
@@ -52,6 +55,7 @@ struct WideShape {
 struct WideArgs {
     LinArgs a;
     CUtensorMap tm_y, tm_r;  // boxes of 128 bytes x 32 rows
+    int direct;              // rows of y or the residual off 16 bytes: moved by the warp, not by TMA
     int tiles_m, tiles_n;
 };
 
@@ -123,6 +127,36 @@ __device__ __forceinline__ void activate_row(uint8_t* row, int lane, int act) {
     }
 }
 
+// A box and its place in memory, element by element (lanes along a row): IN fills
+// the box, else it is stored.  COLS: 64 16-bit or 32 fp32 columns.
+template <int COLS, bool IN>
+__device__ __forceinline__ void move_box(uint8_t* box, void* p, int64_t ld, int m0, int n0, int M, int N, int lane) {
+    constexpr int kSize = 128 / COLS;
+    __syncwarp();
+    const int rows = min(32, M - m0);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+#pragma unroll
+        for (int h = 0; h < COLS / 32; ++h) {
+            const int c = h * 32 + lane;
+            uint8_t* at = box + r * 128 + ((((c * kSize) >> 4) ^ (r & 7)) << 4) + ((c * kSize) & 15);
+            if (n0 + c < N) {
+                const int64_t to = (int64_t)(m0 + r) * ld + n0 + c;
+                if constexpr (kSize == 2) {
+                    uint16_t *s = reinterpret_cast<uint16_t*>(at), *g = static_cast<uint16_t*>(p) + to;
+                    if (IN) *s = *g;
+                    else *g = *s;
+                } else {
+                    uint32_t *s = reinterpret_cast<uint32_t*>(at), *g = static_cast<uint32_t*>(p) + to;
+                    if (IN) *s = *g;
+                    else *g = *s;
+                }
+            }
+        }
+    }
+    __syncwarp();
+}
+
 // Tile t of the sweep: groups of kGroup token tiles, the features outside, the group's tokens inside.
 __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int* tm, int* tn) {
     const int per = kGroup * tiles_n;
@@ -157,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
     if (tid == 0) {
         ptx::prefetch_tmap(&a.tm_w);
         ptx::prefetch_tmap(&a.tm_x);
-        ptx::prefetch_tmap(&p.tm_y);
+        if (!p.direct) ptx::prefetch_tmap(&p.tm_y);
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
@@ -269,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
             if (F8 && m0 + lane < a.M) xs = a.x_scale[m0 + lane];
             const bool rows = m0 < a.M;
             auto load_residual = [&](int n) {
-                if (lane == 0) {
+                if (lane == 0 && !p.direct) {
                     ptx::bulk_wait_read0();  // the box's last store has read it
                     ptx::mbar_arrive_expect_tx(&res[e], kBoxBytes);
                     ptx::tma_load_2d(box, &p.tm_r, &res[e], n, m0);
@@ -325,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                         v[32 * h + c] += __shfl_sync(~0u, box_bias, c);
                     }
                 }
-                if (a.residual) {
+                if (p.direct) {
+                    if (a.residual) move_box<kBoxCols, true>(box, const_cast<void*>(a.residual), a.ldr, m0, n, a.M, a.N, lane);
+                } else if (a.residual) {
                     ok = __all_sync(~0u, wait_for(&res[e], loads & 1));
                     if (!ok) break;
                     ++loads;
@@ -378,6 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                             }
                         }
                     }
+                }
+                if (p.direct) {
+                    move_box<kBoxCols, false>(box, a.y, a.ldy, m0, n, a.M, a.N, lane);
+                    continue;
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -440,12 +480,14 @@ cudaError_t launch(WideArgs& p, bool out16, const void* w, int64_t K, int64_t ld
 }  // namespace
 
 cudaError_t launch_linear_wide(const LinArgs& a, int tn, const void* x, const void* w, int64_t K, int64_t ldx,
-                               int64_t ldw, cudaStream_t s) {
+                               int64_t ldw, bool rows_on_16, cudaStream_t s) {
     WideArgs p{};
     p.a = a;
     p.tiles_m = (a.M + kTileM - 1) / kTileM;
-    if (!rows_map(&p.a.tm_x, a.io, x, a.M, K, ldx, 128) || !box_map(&p.tm_y, a.out, a.y, a.M, a.N, a.ldy) ||
-        (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr)))
+    p.direct = !rows_on_16;
+    if (!rows_map(&p.a.tm_x, a.io, x, a.M, K, ldx, 128)) return cudaErrorInvalidValue;
+    if (rows_on_16 && (!box_map(&p.tm_y, a.out, a.y, a.M, a.N, a.ldy) ||
+                       (a.residual && !box_map(&p.tm_r, a.out, a.residual, a.M, a.N, a.ldr))))
         return cudaErrorInvalidValue;
     const bool f8 = a.io == KDA_DTYPE_E4M3;
     const bool out16 = a.out != KDA_DTYPE_F32;

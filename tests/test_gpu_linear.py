@@ -138,6 +138,29 @@ def test_nothing_outside_the_output(M, N, out):
     assert g.intact()
 
 
+@pytest.mark.parametrize("M,N", [(70, 2049), (300, 4095), (1000, 999), (4097, 1023)])
+@pytest.mark.parametrize("io,out", [(BF16, BF16), (F16, F32), (F8, BF16), (F8, F32)])
+def test_rows_off_16_bytes(M, N, io, out):
+    """y and the residual as columns of wider tensors, no row of them on a set place; what lies around y stays."""
+    x, w, xs, ws = operands(M, N, 320, io, seed=N)
+    kw = dict(act="silu", x_scale=xs, w_scale=ws, out_dtype=out)
+    wide = randn(M, N + 6, seed=7).to(out)
+    buf = wide.clone()
+    y = buf[:, 3 : N + 3]
+    kda.linear(x, w, residual=wide[:, 1 : N + 1], out=y, **kw)
+    xd, wd = x.double(), w.double()
+    if io == F8:
+        xd, wd = xd * xs.double()[:, None], wd * ws.double()[:, None]
+    pre, size, r = xd @ wd.T, xd.abs() @ wd.abs().T, wide[:, 1 : N + 1].double()
+    ref = ACTS["silu"](pre)
+    arith = 1.2 * (320 / 8 + 8) * 2.0 ** -23 * size + 16 * EPS32 * (size + ref.abs() + 1.0 + r.abs())
+    assert_close(y, ref + r, HALF_ULP[out] * 1.01, arith * (1 + HALF_ULP[out]) + TINY[out], (M, N, io, out))
+    assert torch.equal(buf[:, :3], wide[:, :3]) and torch.equal(buf[:, N + 3 :], wide[:, N + 3 :])
+    z = wide.clone()
+    kda.linear(x, w, residual=z[:, 1 : N + 1], out=z[:, 1 : N + 1], **kw)
+    assert torch.equal(z[:, 1 : N + 1], y)
+
+
 def test_bad_rows_stay_by_themselves():
     """An infinity or NaN in a row of x reaches that row of y alone; one in a row of w, that column."""
     for M in (20, 400):
