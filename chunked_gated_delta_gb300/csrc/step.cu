@@ -209,22 +209,25 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
     }
 
     // Inputs of kTokens tokens at a time, whose loads are in flight together: k
-    // and g rows by the first K threads, q by the next 128, v by the first VT.
+    // and g rows by the first K threads, q by the next 128, v by the first VT.  They
+    // are turned into fp32 when they are staged: a load's first use waits for it,
+    // and there each token's waited before the next token's was asked for.
     const int hq = h / a.group;
     const int kr = tid & 127;
-    float in_k[kTokens], in_g[kTokens], in_q[kTokens], in_v[kTokens], in_b[kTokens];
+    uint16_t in_k[kTokens], in_q[kTokens], in_v[kTokens], in_b[kTokens];
+    float in_g[kTokens];
     auto load_tokens = [&](int t0) {
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
             if (t0 + j >= len) break;
             const int64_t row = row0 + t0 + j;
             if (tid < K) {
-                in_k[j] = from_b16<F16>(a.k[row * a.k_stride + (int64_t)hq * K + tid]);
+                in_k[j] = a.k[row * a.k_stride + (int64_t)hq * K + tid];
                 in_g[j] = a.g[row * a.g_stride + (int64_t)h * K + tid];
             }
-            if (tid >= 128 && kr < K) in_q[j] = from_b16<F16>(a.q[row * a.q_stride + (int64_t)hq * K + kr]);
-            if (tid < VT) in_v[j] = from_b16<F16>(a.v[row * a.v_stride + (int64_t)h * a.V + tile * VT + tid]);
-            if (tid == 0) in_b[j] = from_b16<F16>(a.beta[row * a.beta_stride + h]);
+            if (tid >= 128 && kr < K) in_q[j] = a.q[row * a.q_stride + (int64_t)hq * K + kr];
+            if (tid < VT) in_v[j] = a.v[row * a.v_stride + (int64_t)h * a.V + tile * VT + tid];
+            if (tid == 0) in_b[j] = a.beta[row * a.beta_stride + h];
         }
     };
     auto stage_tokens = [&](int t0) {
@@ -232,12 +235,15 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
         for (int j = 0; j < kTokens; ++j) {
             if (t0 + j >= len) break;
             if (tid < K) {
-                s_token[j].kqe[tid].x = in_k[j];
+                s_token[j].kqe[tid].x = from_b16<F16>(in_k[j]);
                 s_token[j].kqe[tid].z = expf(in_g[j]);
             }
-            if (tid >= 128 && kr < K) s_token[j].kqe[kr].y = in_q[j];
-            if (tid < VT) s_token[j].v[tid] = in_v[j];
-            if (tid == 0) s_token[j].beta = a.logits ? 1.f / (1.f + expf(-in_b[j])) : in_b[j];
+            if (tid >= 128 && kr < K) s_token[j].kqe[kr].y = from_b16<F16>(in_q[j]);
+            if (tid < VT) s_token[j].v[tid] = from_b16<F16>(in_v[j]);
+            if (tid == 0) {
+                const float b = from_b16<F16>(in_b[j]);
+                s_token[j].beta = a.logits ? 1.f / (1.f + expf(-b)) : b;
+            }
         }
     };
     load_tokens(0);
