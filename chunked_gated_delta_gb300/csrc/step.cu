@@ -28,7 +28,7 @@
 namespace kda {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 256, kStepWarps = kStepThreads / 32;
 constexpr int kTokens = 4;  // tokens whose inputs are loaded together (even: the exchange buffers alternate)
 
 struct StepArgs {
@@ -64,7 +64,7 @@ template <int K, int COLS>
 struct Token {
     float4 kqe[K];  // per row: k, q, exp(g)
     float v[COLS];
-    float beta, unused[3];
+    float beta, kq, unused[2];  // kq: k . q
 };
 
 // What the warps of THREADS threads exchange of a token: S^T k and S^T q of their rows.
@@ -73,6 +73,11 @@ struct Sums {
     float4 k[THREADS / 32][COLS / 4], q[THREADS / 32][COLS / 4];
 };
 
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
+    return x;
+}
 __device__ __forceinline__ void add4(float4& a, const float4 b) {
     a.x += b.x;
     a.y += b.y;
@@ -120,13 +125,6 @@ __device__ __forceinline__ bool step_token(float4 (&S)[kRows], const Token<K, CO
         sums.k[warp][cg] = pk;
         sums.q[warp][cg] = pq;
     }
-    float kq = 0.f;  // k . q, for the warp that writes o
-    if (warp == 0) {
-#pragma unroll
-        for (int r = 0; r < K; r += 32) kq += in.kqe[r + lane].x * in.kqe[r + lane].y;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) kq += __shfl_xor_sync(~0u, kq, off);
-    }
     if (!sync()) return false;
     float4 d = sums.k[0][cg];
 #pragma unroll
@@ -138,7 +136,7 @@ __device__ __forceinline__ bool step_token(float4 (&S)[kRows], const Token<K, CO
         float4 y = sums.q[0][cg];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) add4(y, sums.q[w][cg]);
-        fma4(y, kq, d);
+        fma4(y, in.kq, d);
         *reinterpret_cast<uint2*>(o) =
             make_uint2(pack_b16x2(scale * y.x, scale * y.y, F16), pack_b16x2(scale * y.z, scale * y.w, F16));
     }
@@ -269,8 +267,16 @@ __global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a
             stage_tokens(t0);
             __syncthreads();
         }
+        const int count = min(kTokens, len - t0), of = (tid >> 5) - kStepWarps / 2;
+        if (of >= 0 && of < count) {  // k . q, read after the first token's barrier
+            float kq = 0.f;
+#pragma unroll
+            for (int r = tid & 31; r < K; r += 32) kq += s_token[of].kqe[r].x * s_token[of].kqe[r].y;
+            kq = warp_sum(kq);
+            if (tid % 32 == 0) s_token[of].kq = kq;
+        }
         if (t0 + kTokens < len) load_tokens(t0 + kTokens);
-        for (int j = 0; j < min(kTokens, len - t0); ++j)
+        for (int j = 0; j < count; ++j)
             step_token<K, VT, F16, kRows, kStepThreads>(S, s_token[j], s_sums[j & 1], a.scale, o + (t0 + j) * o_step, tid,
                                                         [] {
                                                             __syncthreads();
@@ -618,16 +624,20 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                     break;
                 }
                 auto& to = gr.token[s];
+                float kq = 0.f;
 #pragma unroll
                 for (int x = 0; x < kk; ++x) {
-                    to.kqe[lane * kk + x] =
-                        make_float4(rk[d].template at<F16>(x, a.vec), rq[d].template at<F16>(x, a.vec), expf(rg[d][x]), 0.f);
+                    const float fk = rk[d].template at<F16>(x, a.vec), fq = rq[d].template at<F16>(x, a.vec);
+                    to.kqe[lane * kk + x] = make_float4(fk, fq, expf(rg[d][x]), 0.f);
+                    kq = fmaf(fk, fq, kq);
                 }
+                kq = warp_sum(kq);
 #pragma unroll
                 for (int x = 0; x < vv; ++x) to.v[lane * vv + x] = rv[d].template at<F16>(x, a.vec);
                 if (lane == 0) {
                     const float x = from_b16<F16>(rb[d]);
                     to.beta = a.logits ? 1.f / (1.f + expf(-x)) : x;
+                    to.kq = kq;
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&gr.token_full[s]);  // (32 arrivals would queue up at the barrier)
