@@ -18,8 +18,8 @@
 // holds its K x VT part in registers as float4 (a warp's load covers whole
 // 128-byte lines), in fp32 whatever the cache's type, across all the tokens.
 // From two pairs per SM on the streaming kernel below takes over.  Measured at
-// K = V = 128 in fp32, this kernel against that one: 32 pairs 3.4 us, 5.0;
-// 128 pairs 4.6, 5.4; 256 pairs 10.7, 10.5; 512 pairs 18, 16; 16384 pairs 490,
+// K = V = 128 in fp32, this kernel against that one: 32 pairs 2.9 us, 5.0;
+// 128 pairs 4.3, 5.4; 256 pairs 9.7, 10.5; 512 pairs 17, 14; 16384 pairs 490,
 // 350 (6.1 TB/s, 92% of what a copy reaches).
 #include "internal.h"
 #include "layer_ops.cuh"
@@ -163,8 +163,10 @@ __device__ __forceinline__ void store_state(void* p, int64_t four, float4 s) {
         static_cast<float4*>(p)[four] = s;
 }
 
-template <int K, int VT, bool F16, bool STATE16>
-__global__ void __launch_bounds__(kStepThreads) kda_step_kernel(const StepArgs a) {
+// PER_SM: CTAs that an SM has room for, and so the registers of a thread, which hold
+// its part of the state and the loads in flight.
+template <int K, int VT, bool F16, bool STATE16, int PER_SM>
+__global__ void __launch_bounds__(kStepThreads, PER_SM) kda_step_kernel(const StepArgs a) {
     constexpr int kColGroups = VT / 4;                      // threads across a row, 4 columns each
     constexpr int kRowLanes = kStepThreads / kColGroups;    // rows in flight per step of i
     constexpr int kRows = K / kRowLanes;                    // rows a thread holds
@@ -705,12 +707,23 @@ cudaError_t launch_stream(const StepArgs& a, bool f16, bool state16, int sms, cu
     return state16 ? launch_stream<K, V, false, true>(a, sms, s) : launch_stream<K, V, false, false>(a, sms, s);
 }
 
-template <int K, int VT>
-cudaError_t launch(const StepArgs& a, bool f16, bool state16, cudaStream_t s) {
-    const unsigned grid = (unsigned)((int64_t)a.N * a.H * (a.V / VT));
-    auto kern = f16 ? (state16 ? kda_step_kernel<K, VT, true, true> : kda_step_kernel<K, VT, true, false>)
-                    : (state16 ? kda_step_kernel<K, VT, false, true> : kda_step_kernel<K, VT, false, false>);
+template <int K, int VT, int PER_SM>
+cudaError_t launch(const StepArgs& a, bool f16, bool state16, unsigned grid, cudaStream_t s) {
+    auto kern = f16 ? (state16 ? kda_step_kernel<K, VT, true, true, PER_SM> : kda_step_kernel<K, VT, true, false, PER_SM>)
+                    : (state16 ? kda_step_kernel<K, VT, false, true, PER_SM> : kda_step_kernel<K, VT, false, false, PER_SM>);
     return launch_dependent(kern, dim3(grid), dim3(kStepThreads), 0, s, a);
+}
+
+// Calls whose CTAs have an SM each get all its registers where K = 128 (140 a thread
+// instead of 128): 32 pairs with V = 128 2.9 us, for 3.4 with room for two; with more
+// CTAs than SMs 128 pairs take 5.5 us, for 4.3.  K = 64 uses 126 either way (3.2 us for
+// 256 pairs; 3.8 with the 80 that the compiler takes unasked).
+template <int K, int VT>
+cudaError_t launch(const StepArgs& a, bool f16, bool state16, int sms, cudaStream_t s) {
+    const unsigned grid = (unsigned)((int64_t)a.N * a.H * (a.V / VT));
+    if constexpr (K == 128)
+        if (grid <= (unsigned)sms) return launch<K, VT, 1>(a, f16, state16, grid, s);
+    return launch<K, VT, 2>(a, f16, state16, grid, s);
 }
 
 }  // namespace
@@ -788,7 +801,7 @@ extern "C" kda_status kda_step(const void* q, const void* k, const void* v, cons
         else
             e = d.V == 128 ? launch_stream<64, 128>(a, f16, s16, sms, s) : launch_stream<64, 64>(a, f16, s16, sms, s);
     } else {
-        e = d.K == 128 ? launch<128, 64>(a, f16, s16, s) : launch<64, 64>(a, f16, s16, s);
+        e = d.K == 128 ? launch<128, 64>(a, f16, s16, sms, s) : launch<64, 64>(a, f16, s16, sms, s);
     }
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
