@@ -263,52 +263,62 @@ cudaError_t launch(const LinArgs& a, bool f8, int log_split, cudaStream_t s) {
 }
 
 // Which kernel takes a call, and how it cuts it: the least of the modelled
-// times.  The constants (us) were measured on GB300 at K = 2048 and 4096, M = 1
-// to 4096, N = 32 to 8192: what a call costs beside its stages, a stage of k,
-// and the end of a tile.  E.g. at N = K = 4096, 16 bits: M = 64 in tiles of 64
+// times.  The constants (us) were measured on GB300 at K = 32 to 4096, M = 1 to
+// 27367, N = 4 to 8192: what a call costs beside its stages, a stage of k, the end
+// of a tile, what its slices cost to join, and a further round of CTAs; over 160
+// calls of sizes drawn at random its choices took 1% more than the best ones.  E.g. at N = K = 4096, 16 bits: M = 64 in tiles of 64
 // tokens takes 18.2, 13.9, 12.0, 23.0 us for 1, 2, 4, 8 slices of k; M = 256
 // takes 25.3 us in tiles of 64 and two slices, 17.6 in tiles of 128 and two,
 // 18.9 in the wide kernel with 128 features, 26.5 with 256; M = 2048 takes 56.7
 // in the wide kernel with 128, 46.0 with 256.  Rows of y off 16 bytes: 8192 x 4095
 // x 4096 takes 338 us in tiles of 128 tokens, 148 in the wide kernel; 130 x 77 x
-// 4096 6.5 in tiles of 64 and eight slices, 17.2 in the wide kernel.
+// 4096 6.5 in tiles of 64 and eight slices, 17.2 in the wide kernel; 391 x 3136 x
+// 4096 (100 tiles in four slices are three rounds) 32.0 in tiles of 128 tokens and
+// four slices, 20.0 in one, 17.3 in the wide kernel with 128 features.
 struct Plan {
     bool wide;
     int tokens;     // per tile; of the wide kernel: features per tile
     int log_split;  // 2^log_split slices of k
 };
-Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16) {
+Plan choose(int64_t M, int64_t N, int64_t bytes, int kblocks, bool rows_on_16, bool residual, bool f32) {
     const int sms = device_sm_count();
     const double stream = (double)bytes / 6.6e6;  // x and w once from HBM
-    auto cost = [&](int64_t units, int64_t slots, double stages, double per_stage, double end, double call) {
+    auto cost = [&](int64_t units, int64_t slots, double stages, double per_stage, double end, double call, double wave) {
         const double waves = (double)((units + slots - 1) / slots);
-        return call + fmax(waves * stages * per_stage, stream) + waves * end;
+        return call + fmax(waves * stages * per_stage, stream) + waves * end + (waves - 1) * wave;
     };
-    // Rows off 16 bytes go element by element: after every tile of the narrow kernel,
-    // after the last one of the wide kernel, which stores while the next is summed.
-    const double odd = rows_on_16 ? 0.0 : 1.0;
+    // Rows off 16 bytes go element by element, and a residual is waited for: after
+    // every tile of the narrow kernel, after the last one of the wide kernel, which
+    // ends a tile while the next is summed.
+    const double odd = rows_on_16 ? 0.0 : 1.0, slow = odd + (residual ? 0.5 : 0.0);
     Plan best{false, 16, 0};
     double least = 1e30;
     auto offer = [&](Plan p, double c) {
         if (c < least) least = c, best = p;
     };
-    constexpr struct { int tokens; double stage, end; } kNarrow[] = {
-        {16, 0.186, 0.3}, {32, 0.19, 0.5}, {64, 0.205, 1.0}, {128, 0.245, 2.9}};
+    constexpr struct { int tokens; double stage, end, join; } kNarrow[] = {
+        {16, 0.186, 0.3, 0.0}, {32, 0.19, 0.5, 0.0}, {64, 0.205, 1.0, 0.4}, {128, 0.245, 2.9, 2.6}};
     for (const auto& t : kNarrow) {
         if (t.tokens < 64 && t.tokens < M) continue;      // a second token tile would read w again
         if ((M + t.tokens - 1) / t.tokens > 65535) continue;  // (rows of the grid)
         const int64_t tiles = (M + t.tokens - 1) / t.tokens * ((N + kFeatures - 1) / kFeatures);
         for (int ls = 0; ls <= 3 && (ls == 0 || kblocks >> ls >= 4); ++ls) {
-            const int slots = ls < 3 ? sms : 96;          // clusters of 8 leave SMs of a GPC over
+            const int slots = ls < 3 ? sms : 112;         // clusters of 8 leave SMs of a GPC over
             offer({false, t.tokens, ls}, cost(tiles << ls, slots, (double)((kblocks + (1 << ls) - 1) >> ls), t.stage,
-                                              (t.end + odd * t.tokens / 32) / (1 << ls), ls ? 4.5 : 3.3));
+                                              (t.end + slow * (double)min((int64_t)t.tokens, M) / 32) / (1 << ls) + (ls ? t.join : 0.0),
+                                              ls ? 4.5 : M > 64 ? 3.9 : 3.3, 4.0));
         }
         if (t.tokens >= M) break;
     }
     if (M > 64) {
         const int64_t tm = (M + 255) / 256;
-        offer({true, 128, 0}, cost(tm * ((N + 127) / 128), sms / 2, kblocks, 0.215, 0.7, 4.3 + odd));
-        offer({true, 256, 0}, cost(tm * ((N + 255) / 256), sms / 2, kblocks, 0.316, 0.7, 5.5 + 2 * odd));
+        // a tile's sums hide the end of the one before only as far as they last
+        const double end = (f32 ? 3.0 : 1.5) * (1.0 + odd * (2.0 * slow - 1.0));
+        for (int tn = 128; tn <= 256; tn *= 2) {
+            const double stage = tn == 128 ? 0.2 : 0.3, tile_end = tn == 128 ? end : (f32 ? 2.5 : 1.8) * end;
+            offer({true, tn, 0}, cost(tm * ((N + tn - 1) / tn), sms / 2, kblocks, stage, 0.0,
+                                      (tn == 128 ? 2.7 : 2.2) + tile_end, fmax(0.0, tile_end - kblocks * stage)));
+        }
     }
     return best;
 }
@@ -366,7 +376,7 @@ extern "C" kda_status kda_linear(const void* x, const void* w, const float* bias
     const int four = 4 * oes;  // bytes of a lane's features
     a.wide = is_aligned(y, four) && ldy % 4 == 0 && (!residual || (is_aligned(residual, four) && ldr % 4 == 0));
     if (M == 1) return launch_linear_one(a, x, w, K, ldw, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16);
+    const Plan plan = choose(M, N, (M + N) * K * es, kblocks, rows_on_16, residual != nullptr, oes == 4);
     if (plan.wide)
         return launch_linear_wide(a, plan.tokens, x, w, K, ldx, ldw, rows_on_16, s) == cudaSuccess ? KDA_OK
                                                                                                   : KDA_ERR_CUDA;

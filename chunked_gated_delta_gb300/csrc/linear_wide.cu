@@ -128,30 +128,46 @@ __device__ __forceinline__ void activate_row(uint8_t* row, int lane, int act) {
 }
 
 // A box and its place in memory, element by element (lanes along a row): IN fills
-// the box, else it is stored.  COLS: 64 16-bit or 32 fp32 columns.
+// the box, else it is stored.  COLS: 64 16-bit or 32 fp32 columns.  A residual's
+// loads go 16 words at a time, from L2, where the tile's rows are asked for before
+// its sums are waited for: 3259 x 5177 x 2048 with log-sigmoid to fp32 291 us with
+// four at a time and from HBM, 104 with both (79 with 128 features a tile).
 template <int COLS, bool IN>
 __device__ __forceinline__ void move_box(uint8_t* box, void* p, int64_t ld, int m0, int n0, int M, int N, int lane) {
     constexpr int kSize = 128 / COLS;
     __syncwarp();
     const int rows = min(32, M - m0);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
+    constexpr int kBatch = IN ? 512 / COLS : 4;  // rows whose loads are in flight together
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+        uint32_t got[kBatch][COLS / 32];
+        const int64_t to = (int64_t)(m0 + r0) * ld + n0 + lane;
 #pragma unroll
-        for (int h = 0; h < COLS / 32; ++h) {
-            const int c = h * 32 + lane;
-            uint8_t* at = box + r * 128 + ((((c * kSize) >> 4) ^ (r & 7)) << 4) + ((c * kSize) & 15);
-            if (n0 + c < N) {
-                const int64_t to = (int64_t)(m0 + r) * ld + n0 + c;
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int h = 0; h < COLS / 32; ++h) {
+                const int r = r0 + i, c = h * 32 + lane;
+                const int at = r * 128 + ((((c * kSize) >> 4) ^ (r & 7)) << 4) + ((c * kSize) & 15);
+                const bool live = r < rows && n0 + c < N;
                 if constexpr (kSize == 2) {
-                    uint16_t *s = reinterpret_cast<uint16_t*>(at), *g = static_cast<uint16_t*>(p) + to;
-                    if (IN) *s = *g;
-                    else *g = *s;
+                    uint16_t* g = static_cast<uint16_t*>(p) + to + i * ld + h * 32;
+                    if (IN) got[i][h] = live ? *g : 0;
+                    else if (live) *g = *reinterpret_cast<uint16_t*>(box + at);
                 } else {
-                    uint32_t *s = reinterpret_cast<uint32_t*>(at), *g = static_cast<uint32_t*>(p) + to;
-                    if (IN) *s = *g;
-                    else *g = *s;
+                    uint32_t* g = static_cast<uint32_t*>(p) + to + i * ld + h * 32;
+                    if (IN) got[i][h] = live ? *g : 0;
+                    else if (live) *g = *reinterpret_cast<uint32_t*>(box + at);
                 }
             }
+        if constexpr (IN) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int h = 0; h < COLS / 32; ++h) {
+                    const int r = r0 + i, c = h * 32 + lane;
+                    const int at = r * 128 + ((((c * kSize) >> 4) ^ (r & 7)) << 4) + ((c * kSize) & 15);
+                    if constexpr (kSize == 2) *reinterpret_cast<uint16_t*>(box + at) = (uint16_t)got[i][h];
+                    else *reinterpret_cast<uint32_t*>(box + at) = got[i][h];
+                }
         }
     }
     __syncwarp();
@@ -311,6 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __gr
                 }
             };
             if (a.residual && rows && n0 < a.N) load_residual(n0);
+            if (a.residual && p.direct && m0 + lane < a.M && n0 < a.N) {  // into L2 by the time it is asked for
+                constexpr int kSize = OUT16 ? 2 : 4;
+                const uint8_t* from = static_cast<const uint8_t*>(a.residual) + ((int64_t)(m0 + lane) * a.ldr + n0) * kSize;
+                const int bytes = min(kCols, a.N - n0) * kSize;
+                for (int at = 0; at < bytes; at += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + at));
+            }
             float sum[kSegments ? kCols : 1];
             uint32_t acc = 0;
             for (int g = 0; g < segments; ++g, ++n_acc) {
