@@ -11,15 +11,14 @@
 // largest |s w|, which times 1 / sqrt(...) is the largest |y| (to a rounding),
 // so that both are joined at once.  A row is taken by a team: 2 to 32 lanes of a
 // warp for short rows (head norms), so that its sums are shuffles and many rows
-// share a CTA, or a whole CTA for long ones, with one barrier; long rows with a
-// residual go through a ring in shared memory instead (below).  Measured: 1.07 M
-// rows of 128 82 us (6.7 TB/s, what a copy reaches), with residual to e4m3 6.9
-// TB/s; 32768 rows of 4096 84 us (6.4), with residual to e4m3 152 (6.2).
+// share a CTA, or a whole CTA for long ones, with one barrier.  Measured: 1.07 M
+// rows of 128 81 us (6.7 TB/s, what a copy reaches), with residual to e4m3 6.9
+// TB/s; 32768 rows of 4096 84 us (6.4), with residual to e4m3 137 (6.9).
 #include <type_traits>
 
 #include "internal.h"
 #include "layer_ops.cuh"
-#include "waits.cuh"
+#include "ptx.cuh"
 
 namespace kda {
 namespace {
@@ -34,6 +33,7 @@ struct NormArgs {
     int64_t rows, x_stride, r_stride, sum_stride;
     int dim, out, w_f32;
     int y_with_x;  // SHIFT: y's rows lie off 16 bytes as x's do
+    int exchange;  // SHIFT: they do not, and y goes through shared memory (a code's byte gains nothing by it)
     float eps, inv_dim;
 };
 
@@ -104,6 +104,33 @@ __device__ __forceinline__ float2 team_join(float2 v, float2* s, bool with_max) 
     return v;
 }
 
+// Eight elements as they come from memory.
+template <int IO>
+struct Raw {
+    uint4 v[IO == KDA_DTYPE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        constexpr int kSize = IO == KDA_DTYPE_F32 ? 4 : 2;
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * kSize);
+#pragma unroll
+        for (int i = 0; i < kSize / 2; ++i) v[i] = q[i];
+    }
+    __device__ __forceinline__ void unpack(float* f) const {
+        if constexpr (IO == KDA_DTYPE_F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(v[i].x), f[4 * i + 1] = __uint_as_float(v[i].y);
+                f[4 * i + 2] = __uint_as_float(v[i].z), f[4 * i + 3] = __uint_as_float(v[i].w);
+            }
+        } else {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = from_b16x2<IO == KDA_DTYPE_F16>(w[i]);
+                f[2 * i] = u.x, f[2 * i + 1] = u.y;
+            }
+        }
+    }
+};
 // Elements c .. c + 7 of a row of `dim`, of which some may lie outside it (SHIFT).
 template <int IO, int VEC, bool SHIFT>
 __device__ __forceinline__ void load_part(const void* p, int64_t row, int c, int dim, float* f) {
@@ -132,7 +159,7 @@ __device__ __forceinline__ void store_part(void* p, int64_t row, int c, int dim,
 // off by the same: vectors start before the row, at its 16-byte boundary, and
 // only a row's first and last vector go by elements.
 template <int IO, int VEC, int NV, int TEAM, bool SHIFT>
-__global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TEAM ? 256 : SHIFT ? 576 : 1024) kda_norm_kernel(const NormArgs a) {
     __shared__ float2 s_join[32];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -150,23 +177,59 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
     auto column = [&](int i) { return (lane + i * width) * VEC - off; };
     auto inside = [&](int c) { return c < a.dim && (!SHIFT || c + VEC > 0); };
     float s[NV][VEC];
+    // Whole vectors of x and the residual are all asked for first, and only then taken
+    // apart, which waits for them: residual rows to e4m3 152 -> 137 us for 32768 x 4096
+    // (a ring in shared memory filled ahead by bulk copies was at 152, each vector
+    // waited for by itself 170).  Small teams off 16 bytes do better without.
+    constexpr bool kRaw = VEC == 8 && (!SHIFT || TEAM == 0);
+    if constexpr (kRaw) {
+        Raw<IO> rx[NV], rr[NV];
+        auto whole = [&](int c) { return live && c + (SHIFT ? VEC - 1 : 0) < a.dim && (!SHIFT || c >= 0); };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = column(i);
-        if (live && inside(c)) {
-            load_part<IO, VEC, SHIFT>(a.x, row * a.x_stride, c, a.dim, s[i]);
-        } else {
+        for (int i = 0; i < NV; ++i)
+            if (whole(column(i))) rx[i].load(a.x, row * a.x_stride + column(i));
+        if (a.r) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s[i][j] = 0.f;
+            for (int i = 0; i < NV; ++i)
+                if (whole(column(i))) rr[i].load(a.r, row * a.r_stride + column(i));
         }
-    }
-    if (a.r) {
+        auto take = [&](int i, const Raw<IO>& raw, const void* p, int64_t stride, float* f) {
+            const int c = column(i);
+            if (whole(c)) {
+                raw.unpack(f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    f[j] = 0.f;
+                    if (SHIFT && live && c + j >= 0 && c + j < a.dim) load_vec<IO, 1>(p, row * stride + c + j, f + j);
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) take(i, rx[i], a.x, a.x_stride, s[i]);
+        if (a.r) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float r[VEC];
+                take(i, rr[i], a.r, a.r_stride, r);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[i][j] += r[j];
+            }
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = column(i);
-            if (live && inside(c)) {
-                float r[VEC];
-                load_part<IO, VEC, SHIFT>(a.r, row * a.r_stride, c, a.dim, r);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[i][j] = 0.f;
+            if (live && inside(c)) load_part<IO, VEC, SHIFT>(a.x, row * a.x_stride, c, a.dim, s[i]);
+        }
+        if (a.r) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = column(i);
+                float r[VEC] = {};
+                if (live && inside(c)) load_part<IO, VEC, SHIFT>(a.r, row * a.r_stride, c, a.dim, r);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) s[i][j] += r[j];
             }
@@ -189,8 +252,23 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
         if (a.w && inside(c)) {
             float w[VEC];
             if constexpr (SHIFT) {  // (the weight has its own boundary)
+                const bool words = (TEAM == 0 || TEAM == 32) && IO != KDA_DTYPE_F32 && !a.w_f32 && c >= 1 && c + VEC < a.dim;
+                if (words) {
+                    const uint16_t* at = static_cast<const uint16_t*>(a.w) + c;
+                    const int odd = (int)(reinterpret_cast<uintptr_t>(at) >> 1) & 1;
+                    const uint32_t* from = reinterpret_cast<const uint32_t*>(at - odd);
+                    uint32_t u[VEC / 2 + 1];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
+                    for (int j = 0; j < VEC / 2; ++j) u[j] = from[j];
+                    u[VEC / 2] = odd ? from[VEC / 2] : 0u;
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j) {
+                        const float2 v = from_b16x2<IO == KDA_DTYPE_F16>(__funnelshift_r(u[j], u[j + 1], 16 * odd));
+                        w[2 * j] = v.x, w[2 * j + 1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < VEC && !words; ++j) {
                     w[j] = 0.f;
                     if (c + j >= 0 && c + j < a.dim) {
                         if (a.w_f32) load_vec<KDA_DTYPE_F32, 1>(a.w, c + j, w + j);
@@ -223,8 +301,31 @@ __global__ void __launch_bounds__(TEAM ? 256 : 1024) kda_norm_kernel(const NormA
         if (live && inside(c)) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s[i][j] = s[i][j] * rstd * inv;
-            store_part<VEC, SHIFT>(a.y, row * a.dim, c, a.dim, s[i], a.out, a.y_with_x);
         }
+        if constexpr (SHIFT) {
+            if (a.exchange) {
+                // y's own boundary: the lanes of a team, or of a warp, exchange their vectors so
+                // that neighbours store neighbours
+                extern __shared__ __align__(16) float s_row[];
+                constexpr int kLanes = TEAM ? TEAM : 32;
+                const int in_team = lane % kLanes, c0 = c - in_team * VEC;
+                if ((lane - in_team + i * width) * VEC >= a.dim + 8) break;  // (all teams of a warp do)
+                float* piece = s_row + (threadIdx.x - in_team) * VEC;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4)
+                    *reinterpret_cast<float4*>(piece + in_team * VEC + j) =
+                        make_float4(s[i][j], s[i][j + 1], s[i][j + 2], s[i][j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = j * kLanes + in_team;
+                    if (live && c0 + e >= 0 && c0 + e < a.dim) store_vec<1>(a.y, row * a.dim + c0 + e, piece + e, a.out);
+                }
+                continue;
+            }
+        }
+        if (live && inside(c)) store_part<VEC, SHIFT>(a.y, row * a.dim, c, a.dim, s[i], a.out, a.y_with_x);
     }
 }
 
@@ -232,174 +333,14 @@ template <int IO, int VEC, int NV, int TEAM, bool SHIFT = false>
 cudaError_t launch(const NormArgs& a, int threads, cudaStream_t s) {
     const int64_t per = TEAM ? threads / TEAM : 1;
     return launch_dependent(kda_norm_kernel<IO, VEC, NV, TEAM, SHIFT>, dim3((unsigned)((a.rows + per - 1) / per)),
-                            dim3((unsigned)threads), 0, s, a);
+                            dim3((unsigned)threads), SHIFT && a.exchange ? threads * VEC * 4 : 0, s, a);
 }
 
-// ------------------------------------------------------------------ long rows with a residual
-// Two rows to load, two to store, and a barrier between: with a CTA per row (the
-// kernel above) an SM's loads stop while its rows wait for their sums.  Here CTAs
-// are persistent: a warp loads rows of x and the residual into a ring in shared
-// memory with bulk copies, and groups of 128 threads take them in turn, so the
-// loads never stop.  Measured, to e4m3: 32768 rows of 4096 170 -> 152 us (6.2 TB/s,
-// 93% of a copy), 16384 of 8192 175 -> 158; rows of 2048 gain nothing (163, 167).
-constexpr int kRingThreads = 128;  // of a group
-constexpr int kRingGroups = 4;
-constexpr int kRingAll = kRingGroups * kRingThreads + 32;
-constexpr int kMostSlots = 24;
-constexpr int kRingBytes = 200 * 1024;
-
-// Slots of the ring: a multiple of the groups, so that a slot's barriers belong
-// to one group (a group that waits a phase ahead of another's would misread
-// their parity).
-inline int ring_slots(int slot_bytes) {
-    const int n = kRingBytes / slot_bytes / kRingGroups * kRingGroups;
-    return n < kMostSlots ? n : kMostSlots;
-}
-
-template <int IO, int NV>
-__global__ void __launch_bounds__(kRingAll, 1) kda_norm_ring_kernel(const NormArgs a, int slots) {
-    constexpr int kSize = IO == KDA_DTYPE_F32 ? 4 : 2;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(8) uint64_t full[kMostSlots], empty[kMostSlots];
-    __shared__ float2 s_join[kRingGroups][2][kRingThreads / 32];
-    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-    const int row_bytes = a.dim * kSize, slot_bytes = 2 * row_bytes;
-    if (tid < slots) {
-        ptx::mbar_init(&full[tid], 1);
-        ptx::mbar_init(&empty[tid], kRingThreads / 32);
-    }
-    ptx::fence_mbar_init();
-    ptx::grid_dep_launch();
-    __syncthreads();
-    ptx::grid_dep_wait();
-
-    const int count = (int)((a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // rows of this CTA
-    if (warp == kRingGroups * (kRingThreads / 32)) {
-        if (elect_one()) {
-            int i = 0;
-            for (; i < count; ++i) {
-                const int s = i % slots, round = i / slots;
-                if (round > 0 && !wait_for(&empty[s], (round - 1) & 1)) break;
-                const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
-                uint8_t* to = ring + s * slot_bytes;
-                ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)slot_bytes);
-                bulk_load(to, static_cast<const uint8_t*>(a.x) + row * a.x_stride * kSize, (uint32_t)row_bytes, &full[s]);
-                bulk_load(to + row_bytes, static_cast<const uint8_t*>(a.r) + row * a.r_stride * kSize,
-                          (uint32_t)row_bytes, &full[s]);
-            }
-            // (every copy is waited for by the group that takes its row, or here if that gave up)
-            for (int j = max(0, i - slots); j < i; ++j) wait_for(&full[j % slots], (j / slots) & 1);
-        }
-        return;
-    }
-    const int group = warp / (kRingThreads / 32), gt = tid - group * kRingThreads;
-    const bool f8 = a.out == KDA_DTYPE_E4M3;
-    bool ok = true;
-    for (int i = group, k = 0; i < count; i += kRingGroups, ++k) {
-        const int slot = i % slots;
-        const int64_t row = blockIdx.x + (int64_t)i * gridDim.x;
-        const uint8_t* x = ring + slot * slot_bytes;
-        ok = ok && wait_for(&full[slot], (i / slots) & 1);
-        float s[NV][8];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (gt + v * kRingThreads) * 8;
-            if (c < a.dim) {
-                float r[8];
-                load_vec<IO, 8>(x, c, s[v]);
-                load_vec<IO, 8>(x + row_bytes, c, r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[v][j] += r[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[v][j] = 0.f;
-            }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&empty[slot]);
-        float2 stat = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (gt + v * kRingThreads) * 8;
-            if (c < a.dim && a.sum && ok) store_vec<8>(a.sum, row * a.sum_stride + c, s[v], IO);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) stat.x += s[v][j] * s[v][j];
-            if (c < a.dim && a.w) {
-                float w[8];
-                if (a.w_f32) load_vec<KDA_DTYPE_F32, 8>(a.w, c, w);
-                else load_vec<IO, 8>(a.w, c, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[v][j] *= w[j];
-            }
-            if (f8) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) stat.y = max_nan(stat.y, fabsf(s[v][j]));
-            }
-        }
-        stat = team_join<32>(stat, nullptr, f8);
-        if (lane == 0) s_join[group][k & 1][gt >> 5] = stat;
-        asm volatile("barrier.cta.sync %0, %1;" ::"r"(group + 1), "n"(kRingThreads) : "memory");
-        stat = s_join[group][k & 1][0];
-#pragma unroll
-        for (int w = 1; w < kRingThreads / 32; ++w) {
-            const float2 o = s_join[group][k & 1][w];
-            stat.x += o.x;
-            stat.y = max_nan(stat.y, o.y);
-        }
-        const float rstd = 1.f / sqrtf(stat.x * a.inv_dim + a.eps);
-        float inv = 1.f;
-        if (f8) {
-            const float amax = max_nan(kAmaxFloor, stat.y * rstd);
-            inv = kE4m3Max / amax;
-            if (gt == 0 && ok) a.y_scale[row] = amax / kE4m3Max;
-        }
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (gt + v * kRingThreads) * 8;
-            if (c < a.dim && ok) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[v][j] = s[v][j] * rstd * inv;
-                store_vec<8>(a.y, row * a.dim + c, s[v], a.out);
-            }
-        }
-    }
-}
-
-template <int IO, int NV>
-cudaError_t launch_ring(const NormArgs& a, cudaStream_t s) {
-    const int slot_bytes = 2 * a.dim * (IO == KDA_DTYPE_F32 ? 4 : 2), slots = ring_slots(slot_bytes);
-    auto kern = kda_norm_ring_kernel<IO, NV>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3((unsigned)device_sm_count()), dim3(kRingAll), (size_t)(slots * slot_bytes), s, a,
-                            slots);
-}
-
-// Whether a call takes the ring: 16-byte rows long enough for a group of threads
-// and many enough for every SM's ring.
-template <int IO>
-bool ring_fits(const NormArgs& a) {
-    return a.r && a.dim > 2048 && a.dim <= 8192 && ring_slots(2 * a.dim * (IO == KDA_DTYPE_F32 ? 4 : 2)) >= kRingGroups &&
-           a.rows >= 16 * (int64_t)device_sm_count();
-}
-
-// The team for a row of `vecs` vectors.  Four 16-byte loads a thread, whatever
-// the row (two vectors of x and two of the residual, or four of x), are in flight
-// together and keep the sums short.  Measured, of the 6.67 TB/s that a copy
-// reaches: 1.07 M rows of 128 with one vector a thread 5.3 TB/s, with four 6.6;
-// 260000 rows of 512 with residual, e4m3, two vectors 6.1, four 5.4; 32768 rows
-// of 4096 without residual one vector 4.4, two 5.3, four 6.4, eight 4.8.  Few
-// rows leave most SMs idle and take the shortest path instead: one vector a
-// thread (one row of 4096: 2.6 us against 3.9).
 template <int IO, int VEC>
 cudaError_t pick(const NormArgs& a, cudaStream_t s) {
     const int vecs = (a.dim + VEC - 1) / VEC;
     auto threads = [&](int nv) { return (vecs + nv * 32 - 1) / (nv * 32) * 32; };
     if constexpr (VEC == 8) {
-        if (ring_fits<IO>(a)) {
-            if (a.dim <= 4096) return launch_ring<IO, 4>(a, s);
-            return launch_ring<IO, 8>(a, s);
-        }
         if (vecs > 32 && vecs <= 1024 && a.rows <= 2 * device_sm_count())
             return launch<IO, VEC, 1, 0>(a, threads(1), s);
         if (a.r) {
@@ -415,6 +356,8 @@ cudaError_t pick(const NormArgs& a, cudaStream_t s) {
             if (vecs <= 64) return launch<IO, VEC, 4, 16>(a, 256, s);
         }
         if (vecs <= 128) return launch<IO, VEC, 4, 32>(a, 256, s);
+        // (an fp32 vector is two loads: 16384 rows of 4096 with residual 158 us, 180 in fours)
+        if (IO == KDA_DTYPE_F32 && a.r && vecs <= 2048) return launch<IO, VEC, 2, 0>(a, threads(2), s);
         return launch<IO, VEC, 4, 0>(a, threads(4), s);
     } else {
         if (vecs <= 32) return launch<IO, VEC, 4, 8>(a, 256, s);
@@ -425,15 +368,18 @@ cudaError_t pick(const NormArgs& a, cudaStream_t s) {
     }
 }
 
-// Rows off 16 bytes.  (26000 rows of 5003, residual, e4m3: 466 us element by
-// element, 272 in vectors from the boundary before the row.)
+// Rows off 16 bytes.  (26000 rows of 5003 with residual, to e4m3: 466 us element by
+// element, 243 in vectors from the boundary before the row; to fp32, whose rows lie
+// off 16 bytes otherwise than x's, 471 us stored from where the vectors are, 233
+// through shared memory.)
 template <int IO>
 cudaError_t pick_shifted(const NormArgs& a, cudaStream_t s) {
     const int vecs = a.dim / 8 + 2;  // at most
     if (vecs <= 32) return launch<IO, 8, 4, 8, true>(a, 256, s);
+    if (vecs <= 64) return launch<IO, 8, 4, 16, true>(a, 256, s);
     if (vecs <= 128) return launch<IO, 8, 4, 32, true>(a, 256, s);
-    if (vecs <= 4096) return launch<IO, 8, 4, 0, true>(a, (vecs + 127) / 128 * 32, s);
-    return pick<IO, 1>(a, s);
+    if (vecs <= 2048) return launch<IO, 8, 4, 0, true>(a, (vecs + 127) / 128 * 32, s);
+    return launch<IO, 8, 8, 0, true>(a, (vecs + 255) / 256 * 32, s);  // (at most 4097, 544 threads)
 }
 
 }  // namespace
@@ -487,6 +433,7 @@ extern "C" kda_status kda_rms_norm(const void* x, const void* residual, const vo
     const bool shifted = !wide && dim >= 32 && (!residual || with_x(residual, a.r_stride)) &&
                          (!sum || with_x(sum, a.sum_stride));
     a.y_with_x = p.out_dtype == p.io_dtype && with_x(y, dim);
+    a.exchange = !a.y_with_x && p.out_dtype != KDA_DTYPE_E4M3;
     auto run = [&](auto io) {
         constexpr int kIo = decltype(io)::value;
         cudaStream_t s = static_cast<cudaStream_t>(stream);
