@@ -17,8 +17,8 @@
 // CTA finishing a part of the tokens.
 //
 // Bound: for few tokens HBM (w), but at these sizes the fixed parts of a call
-// weigh as much: 59 tokens x 4096 x 4096 in e4m3 with residual 6.7 us (w alone
-// 2.5), 16 tokens in bf16 9.7 (w 5.0).  One token has a kernel of its own
+// weigh as much: 59 tokens x 4096 x 4096 in e4m3 with residual 7.1 us (w alone
+// 2.5), 16 tokens in bf16 9.4 (w 5.0).  One token has a kernel of its own
 // (linear_one.cu), many have linear_wide.cu; choose() below says which and why.
 #include <cmath>
 

@@ -22,8 +22,8 @@
 //
 // Bound: the tensor cores (and, seconds long, the power limit).  A stage of 64
 // 16-bit k takes 0.316 us a pair, 2.0 PFLOP/s over 76 pairs: 32768 x 4096 x 4096
-// with silu 545 us in a burst (cuBLAS's plain product 522 to 546), 655 us kept up
-// for seconds (1.68 PFLOP/s, of 1.73 that cuBLAS keeps up); 16361 tokens in e4m3
+// with silu 545 us in a burst (cuBLAS's plain product 522 to 546), 648 us kept up
+// for seconds (1.70 PFLOP/s, of 1.73 that cuBLAS keeps up); 16361 tokens in e4m3
 // 157 us (3.5 PFLOP/s).  What it took: loads and MMAs issued by an elected lane (a
 // test of the lane number instead cost 713 us: the compiler then puts a loop
 // around every TMA and MMA instruction).

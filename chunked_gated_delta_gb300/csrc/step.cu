@@ -311,8 +311,8 @@ constexpr int kStreamThreads = (kFirstInputWarp + kInputWarps) * 32;
 constexpr int kUnits = 60;  // published units kept
 // Packed sequences are taken longest first, up to this many: the CTAs and groups
 // take units in turn, so neighbours in that order share out evenly (96 sequences
-// of 0 to 5 tokens in their own order: 45.6 us, the last group 1.7 times the
-// mean; sorted: 40.7).  More sequences even out by their number.
+// of 0 to 5 tokens in their own order: 31.8 us, the last group 1.7 times the
+// mean; sorted: 30.1).  More sequences even out by their number.
 constexpr int kMostSorted = 512;
 // Tokens of a sequence (of all, where packed) that the streaming kernel takes: a
 // few tenths of a second at most, well under what its waits allow.
