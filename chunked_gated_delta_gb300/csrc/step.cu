@@ -495,9 +495,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1) kda_step_stream_kernel(cons
                 const int slot = here && a.slots ? a.slots[n] : n;
                 bool taken = false;
                 if (a.slots) {
-                    const int most = __reduce_max_sync(~0u, unit.len > 0 && slot >= 0 ? n : 0);
+                    // 128 earlier slots at a time, handed round by shuffles: one after the
+                    // other they are loads to wait for, while no state is asked for
+                    const int most = __reduce_max_sync(~0u, here ? n : 0);
+                    for (int j0 = 0; j0 < most; j0 += 128) {
+                        int others[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) others[i] = j0 + 32 * i + lane < most ? a.slots[j0 + 32 * i + lane] : -1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (j0 + 32 * i >= most) break;
 #pragma unroll 8
-                    for (int j = 0; j < most; ++j) taken |= a.slots[j] == slot && j < n;
+                            for (int l = 0; l < 32; ++l)
+                                taken |= __shfl_sync(~0u, others[i], l) == slot && j0 + 32 * i + l < n;
+                        }
+                    }
                 }
                 const bool refused = unit.len > 0 && (slot < 0 || slot >= a.num_slots || taken);
                 if (refused) {
