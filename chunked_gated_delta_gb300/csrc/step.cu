@@ -20,7 +20,7 @@
 // From two pairs per SM on the streaming kernel below takes over.  Measured at
 // K = V = 128 in fp32, this kernel against that one: 32 pairs 2.9 us, 5.0;
 // 128 pairs 4.3, 5.4; 256 pairs 9.7, 10.5; 512 pairs 17, 14; 16384 pairs 490,
-// 350 (6.1 TB/s, 92% of what a copy reaches).
+// 341 (6.3 TB/s, 94% of what a copy reaches).
 #include "internal.h"
 #include "layer_ops.cuh"
 #include "waits.cuh"
