@@ -5,7 +5,8 @@ input to its output, for a prompt (kda.fwd) and for new tokens (kda.step).
                 -> linear x 5: q, k, v (silu), g (log-sigmoid, fp32, biased), beta (sigmoid)
                 -> rms_norm of the heads of q and k (unit length)
                 -> fwd | step
-                -> rms_norm of the heads of o -> linear, the residual added
+                -> rms_norm of the heads of o (with e4m3 operands then to 8 bits, a scale a token)
+                -> linear, the residual added
 
 Shapes: x [B, T, D] (or one packed row [1, total, D] with cu_seqlens), hidden
 size D, H heads of K (q, k, g) and V (v, o).  The weights are those of a model
@@ -20,6 +21,9 @@ import torch
 from . import binding as kda
 
 _F8 = torch.float8_e4m3fn
+# rms_norm with these two only turns rows into 8 bits: beside 2^100 the mean square of a row is below the last bit
+# (as long as its elements are below 2^37), so the division is by 2^50, and the weight's 2^50 takes it back, both exactly.
+_NO_NORM_EPS, _NO_NORM_WEIGHT = 2.0 ** 100, 2.0 ** 50
 
 
 def quantise_rows(w):
@@ -50,6 +54,7 @@ class KdaLayer:
         self.eight_bit = q.w.dtype == _F8
         # rms_norm over a head times K^-1/2 is division by the head's length
         self.unit = torch.full((K,), K ** -0.5, dtype=torch.float32, device=norm.device)
+        self.no_norm = torch.full((heads * V,), _NO_NORM_WEIGHT, dtype=torch.float32, device=norm.device)
 
     @classmethod
     def random(cls, D, heads, K, V, eight_bit=False, seed=0, device="cuda", dtype=torch.bfloat16):
@@ -84,8 +89,8 @@ class KdaLayer:
         B, T, H, V = o.shape
         n, _, _ = kda.rms_norm(o, self.head_norm, eps=self.eps)
         n, scale = n.view(B, T, H * V), None
-        if self.eight_bit:  # one scale per token for the projection's operand
-            n, scale, _ = kda.rms_norm(n, None, eps=self.eps, out_dtype=_F8)
+        if self.eight_bit:  # one scale per token for the projection's operand, which is not normed again
+            n, scale, _ = kda.rms_norm(n, self.no_norm, eps=_NO_NORM_EPS, out_dtype=_F8)
         return self.out(n, scale, residual=total, out_dtype=total.dtype)
 
     def prefill(self, x, residual=None, h0=None, cu_seqlens=None, workspace=None):
