@@ -90,27 +90,43 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 
 // exp(-|v|) to about 2^-22: 2^t with t = -|v| log2 e in fp32, times one plus what
 // that product lost (its rounding and the rest of log2 e) times ln 2.  Below
-// exp(-104) it is zero.
-__device__ __forceinline__ float exp_minus_abs(float v) {
+// 2^-126 (|v| > 87.3) it is zero.  With `back`, exp(-|v|) is the result times
+// *back, 2^-64 where t < -64 (adding 64 to such a t is exact), so a product with
+// it can be right where exp(-|v|) by itself is too small.
+__device__ __forceinline__ float exp_minus_abs(float v, float* back = nullptr) {
     constexpr float kLog2e = 1.44269504f, kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.693147181f;
-    const float x = fmaxf(-fabsf(v), -104.f), t = x * kLog2e;
+    const float x = fmaxf(-fabsf(v), -200.f);
+    float t = x * kLog2e;
     const float lost = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+    if (back) {
+        const bool deep = t < -64.f;
+        *back = deep ? 0x1p-64f : 1.f;
+        t = deep ? t + 64.f : t;
+    }
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
     return fmaf(e * kLn2, lost, e);
 }
 // FAST: y has 16 bits, whose rounding (2^-9 or 2^-12) hides the approximate
-// exponential's error, which grows with |v|; else the results are within about
-// 2^-21 (all the epilogue's threads do this for every element, so the library's
-// exact forms would hold up the tiles behind).
+// exponential's error, which grows with |v|; SiLU below v = -87 (1e-36 in size)
+// is zero then.  Else SiLU, sigmoid and log-sigmoid are within about 2^-21 of
+// themselves (and zero below 2^-126 at the latest), GELU within 2^-22 |v|, as
+// 1 + erf gives it: all the epilogue's threads do this for every element, so the
+// library's exact forms would hold up the tiles behind.
 template <int ACT, bool FAST>
 __device__ __forceinline__ float activated(float v) {
     if constexpr (ACT == KDA_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
     if constexpr (ACT == KDA_ACT_SILU || ACT == KDA_ACT_SIGMOID) {
-        const float one = ACT == KDA_ACT_SILU ? v : 1.f;
-        if constexpr (FAST) return __fdividef(one, 1.f + __expf(-v));
-        const float e = exp_minus_abs(v);
-        const float y = __fdividef(v < 0.f ? one * e : one, 1.f + e);
+        if constexpr (FAST) return __fdividef(ACT == KDA_ACT_SILU ? v : 1.f, 1.f + __expf(-v));
+        float y;
+        if constexpr (ACT == KDA_ACT_SILU) {  // v exp(v) is a normal number down to -92, exp(v) to -87
+            float back;
+            const float e = exp_minus_abs(v, &back);
+            y = __fdividef(v < 0.f ? v * e : v, fmaf(e, back, 1.f)) * (v < 0.f ? back : 1.f);
+        } else {
+            const float e = exp_minus_abs(v);
+            y = __fdividef(v < 0.f ? e : 1.f, 1.f + e);
+        }
         return v == v ? y : v;
     }
     if constexpr (ACT == KDA_ACT_LOGSIGMOID) {

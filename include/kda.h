@@ -456,6 +456,9 @@ kda_status kda_rms_norm(const void* x, const void* residual, const void* weight,
  *             with the same stride
  *   act       KDA_ACT_*: SILU v sigmoid(v); GELU v Phi(v) (the error function's
  *             form); SIGMOID (beta); LOGSIGMOID log(sigmoid(v)) (the decay g, in fp32)
+ *             Beside the rounding to out_dtype they are right to about 2^-21 of
+ *             themselves (GELU to 2^-22 |v|; 16-bit outputs to a quarter of their
+ *             last bit); results below 1.2e-38, SiLU to 16 bits below 1.2e-36, may be zero.
  *   *_stride  elements between rows (0: contiguous)
  *   status_word  device int32 or NULL, as in kda_step: KDA_ERR_TIMEOUT if a
  *             pipeline wait ran out (y is then incomplete)
