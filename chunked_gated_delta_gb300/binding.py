@@ -416,7 +416,8 @@ def bwd_dh(scale, do, dv_in, dht, dims: Dims, workspace, want_dhck=True, want_dh
 # ----------------------------------------------------------------- the served layer's operators
 # A decode step calls these once per layer and token, at a few microseconds of
 # kernel time each: their checks and marshalling are in the compiled extension
-# (csrc_torch/layer_calls.cpp).
+# (csrc_torch/layer_calls.cpp).  With ``stream`` they run and allocate their
+# outputs there, as under ``torch.cuda.stream(stream)``.
 _calls = None
 
 

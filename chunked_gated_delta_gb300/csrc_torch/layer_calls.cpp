@@ -18,6 +18,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <optional>
 #include <string>
 
 #include "../../include/kda.h"
@@ -99,16 +100,31 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& 
     return at::Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
 
-// The caller's stream, or the current one of the tensors' device.
-void* stream_of(PyObject* stream, const at::Tensor& t) {
-    if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-    PyObject* handle = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!handle) throw Refused{nullptr, ""};
-    void* p = PyLong_AsVoidPtr(handle);
-    Py_DECREF(handle);
-    if (PyErr_Occurred()) throw Refused{nullptr, ""};
-    return p;
-}
+// The device of a call and the stream that it runs on (the caller's, or the current
+// one).  While this lives both are the current ones, so outputs are allocated for
+// the stream that writes them: memory freed with work still pending on another
+// stream is not given to this one, nor an output that is dropped to another.
+class Place {
+  public:
+    Place(PyObject* stream, const at::Tensor& t) : device_(t.device()) {
+        if (stream == Py_None) {
+            stream_ = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+            return;
+        }
+        PyObject* handle = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!handle) throw Refused{nullptr, ""};
+        stream_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(handle));
+        Py_DECREF(handle);
+        if (PyErr_Occurred()) throw Refused{nullptr, ""};
+        given_.emplace(c10::cuda::getStreamFromExternal(stream_, t.get_device()));
+    }
+    void* stream() const { return stream_; }
+
+  private:
+    c10::cuda::CUDAGuard device_;
+    std::optional<c10::cuda::CUDAStreamGuard> given_;
+    cudaStream_t stream_;
+};
 double number(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
@@ -204,13 +220,13 @@ PyObject* call_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         o.beta_stride = token_stride("beta", beta);
         const kda_dims d{(int32_t)B, (int32_t)T, (int32_t)H, (int32_t)K, (int32_t)V, (int32_t)N};
         const float scale = a[7] == Py_None ? 1.f / std::sqrt((float)K) : (float)number(a[7]);
-        c10::cuda::CUDAGuard device(q.device());
+        const Place place(a[11], q);
         at::Tensor made;
         if (!out) made = empty(v.sizes(), io, q);
         check(kda_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const float*>(g.data_ptr()),
                        beta.data_ptr(), scale, state.data_ptr(), static_cast<const int32_t*>(address(slots)),
                        static_cast<const int32_t*>(address(cu)), out ? out->data_ptr() : made.data_ptr(), &d, &o,
-                       status_word(status), stream_of(a[11], q)),
+                       status_word(status), place.stream()),
               "kda_step");
         return kept(a[9], std::move(made));
     });
@@ -247,7 +263,7 @@ PyObject* call_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         o.x_stride = row_stride("x", x, dim);
         o.residual_stride = residual ? row_stride("residual", *residual, dim) : 0;
         o.sum_stride = sum ? row_stride("residual_out", *sum, dim) : 0;
-        c10::cuda::CUDAGuard device(x.device());
+        const Place place(a[7], x);
         at::Tensor made, made_sum, scale;
         if (!out) made = empty(x.sizes(), to, x);
         if (residual && !sum) made_sum = empty(x.sizes(), io, x);
@@ -256,7 +272,7 @@ PyObject* call_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check(kda_rms_norm(x.data_ptr(), address(residual), address(weight), out ? out->data_ptr() : made.data_ptr(),
                            scale.defined() ? static_cast<float*>(scale.data_ptr()) : nullptr,
                            sum ? sum->data_ptr() : made_sum.defined() ? made_sum.data_ptr() : nullptr,
-                           dim ? x.numel() / dim : 0, dim, &o, stream_of(a[7], x)),
+                           dim ? x.numel() / dim : 0, dim, &o, place.stream()),
               "kda_rms_norm");
         PyObject* y = kept(a[5], std::move(made));
         PyObject* ys = scale.defined() ? THPVariable_Wrap(std::move(scale)) : (Py_INCREF(Py_None), Py_None);
@@ -321,13 +337,13 @@ PyObject* call_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
         o.w_stride = row_stride("w", w, K);
         o.residual_stride = residual ? row_stride("residual", *residual, N) : 0;
         o.y_stride = out ? row_stride("out", *out, N) : 0;
-        c10::cuda::CUDAGuard device(x.device());
+        const Place place(a[10], x);
         at::Tensor made;
         if (!out) made = empty(shape, to, x);
         check(kda_linear(x.data_ptr(), w.data_ptr(), static_cast<const float*>(address(bias)), address(residual),
                          static_cast<const float*>(address(xs)), static_cast<const float*>(address(ws)),
                          out ? out->data_ptr() : made.data_ptr(), K ? x.numel() / K : 0, N, K, &o, status_word(status),
-                         stream_of(a[10], x)),
+                         place.stream()),
               "kda_linear");
         return kept(a[8], std::move(made));
     });
