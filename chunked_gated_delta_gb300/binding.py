@@ -188,6 +188,14 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def on_stream(stream):
+    """The caller's stream (None: the current one) as the current one, so that what a
+    call allocates and fills for its kernels belongs to the stream that they run on."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _check(rc, where):
     if rc != KDA_OK:
         raise KdaError(rc, where)
@@ -257,13 +265,14 @@ def fwd(q, k, v, g, beta, scale=None, h0=None, cu_seqlens=None, output_final_sta
     opts = FwdOpts(IO_F16 if q.dtype == torch.float16 else IO_BF16,
                    STATE_BF16 if state_dtype == torch.bfloat16 else STATE_F32,
                    1 if beta_logits else 0, Hqk if Hqk != H else 0, PLANS[plan])
-    if workspace is None:
-        workspace = new_workspace(dims, q.device)
-    o = out if out is not None else torch.empty((B, T, H, V), dtype=q.dtype, device=q.device)
-    ht = None
-    if output_final_state:
-        ht = final_state if final_state is not None else torch.empty((N, H, K, V), dtype=state_dtype,
-                                                                      device=q.device)
+    with on_stream(stream):
+        if workspace is None:
+            workspace = new_workspace(dims, q.device)
+        o = out if out is not None else torch.empty((B, T, H, V), dtype=q.dtype, device=q.device)
+        ht = None
+        if output_final_state:
+            ht = final_state if final_state is not None else torch.empty((N, H, K, V), dtype=state_dtype,
+                                                                          device=q.device)
     rc = lib.kda_fwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(h0),
                         _ptr(cu_seqlens), _ptr(o), _ptr(ht), ctypes.byref(dims), ctypes.byref(opts),
                         _ptr(workspace), workspace.numel(), _stream_handle(stream))
@@ -294,9 +303,10 @@ def state_map(q, k, v, g, beta, cu_seqlens=None, workspace=None, stream=None):
         raise TypeError("state_map takes the default interface (bf16 I/O, equal heads)")
     dims, N = _dims_of(q, v, cu_seqlens)
     K, V, H = q.shape[-1], v.shape[-1], v.shape[2]
-    if workspace is None:
-        workspace = new_workspace(dims, q.device)
-    pq = torch.empty((N, H, K, K + V), dtype=torch.float32, device=q.device)
+    with on_stream(stream):
+        if workspace is None:
+            workspace = new_workspace(dims, q.device)
+        pq = torch.empty((N, H, K, K + V), dtype=torch.float32, device=q.device)
     rc = load_library().kda_fwd_state_map(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(pq),
                                           ctypes.byref(dims), _ptr(workspace), workspace.numel(),
                                           _stream_handle(stream))
@@ -315,7 +325,8 @@ def chain_states(pq_all, h0=None, stream=None):
     if h0 is not None and (h0.dtype != torch.float32 or not h0.is_cuda or not h0.is_contiguous()
                            or tuple(h0.shape) != (N, H, K, V)):
         raise TypeError("h0 must be a contiguous CUDA float32 tensor [N, H, K, V]")
-    h_in = torch.empty((R, N, H, K, V), dtype=torch.float32, device=pq_all.device)
+    with on_stream(stream):
+        h_in = torch.empty((R, N, H, K, V), dtype=torch.float32, device=pq_all.device)
     rc = load_library().kda_chain_states(_ptr(pq_all), _ptr(h0), _ptr(h_in), R, N, H, K, V, _stream_handle(stream))
     _check(rc, "kda_chain_states")
     return h_in
@@ -372,7 +383,8 @@ def fwd_noalloc(q, k, v, g, beta, scale, h0, cu_seqlens, o, ht, stream=None):
 def selftest_wait_timeout(limit_ns: int = 1_000_000, stream=None) -> int:
     """Run the bounded-wait self-check; returns the status code (6 = timed out as designed)."""
     import torch
-    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with on_stream(stream):
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
     return int(load_library().kda_selftest_wait_timeout(_ptr(word), int(limit_ns), _stream_handle(stream)))
 
 
@@ -401,9 +413,10 @@ def bwd_dh(scale, do, dv_in, dht, dims: Dims, workspace, want_dhck=True, want_dh
     N = dims.num_seqs if dims.num_seqs > 0 else dims.B
     lay = workspace_layout(dims)
     dev = do.device
-    dhck = torch.empty((lay.max_chunks, H, K, V), dtype=torch.bfloat16, device=dev) if want_dhck else None
-    dv2 = torch.zeros((B, T, H, V), dtype=io, device=dev)
-    dh0 = torch.empty((N, H, K, V), dtype=state_dtype, device=dev) if want_dh0 else None
+    with on_stream(stream):
+        dhck = torch.empty((lay.max_chunks, H, K, V), dtype=torch.bfloat16, device=dev) if want_dhck else None
+        dv2 = torch.zeros((B, T, H, V), dtype=io, device=dev)
+        dh0 = torch.empty((N, H, K, V), dtype=state_dtype, device=dev) if want_dh0 else None
     opts = FwdOpts(IO_F16 if io == torch.float16 else IO_BF16,
                    STATE_BF16 if state_dtype == torch.bfloat16 else STATE_F32, 0, 0)
     rc = load_library().kda_bwd_dh_ex(float(scale), _ptr(do), _ptr(dv_in), _ptr(dht), _ptr(dhck), _ptr(dv2),

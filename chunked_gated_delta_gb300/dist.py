@@ -138,9 +138,9 @@ def fwd_shard(sh: Shard, q, k, v, g, beta, scale=None, h0=None, cu_seqlens=None,
     """The forward (the library's kda_fwd through the binding) on this rank's
     block; returns the block's (o, ht)."""
     from . import binding
-    lq, lk, lv, lg, lb, lh0, lcu = take_shard(sh, q, k, v, g, beta, h0, cu_seqlens)
-    return binding.fwd(lq, lk, lv, lg, lb, scale, h0=lh0, cu_seqlens=lcu, output_final_state=output_final_state,
-                       stream=stream)
+    with binding.on_stream(stream):  # (the copies that take_shard makes are the forward's inputs)
+        lq, lk, lv, lg, lb, lh0, lcu = take_shard(sh, q, k, v, g, beta, h0, cu_seqlens)
+        return binding.fwd(lq, lk, lv, lg, lb, scale, h0=lh0, cu_seqlens=lcu, output_final_state=output_final_state)
 
 
 def place_shard(sh: Shard, o_local, ht_local, o, ht=None):
@@ -187,12 +187,13 @@ def context_parallel_finish(pq_all, rank: int, workspace, dims, scale, h0=None, 
     rank, the sequences' final state)."""
     import torch
     from . import binding
-    h_in = binding.chain_states(pq_all, h0, stream=stream)
-    R, N, H, K, KV = pq_all.shape
-    V = KV - K
-    o = torch.empty((dims.B, dims.T, H, V), dtype=torch.bfloat16, device=pq_all.device)
-    ht = torch.empty((N, H, K, V), dtype=torch.float32, device=pq_all.device) if output_final_state else None
-    binding.fwd_scan(scale, h_in[rank], o, ht, dims, workspace, stream)
+    with binding.on_stream(stream):
+        h_in = binding.chain_states(pq_all, h0)
+        R, N, H, K, KV = pq_all.shape
+        V = KV - K
+        o = torch.empty((dims.B, dims.T, H, V), dtype=torch.bfloat16, device=pq_all.device)
+        ht = torch.empty((N, H, K, V), dtype=torch.float32, device=pq_all.device) if output_final_state else None
+        binding.fwd_scan(scale, h_in[rank], o, ht, dims, workspace)
     return o, ht
 
 
@@ -205,9 +206,11 @@ def fwd_context_parallel(q, k, v, g, beta, scale=None, h0=None, cu_seqlens=None,
     (o, ht) as :func:`context_parallel_finish`."""
     import torch
     import torch.distributed as tdist
+    from . import binding
     rank, world = tdist.get_rank(group), tdist.get_world_size(group)
     scale = q.shape[-1] ** -0.5 if scale is None else scale
-    pq, ws, dims = context_parallel_maps(q, k, v, g, beta, cu_seqlens, stream)
-    parts = [torch.empty_like(pq) for _ in range(world)]
-    tdist.all_gather(parts, pq, group=group)
-    return context_parallel_finish(torch.stack(parts), rank, ws, dims, scale, h0, stream=stream)
+    with binding.on_stream(stream):  # (the exchange waits for the maps, and the scan for the exchange)
+        pq, ws, dims = context_parallel_maps(q, k, v, g, beta, cu_seqlens)
+        parts = [torch.empty_like(pq) for _ in range(world)]
+        tdist.all_gather(parts, pq, group=group)
+        return context_parallel_finish(torch.stack(parts), rank, ws, dims, scale, h0)
