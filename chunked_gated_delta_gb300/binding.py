@@ -464,6 +464,7 @@ def step(q, k, v, g, beta, state, slots=None, scale=None, cu_seqlens=None, out=N
     the device, the state of each sequence (negative: padding, o is zero), or
     None for slot n.  ``status``: an int32 CUDA tensor that starts at zero and
     takes the errors found in slots and cu_seqlens; ``binding.status`` reads it.
+    All tensors, and ``stream``, are of one GPU; o is allocated for ``stream``.
     """
     return (_calls or _layer_calls()).step(q, k, v, g, beta, state, slots, scale,
                                            cu_seqlens, out, status, stream, beta_logits)
@@ -479,7 +480,8 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, out_dtype=None, out=None, 
     out_dtype: x's (default), float32 or float8_e4m3fn; the last stores codes
     with one fp32 scale per row, y ~ codes * y_scale[..., None] (y_scale is None
     otherwise).  s, in x's dtype, is returned when there is a residual (else
-    None); ``residual_out`` takes it and may be ``residual`` itself.
+    None); ``residual_out`` takes it and may be ``residual`` itself.  Tensors and
+    ``stream``: as in step.
     """
     return (_calls or _layer_calls()).rms_norm(x, weight, residual, eps, out_dtype, out, residual_out, stream)
 
@@ -494,7 +496,7 @@ def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None,
     w_scale: fp32 [N], with float8 only; bias: fp32 [N]; residual: [..., N] of
     out_dtype.  out_dtype: bf16, fp16 or float32; defaults to x's dtype, bf16
     for float8.  act: None, "silu", "gelu", "sigmoid" or "logsigmoid".  ``out``
-    may be ``residual`` itself.  ``status``: as in step.
+    may be ``residual`` itself.  ``status``, ``stream``: as in step.
     """
     return (_calls or _layer_calls()).linear(x, w, bias, act, residual,
                                              x_scale, w_scale, out_dtype, out, status, stream)

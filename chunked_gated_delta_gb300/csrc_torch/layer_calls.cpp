@@ -47,6 +47,12 @@ bool same_shape(const at::Tensor& t, std::initializer_list<int64_t> shape) {
     return t.sizes() == at::IntArrayRef(shape.begin(), shape.size());
 }
 
+// A tensor of another GPU would reach the kernel as an address of this one.
+void need_one_device(const at::Tensor& first, std::initializer_list<const at::Tensor*> others) {
+    for (const at::Tensor* t : others)
+        need(!t || t->device() == first.device(), "all tensors must be on one device");
+}
+
 // Elements between consecutive token rows of [B, T, ...] (0: contiguous).
 int64_t token_stride(const char* name, const at::Tensor& t) {
     if (t.is_contiguous()) return 0;
@@ -106,7 +112,7 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& 
 // stream is not given to this one, nor an output that is dropped to another.
 class Place {
   public:
-    Place(PyObject* stream, const at::Tensor& t) : device_(t.device()) {
+    Place(PyObject* stream, const at::Tensor& t) : device_(checked(stream, t)) {
         if (stream == Py_None) {
             stream_ = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
             return;
@@ -121,6 +127,17 @@ class Place {
     void* stream() const { return stream_; }
 
   private:
+    static c10::Device checked(PyObject* stream, const at::Tensor& t) {
+        if (stream != Py_None) {
+            PyObject* index = PyObject_GetAttrString(stream, "device_index");
+            if (!index) throw Refused{nullptr, ""};
+            const long i = PyLong_AsLong(index);
+            Py_DECREF(index);
+            if (PyErr_Occurred()) throw Refused{nullptr, ""};
+            need(i == t.get_device(), "stream must be of the tensors' device");
+        }
+        return t.device();
+    }
     c10::cuda::CUDAGuard device_;
     std::optional<c10::cuda::CUDAStreamGuard> given_;
     cudaStream_t stream_;
@@ -204,6 +221,7 @@ PyObject* call_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
              "step takes CUDA tensors");
         need(!out || (out->scalar_type() == io && out->sizes() == v.sizes() && out->is_cuda() && out->is_contiguous()),
              "out must be a contiguous CUDA tensor of v's shape and dtype");
+        need_one_device(q, {&k, &v, &g, &beta, &state, slots, cu, out, status});
         kda_step_opts o{};
         o.io_dtype = io == at::kHalf ? KDA_IO_F16 : KDA_IO_BF16;
         o.state_dtype = s16 ? KDA_STATE_BF16 : KDA_STATE_F32;
@@ -255,6 +273,7 @@ PyObject* call_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
              "residual_out must be a CUDA tensor of x's shape and dtype");
         need(!out || (out->scalar_type() == to && out->sizes() == x.sizes() && out->is_cuda() && out->is_contiguous()),
              "out must be a contiguous CUDA tensor of x's shape and out_dtype");
+        need_one_device(x, {weight, residual, out, sum});
         kda_norm_opts o{};
         o.io_dtype = dtype_code(io);
         o.out_dtype = dtype_code(to);
@@ -331,6 +350,7 @@ PyObject* call_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
              "residual must be a CUDA tensor [..., N] of out_dtype");
         need(!out || (out->scalar_type() == to && out->sizes() == at::IntArrayRef(shape) && out->is_cuda()),
              "out must be a CUDA tensor [..., N] of out_dtype");
+        need_one_device(x, {&w, bias, residual, xs, ws, out, status});
         o.io_dtype = dtype_code(io);
         o.out_dtype = dtype_code(to);
         o.x_stride = row_stride("x", x, K);
