@@ -39,9 +39,9 @@ class Projection:
     scale: torch.Tensor | None = None
     bias: torch.Tensor | None = None
 
-    def __call__(self, x, x_scale, act=None, residual=None, out_dtype=None):
+    def __call__(self, x, x_scale, act=None, residual=None, out_dtype=None, status=None):
         return kda.linear(x, self.w, bias=self.bias, act=act, residual=residual, x_scale=x_scale, w_scale=self.scale,
-                          out_dtype=out_dtype)
+                          out_dtype=out_dtype, status=status)
 
 
 class KdaLayer:
@@ -75,32 +75,35 @@ class KdaLayer:
         """The rows as the projections take them: (codes, scales) or (16 bits, None), and the residual's sum."""
         return kda.rms_norm(x, weight, residual=residual, eps=self.eps, out_dtype=_F8 if self.eight_bit else None)
 
-    def _inputs(self, x, residual):
+    def _inputs(self, x, residual, status):
         B, T, _ = x.shape
         H, io = self.heads, x.dtype
         n, scale, total = self._norm(x, self.norm, residual)
-        q, k, v = (p(n, scale, act="silu", out_dtype=io).view(B, T, H, -1) for p in (self.q, self.k, self.v))
-        g = self.g(n, scale, act="logsigmoid", out_dtype=torch.float32).view(B, T, H, self.K)
-        beta = self.beta(n, scale, act="sigmoid", out_dtype=io)
+        q, k, v = (p(n, scale, act="silu", out_dtype=io, status=status).view(B, T, H, -1)
+                   for p in (self.q, self.k, self.v))
+        g = self.g(n, scale, act="logsigmoid", out_dtype=torch.float32, status=status).view(B, T, H, self.K)
+        beta = self.beta(n, scale, act="sigmoid", out_dtype=io, status=status)
         q, k = (kda.rms_norm(t, self.unit, eps=self.eps)[0] for t in (q, k))
         return (q, k, v, g, beta), x if total is None else total
 
-    def _output(self, o, total):
+    def _output(self, o, total, status=None):
         B, T, H, V = o.shape
         n, _, _ = kda.rms_norm(o, self.head_norm, eps=self.eps)
         n, scale = n.view(B, T, H * V), None
         if self.eight_bit:  # one scale per token for the projection's operand, which is not normed again
             n, scale, _ = kda.rms_norm(n, self.no_norm, eps=_NO_NORM_EPS, out_dtype=_F8)
-        return self.out(n, scale, residual=total, out_dtype=total.dtype)
+        return self.out(n, scale, residual=total, out_dtype=total.dtype, status=status)
 
-    def prefill(self, x, residual=None, h0=None, cu_seqlens=None, workspace=None):
-        """Prompts: (y [B, T, D], the states [N, H, K, V] after them).  y holds x + residual + the layer's output."""
-        inputs, total = self._inputs(x, residual)
+    def prefill(self, x, residual=None, h0=None, cu_seqlens=None, workspace=None, status=None):
+        """Prompts: (y [B, T, D], the states [N, H, K, V] after them).  y holds x + residual + the layer's output.
+        ``status`` takes the projections' errors (see kda.step); the forward's are in ``workspace`` (kda.status)."""
+        inputs, total = self._inputs(x, residual, status)
         o, state = kda.fwd(*inputs, h0=h0, cu_seqlens=cu_seqlens, workspace=workspace)
-        return self._output(o, total), state
+        return self._output(o, total, status), state
 
     def decode(self, x, state, slots=None, residual=None, cu_seqlens=None, status=None):
-        """New tokens: y [B, T, D]; the cache of states [slots, H, K, V] is updated in place (see kda.step)."""
-        inputs, total = self._inputs(x, residual)
+        """New tokens: y [B, T, D]; the cache of states [slots, H, K, V] is updated in place (see kda.step).
+        ``status`` takes the errors of the step and of the projections."""
+        inputs, total = self._inputs(x, residual, status)
         o = kda.step(*inputs, state, slots=slots, cu_seqlens=cu_seqlens, status=status)
-        return self._output(o, total)
+        return self._output(o, total, status)

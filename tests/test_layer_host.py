@@ -72,3 +72,18 @@ def test_eight_bit_output_is_the_sixteen_bit_formula(ops, head_norm, size):
     n = od / torch.sqrt(od.square().mean(-1, keepdim=True) + m.eps) * m.head_norm.double()
     ref = n.reshape(3, 5, H * V) @ (m.out.w.double() * m.out.scale.double()[:, None]).T
     assert (y - ref).norm() <= 0.05 * ref.norm()
+
+
+@pytest.mark.parametrize("eight_bit", [False, True])
+@pytest.mark.parametrize("path", ["prefill", "decode"])
+def test_every_projection_reports_to_the_status_word(ops, path, eight_bit):
+    m = layer.KdaLayer.random(128, 2, 64, 64, eight_bit=eight_bit, seed=1, device="cpu")
+    x = torch.randn((2, 3, 128), generator=torch.Generator().manual_seed(4)).bfloat16()
+    word = torch.zeros(1, dtype=torch.int32)
+    if path == "prefill":
+        m.prefill(x, status=word)
+    else:
+        m.decode(x, torch.zeros((2, 2, 64, 64)), status=word)
+    takes = [(name, status) for name, status in ops.calls if name in ("linear", "step")]
+    assert [name for name, _ in takes].count("linear") == 6
+    assert all(status is word for _, status in takes)
