@@ -7,7 +7,9 @@ are linked into ``chunked_gated_delta_gb300/libkda.so``.  The extension
 (``csrc_torch/layer_calls.cpp``: the Python calls of the served layer's
 operators, on torch's tensors) is compiled beside them against torch's headers
 and linked to the library.  The build is skipped when both are newer than every
-source and header.
+source and header.  The library does not need torch: without it only the library
+is built, and an extension that fails to compile is reported after the library is
+there.
 """
 from __future__ import annotations
 
@@ -48,10 +50,19 @@ def _inputs() -> list[str]:
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [CSRC_TORCH, os.path.abspath(__file__)])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXTENSION):
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXTENSION))
+    return True
+
+
+def up_to_date() -> bool:
+    built = [LIB, EXTENSION] if _have_torch() else [LIB]
+    if not all(os.path.exists(p) for p in built):
+        return False
+    t = min(os.path.getmtime(p) for p in built)
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -111,16 +122,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        extension = ex.submit(_compile_extension)
+        extension = ex.submit(_compile_extension) if _have_torch() else None
         objs = list(ex.map(compile_one, srcs))
-        extension = extension.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of libkda.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_extension(extension)
+    if extension is not None:
+        _link_extension(extension.result())
     return LIB
 
 
