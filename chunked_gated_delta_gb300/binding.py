@@ -443,6 +443,8 @@ def _layer_calls():
         path = _build.EXTENSION
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing; run chunked_gated_delta_gb300.build.build()")
+        if not _build.extension_matches():
+            raise RuntimeError(f"{path} was built for another torch or Python; run chunked_gated_delta_gb300.build.build()")
         loader = importlib.machinery.ExtensionFileLoader("_layer_calls", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_layer_calls", loader))
         loader.exec_module(module)

@@ -7,9 +7,9 @@ are linked into ``chunked_gated_delta_gb300/libkda.so``.  The extension
 (``csrc_torch/layer_calls.cpp``: the Python calls of the served layer's
 operators, on torch's tensors) is compiled beside them against torch's headers
 and linked to the library.  The build is skipped when both are newer than every
-source and header.  The library does not need torch: without it only the library
-is built, and an extension that fails to compile is reported after the library is
-there.
+source and header, and the extension is this interpreter's and its torch's.  The
+library does not need torch: without it only the library is built, and an
+extension that fails to compile is reported after the library is there.
 """
 from __future__ import annotations
 
@@ -28,6 +28,8 @@ CSRC_TORCH = os.path.join(PKG, "csrc_torch", "layer_calls.cpp")
 LIB = os.path.join(PKG, "libkda.so")
 EXTENSION = os.path.join(PKG, "_layer_calls.so")
 OBJDIR = os.path.join(PKG, "_build")
+# What the extension was built against: it reads torch's C++ objects, whose layout is its version's own.
+BUILT_FOR = os.path.join(OBJDIR, "layer_calls.built_for")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -58,9 +60,24 @@ def _have_torch() -> bool:
     return True
 
 
+def _interpreter() -> str:
+    """This interpreter and its torch."""
+    import torch
+    return f"torch {torch.__version__} in {os.path.dirname(torch.__file__)}, Python {sysconfig.get_config_var('SOABI')}\n"
+
+
+def extension_matches() -> bool:
+    """Whether the extension was built for this interpreter and its torch."""
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read() == _interpreter()
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
     built = [LIB, EXTENSION] if _have_torch() else [LIB]
-    if not all(os.path.exists(p) for p in built):
+    if not all(os.path.exists(p) for p in built) or (len(built) > 1 and not extension_matches()):
         return False
     t = min(os.path.getmtime(p) for p in built)
     return all(os.path.getmtime(p) <= t for p in _inputs())
@@ -100,7 +117,11 @@ def _link_extension(obj: str) -> None:
     _run([_host_compiler(), "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + lib,
           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib],
          "linking the Python extension")
+    if os.path.exists(BUILT_FOR):
+        os.remove(BUILT_FOR)
     os.replace(tmp, EXTENSION)
+    with open(BUILT_FOR, "w") as f:
+        f.write(_interpreter())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
