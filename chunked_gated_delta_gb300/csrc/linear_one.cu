@@ -11,9 +11,11 @@
 // k (fewer rows where N is small, to have CTAs for every SM); the shares are
 // joined through shared memory in order.
 //
-// Measured (bf16; the tensor-core kernel in brackets): 4096 x 4096 7.3 us (9.1),
-// 4.6 TB/s; 2048 x 2048 2.8 (4.8); 32 x 4096 2.3 (4.3).  For two tokens the same
-// scheme took 10.8 us against 9.1, so it ends at one.
+// Measured over weights that L2 does not hold (bf16; the tensor-core kernel in
+// brackets): 4096 x 4096 7.2 us (9.1), 4.7 TB/s, and 6.6 us a call where a part
+// of w is still in L2; 2048 x 2048 2.6 (4.8); 32 x 4096 2.3 (4.3).  In e4m3 4096 x
+// 4096 takes 5.7 us: half the bytes, and as many conversions and products.  For
+// two tokens the same scheme took 10.8 us against 9.1, so it ends at one.
 #include "linear.cuh"
 
 namespace kda {

@@ -22,8 +22,8 @@
 //
 // Bound: the tensor cores (and, seconds long, the power limit).  A stage of 64
 // 16-bit k takes 0.316 us a pair, 2.0 PFLOP/s over 76 pairs: 32768 x 4096 x 4096
-// with silu 545 us in a burst (cuBLAS's plain product 522 to 546), 648 us kept up
-// for seconds (1.70 PFLOP/s, of 1.73 that cuBLAS keeps up); 16361 tokens in e4m3
+// with silu 545 us in a burst (cuBLAS's plain product 522 to 546), 648 to 661 kept
+// up for seconds (1.66 to 1.70 PFLOP/s, of 1.73 that cuBLAS keeps up); 16361 tokens in e4m3
 // 157 us (3.5 PFLOP/s).  What it took: loads and MMAs issued by an elected lane (a
 // test of the lane number instead cost 713 us: the compiler then puts a loop
 // around every TMA and MMA instruction).
@@ -185,7 +185,10 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int* tm
 // OUT16: y is bf16 or fp16 (64 columns a box), else fp32 (32 columns a box).  An
 // fp32 y gets more of the sum's accuracy: the tensor cores' own additions drop
 // bits below the running sum, so k is cut into segments of kSegment stages,
-// each in an accumulator of its own, that the epilogue adds in registers.
+// each in an accumulator of its own, that the epilogue adds in registers (1.0e-6
+// against 64 bits for K = 2048 to 32768).  A 16-bit y takes all of k in one: the
+// rounding is all of its error (0.001675 either way for 32768 x 4096 x 4096), but
+// 0.25% of its elements round to the neighbour of what fp32 products would give.
 template <int TN, bool F8, bool OUT16>
 __global__ void __launch_bounds__(kThreads, 1) kda_linear_wide_kernel(const __grid_constant__ WideArgs p) {
     using Shape = WideShape<TN>;

@@ -1,5 +1,5 @@
 // waits.cuh -- bounded waits on mbarriers, the election of one thread of a warp
-// and the untiled bulk load (decode step, norm, projection).
+// and the untiled bulk load (decode step, projection).
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"

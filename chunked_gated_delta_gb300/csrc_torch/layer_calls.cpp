@@ -3,9 +3,10 @@
 //
 // A decode step makes these calls once per layer and token, at a few
 // microseconds of kernel time each.  Checked and marshalled in Python they take
-// 9 to 14 us of host time on the Grace cores; here they take 2.1 to 4.7, by
-// the outputs that they allocate; the launch itself is most of 2.  The module is plain CPython API on torch's
-// tensors; binding.py holds the documented functions that call it.
+// 9 to 14 us of host time on the Grace cores; here they take 2.2 to 5.0, by
+// the outputs that they allocate; the launch itself is most of 2.  The module is
+// plain CPython API on torch's tensors; binding.py holds the documented functions
+// that call it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -463,9 +463,9 @@ kda_status kda_rms_norm(const void* x, const void* residual, const void* weight,
  *   status_word  device int32 or NULL, as in kda_step: KDA_ERR_TIMEOUT if a
  *             pipeline wait ran out (y is then incomplete)
  * M >= 0; N, K >= 1, any of them odd (KDA_ERR_UNSUPPORTED beyond 2^30 of
- * any of the three).  x and w are 16-byte aligned with row strides of a multiple of 16 bytes where they have more than one row (KDA_ERR_ALIGNMENT),
- * which is what a TMA load of their rows needs; y and residual are aligned to
- * their own elements.  No workspace.  Results do not depend on timing (no
+ * any of the three).  x and w are 16-byte aligned with row strides of a multiple
+ * of 16 bytes where they have more than one row (KDA_ERR_ALIGNMENT), which is what
+ * a TMA load of their rows needs; y and residual are aligned to their own elements.  No workspace.  Results do not depend on timing (no
  * atomics); they may differ in the last bits between different M, whose sums
  * are cut differently.
  * Asynchronous on `stream`.
