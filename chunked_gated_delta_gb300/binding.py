@@ -190,10 +190,14 @@ def _stream_handle(stream):
 
 def on_stream(stream):
     """The caller's stream (None: the current one) as the current one, so that what a
-    call allocates and fills for its kernels belongs to the stream that they run on."""
+    call allocates and fills for its kernels belongs to the stream that they run on.
+    Any object with a ``cuda_stream`` handle will do."""
     import contextlib
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def _check(rc, where):

@@ -129,7 +129,7 @@ class Place {
 
   private:
     static c10::Device checked(PyObject* stream, const at::Tensor& t) {
-        if (stream != Py_None) {
+        if (stream != Py_None && PyObject_HasAttrString(stream, "device_index")) {  // (torch's streams have it)
             PyObject* index = PyObject_GetAttrString(stream, "device_index");
             if (!index) throw Refused{nullptr, ""};
             const long i = PyLong_AsLong(index);

@@ -2,6 +2,8 @@
 they run on, and what they fill for their kernels is filled there."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -71,3 +73,16 @@ def test_allocations_on_another_stream(op):
     assert not pending & {t.data_ptr() for t in outs}
     assert all(stream_of_block(t) == side.cuda_stream for t in outs)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("op", ["fwd", "chain_states", "bwd_dh"])
+def test_another_librarys_stream(op):
+    """An object with a handle and no more."""
+    call = calls()[op]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = call(SimpleNamespace(cuda_stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(stream_of_block(t) == side.cuda_stream for t in outs)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, want))

@@ -2,6 +2,8 @@
 memory that the current stream may still use, or soon gives away, is not theirs."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -70,4 +72,17 @@ def test_memory_with_work_pending_is_not_taken(op):
     outs = call(side)
     torch.cuda.synchronize()
     assert not pending & {t.data_ptr() for t in outs}
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("op", ["step", "rms_norm", "linear"])
+def test_another_librarys_stream(op):
+    """An object with a handle and no more."""
+    call = calls()[op]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = call(SimpleNamespace(cuda_stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(stream_of_block(t) == side.cuda_stream for t in outs)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, want))
