@@ -13,6 +13,10 @@ from .binding import (  # noqa: F401
     bwd_dh,
     chain_states,
     chunk_table,
+    decay_bwd,
+    decay_fwd,
+    decay_step,
+    decay_workspace_size,
     exact_path_tiles,
     fwd,
     fwd_host,
@@ -26,6 +30,8 @@ from .binding import (  # noqa: F401
     make_dims,
     new_workspace,
     rms_norm,
+    rotary,
+    rotary_freqs,
     selftest_wait_timeout,
     state_map,
     status,

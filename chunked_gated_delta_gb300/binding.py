@@ -1,5 +1,6 @@
 """ctypes binding of ``libkda.so`` (the C ABI in ``include/kda.h``); the served
-layer's operators (step, rms_norm, linear) go through a compiled extension.
+layers' operators (step, rms_norm, linear; decay_fwd, decay_bwd, decay_step,
+rotary) go through a compiled extension.
 
 Argument marshalling only: every step of the forward runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There
@@ -28,7 +29,8 @@ EXPORTS = ("kda_fwd_workspace_size", "kda_fwd", "kda_fwd_intra", "kda_fwd_scan",
            "kda_status_string", "kda_chunk_table", "kda_workspace_layout", "kda_fwd_host_arena_size",
            "kda_fwd_host", "kda_fwd_noalloc", "kda_selftest_wait_timeout", "kda_bwd_dh",
            "kda_fwd_ex", "kda_fwd_intra_ex", "kda_fwd_scan_ex", "kda_bwd_dh_ex", "kda_fwd_state_map",
-           "kda_chain_states", "kda_step", "kda_rms_norm", "kda_linear")
+           "kda_chain_states", "kda_step", "kda_rms_norm", "kda_linear", "kda_decay_workspace_size",
+           "kda_decay_fwd", "kda_decay_bwd", "kda_decay_step", "kda_rotary")
 
 
 class KdaError(RuntimeError):
@@ -71,6 +73,22 @@ class LinearOpts(ctypes.Structure):
                 ("act", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("x_stride", ctypes.c_int64), ("w_stride", ctypes.c_int64),
                 ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class DecayOpts(ctypes.Structure):
+    """kda_decay_opts: types, heads and row strides of kda_decay_fwd, kda_decay_bwd and kda_decay_step."""
+    _fields_ = [("io_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("qk_heads", ctypes.c_int32),
+                ("head_gate", ctypes.c_int32), ("num_slots", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("g_stride", ctypes.c_int64), ("do_stride", ctypes.c_int64)]
+
+
+class RotaryOpts(ctypes.Structure):
+    """kda_rotary_opts: types, layout and row strides of kda_rotary."""
+    _fields_ = [("io_dtype", ctypes.c_int32), ("pairs", ctypes.c_int32), ("positions_i64", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
 IO_BF16, IO_F16 = 0, 1
@@ -132,6 +150,13 @@ def load_library(build_if_missing: bool = True):
                                             ctypes.POINTER(NormOpts), P]),
             "kda_linear": (ctypes.c_int, [P, P, P, P, P, P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                           ctypes.POINTER(LinearOpts), P, P]),
+            "kda_decay_workspace_size": (SZ, [D, ctypes.POINTER(DecayOpts), I32]),
+            "kda_decay_fwd": (ctypes.c_int, [P, P, P, P, F32, P, P, P, P, D, ctypes.POINTER(DecayOpts), P, P, SZ, P]),
+            "kda_decay_bwd": (ctypes.c_int, [P, P, P, P, P, F32, P, P, P, P, P, P, P, P, D,
+                                             ctypes.POINTER(DecayOpts), P, P, SZ, P]),
+            "kda_decay_step": (ctypes.c_int, [P, P, P, P, F32, P, P, P, P, D, ctypes.POINTER(DecayOpts), P, P]),
+            "kda_rotary": (ctypes.c_int, [P, P, P, P, P, P, ctypes.c_int64, I32, I32, I32,
+                                          ctypes.POINTER(RotaryOpts), P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -506,3 +531,102 @@ def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None,
     """
     return (_calls or _layer_calls()).linear(x, w, bias, act, residual,
                                              x_scale, w_scale, out_dtype, out, status, stream)
+
+
+# ----------------------------------------------------------------- linear attention with a decay per head
+def decay_fwd(q, k, v, g, scale=None, h0=None, cu_seqlens=None, output_final_state=True, state_dtype=None,
+              workspace=None, out=None, final_state=None, status=None, stream=None):
+    """Linear attention with one decay per head over whole prompts (kda_decay_fwd):
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  Returns (o, ht) (ht None if not requested).
+
+    q, k: [B,T,Hqk,K]; v: [B,T,H,V], all bf16 or all fp16 (o follows), the rows of
+    consecutive tokens equally spaced and on 16 bytes; g: fp32 [B,T,H] (natural-log
+    decay), or [H]: a constant one per head.  H is a multiple of Hqk (value head h
+    reads q/k head h // (H // Hqk)).  h0: [N,H,K,V] fp32 or bf16 or None; ht has
+    its dtype, or ``state_dtype``, or fp32.  cu_seqlens: int32 [N+1] on the device
+    (B must be 1) or None.  scale defaults to K**-0.5.  ``workspace``: a uint8 CUDA tensor of
+    decay_workspace_size bytes, on 1024 bytes, or None (then one is allocated per call).
+    ``status``: an int32 CUDA tensor that starts at zero and takes errors in
+    cu_seqlens and waits that ran out (``binding.status`` reads it).  All tensors,
+    and ``stream``, are of one GPU; outputs are allocated for ``stream``.
+    """
+    return (_calls or _layer_calls()).decay_fwd(q, k, v, g, scale, h0, cu_seqlens, output_final_state, state_dtype,
+                                                workspace, out, final_state, status, stream)
+
+
+def decay_bwd(q, k, v, g, do, scale=None, h0=None, dht=None, cu_seqlens=None, want_dh0=True, workspace=None,
+              status=None, stream=None):
+    """Gradients of decay_fwd (kda_decay_bwd), from those of o (do [B,T,H,V]) and of
+    ht (dht [N,H,K,V], of h0's dtype, or None).  Returns (dq, dk, dv, dg, dh0): dq,
+    dk, dv like q, k, v (those of shared q/k heads summed over their value heads),
+    dg fp32 like g, dh0 [N,H,K,V] of the states' dtype, or None without ``want_dh0``.
+    Nothing of the forward is needed beside its inputs.  The rest as in decay_fwd.
+    """
+    return (_calls or _layer_calls()).decay_bwd(q, k, v, g, do, scale, h0, dht, cu_seqlens, want_dh0, workspace,
+                                                status, stream)
+
+
+def decay_step(q, k, v, g, state, slots=None, scale=None, cu_seqlens=None, out=None, status=None, stream=None):
+    """decay_fwd's recurrence for the few new tokens of each sequence (kda_decay_step), on a
+    cache of states [num_slots,H,K,V] updated in place.  Returns o [B,T,H,V].  g as in
+    decay_fwd; state, slots, cu_seqlens, status and stream as in step."""
+    return (_calls or _layer_calls()).decay_step(q, k, v, g, state, slots, scale, cu_seqlens, out, status, stream)
+
+
+def decay_workspace_size(dims: Dims, backward: bool, qk_heads: int = 0, head_gate: bool = False) -> int:
+    """Bytes of workspace of decay_fwd or decay_bwd for these dims (qk_heads: Hqk, 0 for H; head_gate: g is [H])."""
+    opts = DecayOpts(qk_heads=0 if qk_heads == dims.H else int(qk_heads), head_gate=int(bool(head_gate)))
+    n = int(load_library().kda_decay_workspace_size(ctypes.byref(dims), ctypes.byref(opts), int(bool(backward))))
+    if n == ctypes.c_size_t(-1).value:
+        raise KdaError(1, "kda_decay_workspace_size")
+    return n
+
+
+def rotary(q, k, positions, freqs, amplitude=1.0, interleaved=False, inverse=False, q_out=None, k_out=None,
+           stream=None):
+    """Rotary positions (kda_rotary): in every head of q and k the first 2 * len(freqs)
+    elements are turned in pairs by position * freq, the rest is copied.  Returns (q', k').
+
+    q: [B,T,H,D], k: [B,T,Hk,D] or None, bf16, fp16 or fp32, the rows of consecutive
+    tokens equally spaced; positions: int32 or int64 [B,T]; freqs: float64 (radians per
+    position) and ``amplitude`` (of the cosines and sines) as rotary_freqs makes them.
+    Pairs are (i, i + len(freqs)), or with ``interleaved`` (2 i, 2 i + 1).  ``inverse``
+    turns back: the gradients of q and k from those of q' and k'.  ``q_out`` and
+    ``k_out`` may be q and k themselves.  Tensors and ``stream``: as in step.
+    """
+    return (_calls or _layer_calls()).rotary(q, k, positions, freqs, amplitude, interleaved, inverse, q_out, k_out,
+                                             stream)
+
+
+def rotary_freqs(dim, base=10000.0, scaling=None, factor=1.0, original_length=4096, fast=32.0, slow=1.0, device="cuda"):
+    """(freqs, amplitude) of rotary for ``dim`` turned elements of a head, made once per model: freqs
+    [dim / 2] in float64, base^(-2 i / dim), scaled for contexts ``factor`` times as long:
+
+    None: as they are.  "linear": all divided by factor.  "ntk": from the base
+    base * factor^(dim / (dim - 2)), which divides the slowest by factor and keeps the
+    fastest.  "yarn": pairs that turn more than ``fast`` times over original_length
+    positions are kept, those that turn less than ``slow`` times divided by factor, in
+    between a mixture linear in the pair's index; amplitude 0.1 ln(factor) + 1.
+    """
+    import math
+    import torch
+    if dim < 2 or dim % 2 or not base > 0 or not factor > 0:
+        raise ValueError("dim must be even and positive, base and factor positive")
+    i = torch.arange(dim // 2, dtype=torch.float64)
+    amplitude = 1.0
+    if scaling == "ntk":
+        freqs = (base * factor ** (dim / (dim - 2)) if dim > 2 else base) ** (-2.0 * i / dim)
+    else:
+        freqs = float(base) ** (-2.0 * i / dim)
+        if scaling == "linear":
+            freqs = freqs / factor
+        elif scaling == "yarn":
+            def index(turns):  # the pair that turns so often over original_length
+                return dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+            low, high = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), dim - 1)
+            divided = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+            freqs = freqs * (1.0 - divided) + freqs / factor * divided
+            amplitude = 0.1 * math.log(factor) + 1.0
+        elif scaling is not None:
+            raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return freqs.to(device), amplitude

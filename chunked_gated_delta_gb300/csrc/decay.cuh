@@ -1,0 +1,318 @@
+// decay.cuh -- what the kernels of linear attention with a decay per head share
+// (decay_scan.cu: states and output; decay_grads.cu: gradients; decay_api.cu:
+// the C entries).
+//
+// With S the K x V state of one (sequence, head) and g_t <= 0 its log decay,
+//     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+// In chunks of 128 tokens, G_i the sum of g over the chunk's tokens up to i and
+// S the state before the chunk:
+//     o_i = scale (exp(G_i) S^T q_i + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
+//     S'  = exp(G_last) S + sum_j exp(G_last - G_j) k_j v_j^T
+// The decay is one number per token, so it never has to be factored over the
+// key dimension: it multiplies rows and columns of products.
+#pragma once
+#include <cuda.h>
+
+#include "internal.h"
+#include "layer_ops.cuh"
+#include "ptx.cuh"
+#include "tensormap.h"
+#include "waits.cuh"
+
+namespace kda {
+
+constexpr int kDecayChunk = 128;  // tokens: one row of a tcgen05 accumulator each
+
+// Sequences of one call, and how they are cut: `cu` null means B = N sequences
+// of T tokens each.  A piece is a run of seg_chunks chunks of one sequence.
+struct DecaySeqs {
+    const int32_t* cu;   // int32 [N + 1] or null
+    int32_t N, T;        // T: tokens of a sequence, or (packed) of all
+    int32_t seg_chunks;  // chunks per piece
+    int32_t pieces;      // grid size in pieces: exact, or (packed) an upper bound
+};
+
+// Where a state's memory is fp32 or bf16.
+struct DecayState {
+    void* p;      // [N, H, K, V] or null
+    int32_t b16;  // bf16
+};
+
+// One direction of the state scan: S over (k, v) forwards, or dS over (q, do) backwards.
+struct DecayScanDir {
+    CUtensorMap tm_x, tm_y;  // 3-D {dim, heads, rows}: k or q, v or do
+    DecayState start, end;   // h0 and ht, or dht and dh0
+    float* totals;           // fp32 [pieces, H, K, V]: what a piece adds, then (joined) the state that enters it
+    float* decays;           // fp32 [pieces, H]: exp of a piece's whole decay
+    uint8_t* kept;           // [chunks, H]: the state before each chunk, two parts of 16 bits (see scan), or null
+    float* kept_scale;       // fp32 [chunks, H]: what the parts are multiplied by (fp16)
+    float weight;            // of the products that are added: 1, or scale
+    int32_t reverse;
+};
+
+struct DecayScanArgs {
+    DecayScanDir dir[2];
+    CUtensorMap tm_q;    // the output pass
+    DecaySeqs seqs;
+    const float* g;      // fp32: g[row * g_stride + h] (g_stride 0: one decay per head)
+    int64_t g_stride;
+    uint16_t* o;         // [rows, H, V]
+    int32_t* status;     // or null
+    float scale;
+    int32_t H, group;    // value heads, value heads per q/k head
+    int32_t totals_only; // the pass before a join: pieces' totals, nothing else
+};
+
+struct DecayJoinArgs {
+    DecayScanDir dir[2];
+    DecaySeqs seqs;
+    int32_t H, state;    // state: K V
+};
+
+struct DecayGradArgs {
+    CUtensorMap tm_q, tm_k, tm_v, tm_do;
+    DecaySeqs seqs;      // seg_chunks = 1
+    const float* g;
+    int64_t g_stride;
+    const uint8_t *kept, *dkept;
+    const float *kept_scale, *dkept_scale;
+    void *dq, *dk;       // [rows, Hqk, K] 16 bits, or (grouped) fp32 [rows, H, K]
+    uint16_t* dv;        // [rows, H, V]
+    float* dg;           // fp32 [rows, H]
+    int32_t* status;
+    float scale;
+    int32_t H, group;
+};
+
+cudaError_t launch_decay_out(const DecayScanArgs& a, int K, int V, bool f16, cudaStream_t s);
+cudaError_t launch_decay_states(const DecayScanArgs& a, int K, int V, bool f16, int dirs, cudaStream_t s);
+cudaError_t launch_decay_join(const DecayJoinArgs& a, int dirs, cudaStream_t s);
+cudaError_t launch_decay_grads(const DecayGradArgs& a, int K, int V, bool f16, cudaStream_t s);
+// dq, dk [rows, heads, K] in 16 bits from fp32 [rows, heads, group, K]
+cudaError_t launch_decay_group(const float* dq32, const float* dk32, void* dq, void* dk, int64_t rows, int heads, int K,
+                               int group, bool f16, int sms, cudaStream_t s);
+// out [H]: dg [rows, H] summed over the rows; part: fp32 [(rows + 255) / 256, H]
+cudaError_t launch_decay_gate(const float* dg, float* part, float* out, int64_t rows, int H, cudaStream_t s);
+
+namespace {
+
+// ------------------------------------------------------------------ which piece
+struct DecayPiece {
+    int32_t n, piece, pieces;    // sequence (-1: none), piece of it, its pieces
+    int32_t bos, len;            // of the sequence
+    int32_t chunk_base;          // chunks of the sequences before it
+    int32_t piece_base;          // pieces of the sequences before it
+};
+__host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
+
+struct DecayScratch {
+    int32_t warp_pieces[32], warp_chunks[32];
+    DecayPiece found;
+};
+
+// The piece with this index, or the first of sequence `by_seq` (index then a sequence).  Called by
+// all THREADS threads.  A sequence without tokens has one piece where `empty` says so.  Returns
+// false if cu is not 0 = c0 <= c1 <= ... <= cN = T.
+template <int THREADS>
+__device__ __forceinline__ bool find_piece(const DecaySeqs& s, int index, bool by_seq, bool empty, DecayScratch& sm,
+                                           DecayPiece& out) {
+    if (!s.cu) {
+        const int nc = ceil_div(s.T, kDecayChunk);
+        const int per = max(ceil_div(nc, s.seg_chunks), empty ? 1 : 0);
+        out.n = by_seq ? index : per > 0 ? index / per : -1;
+        if (out.n >= s.N) out.n = -1;
+        out.piece = by_seq ? 0 : per > 0 ? index % per : 0;
+        out.pieces = per;
+        out.bos = out.n * s.T;
+        out.len = s.T;
+        out.chunk_base = out.n * nc;
+        out.piece_base = out.n * per;
+        return true;
+    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (s.N + THREADS - 1) / THREADS;
+    const int first = min(tid * each, s.N), last = min(first + each, s.N);
+    int pieces = 0, chunks = 0;
+    bool bad = false;
+    for (int n = first; n < last; ++n) {
+        const int bos = s.cu[n], eos = s.cu[n + 1];
+        bad |= bos < 0 || eos < bos || eos > s.T || (n == 0 && bos != 0) || (n == s.N - 1 && eos != s.T);
+        const int nc = ceil_div(max(eos - bos, 0), kDecayChunk);
+        chunks += nc;
+        pieces += max(ceil_div(nc, s.seg_chunks), empty ? 1 : 0);
+    }
+    int sp = pieces, sc = chunks;  // inclusive sums over the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int p = __shfl_up_sync(~0u, sp, off), c = __shfl_up_sync(~0u, sc, off);
+        if (lane >= off) sp += p, sc += c;
+    }
+    if (lane == 31) sm.warp_pieces[warp] = sp, sm.warp_chunks[warp] = sc;
+    if (tid == 0) sm.found.n = -1;
+    if (__syncthreads_or(bad)) return false;
+    for (int w = 0; w < warp; ++w) sp += sm.warp_pieces[w], sc += sm.warp_chunks[w];
+    sp -= pieces, sc -= chunks;  // before this thread's sequences
+    if (by_seq ? (index >= first && index < last) : (index >= sp && index < sp + pieces)) {
+        for (int n = first; n < last; ++n) {
+            const int bos = s.cu[n], len = s.cu[n + 1] - bos;
+            const int nc = ceil_div(len, kDecayChunk), per = max(ceil_div(nc, s.seg_chunks), empty ? 1 : 0);
+            if (by_seq ? n == index : index < sp + per) {
+                sm.found = DecayPiece{n, by_seq ? 0 : index - sp, per, bos, len, sc, sp};
+                break;
+            }
+            sp += per, sc += nc;
+        }
+    }
+    __syncthreads();
+    out = sm.found;
+    return true;
+}
+
+// ------------------------------------------------------------------ decays
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// A sum of two floats: hi + lo exactly what was added.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair add_pairs(Pair a, Pair b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
+// g in powers of two, to 2^-45 of itself.  A decay below 2^-200 per token leaves nothing of a state
+// in fp32 either way; cutting it there keeps -inf out of the differences.
+__device__ __forceinline__ Pair log2_decay(float g) {
+    constexpr float kLog2e = 1.44269504f, kRest = (float)(1.4426950408889634 - (double)kLog2e);
+    g = g < -140.f ? -140.f : g;
+    const float hi = g * kLog2e;
+    return {hi, fmaf(g, kRest, fmaf(g, kLog2e, -hi))};
+}
+
+// The decays of one chunk up to each of its tokens, in powers of two: differences of these sums are
+// right to 2^-24 of themselves however large the sums have grown, since what the leading parts lost
+// is kept in the second ones.
+struct ChunkDecay {
+    float hi[kDecayChunk], lo[kDecayChunk];
+};
+__device__ __forceinline__ float gap(const ChunkDecay& d, int i, float hi_j, float lo_j) {
+    return (d.hi[i] - hi_j) + (d.lo[i] - lo_j);
+}
+
+// A warp's four tokens per lane of a chunk's g; rows behind the sequence decay by nothing.
+struct LoadedG {
+    float v[4];
+};
+__device__ __forceinline__ LoadedG load_g(const float* g, int64_t stride, int h, int64_t row0, int valid, int lane) {
+    LoadedG r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = lane * 4 + i;
+        r.v[i] = t < valid ? g[(row0 + t) * stride + h] : 0.f;
+    }
+    return r;
+}
+// One warp: the sums of a chunk; the last one is returned to all lanes.
+__device__ __forceinline__ Pair sum_decay(const LoadedG& g, ChunkDecay& out, int lane) {
+    Pair p[4];
+    p[0] = log2_decay(g.v[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) p[i] = add_pairs(p[i - 1], log2_decay(g.v[i]));
+    Pair run = p[3];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Pair up{__shfl_up_sync(~0u, run.hi, off), __shfl_up_sync(~0u, run.lo, off)};
+        if (lane >= off) run = add_pairs(up, run);
+    }
+    Pair before{__shfl_up_sync(~0u, run.hi, 1), __shfl_up_sync(~0u, run.lo, 1)};
+    if (lane == 0) before = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const Pair s = add_pairs(before, p[i]);
+        out.hi[lane * 4 + i] = s.hi;
+        out.lo[lane * 4 + i] = s.lo;
+    }
+    return {__shfl_sync(~0u, run.hi, 31), __shfl_sync(~0u, run.lo, 31)};
+}
+// exp of a chunk's whole decay, to half a last bit: a state of thousands of chunks is multiplied by
+// one after the other, so their errors add up.
+// (2^n times the power series of exp(f ln 2) to its ninth term, |f| <= 1/2: what is left is below 2^-33.)
+__device__ __forceinline__ float whole_decay(Pair p) {
+    const float n = rintf(p.hi);
+    const double x = ((double)(p.hi - n) + (double)p.lo) * 0.6931471805599453;
+    double r = 1.0;
+#pragma unroll 1
+    for (int i = 9; i > 0; --i) r = fma(r, x * (double)(1.f / (float)i), 1.0);
+    return ldexpf((float)r, (int)n);
+}
+
+// ------------------------------------------------------------------ shared memory by 32-bit address
+// (What little L1 is left beside these kernels' shared memory makes a spilled register a trip to L2, so the
+// addresses that loops keep are single registers, and a swizzled row's pieces are one xor away from it.)
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Row `row` of a tile of 128-byte swizzled rows: its 16-byte piece c is at this ^ (c << 4).
+__device__ __forceinline__ uint32_t swizzled_row(uint32_t tile, int row) {
+    return tile + (uint32_t)row * 128u + (uint32_t)((row & 7) << 4);
+}
+
+// ------------------------------------------------------------------ tcgen05
+// D (+)= A B with A in TMEM: lane i, 32-bit column c hold A's row i, elements 2 c and 2 c + 1.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], "
+        "[%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 32 lanes x 32 bits, 16 columns (see tmem_ld16).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* u) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <bool F16>
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, int a_mn, int b_mn) {
+    return F16 ? ptx::idesc_f16_f32(M, N, a_mn, b_mn) : ptx::idesc_bf16_f32(M, N, a_mn, b_mn);
+}
+
+// A barrier of `threads` threads of the block.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bulk_store_async(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// A multiplier 2^n that brings values of up to `top` in size to 2^13 .. 2^14 (1 for zero, infinities and NaN).
+__device__ __forceinline__ float scale_to_f16(uint32_t top_bits) {
+    const int e = (int)(top_bits >> 23) - 127;
+    if (top_bits == 0 || e == 128) return 1.f;
+    const int n = min(max(13 - e, -126), 126);
+    return __uint_as_float((uint32_t)(n + 127) << 23);
+}
+
+}  // namespace
+}  // namespace kda

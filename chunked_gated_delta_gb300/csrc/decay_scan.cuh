@@ -1,0 +1,549 @@
+// decay_scan.cuh -- the state scan of linear attention with a decay per head
+// (formulas: decay.cuh), with its output (decay_out.cu) or by itself
+// (decay_states.cu).
+//
+// One CTA walks the chunks of a piece of one (sequence, head), with the state in
+// the registers of one warpgroup, transposed (thread v has S[:, v]), in fp32.
+// Per chunk of 128 tokens, all as tcgen05 MMAs with M = 128:
+//     scores   q k^T                      token x token, TMEM
+//     far      q S                        S rounded to 16 bits as the operand
+//     near     P v                        P = scale exp(G_i - G_j) scores, 16 bits, from TMEM
+//     added    v^T (exp(G_last - G_j) k)  value x key, in two products
+// and o = scale exp(G_i) far + near; S = exp(G_last) S + added.  The scaled k of
+// the last product does not fit 16 bits as k does, so it is split in two parts,
+// hi = k w rounded and lo = what hi lost, whose products add up: the states keep
+// 2^-17 and better instead of 2^-9 (they are fp32 outputs, and sums over all
+// tokens).
+//
+// Warps: 0 loads (TMA), 1 issues MMAs, 2 sums the chunk's decays; one warpgroup
+// each scales k, holds the state, turns scores into P, and writes o, so that
+// those of neighbouring chunks overlap. Their registers are shared out by what they hold.
+#pragma once
+#include "decay.cuh"
+
+namespace kda {
+namespace {
+
+template <int KB, int VB, bool OUT>
+struct DecayScanShape {
+    static constexpr int K = 64 * KB, V = 64 * VB;
+    static constexpr int kThreads = OUT ? 640 : 384;
+    static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kStateBytes = V * K * 2;
+    // Stages: k and q are read early in a chunk (the scaled parts of k have buffers of their own) and have one each
+    // where two do not fit.
+    static constexpr int kYStages = 2;
+    static constexpr int kRest = kYStages * kYBytes + 2 * kXBytes + (OUT ? 1 : 2) * kStateBytes;
+    static constexpr int kXStages = kRest + (OUT ? 4 : 2) * kXBytes <= 224 * 1024 ? 2 : 1;
+    static constexpr int kY = 0, kX = kYStages * kYBytes, kQ = kX + kXStages * kXBytes;
+    // (where V = 64 the MMAs with v^T read 128 columns, the second half from what follows, into lanes nobody reads)
+    static constexpr int kHi = OUT ? kQ + kXStages * kXBytes : kQ, kLo = kHi + kXBytes, kS = kLo + kXBytes;
+    static constexpr int kSmall = kS + (OUT ? 1 : 2) * kStateBytes;
+    // registers: those that the block is launched with, handed out as control, keys, state, scores, output
+    static constexpr int kControlRegs = OUT ? 64 : 64, kKeyRegs = OUT ? 64 : 176, kStateRegs = OUT ? 184 : 240;
+    static constexpr int kScoreRegs = 80, kOutRegs = 88;
+    static_assert(OUT ? kControlRegs + kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 5 * 96
+                      : kControlRegs + kKeyRegs + kStateRegs <= 3 * 160,
+                  "within what the block is launched with");
+    struct Small {
+        ChunkDecay decay[2];
+        float column[OUT ? kDecayChunk : 1];  // exp of the decay from a column to the end of its 32
+        float whole[2], unscale[2], key_unscale[2];
+        uint32_t top[4], key_top[4];
+        uint64_t x_full[2], x_empty[2], q_full[2], q_empty[2], y_full[2], y_empty[2], g_ready[2], g_free[2];
+        uint64_t scores, p_ready, s_ready, s_read, keys, keys_read, added, o_full, o_free;
+        uint32_t tmem;
+        int32_t fail;
+    };
+    static constexpr int kSmem = kSmall + (int)sizeof(Small);
+    static_assert(sizeof(Small) >= sizeof(DecayScratch), "the search's scratch fits");
+    static_assert(kSmem <= 227 * 1024, "fits an SM");
+    static constexpr uint32_t kScores = 0, kAdded = OUT ? 128 : 0, kFar = 256, kNear = 384;  // TMEM columns
+    static constexpr uint32_t kTmem = OUT ? 512 : 128;
+};
+
+template <int KB, int VB, bool F16, bool OUT>
+__global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
+    kda_decay_scan_kernel(const __grid_constant__ DecayScanArgs a) {
+    using Shape = DecayScanShape<KB, VB, OUT>;
+    constexpr int K = Shape::K, V = Shape::V, NX = Shape::kXStages;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    auto& sm = *reinterpret_cast<typename Shape::Small*>(raw + Shape::kSmall);
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, quarter = warp & 3;
+    const DecayScanDir& dir = a.dir[blockIdx.y];
+    const bool reverse = !OUT && dir.reverse;
+
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int item = blockIdx.x / a.H, h = blockIdx.x - item * a.H;
+    DecayPiece at;
+    if (!find_piece<Shape::kThreads>(a.seqs, item, false, true, *reinterpret_cast<DecayScratch*>(&sm), at)) {
+        if (blockIdx.x == 0 && tid == 0 && a.status) atomicOr(a.status, kStatusBadSeqlens);
+        return;
+    }
+    if (at.n < 0) return;
+    const bool first = reverse ? at.piece == at.pieces - 1 : at.piece == 0;
+    const bool last = reverse ? at.piece == 0 : at.piece == at.pieces - 1;
+    if (a.totals_only && last) return;  // nothing follows it
+    const int c0 = at.piece * a.seqs.seg_chunks;
+    const int chunks = min(ceil_div(at.len, kDecayChunk) - c0, a.seqs.seg_chunks);
+    auto chunk_at = [&](int it) { return c0 + (reverse ? chunks - 1 - it : it); };
+    __syncthreads();  // the search's scratch is free
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&sm.x_full[s], 1);
+            ptx::mbar_init(&sm.x_empty[s], OUT ? 5 : 4);
+            ptx::mbar_init(&sm.q_full[s], 1);
+            ptx::mbar_init(&sm.q_empty[s], 1);
+            ptx::mbar_init(&sm.y_full[s], 1);
+            ptx::mbar_init(&sm.y_empty[s], 1);
+            ptx::mbar_init(&sm.g_ready[s], 1);
+            ptx::mbar_init(&sm.g_free[s], (OUT ? 12 : 4) + 2 * VB);
+        }
+        for (uint64_t* b : {&sm.scores, &sm.s_read, &sm.keys_read, &sm.added, &sm.o_full}) ptx::mbar_init(b, 1);
+        for (uint64_t* b : {&sm.p_ready, &sm.keys, &sm.o_free}) ptx::mbar_init(b, 4);
+        ptx::mbar_init(&sm.s_ready, 2 * VB);
+        ptx::fence_mbar_init();
+        sm.fail = 0;
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&sm.tmem, Shape::kTmem);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem, base = ptx::smem_u32(raw);
+    // A wait that runs out is noted, and from then on nobody waits: every warp still goes through all of its
+    // barriers, so none is left standing at one.  Results are then incomplete, and the status says so.
+    volatile int32_t* fail = &sm.fail;
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+        if (!*fail && !wait_for(&bar, parity)) *fail = 1;
+    };
+    auto arrive = [&](uint64_t& bar) {  // once per warp
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar);
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kControlRegs));
+        if (warp == 0 && elect_one()) {
+            // ---------------------------------------------------------- loads
+            const int hq = h / a.group;
+            int it = 0;
+            for (; it < chunks; ++it) {
+                const int sx = it % NX, sy = it & 1, row = at.bos + chunk_at(it) * kDecayChunk;
+                const uint32_t px = ((it / NX) & 1) ^ 1, py = ((it >> 1) & 1) ^ 1;  // of the stage's last use
+                if (it >= NX) wait(sm.x_empty[sx], px);
+                if (*fail) break;
+                ptx::mbar_arrive_expect_tx(&sm.x_full[sx], Shape::kXBytes);
+                for (int b = 0; b < KB; ++b)
+                    ptx::tma_load_3d(raw + Shape::kX + sx * Shape::kXBytes + b * 16384, &dir.tm_x, &sm.x_full[sx], b * 64,
+                                     hq, row);
+                if constexpr (OUT) {
+                    if (it >= NX) wait(sm.q_empty[sx], px);
+                    ptx::mbar_arrive_expect_tx(&sm.q_full[sx], Shape::kXBytes);
+                    for (int b = 0; b < KB; ++b)
+                        ptx::tma_load_3d(raw + Shape::kQ + sx * Shape::kXBytes + b * 16384, &a.tm_q, &sm.q_full[sx],
+                                         b * 64, hq, row);
+                }
+                if (it >= 2) wait(sm.y_empty[sy], py);
+                ptx::mbar_arrive_expect_tx(&sm.y_full[sy], Shape::kYBytes);
+                for (int b = 0; b < VB; ++b)
+                    ptx::tma_load_3d(raw + Shape::kY + sy * Shape::kYBytes + b * 16384, &dir.tm_y, &sm.y_full[sy], b * 64,
+                                     h, row);
+            }
+            if (*fail)  // let the copies in flight land
+                for (int i = max(0, it - 2); i < it; ++i) {
+                    wait_for(&sm.x_full[i % NX], (i / NX) & 1);
+                    if (OUT) wait_for(&sm.q_full[i % NX], (i / NX) & 1);
+                    wait_for(&sm.y_full[i & 1], (i >> 1) & 1);
+                }
+        } else if (warp == 1 && elect_one()) {
+            // ---------------------------------------------------------- MMAs
+            constexpr uint32_t id_scores = idesc16<F16>(128, 128, 0, 0), id_far = idesc16<F16>(128, V, 0, 0),
+                               id_near = idesc16<F16>(128, V, 0, 1), id_added = idesc16<F16>(128, K, 1, 1);
+            const uint64_t hi_mn = ptx::smem_desc(base + Shape::kHi, 16384, 1024);
+            const uint64_t s_k = ptx::smem_desc(base + Shape::kS, 16, 1024);
+            for (int it = 0; it < chunks && !*fail; ++it) {
+                const int sx = it % NX, sy = it & 1;
+                const uint32_t ph = it & 1, px = (it / NX) & 1;
+                const uint64_t y_mn = ptx::smem_desc(base + Shape::kY + sy * Shape::kYBytes, 16384, 1024);
+                if constexpr (OUT) {
+                    const uint64_t q_k = ptx::smem_desc(base + Shape::kQ + sx * Shape::kXBytes, 16, 1024);
+                    const uint64_t x_k = ptx::smem_desc(base + Shape::kX + sx * Shape::kXBytes, 16, 1024);
+                    wait(sm.x_full[sx], px);
+                    wait(sm.q_full[sx], px);
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int ks = 0; ks < 4 * KB; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        ptx::mma_bf16(tmem + Shape::kScores, q_k + off, x_k + off, id_scores, ks > 0);
+                    }
+                    ptx::mma_commit(&sm.scores);
+                    ptx::mma_commit(&sm.x_empty[sx]);
+                    wait(sm.s_ready, ph);
+                    if (it > 0) wait(sm.o_free, ph ^ 1);
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int ks = 0; ks < 4 * KB; ++ks)
+                        ptx::mma_bf16(tmem + Shape::kFar, q_k + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                                      s_k + (((ks >> 2) * V * 128 + (ks & 3) * 32) >> 4), id_far, ks > 0);
+                    ptx::mma_commit(&sm.s_read);
+                    ptx::mma_commit(&sm.q_empty[sx]);
+                } else {
+                    wait(sm.s_ready, ph);
+                }
+                wait(sm.y_full[sy], (it >> 1) & 1);
+                wait(sm.keys, ph);
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int ks = 0; ks < 16; ++ks)  // hi, then lo
+                    ptx::mma_bf16(tmem + Shape::kAdded, y_mn + (ks & 7) * 128,
+                                  hi_mn + (ks & 7) * 128 + (ks >> 3) * (Shape::kXBytes >> 4), id_added, ks > 0);
+                ptx::mma_commit(&sm.added);
+                ptx::mma_commit(&sm.keys_read);
+                if constexpr (OUT) {
+                    wait(sm.p_ready, ph);
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tmem + Shape::kNear, tmem + Shape::kScores + ks * 8, y_mn + ks * 128, id_near, ks > 0);
+                    ptx::mma_commit(&sm.o_full);
+                }
+                ptx::mma_commit(&sm.y_empty[sy]);
+            }
+        } else if (warp == 2) {
+            // ---------------------------------------------------------- decays
+            auto loaded = [&](int it) {
+                const int c = chunk_at(it);
+                return load_g(a.g, a.g_stride, h, (int64_t)at.bos + c * kDecayChunk, at.len - c * kDecayChunk, lane);
+            };
+            LoadedG next;
+            if (chunks > 0) next = loaded(0);
+            for (int it = 0; it < chunks; ++it) {
+                const int st = it & 1;
+                const LoadedG now = next;
+                if (it + 1 < chunks) next = loaded(it + 1);
+                if (it >= 2) wait(sm.g_free[st], ((it >> 1) - 1) & 1);
+                const Pair all = sum_decay(now, sm.decay[st], lane);
+                if (lane == 0) sm.whole[st] = whole_decay(all);
+                arrive(sm.g_ready[st]);
+            }
+        }
+    } else if (warp < 8) {
+        if constexpr (OUT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
+        // ---------------------------------------------------------- keys: scaled, in two parts
+        const int j = quarter * 32 + lane;  // the token whose row this thread has
+        const uint32_t to = swizzled_row(base + Shape::kHi, j);
+        for (int it = 0; it < chunks; ++it) {
+            const int st = it & 1, sx = it % NX;
+            const bool live = j < at.len - chunk_at(it) * kDecayChunk;
+            wait(sm.g_ready[st], (it >> 1) & 1);
+            const ChunkDecay& d = sm.decay[st];
+            float w = dir.weight * exp2_fast(reverse ? d.hi[j] + d.lo[j]
+                                                     : gap(d, kDecayChunk - 1, d.hi[j], d.lo[j]));
+            arrive(sm.g_free[st]);
+            wait(sm.x_full[sx], (it / NX) & 1);
+            const uint32_t row = swizzled_row(base + Shape::kX + sx * Shape::kXBytes, j);
+            if constexpr (F16) {
+                // The scaled keys may be far below fp16's normal range, where a part keeps no relative precision: a
+                // power of two for all of the chunk's brings the largest near the top of it.
+                __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll 4
+                for (int c = 0; c < K / 8; ++c) {
+                    const uint4 x = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&in[e])));
+                }
+                const float m = live ? fmaxf(__low2float(most), __high2float(most)) * fabsf(w) : 0.f;
+                const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(m));
+                if (lane == 0) sm.key_top[quarter] = top;
+                named_sync(4, 128);
+                const float up = scale_to_f16(max(max(sm.key_top[0], sm.key_top[1]), max(sm.key_top[2], sm.key_top[3])));
+                w *= up;
+                if (j == 0) sm.key_unscale[st] = 1.f / up;
+            }
+            if (it > 0) wait(sm.keys_read, st ^ 1);
+#pragma unroll
+            for (int c0 = 0; c0 < K / 8; c0 += 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = lds128((row ^ (((c0 + i) & 7) << 4)) + (c0 >> 3) * 16384);
+                    if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = from_b16x2<F16>(in[e]);
+                        f = make_float2(f.x * w, f.y * w);
+                        hi[e] = pack_b16x2(f.x, f.y, F16);
+                        const float2 back = from_b16x2<F16>(hi[e]);
+                        lo[e] = pack_b16x2(f.x - back.x, f.y - back.y, F16);
+                    }
+                    const uint32_t p = (to ^ (((c0 + i) & 7) << 4)) + (c0 >> 3) * 16384;
+                    sts128(p, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            arrive(sm.x_empty[sx]);
+            if (at.len - chunk_at(it) * kDecayChunk < kDecayChunk) {
+                // rows behind the sequence are another's, or nobody's: a zero weight would not hold back a NaN
+                wait(sm.y_full[st], (it >> 1) & 1);
+                if (!live) {
+                    const uint32_t y = base + Shape::kY + st * Shape::kYBytes + j * 128;
+#pragma unroll 1
+                    for (int c = 0; c < V / 8; ++c) sts128(y + (c >> 3) * 16384 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            arrive(sm.keys);
+        }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kStateRegs));
+        // ---------------------------------------------------------- the state, transposed: column v of S
+        const int v = quarter * 32 + lane;
+        constexpr int kThreads = 64 * VB;
+        if (quarter < 2 * VB) {
+            float S[K];
+            const int64_t unit = (int64_t)item * a.H + h, seq = (int64_t)at.n * a.H + h;
+            float* piece = dir.totals + unit * K * V + v;  // (null without pieces: not used then)
+            const uint16_t* start16 = static_cast<const uint16_t*>(dir.start.p) + seq * K * V + v;
+            const float* start = first ? static_cast<const float*>(dir.start.p) + seq * K * V + v : piece;
+            const bool none = a.totals_only || (first && !dir.start.p), b16 = first && dir.start.b16;
+#pragma unroll
+            for (int k0 = 0; k0 < K; k0 += 16) {  // (16 loads in flight)
+#pragma unroll
+                for (int k = k0; k < k0 + 16; ++k)
+                    S[k] = none ? 0.f : b16 ? from_b16<false>(start16[k * V]) : start[k * V];
+                asm volatile("" ::: "memory");
+            }
+            const bool keep = !OUT && dir.kept;
+            float decay = 1.f;
+            for (int it = 0; it < chunks; ++it) {
+                const int st = it & 1, ph = it & 1;
+                if (OUT || keep) {
+                    // S as 16 bits (and, kept, what that lost), in rows of 128 bytes as the MMAs read them
+                    if (OUT && it > 0) wait(sm.s_read, ph ^ 1);
+                    if (!OUT && it > 0) {
+                        if (v == 0) ptx::bulk_wait_read0();  // the last chunk's copy has left
+                        named_sync(1, kThreads);
+                    }
+                    float up = 1.f;
+                    if constexpr (F16) {  // fp16's range is kept by a power of two for the whole state
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int k = 0; k < K; ++k) top = max(top, __float_as_uint(S[k]) & 0x7fffffffu);
+                        top = __reduce_max_sync(~0u, top);
+                        if (lane == 0) sm.top[quarter] = top;
+                        named_sync(2, kThreads);
+                        for (int i = 0; i < 2 * VB; ++i) top = max(top, sm.top[i]);
+                        up = scale_to_f16(top);
+                        named_sync(1, kThreads);  // (top is written again in the next chunk)
+                    }
+                    const uint32_t row = swizzled_row(base + Shape::kS, v);
+#pragma unroll
+                    for (int c = 0; c < K / 8; ++c) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = S[8 * c + 2 * e] * up, y = S[8 * c + 2 * e + 1] * up;
+                            hi[e] = pack_b16x2(x, y, F16);
+                            const float2 back = from_b16x2<F16>(hi[e]);
+                            lo[e] = pack_b16x2(x - back.x, y - back.y, F16);
+                        }
+                        const uint32_t p = (row ^ ((c & 7) << 4)) + (c >> 3) * V * 128;
+                        sts128(p, hi[0], hi[1], hi[2], hi[3]);
+                        if (!OUT) sts128(p + Shape::kStateBytes, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    if (OUT) {
+                        if (v == 0) sm.unscale[st] = 1.f / up;
+                    } else {
+                        named_sync(2, kThreads);
+                        if (v == 0) {
+                            const int64_t chunk = (int64_t)(at.chunk_base + chunk_at(it)) * a.H + h;
+                            bulk_store_async(dir.kept + chunk * 2 * Shape::kStateBytes, raw + Shape::kS,
+                                             2 * Shape::kStateBytes);
+                            ptx::bulk_commit();
+                            if (F16) dir.kept_scale[chunk] = 1.f / up;
+                        }
+                    }
+                }
+                arrive(sm.s_ready);  // also: the last chunk's products have been read
+                wait(sm.g_ready[st], (it >> 1) & 1);
+                const float whole = sm.whole[st];
+                arrive(sm.g_free[st]);
+                decay *= whole;
+                wait(sm.added, ph);
+                ptx::tc_fence_after();
+                const float back = F16 ? sm.key_unscale[st] : 1.f;
+#pragma unroll
+                for (int c = 0; c < K / 16; ++c) {
+                    float u[16];
+                    ptx::tmem_ld16(tmem + Shape::kAdded + ((uint32_t)(quarter * 32) << 16) + c * 16, u);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        S[16 * c + e] = F16 ? fmaf(u[e], back, whole * S[16 * c + e]) : fmaf(whole, S[16 * c + e], u[e]);
+                }
+                ptx::tc_fence_before();
+            }
+            if (a.totals_only) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) piece[k * V] = S[k];
+                if (v == 0) dir.decays[unit] = decay;
+            } else if (last && dir.end.p) {
+                if (dir.end.b16) {
+                    uint16_t* p = static_cast<uint16_t*>(dir.end.p) + seq * K * V + v;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) p[k * V] = to_b16(S[k], false);
+                } else {
+                    float* p = static_cast<float*>(dir.end.p) + seq * K * V + v;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) p[k * V] = S[k];
+                }
+            }
+            if (keep && v == 0) ptx::bulk_wait0();
+        }
+    } else if (warp < 16) {
+        if constexpr (OUT) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kScoreRegs));
+            // ------------------------------------------------------ P: row i of the scores
+            const int i = quarter * 32 + lane;
+            const uint32_t t_row = tmem + Shape::kScores + ((uint32_t)(quarter * 32) << 16);
+            for (int it = 0; it < chunks; ++it) {
+                const int st = it & 1;
+                wait(sm.g_ready[st], (it >> 1) & 1);
+                const ChunkDecay& d = sm.decay[st];
+                const float hi = d.hi[i], lo = d.lo[i];
+                named_sync(3, 128);  // the last chunk's factors have been read
+                sm.column[i] = exp2_fast(gap(d, quarter * 32 + 31, hi, lo));
+                named_sync(3, 128);
+                wait(sm.scores, it & 1);
+                ptx::tc_fence_after();
+                // Left of the diagonal's 32 x 32 block a pair's decay is taken in two steps, from the token to
+                // the end of its 32 and from there to i, both at most one: one multiplication each
+                // instead of an exponential per pair.
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t p[16];
+                    if (b <= quarter) {
+                        float s[32];
+                        ptx::tmem_ld16(t_row + 32 * b, s);
+                        ptx::tmem_ld16(t_row + 32 * b + 16, s + 16);
+                        if (b < quarter) {
+                            const int end = 32 * b + 31;
+                            const float r = a.scale * exp2_fast((hi - d.hi[end]) + (lo - d.lo[end]));
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 c = *reinterpret_cast<const float4*>(&sm.column[32 * b + 4 * e]);
+                                s[4 * e] *= r * c.x;
+                                s[4 * e + 1] *= r * c.y;
+                                s[4 * e + 2] *= r * c.z;
+                                s[4 * e + 3] *= r * c.w;
+                            }
+                        } else {
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 h4 = *reinterpret_cast<const float4*>(&d.hi[32 * b + 4 * e]);
+                                const float4 l4 = *reinterpret_cast<const float4*>(&d.lo[32 * b + 4 * e]);
+                                const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) {
+                                    const float w = a.scale * exp2_fast((hi - hj[f]) + (lo - lj[f]));
+                                    s[4 * e + f] = 4 * e + f <= lane ? s[4 * e + f] * w : 0.f;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = pack_b16x2(s[2 * e], s[2 * e + 1], F16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = 0u;
+                    }
+                    tmem_st16(t_row + 16 * b, p);  // (over scores that have been read)
+                }
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                arrive(sm.g_free[st]);
+                arrive(sm.p_ready);
+            }
+        }
+    } else {
+        if constexpr (OUT) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kOutRegs));
+            // ------------------------------------------------------ o: row i
+            const int i = quarter * 32 + lane;
+            const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
+            for (int it = 0; it < chunks; ++it) {
+                const int st = it & 1, tok = chunk_at(it) * kDecayChunk + i;
+                wait(sm.g_ready[st], (it >> 1) & 1);
+                float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]);
+                arrive(sm.g_free[st]);
+                wait(sm.o_full, it & 1);
+                ptx::tc_fence_after();
+                if (F16) f *= sm.unscale[st];
+                uint16_t* o = a.o + (((int64_t)at.bos + tok) * a.H + h) * V;
+#pragma unroll
+                for (int c = 0; c < V / 32; ++c) {
+                    float far[32], near[32];
+                    ptx::tmem_ld16(t_row + Shape::kFar + 32 * c, far);
+                    ptx::tmem_ld16(t_row + Shape::kNear + 32 * c, near);
+                    ptx::tmem_ld16(t_row + Shape::kFar + 32 * c + 16, far + 16);
+                    ptx::tmem_ld16(t_row + Shape::kNear + 32 * c + 16, near + 16);
+                    ptx::tmem_ld_wait();
+                    if (c == V / 32 - 1) {
+                        ptx::tc_fence_before();
+                        arrive(sm.o_free);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = pack_b16x2(fmaf(f, far[8 * g + 2 * e], near[8 * g + 2 * e]),
+                                              fmaf(f, far[8 * g + 2 * e + 1], near[8 * g + 2 * e + 1]), F16);
+                        if (tok < at.len) *reinterpret_cast<uint4*>(o + 32 * c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem, Shape::kTmem);
+    if (sm.fail && tid == 0 && a.status) atomicOr(a.status, kStatusTimeout);
+}
+
+template <int KB, int VB, bool F16, bool OUT>
+cudaError_t launch_scan_shape(const DecayScanArgs& a, int dirs, cudaStream_t s) {
+    using Shape = DecayScanShape<KB, VB, OUT>;
+    auto kern = kda_decay_scan_kernel<KB, VB, F16, OUT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3((unsigned)(a.seqs.pieces * a.H), (unsigned)dirs), dim3(Shape::kThreads),
+                            (size_t)Shape::kSmem, s, a);
+}
+template <bool OUT>
+cudaError_t launch_scan_any(const DecayScanArgs& a, int K, int V, bool f16, int dirs, cudaStream_t s) {
+    if (K == 128) {
+        if (V == 128) return f16 ? launch_scan_shape<2, 2, true, OUT>(a, dirs, s) : launch_scan_shape<2, 2, false, OUT>(a, dirs, s);
+        return f16 ? launch_scan_shape<2, 1, true, OUT>(a, dirs, s) : launch_scan_shape<2, 1, false, OUT>(a, dirs, s);
+    }
+    if (V == 128) return f16 ? launch_scan_shape<1, 2, true, OUT>(a, dirs, s) : launch_scan_shape<1, 2, false, OUT>(a, dirs, s);
+    return f16 ? launch_scan_shape<1, 1, true, OUT>(a, dirs, s) : launch_scan_shape<1, 1, false, OUT>(a, dirs, s);
+}
+
+}  // namespace
+}  // namespace kda

@@ -1,0 +1,244 @@
+// decay_step.cu -- kda_decay_step: linear attention with a decay per head for the
+// few new tokens of a decode step, on a cache of states addressed by slot and
+// updated in place:  S <- exp(g) S + k v^T,  o = scale S^T q.
+//
+// Unlike the delta rule's, a token's update does not depend on what the state
+// answers, so the tokens of a batch follow one another in registers and only
+// their outputs, which sum over the rows that the threads share, meet in shared memory.
+//
+// Bound: each state is read and written once per call, 2 K V 4 bytes (128 KB at
+// K = V = 128 in fp32) against 5 K V flops a token: HBM, or for a handful of states the
+// launch and one trip to memory.
+#include "decay.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kStepTokens = 4;  // tokens whose inputs are loaded together
+
+struct DecayStepArgs {
+    const uint16_t *q, *k, *v;
+    const float* g;
+    void* state;
+    const int32_t* slots;  // or null
+    const int32_t* cu;     // or null
+    uint16_t* o;
+    int32_t* status;       // or null
+    int64_t q_stride, k_stride, v_stride, g_stride;
+    float scale;
+    int32_t N, T, H, V, group, num_slots;
+};
+
+template <bool STATE16>
+__device__ __forceinline__ float4 load_four(const void* p, int64_t four) {
+    if constexpr (STATE16) {
+        const uint2 w = static_cast<const uint2*>(p)[four];
+        const float2 a = from_b16x2<false>(w.x), b = from_b16x2<false>(w.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    } else {
+        return static_cast<const float4*>(p)[four];
+    }
+}
+template <bool STATE16>
+__device__ __forceinline__ void store_four(void* p, int64_t four, float4 s) {
+    if constexpr (STATE16)
+        static_cast<uint2*>(p)[four] = make_uint2(pack_b16x2(s.x, s.y, false), pack_b16x2(s.z, s.w, false));
+    else
+        static_cast<float4*>(p)[four] = s;
+}
+
+// One CTA has VT columns of one (sequence, head): THREADS threads, each kRows rows of four columns.
+template <int K, int VT, int THREADS, bool F16, bool STATE16, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const DecayStepArgs a) {
+    constexpr int kColGroups = VT / 4, kRowLanes = THREADS / kColGroups, kRows = K / kRowLanes;
+    constexpr int kWarps = THREADS / 32, kParts = kColGroups >= 32 ? kRowLanes : kWarps;
+    static_assert(kRows >= 1 && kRows * kRowLanes == K, "the threads tile the K rows");
+    __shared__ float s_k[kStepTokens][K], s_q[kStepTokens][K];
+    __shared__ float4 s_v[kStepTokens][kColGroups];
+    __shared__ float s_decay[kStepTokens];
+    __shared__ float4 s_o[kStepTokens][kParts][kColGroups];
+
+    const int tid = threadIdx.x;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int tiles = a.V / VT;
+    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % a.H, n = blockIdx.x / tiles / a.H;
+    const bool first = tile == 0 && h == 0 && tid == 0;
+
+    int64_t row0 = (int64_t)n * a.T;
+    int len = a.T;
+    if (a.cu) {
+        const int bos = a.cu[n], eos = a.cu[n + 1];
+        if (bos < 0 || eos < bos || eos > a.T || (n == 0 && bos != 0) || (n == a.N - 1 && eos != a.T)) {
+            if (first && a.status) atomicOr(a.status, kStatusBadSeqlens);
+            return;
+        }
+        row0 = bos;
+        len = eos - bos;
+    }
+    if (len == 0) return;
+    const int slot = a.slots ? a.slots[n] : n;
+    const bool in_cache = slot >= 0 && slot < a.num_slots;
+
+    const int cg = tid % kColGroups, rl = tid / kColGroups;
+    const int64_t at = in_cache ? ((((int64_t)slot * a.H + h) * K + rl) * a.V + tile * VT) / 4 + cg : 0;
+    const int64_t row_step = (int64_t)kRowLanes * a.V / 4;
+    float4 S[kRows];
+    if (in_cache) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) S[i] = load_four<STATE16>(a.state, at + i * row_step);
+    }
+    const int hq = h / a.group;
+    auto stage = [&](int t0) {
+        for (int e = tid; e < kStepTokens * K; e += THREADS) {
+            const int j = e / K, r = e % K;
+            if (t0 + j < len) {
+                const int64_t row = row0 + t0 + j;
+                s_k[j][r] = from_b16<F16>(a.k[row * a.k_stride + (int64_t)hq * K + r]);
+                s_q[j][r] = from_b16<F16>(a.q[row * a.q_stride + (int64_t)hq * K + r]);
+            }
+        }
+        for (int e = tid; e < kStepTokens * VT; e += THREADS) {
+            const int j = e / VT, c = e % VT;
+            if (t0 + j < len)
+                reinterpret_cast<float*>(s_v[j])[c] =
+                    from_b16<F16>(a.v[(row0 + t0 + j) * a.v_stride + (int64_t)h * a.V + tile * VT + c]);
+        }
+        if (tid < kStepTokens && t0 + tid < len) s_decay[tid] = expf(a.g[(row0 + t0 + tid) * a.g_stride + h]);
+    };
+    // The same slot twice would race: the first sequence that names it has it.
+    bool taken = false;
+    if (in_cache && a.slots)
+        for (int j = tid; j < n; j += THREADS) taken |= a.slots[j] == slot;
+    stage(0);
+    taken = __syncthreads_or(taken);
+
+    uint16_t* o = a.o + (row0 * a.H + h) * a.V + tile * VT;
+    const int64_t o_step = (int64_t)a.H * a.V;
+    if (!in_cache || taken) {
+        if (first && (taken || slot >= a.num_slots) && a.status) atomicOr(a.status, kStatusBadSlots);
+        for (int t = rl; t < len; t += kRowLanes) *reinterpret_cast<uint2*>(o + t * o_step + cg * 4) = make_uint2(0u, 0u);
+        return;
+    }
+    for (int t0 = 0; t0 < len; t0 += kStepTokens) {
+        if (t0 > 0) {
+            __syncthreads();  // the tokens before, and their sums, have been read
+            stage(t0);
+            __syncthreads();
+        }
+        const int count = min(kStepTokens, len - t0);
+        for (int j = 0; j < count; ++j) {
+            const float d = s_decay[j];
+            const float4 v = s_v[j][cg];
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const float k = s_k[j][rl + i * kRowLanes], q = s_q[j][rl + i * kRowLanes];
+                S[i] = make_float4(fmaf(d, S[i].x, k * v.x), fmaf(d, S[i].y, k * v.y), fmaf(d, S[i].z, k * v.z),
+                                   fmaf(d, S[i].w, k * v.w));
+                y = make_float4(fmaf(q, S[i].x, y.x), fmaf(q, S[i].y, y.y), fmaf(q, S[i].z, y.z), fmaf(q, S[i].w, y.w));
+            }
+#pragma unroll
+            for (int off = kColGroups; off < 32; off <<= 1) {  // row lanes of the same columns in this warp
+                y.x += __shfl_xor_sync(~0u, y.x, off);
+                y.y += __shfl_xor_sync(~0u, y.y, off);
+                y.z += __shfl_xor_sync(~0u, y.z, off);
+                y.w += __shfl_xor_sync(~0u, y.w, off);
+            }
+            if (kColGroups >= 32) s_o[j][rl][cg] = y;
+            else if ((tid & 31) < kColGroups) s_o[j][tid >> 5][cg] = y;
+        }
+        if (t0 + count >= len) {  // (the stores leave while the outputs are summed)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) store_four<STATE16>(a.state, at + i * row_step, S[i]);
+        }
+        __syncthreads();
+        for (int e = tid; e < count * kColGroups; e += THREADS) {
+            const int j = e / kColGroups, c = e % kColGroups;
+            float4 y = s_o[j][0][c];
+#pragma unroll
+            for (int w = 1; w < kParts; ++w) {
+                const float4 x = s_o[j][w][c];
+                y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+            }
+            *reinterpret_cast<uint2*>(o + (t0 + j) * o_step + c * 4) =
+                make_uint2(pack_b16x2(a.scale * y.x, a.scale * y.y, F16), pack_b16x2(a.scale * y.z, a.scale * y.w, F16));
+        }
+    }
+}
+
+template <int K, int VT, int THREADS, int PER_SM>
+cudaError_t launch(const DecayStepArgs& a, bool f16, bool s16, cudaStream_t s) {
+    const dim3 grid((unsigned)((int64_t)a.N * a.H * (a.V / VT)));
+    if (f16)
+        return s16 ? launch_dependent(kda_decay_step_kernel<K, VT, THREADS, true, true, PER_SM>, grid, dim3(THREADS), 0, s, a)
+                   : launch_dependent(kda_decay_step_kernel<K, VT, THREADS, true, false, PER_SM>, grid, dim3(THREADS), 0, s, a);
+    return s16 ? launch_dependent(kda_decay_step_kernel<K, VT, THREADS, false, true, PER_SM>, grid, dim3(THREADS), 0, s, a)
+               : launch_dependent(kda_decay_step_kernel<K, VT, THREADS, false, false, PER_SM>, grid, dim3(THREADS), 0, s, a);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_decay_step(const void* q, const void* k, const void* v, const float* g, float scale,
+                                     void* state, const int32_t* slots, const int32_t* cu_seqlens, void* o,
+                                     const kda_dims* dims, const kda_decay_opts* opts, int32_t* status_word,
+                                     void* stream) {
+    if (!dims || !opts) return KDA_ERR_INVALID_ARG;
+    const kda_dims& d = *dims;
+    const bool packed = cu_seqlens != nullptr;
+    if (packed != (d.num_seqs > 0) || d.num_seqs < 0 || d.B < 1 || d.T < 0 || d.H < 1 || (packed && d.B != 1))
+        return KDA_ERR_INVALID_ARG;
+    if ((d.K != 64 && d.K != 128) || (d.V != 64 && d.V != 128)) return KDA_ERR_UNSUPPORTED;
+    const kda_decay_opts& p = *opts;
+    if ((p.io_dtype != KDA_IO_BF16 && p.io_dtype != KDA_IO_F16) ||
+        (p.state_dtype != KDA_STATE_F32 && p.state_dtype != KDA_STATE_BF16) || (p.head_gate != 0 && p.head_gate != 1) ||
+        p.reserved != 0 || p.num_slots < 1 || p.do_stride != 0 || p.qk_heads < 0 ||
+        (p.qk_heads > 0 && (p.qk_heads > d.H || d.H % p.qk_heads != 0)))
+        return KDA_ERR_INVALID_ARG;
+    const int N = packed ? d.num_seqs : d.B;
+    if (!slots && N > p.num_slots) return KDA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)d.B * d.T;
+    if (rows > INT32_MAX / 2 || (int64_t)N * d.H * (d.V / 32) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    const int hq = p.qk_heads > 0 ? p.qk_heads : d.H;
+    const int64_t wq = (int64_t)hq * d.K, wv = (int64_t)d.H * d.V;
+    DecayStepArgs a{};
+    a.q_stride = p.q_stride ? p.q_stride : wq;
+    a.k_stride = p.k_stride ? p.k_stride : wq;
+    a.v_stride = p.v_stride ? p.v_stride : wv;
+    a.g_stride = p.head_gate ? 0 : p.g_stride ? p.g_stride : d.H;
+    if (a.q_stride < wq || a.k_stride < wq || a.v_stride < wv || (p.head_gate ? p.g_stride != 0 : a.g_stride < d.H))
+        return KDA_ERR_INVALID_ARG;
+    if ((slots && !is_aligned(slots, 4)) || (packed && !is_aligned(cu_seqlens, 4)) ||
+        (status_word && !is_aligned(status_word, 4)))
+        return KDA_ERR_ALIGNMENT;
+    if (rows == 0 && !packed) return KDA_OK;
+    if (rows > 0) {
+        if (!q || !k || !v || !g || !state || !o) return KDA_ERR_INVALID_ARG;
+        if (!is_aligned(q, 2) || !is_aligned(k, 2) || !is_aligned(v, 2) || !is_aligned(g, 4) || !is_aligned(o, 16) ||
+            !is_aligned(state, 16))
+            return KDA_ERR_ALIGNMENT;
+    }
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.g = g;
+    a.state = state;
+    a.slots = slots;
+    a.cu = cu_seqlens;
+    a.o = static_cast<uint16_t*>(o);
+    a.status = status_word;
+    a.scale = scale;
+    a.N = N;
+    a.T = d.T;
+    a.H = d.H;
+    a.V = d.V;
+    a.group = d.H / hq;
+    a.num_slots = p.num_slots;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f16 = p.io_dtype == KDA_IO_F16, s16 = p.state_dtype == KDA_STATE_BF16;
+    const cudaError_t e = d.K == 128 ? launch<128, 64, 256, 2>(a, f16, s16, s) : launch<64, 64, 256, 2>(a, f16, s16, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}

@@ -1,0 +1,248 @@
+// rotary.cu -- kda_rotary: the positions of q and k. Pairs (x, y) of a head's first
+// 2 * pairs elements are turned by the angle position * freq:
+//     x' = amplitude (x cos - y sin),  y' = amplitude (x sin + y cos),
+// the rest of the head is copied.
+//
+// The angle of a far position is hundreds of thousands of radians, of which fp32 would
+// keep a few hundredths. It is taken in turns, as a fraction of 64 bits: position times
+// that fraction, as integers, wraps around where the angle does, so nothing is
+// lost to its size (beside the frequency's own 53 bits), without any 64-bit float
+// arithmetic per token.
+//
+// Bound: q and k read and written once. A CTA goes through tokens; its threads
+// make a token's cosines and sines once for all heads, in shared memory, while
+// the rows of that token are on their way, 16 bytes a load.
+#include "internal.h"
+#include "layer_ops.cuh"
+#include "ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRotaryThreads = 128;
+constexpr int kMostPairs = 512;
+constexpr int kItems = 4;  // pieces of a row that a thread has in flight
+
+struct RotaryArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const void* positions;  // int64 or int32
+    const double* freqs;
+    int64_t tokens, q_stride, k_stride, q_out_stride, k_out_stride;  // in elements
+    int32_t q_heads, k_heads, dim, pairs, positions64, inverse;
+    float amplitude;
+};
+
+template <int IO>
+struct Io;
+template <>
+struct Io<KDA_DTYPE_BF16> {
+    using T = uint16_t;
+    static __device__ __forceinline__ float get(T x) { return from_b16<false>(x); }
+    static __device__ __forceinline__ T put(float x) { return to_b16(x, false); }
+};
+template <>
+struct Io<KDA_DTYPE_F16> {
+    using T = uint16_t;
+    static __device__ __forceinline__ float get(T x) { return from_b16<true>(x); }
+    static __device__ __forceinline__ T put(float x) { return to_b16(x, true); }
+};
+template <>
+struct Io<KDA_DTYPE_F32> {
+    using T = float;
+    static __device__ __forceinline__ float get(T x) { return x; }
+    static __device__ __forceinline__ T put(float x) { return x; }
+};
+
+// C elements (16 bytes, or one) in a register block.
+template <typename T, int C>
+struct alignas(sizeof(T) * C) Piece {
+    T x[C];
+};
+
+// C: elements of a load. A row of a head is items: those of pairs (two loads: in the half layout the
+// x and the y of C pairs, else 2 C elements of C pairs), then those that are copied (one load each, two in an item).
+template <int IO, int C, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRotaryThreads) kda_rotary_kernel(const RotaryArgs a) {
+    using T = typename Io<IO>::T;
+    using P = Piece<T, C>;
+    __shared__ float2 s_turn[2][kMostPairs];  // cos, sin
+    const int tid = threadIdx.x;
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    constexpr int kOwn = kMostPairs / kRotaryThreads;
+    uint64_t turn[kOwn];  // of the pairs that this thread looks after: one position's share of a turn, times 2^64
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int p = tid + i * kRotaryThreads;
+        double t = p < a.pairs ? a.freqs[p] * 0.15915494309189535 : 0.0;
+        t -= floor(t);
+        turn[i] = __double2ull_rn(t * 18446744073709551616.0);
+    }
+    const int turned = a.pairs / C;                               // items of pairs in a head
+    const int copied = (a.dim - 2 * a.pairs + 2 * C - 1) / (2 * C);
+    const int per_head = turned + copied, heads = a.q_heads + a.k_heads, items = heads * per_head;
+
+    auto angles = [&](int64_t tok, float2* to) {
+        const uint64_t pos = a.positions64 ? static_cast<const uint64_t*>(a.positions)[tok]
+                                           : (uint64_t)(int64_t)static_cast<const int32_t*>(a.positions)[tok];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int p = tid + i * kRotaryThreads;
+            if (p >= a.pairs) break;
+            // (the leading 32 bits of the fraction, as half turns in -1 .. 1)
+            const float half_turns = (float)(int32_t)(uint32_t)((pos * turn[i]) >> 32) * 0x1p-31f;
+            float s, c;
+            sincospif(half_turns, &s, &c);
+            to[p] = make_float2(a.amplitude * c, a.inverse ? -a.amplitude * s : a.amplitude * s);
+        }
+    };
+    struct At {
+        const T* in;
+        T* out;
+        int first, second, pair, count;  // offsets of the two loads; first pair (-1: copied), loads of an item
+    };
+    auto item_at = [&](int64_t tok, int e) {
+        const int head = e / per_head, i = e - head * per_head;
+        At r;
+        if (head < a.q_heads) {
+            r.in = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * a.dim;
+            r.out = static_cast<T*>(a.q_out) + tok * a.q_out_stride + (int64_t)head * a.dim;
+        } else {
+            r.in = static_cast<const T*>(a.k) + tok * a.k_stride + (int64_t)(head - a.q_heads) * a.dim;
+            r.out = static_cast<T*>(a.k_out) + tok * a.k_out_stride + (int64_t)(head - a.q_heads) * a.dim;
+        }
+        r.count = 2;
+        if (i < turned) {
+            r.pair = i * C;
+            r.first = INTERLEAVED ? 2 * r.pair : r.pair;
+            r.second = INTERLEAVED ? r.first + C : r.pair + a.pairs;
+        } else {
+            r.pair = -1;
+            r.first = 2 * a.pairs + (i - turned) * 2 * C;
+            r.second = r.first + C;
+            if (r.second >= a.dim) r.count = 1;
+        }
+        return r;
+    };
+
+    int buf = 0;
+    for (int64_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x, buf ^= 1) {
+        for (int e0 = tid; e0 - tid < items; e0 += kItems * kRotaryThreads) {
+            P x[kItems], y[kItems];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int e = e0 + i * kRotaryThreads;
+                if (e < items) {
+                    const At at = item_at(tok, e);
+                    x[i] = *reinterpret_cast<const P*>(at.in + at.first);
+                    if (at.count == 2) y[i] = *reinterpret_cast<const P*>(at.in + at.second);
+                }
+            }
+            if (e0 == tid) {  // (one barrier per token: the buffer before last has been read by all)
+                angles(tok, s_turn[buf]);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int e = e0 + i * kRotaryThreads;
+                if (e >= items) break;
+                const At at = item_at(tok, e);
+                if (at.pair >= 0) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float2 t = s_turn[buf][at.pair + c];
+                        T *u, *w;
+                        if constexpr (INTERLEAVED) {
+                            u = 2 * c < C ? &x[i].x[2 * c % C] : &y[i].x[2 * c % C];
+                            w = 2 * c + 1 < C ? &x[i].x[(2 * c + 1) % C] : &y[i].x[(2 * c + 1) % C];
+                        } else {
+                            u = &x[i].x[c];
+                            w = &y[i].x[c];
+                        }
+                        const float m = Io<IO>::get(*u), n = Io<IO>::get(*w);
+                        *u = Io<IO>::put(m * t.x - n * t.y);
+                        *w = Io<IO>::put(m * t.y + n * t.x);
+                    }
+                } else if (at.in == at.out) {
+                    continue;
+                }
+                *reinterpret_cast<P*>(at.out + at.first) = x[i];
+                if (at.count == 2) *reinterpret_cast<P*>(at.out + at.second) = y[i];
+            }
+        }
+    }
+}
+
+template <int IO, int C>
+cudaError_t launch(const RotaryArgs& a, bool interleaved, unsigned grid, cudaStream_t s) {
+    return interleaved ? launch_dependent(kda_rotary_kernel<IO, C, true>, dim3(grid), dim3(kRotaryThreads), 0, s, a)
+                       : launch_dependent(kda_rotary_kernel<IO, C, false>, dim3(grid), dim3(kRotaryThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_rotary(const void* q, const void* k, const void* positions, const double* freqs, void* q_out,
+                                 void* k_out, int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t dim,
+                                 const kda_rotary_opts* opts, void* stream) {
+    if (!opts) return KDA_ERR_INVALID_ARG;
+    const kda_rotary_opts& p = *opts;
+    if (tokens < 0 || q_heads < 1 || k_heads < 0 || dim < 1 || p.pairs < 1 || p.pairs > dim / 2 ||
+        (p.io_dtype != KDA_DTYPE_BF16 && p.io_dtype != KDA_DTYPE_F16 && p.io_dtype != KDA_DTYPE_F32) ||
+        (p.positions_i64 != 0 && p.positions_i64 != 1) || (p.interleaved != 0 && p.interleaved != 1) ||
+        (p.inverse != 0 && p.inverse != 1) || p.reserved != 0)
+        return KDA_ERR_INVALID_ARG;
+    if (p.pairs > kMostPairs || (int64_t)(q_heads + (int64_t)k_heads) * dim > INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
+    const int64_t wq = (int64_t)q_heads * dim, wk = (int64_t)k_heads * dim;
+    RotaryArgs a{};
+    a.q_stride = p.q_stride ? p.q_stride : wq;
+    a.k_stride = p.k_stride ? p.k_stride : wk;
+    a.q_out_stride = p.q_out_stride ? p.q_out_stride : wq;
+    a.k_out_stride = p.k_out_stride ? p.k_out_stride : wk;
+    if (a.q_stride < wq || a.k_stride < wk || a.q_out_stride < wq || a.k_out_stride < wk) return KDA_ERR_INVALID_ARG;
+    if (tokens == 0) return KDA_OK;
+    if (!q || !q_out || !positions || !freqs || (k_heads > 0 && (!k || !k_out))) return KDA_ERR_INVALID_ARG;
+    // in place, rows as they lie, or apart
+    if ((q == q_out && a.q_stride != a.q_out_stride) || (k_heads > 0 && k == k_out && a.k_stride != a.k_out_stride))
+        return KDA_ERR_INVALID_ARG;
+    const int es = dtype_bytes(p.io_dtype);
+    if (!is_aligned(q, es) || !is_aligned(q_out, es) || (k_heads > 0 && (!is_aligned(k, es) || !is_aligned(k_out, es))) ||
+        !is_aligned(positions, p.positions_i64 ? 8 : 4) || !is_aligned(freqs, 8))
+        return KDA_ERR_ALIGNMENT;
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.positions = positions;
+    a.freqs = freqs;
+    a.tokens = tokens;
+    a.q_heads = q_heads;
+    a.k_heads = k_heads;
+    a.dim = dim;
+    a.pairs = p.pairs;
+    a.positions64 = p.positions_i64;
+    a.inverse = p.inverse;
+    a.amplitude = p.amplitude;
+    const int C = 16 / es;
+    bool wide = dim % C == 0 && p.pairs % C == 0;
+    for (const void* x : {q, static_cast<const void*>(q_out)}) wide = wide && is_aligned(x, 16);
+    for (int64_t x : {a.q_stride, a.q_out_stride}) wide = wide && x % C == 0;
+    if (k_heads > 0) {
+        for (const void* x : {k, static_cast<const void*>(k_out)}) wide = wide && is_aligned(x, 16);
+        for (int64_t x : {a.k_stride, a.k_out_stride}) wide = wide && x % C == 0;
+    }
+    const int64_t most = (int64_t)device_sm_count() * 12;
+    const unsigned grid = (unsigned)(tokens < most ? tokens : most);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (p.io_dtype == KDA_DTYPE_F32)
+        e = wide ? launch<KDA_DTYPE_F32, 4>(a, p.interleaved, grid, s) : launch<KDA_DTYPE_F32, 1>(a, p.interleaved, grid, s);
+    else if (p.io_dtype == KDA_DTYPE_F16)
+        e = wide ? launch<KDA_DTYPE_F16, 8>(a, p.interleaved, grid, s) : launch<KDA_DTYPE_F16, 1>(a, p.interleaved, grid, s);
+    else
+        e = wide ? launch<KDA_DTYPE_BF16, 8>(a, p.interleaved, grid, s) : launch<KDA_DTYPE_BF16, 1>(a, p.interleaved, grid, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}

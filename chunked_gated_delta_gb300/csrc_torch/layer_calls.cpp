@@ -1,5 +1,6 @@
-// layer_calls.cpp -- the Python calls of the served layer's operators (step,
-// rms_norm, linear): argument checks, output allocation and the C-ABI call.
+// layer_calls.cpp -- the Python calls of the served layers' operators (step,
+// rms_norm, linear; decay_fwd, decay_bwd, decay_step, rotary): argument checks,
+// output allocation and the C-ABI call.
 //
 // A decode step makes these calls once per layer and token, at a few
 // microseconds of kernel time each.  Checked and marshalled in Python they take
@@ -370,6 +371,247 @@ PyObject* call_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------------------- linear attention with a decay per head
+// What decay_fwd, decay_bwd and decay_step check alike: q, k [B,T,Hqk,K], v [B,T,H,V], g [B,T,H] or [H].
+struct DecayInputs {
+    const at::Tensor &q, &k, &v, &g;
+    const at::Tensor* cu;
+    at::ScalarType io;
+    int64_t B, T, Hqk, K, H, V, N;
+    kda_decay_opts o{};
+    kda_dims d{};
+
+    DecayInputs(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* g_, PyObject* cu_)
+        : q(tensor(q_, "q")), k(tensor(k_, "k")), v(tensor(v_, "v")), g(tensor(g_, "g")), cu(optional(cu_, "cu_seqlens")) {
+        io = q.scalar_type();
+        need(io == at::kBFloat16 || io == at::kHalf, "q must be bf16 or fp16");
+        need(q.dim() == 4 && k.sizes() == q.sizes() && v.dim() == 4 && v.size(0) == q.size(0) && v.size(1) == q.size(1),
+             "q and k are [B,T,Hqk,K], v is [B,T,H,V]");
+        B = q.size(0), T = q.size(1), Hqk = q.size(2), K = q.size(3), H = v.size(2), V = v.size(3);
+        need(k.scalar_type() == io && v.scalar_type() == io && g.scalar_type() == at::kFloat,
+             "k and v have q's dtype, g is float32");
+        const bool head_gate = g.dim() == 1;
+        need(head_gate ? same_shape(g, {H}) && g.is_contiguous() : same_shape(g, {B, T, H}), "g is [B,T,H] or contiguous [H]");
+        need(B <= INT32_MAX && T <= INT32_MAX && H <= INT32_MAX, "sizes beyond 32 bits");
+        need(Hqk > 0 || H == 0, "q and k have no heads");
+        N = B;
+        if (cu) {
+            N = cu->numel() - 1;
+            need(cu->scalar_type() == at::kInt && cu->is_cuda() && cu->is_contiguous() && N >= 1 && N <= INT32_MAX,
+                 "cu_seqlens must be a contiguous CUDA int32 tensor [N+1]");
+        }
+        need(q.is_cuda() && k.is_cuda() && v.is_cuda() && g.is_cuda(), "q, k, v and g must be CUDA tensors");
+        o.io_dtype = io == at::kHalf ? KDA_IO_F16 : KDA_IO_BF16;
+        o.qk_heads = Hqk == H ? 0 : (int32_t)Hqk;
+        o.head_gate = head_gate;
+        o.q_stride = token_stride("q", q);
+        o.k_stride = token_stride("k", k);
+        o.v_stride = token_stride("v", v);
+        if (!head_gate) o.g_stride = token_stride("g", g);
+        d = kda_dims{(int32_t)B, (int32_t)T, (int32_t)H, (int32_t)K, (int32_t)V, cu ? (int32_t)N : 0};
+    }
+    float scale(PyObject* s) const { return s == Py_None ? 1.f / std::sqrt((float)K) : (float)number(s); }
+    const float* gates() const { return static_cast<const float*>(g.data_ptr()); }
+    const int32_t* offsets() const { return static_cast<const int32_t*>(address(cu)); }
+    // A state of [N,H,K,V], fp32 or bf16.
+    void need_state(const at::Tensor* s, const char* text) const {
+        need(!s || ((s->scalar_type() == at::kFloat || s->scalar_type() == at::kBFloat16) && s->is_cuda() &&
+                    s->is_contiguous() && same_shape(*s, {N, H, K, V})),
+             text);
+    }
+    void need_like(const at::Tensor* t, const at::Tensor& like, const char* text) const {
+        need(!t || (t->scalar_type() == io && t->sizes() == like.sizes() && t->is_cuda() && t->is_contiguous()), text);
+    }
+};
+// The workspace that the call needs: the caller's, or one allocated for its stream.
+at::Tensor workspace_of(const DecayInputs& x, const at::Tensor* given, bool backward, size_t* bytes, void** at_) {
+    const size_t want = kda_decay_workspace_size(&x.d, &x.o, backward);
+    at::Tensor made;
+    if (given) {
+        need(given->scalar_type() == at::kByte && given->is_cuda() && given->is_contiguous(),
+             "workspace must be a contiguous CUDA uint8 tensor");
+        *bytes = (size_t)given->numel();
+        *at_ = given->data_ptr();
+    } else {
+        *bytes = want == (size_t)-1 ? 0 : want;
+        if (*bytes) {  // (torch's blocks start on 512 bytes, the workspace on 1024)
+            made = empty({(int64_t)*bytes + 512}, at::kByte, x.q);
+            *at_ = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(made.data_ptr()) + 1023) & ~(uintptr_t)1023);
+        } else {
+            *at_ = nullptr;
+        }
+    }
+    return made;
+}
+PyObject* wrapped(at::Tensor&& t) {
+    if (t.defined()) return THPVariable_Wrap(std::move(t));
+    Py_RETURN_NONE;
+}
+PyObject* packed_up(std::initializer_list<PyObject*> items) {  // a tuple that takes the references
+    bool all = true;
+    for (PyObject* i : items) all = all && i;
+    PyObject* t = all ? PyTuple_New((Py_ssize_t)items.size()) : nullptr;
+    Py_ssize_t n = 0;
+    for (PyObject* i : items) {
+        if (t) PyTuple_SET_ITEM(t, n++, i);
+        else Py_XDECREF(i);
+    }
+    return t;
+}
+
+// q, k, v, g, scale, h0, cu_seqlens, output_final_state, state_dtype, workspace, out, final_state, status, stream
+PyObject* call_decay_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 14, [&]() -> PyObject* {
+        DecayInputs x(a[0], a[1], a[2], a[3], a[6]);
+        const at::Tensor *h0 = optional(a[5], "h0"), *ws = optional(a[9], "workspace"), *out = optional(a[10], "out"),
+                         *final_state = optional(a[11], "final_state"), *status = optional(a[12], "status");
+        const int with_state = PyObject_IsTrue(a[7]);
+        if (with_state < 0) throw Refused{nullptr, ""};
+        x.need_state(h0, "h0 must be a contiguous CUDA tensor [N,H,K,V] of float32 or bfloat16");
+        x.need_state(final_state, "final_state must be a contiguous CUDA tensor [N,H,K,V] of float32 or bfloat16");
+        at::ScalarType st = h0 ? h0->scalar_type() : final_state ? final_state->scalar_type() : at::kFloat;
+        if (a[8] != Py_None) {
+            if (!THPDtype_Check(a[8])) refuse("state_dtype must be a torch.dtype");
+            st = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+        }
+        need(st == at::kFloat || st == at::kBFloat16, "the state dtype is float32 or bfloat16");
+        need((!h0 || h0->scalar_type() == st) && (!final_state || final_state->scalar_type() == st),
+             "h0 and ht must have the same dtype");
+        x.need_like(out, x.v, "out must be a contiguous CUDA tensor of v's shape and dtype");
+        need_one_device(x.q, {&x.k, &x.v, &x.g, x.cu, h0, ws, out, final_state, status});
+        x.o.state_dtype = st == at::kBFloat16 ? KDA_STATE_BF16 : KDA_STATE_F32;
+        const float scale = x.scale(a[4]);
+        const Place place(a[13], x.q);
+        size_t bytes = 0;
+        void* at_ = nullptr;
+        const at::Tensor held = workspace_of(x, ws, false, &bytes, &at_);
+        at::Tensor made, ht;
+        if (!out) made = empty(x.v.sizes(), x.io, x.q);
+        if (with_state && !final_state) ht = empty({x.N, x.H, x.K, x.V}, st, x.q);
+        check(kda_decay_fwd(x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(), x.gates(), scale, address(h0), x.offsets(),
+                            out ? out->data_ptr() : made.data_ptr(),
+                            !with_state ? nullptr : final_state ? final_state->data_ptr() : ht.data_ptr(), &x.d, &x.o,
+                            status_word(status), at_, bytes, place.stream()),
+              "kda_decay_fwd");
+        PyObject* state = with_state ? kept(a[11], std::move(ht)) : (Py_INCREF(Py_None), Py_None);
+        return packed_up({kept(a[10], std::move(made)), state});
+    });
+}
+
+// q, k, v, g, do, scale, h0, dht, cu_seqlens, want_dh0, workspace, status, stream
+PyObject* call_decay_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject* {
+        DecayInputs x(a[0], a[1], a[2], a[3], a[8]);
+        const at::Tensor& d_o = tensor(a[4], "do");
+        const at::Tensor *h0 = optional(a[6], "h0"), *dht = optional(a[7], "dht"), *ws = optional(a[10], "workspace"),
+                         *status = optional(a[11], "status");
+        const int want = PyObject_IsTrue(a[9]);
+        if (want < 0) throw Refused{nullptr, ""};
+        need(d_o.scalar_type() == x.io && d_o.sizes() == x.v.sizes() && d_o.is_cuda(), "do must be a CUDA tensor of v's shape and dtype");
+        x.need_state(h0, "h0 must be a contiguous CUDA tensor [N,H,K,V] of float32 or bfloat16");
+        x.need_state(dht, "dht must be a contiguous CUDA tensor [N,H,K,V] of float32 or bfloat16");
+        const at::ScalarType st = h0 ? h0->scalar_type() : dht ? dht->scalar_type() : at::kFloat;
+        need(!dht || dht->scalar_type() == st, "h0 and dht must have the same dtype");
+        need_one_device(x.q, {&x.k, &x.v, &x.g, &d_o, x.cu, h0, dht, ws, status});
+        x.o.state_dtype = st == at::kBFloat16 ? KDA_STATE_BF16 : KDA_STATE_F32;
+        x.o.do_stride = token_stride("do", d_o);
+        const float scale = x.scale(a[5]);
+        const Place place(a[12], x.q);
+        size_t bytes = 0;
+        void* at_ = nullptr;
+        const at::Tensor held = workspace_of(x, ws, true, &bytes, &at_);
+        at::Tensor dq = empty(x.q.sizes(), x.io, x.q), dk = empty(x.q.sizes(), x.io, x.q), dv = empty(x.v.sizes(), x.io, x.q),
+                   dg = empty(x.g.sizes(), at::kFloat, x.q), dh0;
+        if (want) dh0 = empty({x.N, x.H, x.K, x.V}, st, x.q);
+        check(kda_decay_bwd(x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(), x.gates(), d_o.data_ptr(), scale, address(h0),
+                            address(dht), x.offsets(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                            static_cast<float*>(dg.data_ptr()), want ? dh0.data_ptr() : nullptr, &x.d, &x.o,
+                            status_word(status), at_, bytes, place.stream()),
+              "kda_decay_bwd");
+        return packed_up({wrapped(std::move(dq)), wrapped(std::move(dk)), wrapped(std::move(dv)), wrapped(std::move(dg)),
+                          wrapped(std::move(dh0))});
+    });
+}
+
+// q, k, v, g, state, slots, scale, cu_seqlens, out, status, stream
+PyObject* call_decay_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        DecayInputs x(a[0], a[1], a[2], a[3], a[7]);
+        const at::Tensor& state = tensor(a[4], "state");
+        const at::Tensor *slots = optional(a[5], "slots"), *out = optional(a[8], "out"), *status = optional(a[9], "status");
+        const bool s16 = state.scalar_type() == at::kBFloat16;
+        need((s16 || state.scalar_type() == at::kFloat) && state.is_contiguous() && state.dim() == 4 && state.is_cuda() &&
+                 same_shape(state, {state.size(0), x.H, x.K, x.V}) && state.size(0) <= INT32_MAX,
+             "state must be a contiguous CUDA float32 or bfloat16 tensor [num_slots,H,K,V]");
+        need(!slots || (slots->scalar_type() == at::kInt && slots->is_cuda() && slots->is_contiguous() && slots->numel() == x.N),
+             "slots must be a contiguous CUDA int32 tensor, one per sequence");
+        x.need_like(out, x.v, "out must be a contiguous CUDA tensor of v's shape and dtype");
+        need_one_device(x.q, {&x.k, &x.v, &x.g, &state, slots, x.cu, out, status});
+        x.o.state_dtype = s16 ? KDA_STATE_BF16 : KDA_STATE_F32;
+        x.o.num_slots = (int32_t)state.size(0);
+        const float scale = x.scale(a[6]);
+        const Place place(a[10], x.q);
+        at::Tensor made;
+        if (!out) made = empty(x.v.sizes(), x.io, x.q);
+        check(kda_decay_step(x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(), x.gates(), scale, state.data_ptr(),
+                             static_cast<const int32_t*>(address(slots)), x.offsets(), out ? out->data_ptr() : made.data_ptr(),
+                             &x.d, &x.o, status_word(status), place.stream()),
+              "kda_decay_step");
+        return kept(a[8], std::move(made));
+    });
+}
+
+// q, k, positions, freqs, amplitude, interleaved, inverse, q_out, k_out, stream
+PyObject* call_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &pos = tensor(a[2], "positions"), &freqs = tensor(a[3], "freqs");
+        const at::Tensor *k = optional(a[1], "k"), *q_out = optional(a[7], "q_out"), *k_out = optional(a[8], "k_out");
+        const at::ScalarType io = q.scalar_type();
+        need((io == at::kBFloat16 || io == at::kHalf || io == at::kFloat) && q.is_cuda() && q.dim() == 4,
+             "q must be a CUDA tensor [B,T,H,D] of bf16, fp16 or fp32");
+        const int64_t B = q.size(0), T = q.size(1), D = q.size(3);
+        need(!k || (k->scalar_type() == io && k->is_cuda() && k->dim() == 4 && k->size(0) == B && k->size(1) == T && k->size(3) == D),
+             "k must be a CUDA tensor [B,T,Hk,D] of q's dtype");
+        need((pos.scalar_type() == at::kInt || pos.scalar_type() == at::kLong) && pos.is_cuda() && pos.is_contiguous() &&
+                 same_shape(pos, {B, T}),
+             "positions must be a contiguous CUDA int32 or int64 tensor [B,T]");
+        need(freqs.scalar_type() == at::kDouble && freqs.is_cuda() && freqs.is_contiguous() && freqs.dim() == 1 &&
+                 freqs.numel() >= 1 && 2 * freqs.numel() <= D,
+             "freqs must be a contiguous CUDA float64 tensor of at most D / 2 frequencies");
+        need(!q_out || (q_out->scalar_type() == io && q_out->sizes() == q.sizes() && q_out->is_cuda()),
+             "q_out must be a CUDA tensor of q's shape and dtype");
+        need(!k_out || (k && k_out->scalar_type() == io && k_out->sizes() == k->sizes() && k_out->is_cuda()),
+             "k_out must be a CUDA tensor of k's shape and dtype");
+        need(q.size(2) >= 1 && q.size(2) <= INT32_MAX && D <= INT32_MAX && (!k || (k->size(2) >= 1 && k->size(2) <= INT32_MAX)),
+             "q and k have at least one head");
+        need_one_device(q, {k, &pos, &freqs, q_out, k_out});
+        kda_rotary_opts o{};
+        o.io_dtype = dtype_code(io);
+        o.pairs = (int32_t)freqs.numel();
+        o.positions_i64 = pos.scalar_type() == at::kLong;
+        const int inter = PyObject_IsTrue(a[5]), inv = PyObject_IsTrue(a[6]);
+        if (inter < 0 || inv < 0) throw Refused{nullptr, ""};
+        o.interleaved = inter;
+        o.inverse = inv;
+        o.amplitude = (float)number(a[4]);
+        o.q_stride = token_stride("q", q);
+        o.k_stride = k ? token_stride("k", *k) : 0;
+        o.q_out_stride = q_out ? token_stride("q_out", *q_out) : 0;
+        o.k_out_stride = k_out ? token_stride("k_out", *k_out) : 0;
+        const Place place(a[9], q);
+        at::Tensor qm, km;
+        if (!q_out) qm = empty(q.sizes(), io, q);
+        if (k && !k_out) km = empty(k->sizes(), io, q);
+        check(kda_rotary(q.data_ptr(), address(k), pos.data_ptr(), static_cast<const double*>(freqs.data_ptr()),
+                         q_out ? q_out->data_ptr() : qm.data_ptr(),
+                         !k ? nullptr : k_out ? k_out->data_ptr() : km.data_ptr(), B * T, (int32_t)q.size(2),
+                         k ? (int32_t)k->size(2) : 0, (int32_t)D, &o, place.stream()),
+              "kda_rotary");
+        PyObject* second = k ? kept(a[8], std::move(km)) : (Py_INCREF(Py_None), Py_None);
+        return packed_up({kept(a[7], std::move(qm)), second});
+    });
+}
+
 // KdaError, called as KdaError(code, where)
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_INCREF(type);
@@ -382,6 +624,10 @@ PyMethodDef kMethods[] = {
     {"step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_step)), METH_FASTCALL, nullptr},
     {"rms_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_rms_norm)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_linear)), METH_FASTCALL, nullptr},
+    {"decay_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_decay_fwd)), METH_FASTCALL, nullptr},
+    {"decay_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_decay_bwd)), METH_FASTCALL, nullptr},
+    {"decay_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_decay_step)), METH_FASTCALL, nullptr},
+    {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call_rotary)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -486,6 +486,103 @@ kda_status kda_linear(const void* x, const void* w, const float* bias, const voi
                       const float* w_scale, void* y, int64_t M, int64_t N, int64_t K, const kda_linear_opts* opts,
                       int32_t* status_word, void* stream);
 
+/*
+ * Linear attention with one decay per head, a state S [K, V] per (sequence, head):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t.
+ * kda_decay_fwd takes whole prompts (in chunks of 128 tokens on the tensor cores),
+ * kda_decay_bwd their gradients, kda_decay_step the few new tokens of a decode step.
+ * The dims and packed sequences are kda_fwd's; K, V in {64, 128}.
+ *   q, k      [B, T, Hqk, K], v, o [B, T, H, V]: bf16 or fp16 (io_dtype); Hqk =
+ *             qk_heads divides H, value head h reads q/k head h / (H / Hqk)
+ *   g         fp32 [B, T, H] natural-log decay (g <= 0 expected; below -140 a state is
+ *             lost either way, and g counts as -140), or, with head_gate, [H]: a constant decay per head
+ *   state_dtype  of h0, ht, dht, dh0 [N, H, K, V] and of the step's cache
+ *   *_stride  elements between the rows of consecutive tokens (0: contiguous); do_stride: of d_o
+ *   status_word  device int32 or NULL: takes errors in the contents of cu_seqlens (then nothing
+ *             is written) and slots, and waits that ran out (results are then incomplete), as in kda_step
+ * q, k, v and d_o of fwd and bwd are 16-byte aligned with strides of a multiple of 8
+ * elements; o, states and gradients are contiguous and 16-byte aligned (KDA_ERR_ALIGNMENT).
+ * Inputs are finite: a value that is not reaches the other tokens of its chunk.
+ * Scores and states are rounded to io_dtype as operands of their products (states in
+ * fp16 by a common power of two, so they keep fp32's range); the states themselves, and
+ * what adds to them, keep 2^-17 of themselves or better. Results do not depend on timing (no atomics).
+ */
+typedef struct kda_decay_opts {
+    int32_t io_dtype;
+    int32_t state_dtype;
+    int32_t qk_heads;   /* 0: H */
+    int32_t head_gate;
+    int32_t num_slots;  /* kda_decay_step only, else 0 */
+    int32_t reserved;   /* 0 */
+    int64_t q_stride, k_stride, v_stride, g_stride, do_stride;
+} kda_decay_opts;
+
+/*
+ * Bytes of workspace that kda_decay_fwd (backward = 0) or kda_decay_bwd (1) needs, a function of the
+ * dims and opts alone (0 can be enough: many sequences x heads, forwards). (size_t)-1 for invalid dims.
+ * Long sequences of few heads are cut into pieces that run side by side: a pass over k and v
+ * finds what each adds to the state, a join gives each its entry state. The backward keeps
+ * the state before every chunk and its gradient: 8 K V bytes per 128 tokens and head.
+ * Workspaces are 1024-byte aligned; calls that may run concurrently do not share one.
+ */
+size_t kda_decay_workspace_size(const kda_dims* dims, const kda_decay_opts* opts, int32_t backward);
+
+/*
+ * The forward: o and the states after the sequences. h0, ht: state_dtype or NULL (zeros, not stored); ht is
+ * not h0's memory (KDA_ERR_INVALID_ARG). A sequence without tokens has ht = h0.
+ */
+kda_status kda_decay_fwd(const void* q, const void* k, const void* v, const float* g, float scale, const void* h0,
+                         const int32_t* cu_seqlens, void* o, void* ht, const kda_dims* dims, const kda_decay_opts* opts,
+                         int32_t* status_word, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, from those of o (d_o [B, T, H, V] of io_dtype) and ht (dht, or NULL: zeros):
+ *   dq, dk    [B, T, Hqk, K] of io_dtype, summed over the value heads that share them
+ *   dv        [B, T, H, V] of io_dtype
+ *   dg        fp32 [B, T, H], or [H] with head_gate
+ *   dh0       [N, H, K, V] of state_dtype, or NULL: not stored; neither h0's memory nor dht's
+ * The forward is computed again as far as needed; nothing of it has to be kept.
+ */
+kda_status kda_decay_bwd(const void* q, const void* k, const void* v, const float* g, const void* d_o, float scale,
+                         const void* h0, const void* dht, const int32_t* cu_seqlens, void* dq, void* dk, void* dv,
+                         float* dg, void* dh0, const kda_dims* dims, const kda_decay_opts* opts, int32_t* status_word,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode step, token by token in fp32 on chip: state [num_slots, H, K, V], slots, cu_seqlens, padding
+ * and errors as in kda_step. q, k and v are aligned to their elements.
+ */
+kda_status kda_decay_step(const void* q, const void* k, const void* v, const float* g, float scale, void* state,
+                          const int32_t* slots, const int32_t* cu_seqlens, void* o, const kda_dims* dims,
+                          const kda_decay_opts* opts, int32_t* status_word, void* stream);
+
+/*
+ * Rotary positions: in every head of q and k the first 2 * pairs elements are turned in pairs (x, y),
+ *     x' = amplitude (x cos a - y sin a),  y' = amplitude (x sin a + y cos a),  a = position * freq,
+ * and the rest is copied. Pairs are (i, i + pairs), or with `interleaved` (2 i, 2 i + 1). With
+ * `inverse` the angle is -a (the gradients of q and k from those of their turned values).
+ *   q, q_out  [tokens, q_heads, dim], k, k_out [tokens, k_heads, dim] bf16, fp16 or fp32 (io_dtype);
+ *             k_heads = 0: no k.  An output may be its input with the same stride.
+ *   positions int32, or int64 with positions_i64, [tokens]: any value
+ *   freqs     fp64 [pairs] radians per position; a is right to 2^-31 of a turn beside 2^-53 of position * freq
+ *   *_stride  elements between tokens (0: contiguous); any alignment of the elements' own size is
+ *             taken, rows on 16 bytes with dim and pairs of whole 16-byte pieces in 16-byte loads
+ * pairs in 1 .. 512 (KDA_ERR_UNSUPPORTED above), at most dim / 2.  Asynchronous on `stream`.
+ */
+typedef struct kda_rotary_opts {
+    int32_t io_dtype;  /* KDA_DTYPE_BF16, _F16 or _F32 */
+    int32_t pairs;
+    int32_t positions_i64;
+    int32_t interleaved;
+    int32_t inverse;
+    int32_t reserved;  /* 0 */
+    float amplitude;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} kda_rotary_opts;
+kda_status kda_rotary(const void* q, const void* k, const void* positions, const double* freqs, void* q_out,
+                      void* k_out, int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t dim,
+                      const kda_rotary_opts* opts, void* stream);
+
 /* Static description of a status code.  Never NULL. */
 const char* kda_status_string(kda_status s);
 
