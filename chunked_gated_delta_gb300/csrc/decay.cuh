@@ -57,6 +57,7 @@ struct DecayScanArgs {
     const float* g;      // fp32: g[row * g_stride + h] (g_stride 0: one decay per head)
     int64_t g_stride;
     uint16_t* o;         // [rows, H, V]
+    CUtensorMap tm_o;    // the same, 3-D {V, H, rows}, boxes of 64 x 32 rows
     int32_t* status;     // or null
     float scale;
     int32_t H, group;    // value heads, value heads per q/k head
@@ -238,16 +239,42 @@ __device__ __forceinline__ Pair sum_decay(const LoadedG& g, ChunkDecay& out, int
     }
     return {__shfl_sync(~0u, run.hi, 31), __shfl_sync(~0u, run.lo, 31)};
 }
-// exp of a chunk's whole decay, to half a last bit: a state of thousands of chunks is multiplied by
-// one after the other, so their errors add up.
-// (2^n times the power series of exp(f ln 2) to its ninth term, |f| <= 1/2: what is left is below 2^-33.)
+// exp of a chunk's whole decay, to less than its last bit: a state of thousands of chunks is multiplied by
+// one after the other, so their errors add up. 2^n times the power series of exp(x), |x| <= ln(2) / 2, to its
+// ninth term (what is left is below 2^-33); only the last addition rounds at the size of the result.
 __device__ __forceinline__ float whole_decay(Pair p) {
     const float n = rintf(p.hi);
-    const double x = ((double)(p.hi - n) + (double)p.lo) * 0.6931471805599453;
-    double r = 1.0;
-#pragma unroll 1
-    for (int i = 9; i > 0; --i) r = fma(r, x * (double)(1.f / (float)i), 1.0);
-    return ldexpf((float)r, (int)n);
+    const float x = ((p.hi - n) + p.lo) * 0.693147181f;
+    float r = fmaf(x, 1.f / 362880, 1.f / 40320);
+    r = fmaf(x, r, 1.f / 5040);
+    r = fmaf(x, r, 1.f / 720);
+    r = fmaf(x, r, 1.f / 120);
+    r = fmaf(x, r, 1.f / 24);
+    r = fmaf(x, r, 1.f / 6);
+    r = fmaf(x, r, 0.5f);
+    return ldexpf(1.f + fmaf(x * x, r, x), (int)n);
+}
+
+// ------------------------------------------------------------------ two fp32 at a time
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 floats_of(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // ------------------------------------------------------------------ shared memory by 32-bit address
@@ -264,6 +291,29 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // Row `row` of a tile of 128-byte swizzled rows: its 16-byte piece c is at this ^ (c << 4).
 __device__ __forceinline__ uint32_t swizzled_row(uint32_t tile, int row) {
     return tile + (uint32_t)row * 128u + (uint32_t)((row & 7) << 4);
+}
+
+// ------------------------------------------------------------------ waits
+// A wait that runs out (after kWaitLimitNs, like all of them) is noted in `fail`, and from then on nobody waits: every
+// warp still goes through all of its barriers, so none is left standing at one. Results are then incomplete, and the
+// status says so. Few instructions, since every role has many of these in a loop that it goes through once per chunk.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ void wait_or_note(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
+    static_assert(kWaitLimitNs < (1ull << 32), "the timer's low word wraps around in 4.3 s");
+    // (the timer takes hundreds of cycles to read: after each thousand tries)
+    uint32_t tries = 0, t0 = 0;
+#pragma unroll 1
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if ((++tries & 1023) != 0) continue;
+        if (*fail) return;
+        const uint32_t t = globaltimer_lo();
+        if (tries == 1024) t0 = t;
+        else if (t - t0 > (uint32_t)kWaitLimitNs) *fail = 1;
+    }
 }
 
 // ------------------------------------------------------------------ tcgen05

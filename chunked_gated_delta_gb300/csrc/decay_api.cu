@@ -6,11 +6,16 @@ namespace kda {
 namespace {
 
 // How sequences are cut. The scan walks a piece's chunks one after the other; pieces are worth a pass over k
-// and v (what each adds to the state) where uncut sequences leave SMs idle. The model: microseconds
-// per chunk of a CTA with output and without, CTAs in rounds of the SMs, and the extra launches. It
-// depends on the dims alone, as the workspace does.
+// and v (what each adds to the state) where uncut sequences leave SMs idle. The model, in measured microseconds: a
+// CTA's start and each of its chunks, with output, without, and keeping the states (backward); CTAs in
+// rounds of the SMs (packed: their work shared out, and the longest); and the join. It depends on the dims
+// alone, as the workspace does.
 constexpr int kDecaySMs = 152;
-constexpr double kOutUs = 2.4, kStateUs = 1.4, kJoinUs = 6.0;
+struct PassUs {
+    double start, chunk;
+};
+constexpr PassUs kOutUs{8.0, 3.0}, kTotalsUs{6.0, 2.0}, kKeepUs{7.0, 2.9};
+constexpr double kJoinUs = 7.0;
 constexpr int kUncut = 1 << 23;   // chunks per piece: more than any sequence has
 constexpr int kMostPieces = 64;   // per sequence
 
@@ -27,18 +32,25 @@ DecayPlan decay_plan(const kda_dims& d, bool backward) {
     // packed lengths are not known here: a few times their mean is planned for
     const int64_t mean = (all + N - 1) / N, nc = !packed ? all : all < 4 * mean ? all : 4 * mean;
     const int dirs = backward ? 2 : 1;
-    const double pass = backward ? kStateUs : kOutUs;
-    auto rounds = [](int64_t ctas) { return (double)((ctas + kDecaySMs - 1) / kDecaySMs); };
+    const PassUs pass = backward ? kKeepUs : kOutUs;
+    const int64_t units = N * d.H * dirs;
     auto pieces_of = [&](int64_t len) { return packed ? all / len + N : N * ((all + len - 1) / len); };
+    auto time_of = [&](const PassUs& us, int64_t ctas, int64_t len) {
+        if (packed) {
+            const double work = (us.start * (double)ctas + us.chunk * (double)(all * d.H * dirs)) / kDecaySMs;
+            const double longest = us.start + us.chunk * (double)len;
+            return work > longest ? work : longest;
+        }
+        return (us.start + us.chunk * (double)len) * (double)((ctas + kDecaySMs - 1) / kDecaySMs);
+    };
     DecayPlan p{};
     p.N = (int32_t)N;
     p.seg_chunks = kUncut;
     p.chunks = packed ? d.T / kDecayChunk + N : N * all;
-    double best = 0.9 * (double)nc * pass * rounds(N * d.H * dirs);
+    double best = 0.9 * time_of(pass, units, nc);
     for (int64_t S = 2; S <= kMostPieces && 2 * S <= nc; ++S) {
-        const int64_t len = (nc + S - 1) / S;
-        const int64_t n = pieces_of(len) * d.H * dirs;
-        const double cost = (double)len * (kStateUs * rounds(n - N * d.H * dirs) + pass * rounds(n)) + kJoinUs;
+        const int64_t len = (nc + S - 1) / S, n = pieces_of(len) * d.H * dirs;
+        const double cost = time_of(kTotalsUs, n - units, len) + time_of(pass, n, len) + kJoinUs;
         if (cost < best) best = cost, p.seg_chunks = (int32_t)len;
     }
     p.pieces = p.cut() ? pieces_of(p.seg_chunks) : N;
@@ -113,11 +125,11 @@ kda_status strides_of(const kda_dims& d, const kda_decay_opts& p, bool backward,
     return KDA_OK;
 }
 
-bool token_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t rows, int64_t stride) {
+bool token_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t rows, int64_t stride, int box_rows = kDecayChunk) {
     if (rows == 0) return true;  // (never read)
     const uint64_t dims[3] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)rows};
     const uint64_t strides[2] = {(uint64_t)dim * 2, (uint64_t)stride * 2};
-    const uint32_t box[3] = {64, 1, (uint32_t)kDecayChunk};
+    const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
     return make_tensormap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -159,7 +171,7 @@ extern "C" kda_status kda_decay_fwd(const void* q, const void* k, const void* v,
     const bool f16 = opts->io_dtype == KDA_IO_F16;
     DecayScanArgs a{};
     if (!token_map(&a.dir[0].tm_x, k, d.K, hq, rows, sd.k) || !token_map(&a.dir[0].tm_y, v, d.V, d.H, rows, sd.v) ||
-        !token_map(&a.tm_q, q, d.K, hq, rows, sd.q))
+        !token_map(&a.tm_q, q, d.K, hq, rows, sd.q) || !token_map(&a.tm_o, o, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
         return KDA_ERR_CUDA;
     const int32_t b16 = opts->state_dtype == KDA_STATE_BF16;
     a.dir[0].start = {const_cast<void*>(h0), b16};

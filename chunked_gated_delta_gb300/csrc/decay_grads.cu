@@ -106,10 +106,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    // (A wait that runs out is noted, and from then on nobody waits; see decay_scan.cuh.)
     volatile int32_t* fail = &sm.fail;
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-        if (!*fail && !wait_for(&bar, parity)) *fail = 1;
+        wait_or_note(&bar, parity, fail);
         return !*fail;
     };
 

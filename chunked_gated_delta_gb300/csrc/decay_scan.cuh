@@ -29,15 +29,16 @@ struct DecayScanShape {
     static constexpr int K = 64 * KB, V = 64 * VB;
     static constexpr int kThreads = OUT ? 640 : 384;
     static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kStateBytes = V * K * 2;
-    // Stages: k and q are read early in a chunk (the scaled parts of k have buffers of their own) and have one each
-    // where two do not fit.
-    static constexpr int kYStages = 2;
-    static constexpr int kRest = kYStages * kYBytes + 2 * kXBytes + (OUT ? 1 : 2) * kStateBytes;
-    static constexpr int kXStages = kRest + (OUT ? 4 : 2) * kXBytes <= 224 * 1024 ? 2 : 1;
-    static constexpr int kY = 0, kX = kYStages * kYBytes, kQ = kX + kXStages * kXBytes;
+    // Stages: every tensor's tile is read early in a chunk (the scaled parts of k have buffers of their own, and so has
+    // o), so one of each is enough where two do not fit.
+    static constexpr int kOne = kXBytes * (OUT ? 2 : 1) + kYBytes;
+    static constexpr int kFixed = 2 * kXBytes + (OUT ? 1 : 2) * kStateBytes + (OUT ? kYBytes : 0);
+    static constexpr int kStages = kFixed + 2 * kOne <= 224 * 1024 ? 2 : 1;
+    static constexpr int kY = 0, kX = kStages * kYBytes, kQ = kX + kStages * kXBytes;
     // (where V = 64 the MMAs with v^T read 128 columns, the second half from what follows, into lanes nobody reads)
-    static constexpr int kHi = OUT ? kQ + kXStages * kXBytes : kQ, kLo = kHi + kXBytes, kS = kLo + kXBytes;
-    static constexpr int kSmall = kS + (OUT ? 1 : 2) * kStateBytes;
+    static constexpr int kHi = OUT ? kQ + kStages * kXBytes : kQ, kLo = kHi + kXBytes, kS = kLo + kXBytes;
+    static constexpr int kO = kS + (OUT ? 1 : 2) * kStateBytes;
+    static constexpr int kSmall = kO + (OUT ? kYBytes : 0);
     // registers: those that the block is launched with, handed out as control, keys, state, scores, output
     static constexpr int kControlRegs = OUT ? 64 : 64, kKeyRegs = OUT ? 64 : 176, kStateRegs = OUT ? 184 : 240;
     static constexpr int kScoreRegs = 80, kOutRegs = 88;
@@ -65,7 +66,7 @@ template <int KB, int VB, bool F16, bool OUT>
 __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     kda_decay_scan_kernel(const __grid_constant__ DecayScanArgs a) {
     using Shape = DecayScanShape<KB, VB, OUT>;
-    constexpr int K = Shape::K, V = Shape::V, NX = Shape::kXStages;
+    constexpr int K = Shape::K, V = Shape::V, NS = Shape::kStages;
     extern __shared__ __align__(1024) uint8_t raw[];
     auto& sm = *reinterpret_cast<typename Shape::Small*>(raw + Shape::kSmall);
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31, quarter = warp & 3;
@@ -114,12 +115,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem, base = ptx::smem_u32(raw);
-    // A wait that runs out is noted, and from then on nobody waits: every warp still goes through all of its
-    // barriers, so none is left standing at one.  Results are then incomplete, and the status says so.
     volatile int32_t* fail = &sm.fail;
-    auto wait = [&](uint64_t& bar, uint32_t parity) {
-        if (!*fail && !wait_for(&bar, parity)) *fail = 1;
-    };
+    auto wait = [&](uint64_t& bar, uint32_t parity) { wait_or_note(&bar, parity, fail); };
     auto arrive = [&](uint64_t& bar) {  // once per warp
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bar);
@@ -132,32 +129,32 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             const int hq = h / a.group;
             int it = 0;
             for (; it < chunks; ++it) {
-                const int sx = it % NX, sy = it & 1, row = at.bos + chunk_at(it) * kDecayChunk;
-                const uint32_t px = ((it / NX) & 1) ^ 1, py = ((it >> 1) & 1) ^ 1;  // of the stage's last use
-                if (it >= NX) wait(sm.x_empty[sx], px);
+                const int sx = it % NS, row = at.bos + chunk_at(it) * kDecayChunk;
+                const uint32_t px = ((it / NS) & 1) ^ 1;  // of the stage's last use
+                if (it >= NS) wait(sm.x_empty[sx], px);
                 if (*fail) break;
                 ptx::mbar_arrive_expect_tx(&sm.x_full[sx], Shape::kXBytes);
                 for (int b = 0; b < KB; ++b)
                     ptx::tma_load_3d(raw + Shape::kX + sx * Shape::kXBytes + b * 16384, &dir.tm_x, &sm.x_full[sx], b * 64,
                                      hq, row);
                 if constexpr (OUT) {
-                    if (it >= NX) wait(sm.q_empty[sx], px);
+                    if (it >= NS) wait(sm.q_empty[sx], px);
                     ptx::mbar_arrive_expect_tx(&sm.q_full[sx], Shape::kXBytes);
                     for (int b = 0; b < KB; ++b)
                         ptx::tma_load_3d(raw + Shape::kQ + sx * Shape::kXBytes + b * 16384, &a.tm_q, &sm.q_full[sx],
                                          b * 64, hq, row);
                 }
-                if (it >= 2) wait(sm.y_empty[sy], py);
-                ptx::mbar_arrive_expect_tx(&sm.y_full[sy], Shape::kYBytes);
+                if (it >= NS) wait(sm.y_empty[sx], px);
+                ptx::mbar_arrive_expect_tx(&sm.y_full[sx], Shape::kYBytes);
                 for (int b = 0; b < VB; ++b)
-                    ptx::tma_load_3d(raw + Shape::kY + sy * Shape::kYBytes + b * 16384, &dir.tm_y, &sm.y_full[sy], b * 64,
+                    ptx::tma_load_3d(raw + Shape::kY + sx * Shape::kYBytes + b * 16384, &dir.tm_y, &sm.y_full[sx], b * 64,
                                      h, row);
             }
             if (*fail)  // let the copies in flight land
-                for (int i = max(0, it - 2); i < it; ++i) {
-                    wait_for(&sm.x_full[i % NX], (i / NX) & 1);
-                    if (OUT) wait_for(&sm.q_full[i % NX], (i / NX) & 1);
-                    wait_for(&sm.y_full[i & 1], (i >> 1) & 1);
+                for (int i = max(0, it - NS); i < it; ++i) {
+                    wait_for(&sm.x_full[i % NS], (i / NS) & 1);
+                    if (OUT) wait_for(&sm.q_full[i % NS], (i / NS) & 1);
+                    wait_for(&sm.y_full[i % NS], (i / NS) & 1);
                 }
         } else if (warp == 1 && elect_one()) {
             // ---------------------------------------------------------- MMAs
@@ -166,9 +163,9 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             const uint64_t hi_mn = ptx::smem_desc(base + Shape::kHi, 16384, 1024);
             const uint64_t s_k = ptx::smem_desc(base + Shape::kS, 16, 1024);
             for (int it = 0; it < chunks && !*fail; ++it) {
-                const int sx = it % NX, sy = it & 1;
-                const uint32_t ph = it & 1, px = (it / NX) & 1;
-                const uint64_t y_mn = ptx::smem_desc(base + Shape::kY + sy * Shape::kYBytes, 16384, 1024);
+                const int sx = it % NS;
+                const uint32_t ph = it & 1, px = (it / NS) & 1;
+                const uint64_t y_mn = ptx::smem_desc(base + Shape::kY + sx * Shape::kYBytes, 16384, 1024);
                 if constexpr (OUT) {
                     const uint64_t q_k = ptx::smem_desc(base + Shape::kQ + sx * Shape::kXBytes, 16, 1024);
                     const uint64_t x_k = ptx::smem_desc(base + Shape::kX + sx * Shape::kXBytes, 16, 1024);
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 } else {
                     wait(sm.s_ready, ph);
                 }
-                wait(sm.y_full[sy], (it >> 1) & 1);
+                wait(sm.y_full[sx], px);
                 wait(sm.keys, ph);
                 ptx::tc_fence_after();
 #pragma unroll 1
@@ -211,7 +208,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                         mma_ts(tmem + Shape::kNear, tmem + Shape::kScores + ks * 8, y_mn + ks * 128, id_near, ks > 0);
                     ptx::mma_commit(&sm.o_full);
                 }
-                ptx::mma_commit(&sm.y_empty[sy]);
+                ptx::mma_commit(&sm.y_empty[sx]);
             }
         } else if (warp == 2) {
             // ---------------------------------------------------------- decays
@@ -238,14 +235,14 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         const int j = quarter * 32 + lane;  // the token whose row this thread has
         const uint32_t to = swizzled_row(base + Shape::kHi, j);
         for (int it = 0; it < chunks; ++it) {
-            const int st = it & 1, sx = it % NX;
+            const int st = it & 1, sx = it % NS;
             const bool live = j < at.len - chunk_at(it) * kDecayChunk;
             wait(sm.g_ready[st], (it >> 1) & 1);
             const ChunkDecay& d = sm.decay[st];
             float w = dir.weight * exp2_fast(reverse ? d.hi[j] + d.lo[j]
                                                      : gap(d, kDecayChunk - 1, d.hi[j], d.lo[j]));
             arrive(sm.g_free[st]);
-            wait(sm.x_full[sx], (it / NX) & 1);
+            wait(sm.x_full[sx], (it / NS) & 1);
             const uint32_t row = swizzled_row(base + Shape::kX + sx * Shape::kXBytes, j);
             if constexpr (F16) {
                 // The scaled keys may be far below fp16's normal range, where a part keeps no relative precision: a
@@ -267,12 +264,15 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 if (j == 0) sm.key_unscale[st] = 1.f / up;
             }
             if (it > 0) wait(sm.keys_read, st ^ 1);
-#pragma unroll
+            const uint64_t w2 = pair_of(w, w), minus = pair_of(-1.f, -1.f);
+            // (A loop of few instructions: five warps with code of their own share what a scheduler keeps of it.)
+#pragma unroll 1
             for (int c0 = 0; c0 < K / 8; c0 += 4) {
+                const uint32_t block = (uint32_t)(c0 >> 3) * 16384u;
                 uint4 x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[i] = lds128((row ^ (((c0 + i) & 7) << 4)) + (c0 >> 3) * 16384);
+                    x[i] = lds128((row ^ (((c0 + i) & 7) << 4)) + block);
                     if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll
@@ -282,12 +282,14 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float2 f = from_b16x2<F16>(in[e]);
-                        f = make_float2(f.x * w, f.y * w);
+                        const uint64_t p = mul2(pair_of(f.x, f.y), w2);
+                        f = floats_of(p);
                         hi[e] = pack_b16x2(f.x, f.y, F16);
-                        const float2 back = from_b16x2<F16>(hi[e]);
-                        lo[e] = pack_b16x2(f.x - back.x, f.y - back.y, F16);
+                        f = from_b16x2<F16>(hi[e]);
+                        f = floats_of(fma2(pair_of(f.x, f.y), minus, p));
+                        lo[e] = pack_b16x2(f.x, f.y, F16);
                     }
-                    const uint32_t p = (to ^ (((c0 + i) & 7) << 4)) + (c0 >> 3) * 16384;
+                    const uint32_t p = (to ^ (((c0 + i) & 7) << 4)) + block;
                     sts128(p, hi[0], hi[1], hi[2], hi[3]);
                     sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -295,9 +297,9 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             arrive(sm.x_empty[sx]);
             if (at.len - chunk_at(it) * kDecayChunk < kDecayChunk) {
                 // rows behind the sequence are another's, or nobody's: a zero weight would not hold back a NaN
-                wait(sm.y_full[st], (it >> 1) & 1);
+                wait(sm.y_full[sx], (it / NS) & 1);
                 if (!live) {
-                    const uint32_t y = base + Shape::kY + st * Shape::kYBytes + j * 128;
+                    const uint32_t y = base + Shape::kY + sx * Shape::kYBytes + j * 128;
 #pragma unroll 1
                     for (int c = 0; c < V / 8; ++c) sts128(y + (c >> 3) * 16384 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
                 }
@@ -390,8 +392,12 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     ptx::tmem_ld16(tmem + Shape::kAdded + ((uint32_t)(quarter * 32) << 16) + c * 16, u);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        S[16 * c + e] = F16 ? fmaf(u[e], back, whole * S[16 * c + e]) : fmaf(whole, S[16 * c + e], u[e]);
+                    for (int e = 0; e < 16; e += 2) {
+                        float* s = S + 16 * c + e;
+                        const uint64_t w = pair_of(whole, whole), now = pair_of(s[0], s[1]), more = pair_of(u[e], u[e + 1]);
+                        const float2 r = floats_of(F16 ? fma2(more, pair_of(back, back), mul2(w, now)) : fma2(w, now, more));
+                        s[0] = r.x, s[1] = r.y;
+                    }
                 }
                 ptx::tc_fence_before();
             }
@@ -445,10 +451,11 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 const float4 c = *reinterpret_cast<const float4*>(&sm.column[32 * b + 4 * e]);
-                                s[4 * e] *= r * c.x;
-                                s[4 * e + 1] *= r * c.y;
-                                s[4 * e + 2] *= r * c.z;
-                                s[4 * e + 3] *= r * c.w;
+                                float* x = s + 4 * e;
+                                const uint64_t r2 = pair_of(r, r);
+                                const float2 u = floats_of(mul2(pair_of(x[0], x[1]), mul2(r2, pair_of(c.x, c.y))));
+                                const float2 v = floats_of(mul2(pair_of(x[2], x[3]), mul2(r2, pair_of(c.z, c.w))));
+                                x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
                             }
                         } else {
                             ptx::tmem_ld_wait();
@@ -482,18 +489,24 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         if constexpr (OUT) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kOutRegs));
             // ------------------------------------------------------ o: row i
+            // A warp's 32 rows leave by TMA out of a swizzled copy (rows stored by their threads are 32 lines a store);
+            // where the sequence ends among them, by their threads.
             const int i = quarter * 32 + lane;
-            const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16), box = base + Shape::kO + quarter * 4096;
+            const uint32_t to = swizzled_row(box, lane);
             for (int it = 0; it < chunks; ++it) {
                 const int st = it & 1, tok = chunk_at(it) * kDecayChunk + i;
+                const bool whole = tok - lane + 32 <= at.len;
                 wait(sm.g_ready[st], (it >> 1) & 1);
                 float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]);
                 arrive(sm.g_free[st]);
+                if (lane == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
                 wait(sm.o_full, it & 1);
                 ptx::tc_fence_after();
+                __syncwarp();
                 if (F16) f *= sm.unscale[st];
                 uint16_t* o = a.o + (((int64_t)at.bos + tok) * a.H + h) * V;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < V / 32; ++c) {
                     float far[32], near[32];
                     ptx::tmem_ld16(t_row + Shape::kFar + 32 * c, far);
@@ -501,21 +514,30 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     ptx::tmem_ld16(t_row + Shape::kFar + 32 * c + 16, far + 16);
                     ptx::tmem_ld16(t_row + Shape::kNear + 32 * c + 16, near + 16);
                     ptx::tmem_ld_wait();
-                    if (c == V / 32 - 1) {
-                        ptx::tc_fence_before();
-                        arrive(sm.o_free);
-                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = pack_b16x2(fmaf(f, far[8 * g + 2 * e], near[8 * g + 2 * e]),
-                                              fmaf(f, far[8 * g + 2 * e + 1], near[8 * g + 2 * e + 1]), F16);
-                        if (tok < at.len) *reinterpret_cast<uint4*>(o + 32 * c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int n = 8 * g + 2 * e;
+                            const float2 r = floats_of(fma2(pair_of(f, f), pair_of(far[n], far[n + 1]), pair_of(near[n], near[n + 1])));
+                            y[e] = pack_b16x2(r.x, r.y, F16);
+                        }
+                        if (whole) sts128((to ^ ((((c & 1) << 2) + g) << 4)) + (c >> 1) * 16384, y[0], y[1], y[2], y[3]);
+                        else if (tok < at.len) *reinterpret_cast<uint4*>(o + 32 * c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
+                ptx::tc_fence_before();
+                ptx::fence_proxy_async_smem();
+                arrive(sm.o_free);
+                if (whole && lane == 0) {
+#pragma unroll
+                    for (int b = 0; b < VB; ++b)
+                        ptx::tma_store_3d(&a.tm_o, raw + Shape::kO + quarter * 4096 + b * 16384, b * 64, h, at.bos + tok);
+                    ptx::bulk_commit();
+                }
             }
+            if (lane == 0) ptx::bulk_wait0();
         }
     }
     __syncwarp();

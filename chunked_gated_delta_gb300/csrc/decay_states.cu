@@ -32,15 +32,25 @@ __global__ void __launch_bounds__(kJoinThreads) kda_decay_join_kernel(const __gr
             S = *reinterpret_cast<const float4*>(static_cast<const float*>(dir.start.p) + seq);
         }
     }
-    for (int i = 0; i + 1 < at.pieces; ++i) {
-        const int p = at.piece_base + (dir.reverse ? at.pieces - 1 - i : i);
-        const int64_t unit = (int64_t)p * a.H + h;
-        const int64_t into = unit + (dir.reverse ? -a.H : a.H);
-        const float4 t = *reinterpret_cast<const float4*>(dir.totals + unit * a.state + e);
-        const float d = dir.decays[unit];
-        if (i > 0) *reinterpret_cast<float4*>(dir.totals + unit * a.state + e) = S;
-        S = make_float4(fmaf(d, S.x, t.x), fmaf(d, S.y, t.y), fmaf(d, S.z, t.z), fmaf(d, S.w, t.w));
-        if (i + 2 == at.pieces) *reinterpret_cast<float4*>(dir.totals + into * a.state + e) = S;
+    // Eight pieces' totals are asked for together: one after the other, each would wait for memory.
+    constexpr int kBatch = 8;
+    auto unit_at = [&](int i) { return (int64_t)(at.piece_base + (dir.reverse ? at.pieces - 1 - i : i)) * a.H + h; };
+    for (int i0 = 0; i0 < at.pieces; i0 += kBatch) {
+        float4 t[kBatch];
+        float d[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i0 + i + 1 < at.pieces) {
+                t[i] = *reinterpret_cast<const float4*>(dir.totals + unit_at(i0 + i) * a.state + e);
+                d[i] = dir.decays[unit_at(i0 + i)];
+            }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i0 + i >= at.pieces) break;
+            if (i0 + i > 0) *reinterpret_cast<float4*>(dir.totals + unit_at(i0 + i) * a.state + e) = S;
+            if (i0 + i + 1 < at.pieces)
+                S = make_float4(fmaf(d[i], S.x, t[i].x), fmaf(d[i], S.y, t[i].y), fmaf(d[i], S.z, t[i].z), fmaf(d[i], S.w, t[i].w));
+        }
     }
 }
 
