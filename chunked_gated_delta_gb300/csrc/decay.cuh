@@ -72,6 +72,7 @@ struct DecayJoinArgs {
 
 struct DecayGradArgs {
     CUtensorMap tm_q, tm_k, tm_v, tm_do;
+    CUtensorMap tm_dq, tm_dk, tm_dv;  // boxes of 64 x 32 rows (dq, dk: not grouped)
     DecaySeqs seqs;      // seg_chunks = 1
     const float* g;
     int64_t g_stride;
@@ -82,7 +83,7 @@ struct DecayGradArgs {
     float* dg;           // fp32 [rows, H]
     int32_t* status;
     float scale;
-    int32_t H, group;
+    int32_t H, group, sms;
 };
 
 cudaError_t launch_decay_out(const DecayScanArgs& a, int K, int V, bool f16, cudaStream_t s);

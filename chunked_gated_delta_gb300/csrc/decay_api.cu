@@ -229,7 +229,9 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
     const bool f16 = opts->io_dtype == KDA_IO_F16, grouped = hq != d.H;
     DecayGradArgs a{};
     if (!token_map(&a.tm_q, q, d.K, hq, rows, sd.q) || !token_map(&a.tm_k, k, d.K, hq, rows, sd.k) ||
-        !token_map(&a.tm_v, v, d.V, d.H, rows, sd.v) || !token_map(&a.tm_do, d_o, d.V, d.H, rows, sd.d_o))
+        !token_map(&a.tm_v, v, d.V, d.H, rows, sd.v) || !token_map(&a.tm_do, d_o, d.V, d.H, rows, sd.d_o) ||
+        !token_map(&a.tm_dq, dq, d.K, hq, rows, (int64_t)hq * d.K, 32) ||
+        !token_map(&a.tm_dk, dk, d.K, hq, rows, (int64_t)hq * d.K, 32) || !token_map(&a.tm_dv, dv, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
         return KDA_ERR_CUDA;
     DecayScanArgs c{};
     const int32_t b16 = opts->state_dtype == KDA_STATE_BF16;
@@ -283,6 +285,7 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
         a.scale = scale;
         a.H = d.H;
         a.group = d.H / hq;
+        a.sms = device_sm_count();
         if (e == cudaSuccess) e = launch_decay_grads(a, d.K, d.V, f16, s);
         if (e == cudaSuccess && grouped)
             e = launch_decay_group(static_cast<const float*>(a.dq), static_cast<const float*>(a.dk), dq, dk, rows, hq, d.K,

@@ -24,15 +24,15 @@
 namespace kda {
 namespace {
 
-constexpr int kWorkers = 256, kGradThreads = kWorkers + 32;
+constexpr int kWorkers = 512, kWorkerWarps = kWorkers / 32, kGradThreads = kWorkers + 32;
 
 template <int KB, int VB>
 struct GradShape {
     static constexpr int K = 64 * KB, V = 64 * VB;
-    static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kPart = V * 128, kStateBytes = V * K * 2;
+    static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kPart = K * 128, kStateBytes = V * K * 2;
     static constexpr int kQ = 0, kK = kQ + kXBytes, kV = kK + kXBytes, kDo = kV + kYBytes;
     static constexpr int kDp = kDo + kYBytes;         // dP^T [j][i]
-    static constexpr int kRing = kDp + 32768;         // 64 keys of S (hi, lo) and dS (hi, lo)
+    static constexpr int kRing = kDp + 32768;         // 64 values of S (hi, lo) and dS (hi, lo), each x all keys
     static constexpr int kSmall = kRing + 4 * kPart;
     struct Small {
         ChunkDecay decay;
@@ -44,17 +44,19 @@ struct GradShape {
     };
     // when everything else is done, in place of dP: the parts of dg
     struct Sums {
-        float far_q[2][kDecayChunk], far_k[2][kDecayChunk], near_k[2][kDecayChunk], near_q[4][kDecayChunk], across[8];
+        float far_q[4][kDecayChunk], far_k[4][kDecayChunk], near_k[4][kDecayChunk], near_q[4][kDecayChunk];
+        float across[kWorkerWarps];
     };
     static constexpr int kSmem = kSmall + (int)sizeof(Small);
     static_assert(sizeof(Small) >= sizeof(DecayScratch) && sizeof(Sums) <= 32768, "what shares memory fits");
     static_assert(kSmem <= 227 * 1024, "fits an SM");
+    // Where part `part` of 64 values of dS lies, the vb'th time.
+    static __host__ __device__ constexpr int d_state(int vb, int part) {
+        return vb == 0 ? kRing + (2 + part) * kPart : part == 0 ? kRing + 3 * kPart : kV;
+    }
 };
-// TMEM columns. P^T lies at 0 .. 31 and 96 .. 127 of the first scores' (each half written by those who have read what
-// was there), dP^T likewise of the second's; dv in the middle of both.
-constexpr uint32_t kT0 = 0, kT1 = 128, kTdq = 256, kTdk = 384;
-__device__ __forceinline__ constexpr uint32_t p_column(int ks) { return (uint32_t)(ks * 8 + (ks >= 4 ? 64 : 0)); }
-__device__ __forceinline__ constexpr uint32_t dv_column(int vb) { return (uint32_t)(32 + vb * 128); }
+// TMEM columns: the scores, and when all of them have been read P^T, dP^T and dv in their place; dq and dk.
+constexpr uint32_t kT0 = 0, kT1 = 128, kTp = kT0, kTdp = kT0 + 64, kTdv = kT1, kTdq = 256, kTdk = 384;
 
 // x[0 .. 31] of each lane: lane l gets the sum over the lanes of x[l].
 __device__ __forceinline__ float transposed_sum(float (&x)[32], int lane) {
@@ -94,11 +96,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     if (tid == 0) {
         for (uint64_t* b : {&sm.in_full, &sm.scores, &sm.s_full, &sm.ring_done, &sm.far, &sm.dv_far, &sm.dqk, &sm.dv})
             ptx::mbar_init(b, 1);
-        for (uint64_t* b : {&sm.clean, &sm.ring_read, &sm.far_ok, &sm.p_ok, &sm.dv_ok}) ptx::mbar_init(b, kWorkers / 32);
+        for (uint64_t* b : {&sm.clean, &sm.ring_read, &sm.far_ok, &sm.p_ok, &sm.dv_ok}) ptx::mbar_init(b, kWorkerWarps);
         ptx::fence_mbar_init();
         sm.fail = 0;
     }
-    if (warp == 8) {
+    if (warp == kWorkerWarps) {
         ptx::tmem_alloc(&sm.tmem, 512);
         ptx::tmem_relinquish();
     }
@@ -112,17 +114,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         return !*fail;
     };
 
-    if (warp == 8) {
+    if (warp == kWorkerWarps) {
         if (elect_one()) {
             const uint8_t* S = a.kept + unit * 2 * Shape::kStateBytes;
             const uint8_t* dS = a.dkept + unit * 2 * Shape::kStateBytes;
-            uint8_t* ring = raw + Shape::kRing;
-            auto load_states = [&](int kb) {
+            // 64 values of the states at a time. The second time dS's leading part has the place of the first's other
+            // part (the first is kept for dv), and its own other part that of v's first half, which is done with.
+            auto load_states = [&](int vb) {
                 ptx::mbar_arrive_expect_tx(&sm.s_full, 4 * Shape::kPart);
                 for (int part = 0; part < 2; ++part) {
-                    const int64_t off = part * Shape::kStateBytes + kb * Shape::kPart;
-                    bulk_load(ring + part * Shape::kPart, S + off, Shape::kPart, &sm.s_full);
-                    bulk_load(ring + (2 + part) * Shape::kPart, dS + off, Shape::kPart, &sm.s_full);
+                    const int64_t off = part * Shape::kStateBytes + vb * Shape::kPart;
+                    bulk_load(raw + Shape::kRing + part * Shape::kPart, S + off, Shape::kPart, &sm.s_full);
+                    bulk_load(raw + Shape::d_state(vb, part), dS + off, Shape::kPart, &sm.s_full);
                 }
             };
             ptx::mbar_arrive_expect_tx(&sm.in_full, 2 * Shape::kXBytes + 2 * Shape::kYBytes);
@@ -141,8 +144,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             const uint64_t v_k = ptx::smem_desc(base + Shape::kV, 16, 1024), do_k = ptx::smem_desc(base + Shape::kDo, 16, 1024);
             const uint64_t q_mn = ptx::smem_desc(base + Shape::kQ, 16384, 1024), k_mn = ptx::smem_desc(base + Shape::kK, 16384, 1024);
             const uint64_t do_mn = ptx::smem_desc(base + Shape::kDo, 16384, 1024), dp_mn = ptx::smem_desc(base + Shape::kDp, 16384, 1024);
-            const uint64_t ring_mn = ptx::smem_desc(base + Shape::kRing, 16384, 1024);
-            const uint64_t ring_k = ptx::smem_desc(base + Shape::kRing, 16, 1024);
+            auto part_mn = [&](int at) { return ptx::smem_desc(base + at, 8192, 1024); };  // 64 values x keys, N = keys
+            auto part_k = [&](int at) { return ptx::smem_desc(base + at, 16, 1024); };     // the same, N = values
             auto step = [](int ks) { return (uint64_t)(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4); };  // along rows of 64
             bool ok = false;
             do {
@@ -156,55 +159,68 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 ptx::mma_commit(&sm.scores);
                 bool through = true;
 #pragma unroll 1
-                for (int kb = 0; kb < KB && through; ++kb) {
-                    if (!(through = wait(sm.s_full, kb & 1))) break;
+                for (int vb = 0; vb < VB && through; ++vb) {
+                    if (!(through = wait(sm.s_full, vb & 1))) break;
                     ptx::tc_fence_after();
-                    constexpr uint32_t id = idesc16<F16>(128, 64, 0, 1);
+                    constexpr uint32_t id = idesc16<F16>(128, K, 0, 1);
 #pragma unroll 1
-                    for (int ks = 0; ks < 8 * VB; ++ks) {  // hi, then lo
-                        const int part = ks / (4 * VB), kv = ks % (4 * VB);
-                        const uint64_t at_v = (uint64_t)((part * Shape::kPart + kv * 2048) >> 4);
-                        ptx::mma_bf16(tmem + kTdq + kb * 64, do_k + step(kv), ring_mn + at_v, id, ks > 0);
-                        ptx::mma_bf16(tmem + kTdk + kb * 64, v_k + step(kv), ring_mn + (2 * Shape::kPart >> 4) + at_v, id, ks > 0);
+                    for (int part = 0; part < 2; ++part) {
+                        const uint64_t s = part_mn(Shape::kRing + part * Shape::kPart), ds = part_mn(Shape::d_state(vb, part));
+#pragma unroll 1
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint32_t more = vb + part + ks > 0;
+                            ptx::mma_bf16(tmem + kTdq, do_k + step(4 * vb + ks), s + ks * 128, id, more);
+                            ptx::mma_bf16(tmem + kTdk, v_k + step(4 * vb + ks), ds + ks * 128, id, more);
+                        }
                     }
-                    if (kb == KB - 1) ptx::mma_commit(&sm.far);
-                    ptx::mma_commit(&sm.ring_done);
-                    if (!(through = wait(sm.ring_done, kb & 1) && wait(sm.ring_read, kb & 1))) break;
-                    if (kb + 1 < KB) {
-                        load_states(kb + 1);
-                    } else {  // dS once more, its leading parts
-                        ptx::mbar_arrive_expect_tx(&sm.s_full, KB * Shape::kPart);
-                        for (int b = 0; b < KB; ++b)
-                            bulk_load(ring + b * Shape::kPart, dS + b * Shape::kPart, Shape::kPart, &sm.s_full);
+                    if (vb == VB - 1) ptx::mma_commit(&sm.far);
+                    if (vb + 1 < VB) {
+                        ptx::mma_commit(&sm.ring_done);
+                        if (!(through = wait(sm.ring_done, 0) && wait(sm.ring_read, 0))) break;
+                        load_states(vb + 1);
+                        ++loads;
                     }
-                    ++loads;
                 }
-                if (!through || !wait(sm.p_ok, 0) || !wait(sm.s_full, KB & 1)) break;
+                // The tile that probably comes next on this SM, if it is of this sequence, into L2.
+                const int ahead = (blockIdx.x + a.sms) / a.H - item, next_h = (blockIdx.x + a.sms) % a.H;
+                if (at.piece + ahead < at.pieces) {
+                    const int row = row0 + ahead * kDecayChunk, next_hq = next_h / a.group;
+                    for (int b = 0; b < KB; ++b) {
+                        ptx::tma_prefetch_3d(&a.tm_q, b * 64, next_hq, row);
+                        ptx::tma_prefetch_3d(&a.tm_k, b * 64, next_hq, row);
+                    }
+                    for (int b = 0; b < VB; ++b) {
+                        ptx::tma_prefetch_3d(&a.tm_v, b * 64, next_h, row);
+                        ptx::tma_prefetch_3d(&a.tm_do, b * 64, next_h, row);
+                    }
+                    const int64_t next = (int64_t)(at.chunk_base + at.piece + ahead) * a.H + next_h;
+                    ptx::bulk_prefetch_l2(a.kept + next * 2 * Shape::kStateBytes, 2 * Shape::kStateBytes);
+                    ptx::bulk_prefetch_l2(a.dkept + next * 2 * Shape::kStateBytes, 2 * Shape::kStateBytes);
+                }
+                if (!through || !wait(sm.p_ok, 0)) break;
                 ptx::tc_fence_after();
 #pragma unroll 1
-                for (int vb = 0; vb < VB; ++vb)
+                for (int vb = 0; vb < VB; ++vb) {
+                    const uint64_t ds = part_k(Shape::d_state(vb, 0));
 #pragma unroll 1
                     for (int ks = 0; ks < 4 * KB; ++ks)
-                        ptx::mma_bf16(tmem + dv_column(vb), k_k + step(ks),
-                                      ring_k + (((ks >> 2) * Shape::kPart + vb * 8192 + (ks & 3) * 32) >> 4),
+                        ptx::mma_bf16(tmem + kTdv + vb * 64, k_k + step(ks), ds + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
                                       idesc16<F16>(128, 64, 0, 0), ks > 0);
+                }
                 ptx::mma_commit(&sm.dv_far);
                 if (!wait(sm.far_ok, 0)) break;
                 ptx::tc_fence_after();
 #pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks) {
                     ptx::mma_bf16(tmem + kTdq, dp_mn + ks * 128, k_mn + ks * 128, idesc16<F16>(128, K, 1, 1), 1);
-                    mma_ts(tmem + kTdk, tmem + kT1 + p_column(ks), q_mn + ks * 128, idesc16<F16>(128, K, 0, 1), 1);
+                    mma_ts(tmem + kTdk, tmem + kTdp + ks * 8, q_mn + ks * 128, idesc16<F16>(128, K, 0, 1), 1);
                 }
                 ptx::mma_commit(&sm.dqk);
                 if (!wait(sm.dv_ok, 0)) break;
                 ptx::tc_fence_after();
 #pragma unroll 1
-                for (int vb = 0; vb < VB; ++vb)
-#pragma unroll 1
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem + dv_column(vb), tmem + kT0 + p_column(ks), do_mn + ks * 128 + vb * 1024,
-                               idesc16<F16>(128, 64, 0, 1), 1);
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(tmem + kTdv, tmem + kTp + ks * 8, do_mn + ks * 128, idesc16<F16>(128, V, 0, 1), 1);
                 ptx::mma_commit(&sm.dv);
                 ok = true;
             } while (false);
@@ -214,248 +230,263 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             }
         }
     } else {
-        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-        const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
-        constexpr int kCols = K / 2, kColsV = V / 2;  // columns of a thread
+        // 16 warps: a quarter of the rows each (TMEM's lanes), and a quarter of the columns.
+        const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
+        const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16), base = ptx::smem_u32(raw);
+        constexpr int kCols = K / 4, kColsV = V / 4;  // columns of a thread
         auto arrive = [&](uint64_t& bar) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bar);
         };
-        float far_q = 0.f, far_k = 0.f, near_k = 0.f, near_q[2] = {0.f, 0.f}, across = 0.f;
+        float far_q = 0.f, far_k = 0.f, near_k = 0.f, near_q = 0.f, across = 0.f;
+        if (warp == 0) {
+            const Pair all = sum_decay(load_g(a.g, a.g_stride, h, row0, valid, lane), sm.decay, lane);
+            if (lane == 0) sm.whole = whole_decay(all);
+        }
+        float up_q = 1.f, up_k = 1.f;
+        if (F16) up_q = a.kept_scale[unit], up_k = a.dkept_scale[unit];
+        named_sync(1, kWorkers);
+        const ChunkDecay& d = sm.decay;
+        const float hi = d.hi[row], lo = d.lo[row];
+        if (part == 0 && quarter > 0) sm.column[row] = exp2_fast((hi - d.hi[quarter * 32 - 1]) + (lo - d.lo[quarter * 32 - 1]));
+        wait(sm.in_full, 0);
+        if (valid < kDecayChunk) {  // rows behind the sequence: a zero factor would not hold back a NaN
+            if (row >= valid && part < 4) {
+                const uint32_t to = base + (part == 0 ? Shape::kQ : part == 1 ? Shape::kK : part == 2 ? Shape::kV : Shape::kDo) + row * 128;
+#pragma unroll 1
+                for (int c = 0; c < 8 * (part < 2 ? KB : VB); ++c) sts128(to + (c >> 3) * 16384 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+            }
+        }
+        ptx::fence_proxy_async_smem();
+        arrive(sm.clean);
+
+        // <S, dS>, 64 values at a time: the same element of all four tiles, wherever it lies
+        auto dot_states = [&](int vb) {
+            wait(sm.s_full, vb & 1);
+            const uint32_t s = base + Shape::kRing + tid * 16, ds = base + Shape::d_state(vb, 0) + tid * 16,
+                           dsl = base + Shape::d_state(vb, 1) + tid * 16;
+#pragma unroll 1
+            for (int c = 0; c < Shape::kPart; c += kWorkers * 16) {
+                const uint4 w[4] = {lds128(s + c), lds128(s + c + Shape::kPart), lds128(ds + c), lds128(dsl + c)};
+                auto dot = [&](uint32_t s, uint32_t sl, uint32_t t, uint32_t tl) {
+                    const float2 x = from_b16x2<F16>(s), xl = from_b16x2<F16>(sl), y = from_b16x2<F16>(t), yl = from_b16x2<F16>(tl);
+                    across = fmaf(x.x + xl.x, y.x + yl.x, across);
+                    across = fmaf(x.y + xl.y, y.y + yl.y, across);
+                };
+                dot(w[0].x, w[1].x, w[2].x, w[3].x);
+                dot(w[0].y, w[1].y, w[2].y, w[3].y);
+                dot(w[0].z, w[1].z, w[2].z, w[3].z);
+                dot(w[0].w, w[1].w, w[2].w, w[3].w);
+            }
+            arrive(sm.ring_read);
+        };
+        dot_states(0);
+        named_sync(1, kWorkers);  // column is there
+
+        // P^T and dP^T: row j, 32 columns i
+        wait(sm.scores, 0);
+        ptx::tc_fence_after();
         {
-            if (warp == 0) {
-                const Pair all = sum_decay(load_g(a.g, a.g_stride, h, row0, valid, lane), sm.decay, lane);
-                if (lane == 0) sm.whole = whole_decay(all);
-            }
-            named_sync(1, kWorkers);
-            const ChunkDecay& d = sm.decay;
-            const float hi = d.hi[row], lo = d.lo[row];
-            if (half == 0 && quarter > 0) sm.column[row] = exp2_fast((hi - d.hi[quarter * 32 - 1]) + (lo - d.lo[quarter * 32 - 1]));
-            wait(sm.in_full, 0);
-            if (row >= valid) {  // rows behind the sequence: a zero factor would not hold back a NaN
-                uint8_t* p = raw + (half ? Shape::kV : Shape::kQ) + row * 128;
-                constexpr int kMost = KB > VB ? KB : VB;
-#pragma unroll 1
-                for (int c = 0; c < 16 * kMost; ++c) {
-                    const int blocks = half ? VB : KB, which = c / (8 * kMost), in = c % (8 * kMost);
-                    if ((in >> 3) < blocks)
-                        *reinterpret_cast<uint4*>(p + (which * blocks + (in >> 3)) * 16384 + ((in & 7) << 4)) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-            ptx::fence_proxy_async_smem();
-            arrive(sm.clean);
-            named_sync(1, kWorkers);  // column is there
-
-            // <S, dS>, 64 keys at a time: the same element of all four tiles, wherever it lies
-#pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
-                wait(sm.s_full, kb & 1);
-                const uint8_t* p = raw + Shape::kRing + tid * 16;
-#pragma unroll 2
-                for (int c = 0; c < Shape::kPart / 4096; ++c, p += 4096) {
-                    uint4 w[4];
+            const int b = part;
+            uint32_t p[16], dp[16];
+            if (b >= quarter) {
+                float s[32], e[32];
+                ptx::tmem_ld16(t_row + kT0 + 32 * b, s);
+                ptx::tmem_ld16(t_row + kT0 + 32 * b + 16, s + 16);
+                ptx::tmem_ld16(t_row + kT1 + 32 * b, e);
+                ptx::tmem_ld16(t_row + kT1 + 32 * b + 16, e + 16);
+                ptx::tmem_ld_wait();
+                if (b > quarter) {
+                    const int end = 32 * b - 1;
+                    const float r = a.scale * exp2_fast((d.hi[end] - hi) + (d.lo[end] - lo));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(p + i * Shape::kPart);
-                    auto dot = [&](uint32_t s, uint32_t sl, uint32_t t, uint32_t tl) {
-                        const float2 x = from_b16x2<F16>(s), xl = from_b16x2<F16>(sl), y = from_b16x2<F16>(t), yl = from_b16x2<F16>(tl);
-                        across = fmaf(x.x + xl.x, y.x + yl.x, across);
-                        across = fmaf(x.y + xl.y, y.y + yl.y, across);
-                    };
-                    dot(w[0].x, w[1].x, w[2].x, w[3].x);
-                    dot(w[0].y, w[1].y, w[2].y, w[3].y);
-                    dot(w[0].z, w[1].z, w[2].z, w[3].z);
-                    dot(w[0].w, w[1].w, w[2].w, w[3].w);
-                }
-                arrive(sm.ring_read);
-            }
-            float up_q = 1.f, up_k = 1.f;
-            if (F16) up_q = a.kept_scale[unit], up_k = a.dkept_scale[unit];
-            across *= up_q * up_k;
-
-            // P^T and dP^T: row j, half of the columns i, 32 at a time, inwards from the ends (see kT0)
-            wait(sm.scores, 0);
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int n = 0; n < 2; ++n) {
-                const int b = half ? 3 - n : n;
-                uint32_t p[16], dp[16];
-                if (b >= quarter) {
-                    float s[32], e[32];
-                    ptx::tmem_ld16(t_row + kT0 + 32 * b, s);
-                    ptx::tmem_ld16(t_row + kT0 + 32 * b + 16, s + 16);
-                    ptx::tmem_ld16(t_row + kT1 + 32 * b, e);
-                    ptx::tmem_ld16(t_row + kT1 + 32 * b + 16, e + 16);
-                    ptx::tmem_ld_wait();
-                    if (b > quarter) {
-                        const int end = 32 * b - 1;
-                        const float r = a.scale * exp2_fast((d.hi[end] - hi) + (d.lo[end] - lo));
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float2 f = *reinterpret_cast<const float2*>(&sm.column[32 * b + 2 * c]);
-                            const float f0 = r * f.x, f1 = r * f.y;
-                            p[c] = pack_b16x2(s[2 * c] * f0, s[2 * c + 1] * f1, F16);
-                            e[2 * c] *= f0, e[2 * c + 1] *= f1;
-                            dp[c] = pack_b16x2(e[2 * c], e[2 * c + 1], F16);
-                            s[2 * c] *= e[2 * c], s[2 * c + 1] *= e[2 * c + 1];
-                            near_k += s[2 * c] + s[2 * c + 1];
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float f = a.scale * exp2_fast((d.hi[32 * b + c] - hi) + (d.lo[32 * b + c] - lo));
-                            const float x = c >= lane ? s[c] * f : 0.f;
-                            e[c] = c >= lane ? e[c] * f : 0.f;
-                            s[c] = c > lane ? s[c] * e[c] : 0.f;  // (a token's pair with itself has no decay)
-                            near_k += s[c];
-                            if (c & 1) {
-                                p[c >> 1] = pack_b16x2(__uint_as_float(p[c >> 1]), x, F16);
-                                dp[c >> 1] = pack_b16x2(e[c - 1], e[c], F16);
-                            } else {
-                                p[c >> 1] = __float_as_uint(x);
-                            }
-                        }
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 f = *reinterpret_cast<const float2*>(&sm.column[32 * b + 2 * c]);
+                        const float f0 = r * f.x, f1 = r * f.y;
+                        p[c] = pack_b16x2(s[2 * c] * f0, s[2 * c + 1] * f1, F16);
+                        e[2 * c] *= f0, e[2 * c + 1] *= f1;
+                        dp[c] = pack_b16x2(e[2 * c], e[2 * c + 1], F16);
+                        s[2 * c] *= e[2 * c], s[2 * c + 1] *= e[2 * c + 1];
+                        near_k += s[2 * c] + s[2 * c + 1];
                     }
-                    near_q[b & 1] = transposed_sum(s, lane);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) p[c] = dp[c] = 0u;
-                }
-                const uint32_t column = p_column(2 * b);
-                tmem_st16(t_row + kT0 + column, p);
-                tmem_st16(t_row + kT1 + column, dp);
-                uint8_t* to = raw + Shape::kDp + (b >> 1) * 16384 + row * 128;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(to + ((((b & 1) * 4 + c) ^ (row & 7)) << 4)) =
-                        make_uint4(dp[4 * c], dp[4 * c + 1], dp[4 * c + 2], dp[4 * c + 3]);
-            }
-            tmem_st_wait();
-            ptx::tc_fence_before();
-            ptx::fence_proxy_async_smem();
-            arrive(sm.p_ok);
-
-            // the far parts of dq and dk: scaled by rows, and their products with q and k
-            const float seen = exp2_fast(hi + lo), kept = exp2_fast(gap(d, kDecayChunk - 1, hi, lo));
-            wait(sm.far, 0);
-            ptx::tc_fence_after();
-            auto scaled = [&](uint32_t column, float f, const uint8_t* x) {
-                float sum = 0.f;
-#pragma unroll 1
-                for (int c0 = half * kCols; c0 < (half + 1) * kCols; c0 += 16) {
-                    float u[16];
-                    ptx::tmem_ld16(t_row + column + c0, u);
-                    ptx::tmem_ld_wait();
-                    const uint8_t* p = x + (c0 >> 6) * 16384 + row * 128;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(p + (((((c0 & 63) >> 3) + g) ^ (row & 7)) << 4));
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = from_b16x2<F16>(in[e]);
-                            u[8 * g + 2 * e] *= f, u[8 * g + 2 * e + 1] *= f;
-                            sum = fmaf(u[8 * g + 2 * e], y.x, sum);
-                            sum = fmaf(u[8 * g + 2 * e + 1], y.y, sum);
+                    for (int c = 0; c < 32; ++c) {
+                        const float f = a.scale * exp2_fast((d.hi[32 * b + c] - hi) + (d.lo[32 * b + c] - lo));
+                        const float x = c >= lane ? s[c] * f : 0.f;
+                        e[c] = c >= lane ? e[c] * f : 0.f;
+                        s[c] = c > lane ? s[c] * e[c] : 0.f;  // (a token's pair with itself has no decay)
+                        near_k += s[c];
+                        if (c & 1) {
+                            p[c >> 1] = pack_b16x2(__uint_as_float(p[c >> 1]), x, F16);
+                            dp[c >> 1] = pack_b16x2(e[c - 1], e[c], F16);
+                        } else {
+                            p[c >> 1] = __float_as_uint(x);
                         }
                     }
-                    tmem_st16(t_row + column + c0, reinterpret_cast<const uint32_t*>(u));
                 }
-                return sum;
-            };
-            far_q = scaled(kTdq, a.scale * seen * up_q, raw + Shape::kQ);
-            far_k = scaled(kTdk, kept * up_k, raw + Shape::kK);
-            tmem_st_wait();
+                near_q = transposed_sum(s, lane);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) p[c] = dp[c] = 0u;
+            }
+            const uint32_t to = swizzled_row(base + Shape::kDp + (b >> 1) * 16384, row);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sts128(to ^ (((b & 1) * 4 + c) << 4), dp[4 * c], dp[4 * c + 1], dp[4 * c + 2], dp[4 * c + 3]);
             ptx::tc_fence_before();
-            arrive(sm.far_ok);
-
-            wait(sm.dv_far, 0);
+            named_sync(1, kWorkers);  // all scores have been read
             ptx::tc_fence_after();
-            // (a thread's half of V: a block of 64 columns of it, or half of one)
-            const uint32_t t_dv = t_row + (VB == 2 ? dv_column(half) : dv_column(0) + half * kColsV);
+            tmem_st16(t_row + kTp + 16 * b, p);
+            tmem_st16(t_row + kTdp + 16 * b, dp);
+        }
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::fence_proxy_async_smem();
+        arrive(sm.p_ok);
 #pragma unroll 1
-            for (int c = 0; c < kColsV; c += 16) {
+        for (int vb = 1; vb < VB; ++vb) dot_states(vb);
+        across *= up_q * up_k;
+
+        // the far parts of dq and dk: scaled by rows, and their products with q and k
+        const float seen = exp2_fast(hi + lo), kept = exp2_fast(gap(d, kDecayChunk - 1, hi, lo));
+        wait(sm.far, 0);
+        ptx::tc_fence_after();
+        auto scaled = [&](uint32_t column, float f, uint32_t x) {
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 16) {
                 float u[16];
-                ptx::tmem_ld16(t_dv + c, u);
+                ptx::tmem_ld16(t_row + column + c0, u);
+                const uint32_t p = swizzled_row(x + (c0 >> 6) * 16384, row);
+                const uint4 w[2] = {lds128(p ^ ((c0 & 63) << 1)), lds128(p ^ (((c0 & 63) << 1) + 16))};
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] *= kept * up_k;
-                tmem_st16(t_dv + c, reinterpret_cast<const uint32_t*>(u));
-            }
-            tmem_st_wait();
-            ptx::tc_fence_before();
-            arrive(sm.dv_ok);
-
-            // out
-            const bool live = row < valid;
-            const int64_t tok = (int64_t)row0 + row;
-            auto store16 = [&](uint32_t t, uint16_t* to, int count) {
-#pragma unroll 1
-                for (int c = 0; c < count; c += 16) {
-                    float u[16];
-                    ptx::tmem_ld16(t + c, u);
-                    ptx::tmem_ld_wait();
-                    uint32_t w[8];
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t in[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = pack_b16x2(u[2 * e], u[2 * e + 1], F16);
-                    if (live) {
-                        *reinterpret_cast<uint4*>(to + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4*>(to + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = from_b16x2<F16>(in[e]);
+                        u[8 * g + 2 * e] *= f, u[8 * g + 2 * e + 1] *= f;
+                        sum = fmaf(u[8 * g + 2 * e], y.x, sum);
+                        sum = fmaf(u[8 * g + 2 * e + 1], y.y, sum);
                     }
                 }
-            };
-            auto store32 = [&](uint32_t t, float* to, int count) {
-#pragma unroll 1
-                for (int c = 0; c < count; c += 16) {
-                    float u[16];
-                    ptx::tmem_ld16(t + c, u);
-                    ptx::tmem_ld_wait();
-                    if (live)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<float4*>(to + c + 4 * e) = make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-                }
-            };
-            wait(sm.dqk, 0);
-            ptx::tc_fence_after();
-            if (a.group == 1) {
-                const int64_t to = (tok * a.H + h) * K + half * kCols;
-                store16(t_row + kTdq + half * kCols, static_cast<uint16_t*>(a.dq) + to, kCols);
-                store16(t_row + kTdk + half * kCols, static_cast<uint16_t*>(a.dk) + to, kCols);
-            } else {
-                const int64_t to = (tok * a.H + h) * K + half * kCols;
-                store32(t_row + kTdq + half * kCols, static_cast<float*>(a.dq) + to, kCols);
-                store32(t_row + kTdk + half * kCols, static_cast<float*>(a.dk) + to, kCols);
+                tmem_st16(t_row + column + c0, reinterpret_cast<const uint32_t*>(u));
             }
-            wait(sm.dv, 0);
-            ptx::tc_fence_after();
-            store16(t_dv, a.dv + (tok * a.H + h) * V + half * kColsV, kColsV);
+            return sum;
+        };
+        far_q = scaled(kTdq, a.scale * seen * up_q, base + Shape::kQ);
+        far_k = scaled(kTdk, kept * up_k, base + Shape::kK);
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(sm.far_ok);
+
+        const uint32_t t_dv = t_row + kTdv + part * kColsV;
+        wait(sm.dv_far, 0);
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kColsV; c += 16) {
+            float u[16];
+            ptx::tmem_ld16(t_dv + c, u);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] *= kept * up_k;
+            tmem_st16(t_dv + c, reinterpret_cast<const uint32_t*>(u));
         }
+        tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(sm.dv_ok);
+
+        // Out: whole tiles by TMA, from where their inputs were (q, k and v have been read by then); rows of a
+        // sequence's last chunk, and fp32 parts of a group, by their threads.
+        const bool live = row < valid, staged = valid == kDecayChunk;
+        const int64_t tok = (int64_t)row0 + row;
+        auto store16 = [&](uint32_t t, int col, int count, uint32_t tile, uint16_t* to) {
+#pragma unroll 1
+            for (int c = 0; c < count; c += 16) {
+                float u[16];
+                ptx::tmem_ld16(t + c, u);
+                ptx::tmem_ld_wait();
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack_b16x2(u[2 * e], u[2 * e + 1], F16);
+                const int at_col = col + c;
+                if (staged) {
+                    const uint32_t p = swizzled_row(tile + (at_col >> 6) * 16384, row);
+                    sts128(p ^ ((at_col & 63) << 1), w[0], w[1], w[2], w[3]);
+                    sts128(p ^ (((at_col & 63) << 1) + 16), w[4], w[5], w[6], w[7]);
+                } else if (live) {
+                    *reinterpret_cast<uint4*>(to + at_col) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(to + at_col + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+        };
+        auto store32 = [&](uint32_t t, float* to) {
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 16) {
+                float u[16];
+                ptx::tmem_ld16(t + c, u);
+                ptx::tmem_ld_wait();
+                if (live)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<float4*>(to + c + 4 * e) = make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            }
+        };
+        wait(sm.dqk, 0);
+        ptx::tc_fence_after();
+        const int64_t to = (tok * a.H + h) * K;
+        if (a.group == 1) {
+            store16(t_row + kTdq + part * kCols, part * kCols, kCols, base + Shape::kQ, static_cast<uint16_t*>(a.dq) + to);
+            store16(t_row + kTdk + part * kCols, part * kCols, kCols, base + Shape::kK, static_cast<uint16_t*>(a.dk) + to);
+        } else {
+            store32(t_row + kTdq + part * kCols, static_cast<float*>(a.dq) + to + part * kCols);
+            store32(t_row + kTdk + part * kCols, static_cast<float*>(a.dk) + to + part * kCols);
+        }
+        // (the four warps of these rows: one of them sends what all have written)
+        auto send = [&](bool what, auto store) {
+            ptx::fence_proxy_async_smem();
+            named_sync(2 + quarter, 128);
+            if (staged && what && part == 0 && lane == 0) {
+                store();
+                ptx::bulk_commit();
+            }
+        };
+        send(a.group == 1, [&] {
+            for (int b = 0; b < KB; ++b) {
+                ptx::tma_store_3d(&a.tm_dq, raw + Shape::kQ + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
+                ptx::tma_store_3d(&a.tm_dk, raw + Shape::kK + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
+            }
+        });
+        wait(sm.dv, 0);
+        ptx::tc_fence_after();
+        store16(t_dv, part * kColsV, kColsV, base + Shape::kV, a.dv + (tok * a.H + h) * V);
+        send(true, [&] {
+            for (int b = 0; b < VB; ++b)
+                ptx::tma_store_3d(&a.tm_dv, raw + Shape::kV + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
+        });
         // dg, from sums that every thread has a part of (dP has been read)
         auto& sums = *reinterpret_cast<typename Shape::Sums*>(raw + Shape::kDp);
-        across += __shfl_xor_sync(~0u, across, 16);
-        across += __shfl_xor_sync(~0u, across, 8);
-        across += __shfl_xor_sync(~0u, across, 4);
-        across += __shfl_xor_sync(~0u, across, 2);
-        across += __shfl_xor_sync(~0u, across, 1);
-        named_sync(1, kWorkers);
-        sums.far_q[half][row] = far_q;
-        sums.far_k[half][row] = far_k;
-        sums.near_k[half][row] = near_k;
-        sums.near_q[quarter][half * 64 + lane] = near_q[0];
-        sums.near_q[quarter][half * 64 + 32 + lane] = near_q[1];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) across += __shfl_xor_sync(~0u, across, off);
+        sums.far_q[part][row] = far_q;
+        sums.far_k[part][row] = far_k;
+        sums.near_k[part][row] = near_k;
+        sums.near_q[quarter][part * 32 + lane] = near_q;
         if (lane == 0) sums.across[warp] = across;
         named_sync(1, kWorkers);
         if (warp == 0 && !sm.fail) {
             float later[4], before[4], all = 0.f;
-            for (int w = 0; w < 8; ++w) all += sums.across[w];
+#pragma unroll
+            for (int w = 0; w < kWorkerWarps; ++w) all += sums.across[w];
             all *= sm.whole;
+            auto four = [](const float (&x)[4][kDecayChunk], int t) { return (x[0][t] + x[1][t]) + (x[2][t] + x[3][t]); };
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int t = 4 * lane + i;
-                const float nq = (sums.near_q[0][t] + sums.near_q[1][t]) + (sums.near_q[2][t] + sums.near_q[3][t]);
-                later[i] = (sums.far_q[0][t] + sums.far_q[1][t]) + (nq - (sums.near_k[0][t] + sums.near_k[1][t]));
-                before[i] = sums.far_k[0][t] + sums.far_k[1][t];
+                later[i] = four(sums.far_q, t) + (four(sums.near_q, t) - four(sums.near_k, t));
+                before[i] = four(sums.far_k, t);
             }
             // later: sums from t on; before: sums up to t, t itself not among them
 #pragma unroll
@@ -479,12 +510,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 if (t < valid) a.dg[((int64_t)row0 + t) * a.H + h] = all + (later[i] + right) + (left + (i ? before[i - 1] : 0.f));
             }
         }
+        if (part == 0 && lane == 0) ptx::bulk_wait_read0();
     }
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 8) ptx::tmem_dealloc(tmem, 512);
+    if (warp == kWorkerWarps) ptx::tmem_dealloc(tmem, 512);
     if (sm.fail && tid == 0 && a.status) atomicOr(a.status, kStatusTimeout);
 }
 

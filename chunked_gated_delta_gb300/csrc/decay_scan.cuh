@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                         up = scale_to_f16(top);
                         named_sync(1, kThreads);  // (top is written again in the next chunk)
                     }
-                    const uint32_t row = swizzled_row(base + Shape::kS, v);
+                    // (kept: 64 values x all keys after another, as the gradients take them)
+                    const uint32_t row = OUT ? swizzled_row(base + Shape::kS, v)
+                                             : swizzled_row(base + Shape::kS + (v >> 6) * KB * 8192, v & 63);
 #pragma unroll
                     for (int c = 0; c < K / 8; ++c) {
                         uint32_t hi[4], lo[4];
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                             const float2 back = from_b16x2<F16>(hi[e]);
                             lo[e] = pack_b16x2(x - back.x, y - back.y, F16);
                         }
-                        const uint32_t p = (row ^ ((c & 7) << 4)) + (c >> 3) * V * 128;
+                        const uint32_t p = (row ^ ((c & 7) << 4)) + (c >> 3) * (OUT ? V * 128 : 8192);
                         sts128(p, hi[0], hi[1], hi[2], hi[3]);
                         if (!OUT) sts128(p + Shape::kStateBytes, lo[0], lo[1], lo[2], lo[3]);
                     }
