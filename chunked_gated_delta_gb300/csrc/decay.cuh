@@ -30,6 +30,7 @@ struct DecaySeqs {
     int32_t N, T;        // T: tokens of a sequence, or (packed) of all
     int32_t seg_chunks;  // chunks per piece
     int32_t pieces;      // grid size in pieces: exact, or (packed) an upper bound
+    int32_t whole;       // no sequence is cut: a piece is a sequence
 };
 
 // Where a state's memory is fp32 or bf16.
@@ -107,17 +108,22 @@ struct DecayPiece {
 };
 __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
 
+constexpr int kMostSorted = 512;  // sequences that are taken longest first
 struct DecayScratch {
     int32_t warp_pieces[32], warp_chunks[32];
     DecayPiece found;
 };
+struct DecaySortScratch : DecayScratch {
+    int32_t len[kMostSorted];
+};
 
 // The piece with this index, or the first of sequence `by_seq` (index then a sequence).  Called by
 // all THREADS threads.  A sequence without tokens has one piece where `empty` says so.  Returns
-// false if cu is not 0 = c0 <= c1 <= ... <= cN = T.
+// false if cu is not 0 = c0 <= c1 <= ... <= cN = T.  With `len` (kMostSorted, if there are not more sequences, uncut) the
+// index'th longest sequence: CTAs start in the order of their index, and a long one that starts last is waited for alone.
 template <int THREADS>
 __device__ __forceinline__ bool find_piece(const DecaySeqs& s, int index, bool by_seq, bool empty, DecayScratch& sm,
-                                           DecayPiece& out) {
+                                           DecayPiece& out, int32_t* len = nullptr) {
     if (!s.cu) {
         const int nc = ceil_div(s.T, kDecayChunk);
         const int per = max(ceil_div(nc, s.seg_chunks), empty ? 1 : 0);
@@ -132,6 +138,20 @@ __device__ __forceinline__ bool find_piece(const DecaySeqs& s, int index, bool b
         return true;
     }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (len && s.N <= kMostSorted) {
+        for (int n = tid; n < s.N; n += THREADS) len[n] = s.cu[n + 1] - s.cu[n];
+        if (tid == 0) sm.found.n = 0;
+        __syncthreads();
+        for (int n = tid; n < s.N; n += THREADS) {
+            int ahead = 0;
+            for (int m = 0; m < s.N; ++m) ahead += len[m] > len[n] || (len[m] == len[n] && m < n);
+            if (ahead == index) sm.found.n = n;
+        }
+        __syncthreads();
+        index = sm.found.n;
+        by_seq = true;
+        __syncthreads();
+    }
     const int each = (s.N + THREADS - 1) / THREADS;
     const int first = min(tid * each, s.N), last = min(first + each, s.N);
     int pieces = 0, chunks = 0;
@@ -211,34 +231,30 @@ struct LoadedG {
 };
 __device__ __forceinline__ LoadedG load_g(const float* g, int64_t stride, int h, int64_t row0, int valid, int lane) {
     LoadedG r;
+    const float* p = g + (row0 + lane * 4) * stride + h;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = lane * 4 + i;
-        r.v[i] = t < valid ? g[(row0 + t) * stride + h] : 0.f;
-    }
+    for (int i = 0; i < 4; ++i, p += stride) r.v[i] = lane * 4 + i < valid ? *p : 0.f;
     return r;
 }
 // One warp: the sums of a chunk; the last one is returned to all lanes.
 __device__ __forceinline__ Pair sum_decay(const LoadedG& g, ChunkDecay& out, int lane) {
-    Pair p[4];
-    p[0] = log2_decay(g.v[0]);
+    Pair run = log2_decay(g.v[0]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) p[i] = add_pairs(p[i - 1], log2_decay(g.v[i]));
-    Pair run = p[3];
-#pragma unroll
+    for (int i = 1; i < 4; ++i) run = add_pairs(run, log2_decay(g.v[i]));
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const Pair up{__shfl_up_sync(~0u, run.hi, off), __shfl_up_sync(~0u, run.lo, off)};
         if (lane >= off) run = add_pairs(up, run);
     }
-    Pair before{__shfl_up_sync(~0u, run.hi, 1), __shfl_up_sync(~0u, run.lo, 1)};
-    if (lane == 0) before = {0.f, 0.f};
+    Pair s{__shfl_up_sync(~0u, run.hi, 1), __shfl_up_sync(~0u, run.lo, 1)};
+    if (lane == 0) s = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const Pair s = add_pairs(before, p[i]);
+        s = add_pairs(s, log2_decay(g.v[i]));
         out.hi[lane * 4 + i] = s.hi;
         out.lo[lane * 4 + i] = s.lo;
     }
-    return {__shfl_sync(~0u, run.hi, 31), __shfl_sync(~0u, run.lo, 31)};
+    return {__shfl_sync(~0u, s.hi, 31), __shfl_sync(~0u, s.lo, 31)};
 }
 // exp of a chunk's whole decay, to less than its last bit: a state of thousands of chunks is multiplied by
 // one after the other, so their errors add up. 2^n times the power series of exp(x), |x| <= ln(2) / 2, to its
@@ -295,25 +311,22 @@ __device__ __forceinline__ uint32_t swizzled_row(uint32_t tile, int row) {
 }
 
 // ------------------------------------------------------------------ waits
-// A wait that runs out (after kWaitLimitNs, like all of them) is noted in `fail`, and from then on nobody waits: every
-// warp still goes through all of its barriers, so none is left standing at one. Results are then incomplete, and the
-// status says so. Few instructions, since every role has many of these in a loop that it goes through once per chunk.
-__device__ __forceinline__ uint32_t globaltimer_lo() {
+// A wait that runs out (after kDecayWaitCycles) is noted in `fail`, and from then on nobody waits: every warp still goes
+// through all of its barriers, so none is left standing at one. Results are then incomplete, and the status says so.
+// Few instructions, since every role has many of these in its loop: the roles of a scan run side by side, and what they
+// go through once per chunk has to fit the SM's instruction cache together (with 45 KB of it a prefill took 255 us).
+constexpr uint32_t kDecayWaitCycles = 4000000000u;  // about two seconds; the counter wraps around above it
+__device__ __forceinline__ uint32_t clock_lo() {
     uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
     return t;
 }
 __device__ __forceinline__ void wait_or_note(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
-    static_assert(kWaitLimitNs < (1ull << 32), "the timer's low word wraps around in 4.3 s");
-    // (the timer takes hundreds of cycles to read: after each thousand tries)
-    uint32_t tries = 0, t0 = 0;
+    const uint32_t t0 = clock_lo();
 #pragma unroll 1
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if ((++tries & 1023) != 0) continue;
-        if (*fail) return;
-        const uint32_t t = globaltimer_lo();
-        if (tries == 1024) t0 = t;
-        else if (t - t0 > (uint32_t)kWaitLimitNs) *fail = 1;
+        if (*fail) break;
+        if (clock_lo() - t0 > kDecayWaitCycles) *fail = 1;
     }
 }
 
@@ -325,6 +338,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], "
         "[%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with descriptors by their lower words (address and leading offset; of all operands here groups of rows are
+// 1024 bytes apart): the issuing thread's registers are few.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) & 0x3FFFu) << 16;
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .b64 b;\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi)
         : "memory");
 }
 // 32 lanes x 32 bits, 16 columns (see tmem_ld16).

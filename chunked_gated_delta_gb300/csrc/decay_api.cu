@@ -134,7 +134,7 @@ bool token_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t row
 }
 
 DecaySeqs seqs_of(const kda_dims& d, const int32_t* cu, int64_t pieces, int32_t seg_chunks, int32_t N) {
-    return DecaySeqs{cu, N, d.T, seg_chunks, (int32_t)pieces};
+    return DecaySeqs{cu, N, d.T, seg_chunks, (int32_t)pieces, seg_chunks == kUncut};
 }
 
 }  // namespace

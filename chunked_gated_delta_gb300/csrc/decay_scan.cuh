@@ -27,7 +27,9 @@ namespace {
 template <int KB, int VB, bool OUT>
 struct DecayScanShape {
     static constexpr int K = 64 * KB, V = 64 * VB;
-    static constexpr int kThreads = OUT ? 640 : 384;
+    static constexpr int kKeyWarps = OUT ? 8 : 4;  // (a thread has a token's row, or half of it)
+    static constexpr int kFirstState = 4 + kKeyWarps;
+    static constexpr int kThreads = 32 * (kFirstState + 4 + (OUT ? 8 : 0));
     static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kStateBytes = V * K * 2;
     // Stages: every tensor's tile is read early in a chunk (the scaled parts of k have buffers of their own, and so has
     // o), so one of each is enough where two do not fit.
@@ -40,25 +42,25 @@ struct DecayScanShape {
     static constexpr int kO = kS + (OUT ? 1 : 2) * kStateBytes;
     static constexpr int kSmall = kO + (OUT ? kYBytes : 0);
     // registers: those that the block is launched with, handed out as control, keys, state, scores, output
-    static constexpr int kControlRegs = OUT ? 64 : 64, kKeyRegs = OUT ? 64 : 176, kStateRegs = OUT ? 184 : 240;
-    static constexpr int kScoreRegs = 80, kOutRegs = 88;
-    static_assert(OUT ? kControlRegs + kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 5 * 96
+    static constexpr int kControlRegs = OUT ? 56 : 64, kKeyRegs = OUT ? 64 : 176, kStateRegs = OUT ? 168 : 240;
+    static constexpr int kScoreRegs = 64, kOutRegs = 64;
+    static_assert(OUT ? kControlRegs + 2 * kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 6 * 80
                       : kControlRegs + kKeyRegs + kStateRegs <= 3 * 160,
                   "within what the block is launched with");
     struct Small {
         ChunkDecay decay[2];
         float column[OUT ? kDecayChunk : 1];  // exp of the decay from a column to the end of its 32
         float whole[2], unscale[2], key_unscale[2];
-        uint32_t top[4], key_top[4];
+        uint32_t top[4], key_top[2][8];
         uint64_t x_full[2], x_empty[2], q_full[2], q_empty[2], y_full[2], y_empty[2], g_ready[2], g_free[2];
-        uint64_t scores, p_ready, s_ready, s_read, keys, keys_read, added, o_full, o_free;
+        uint64_t scores, p_ready, s_ready, keys, keys_read, added, added_read, far, far_ok, o_full, o_free[2];
         uint32_t tmem;
         int32_t fail;
     };
     static constexpr int kSmem = kSmall + (int)sizeof(Small);
-    static_assert(sizeof(Small) >= sizeof(DecayScratch), "the search's scratch fits");
+    static_assert(sizeof(Small) >= sizeof(DecaySortScratch), "the search's scratch fits");
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    static constexpr uint32_t kScores = 0, kAdded = OUT ? 128 : 0, kFar = 256, kNear = 384;  // TMEM columns
+    static constexpr uint32_t kScores = 0, kAdded = OUT ? 128 : 0, kOut = 256;  // TMEM columns (kOut: twice 128)
     static constexpr uint32_t kTmem = OUT ? 512 : 128;
 };
 
@@ -77,7 +79,9 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     ptx::grid_dep_wait();
     const int item = blockIdx.x / a.H, h = blockIdx.x - item * a.H;
     DecayPiece at;
-    if (!find_piece<Shape::kThreads>(a.seqs, item, false, true, *reinterpret_cast<DecayScratch*>(&sm), at)) {
+    auto& scratch = *reinterpret_cast<DecaySortScratch*>(&sm);
+    if (!find_piece<Shape::kThreads>(a.seqs, item, false, true, scratch, at,
+                                     a.seqs.whole ? scratch.len : nullptr)) {
         if (blockIdx.x == 0 && tid == 0 && a.status) atomicOr(a.status, kStatusBadSeqlens);
         return;
     }
@@ -93,17 +97,19 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&sm.x_full[s], 1);
-            ptx::mbar_init(&sm.x_empty[s], OUT ? 5 : 4);
+            ptx::mbar_init(&sm.x_empty[s], Shape::kKeyWarps + (OUT ? 1 : 0));
             ptx::mbar_init(&sm.q_full[s], 1);
             ptx::mbar_init(&sm.q_empty[s], 1);
             ptx::mbar_init(&sm.y_full[s], 1);
             ptx::mbar_init(&sm.y_empty[s], 1);
             ptx::mbar_init(&sm.g_ready[s], 1);
-            ptx::mbar_init(&sm.g_free[s], (OUT ? 12 : 4) + 2 * VB);
+            ptx::mbar_init(&sm.g_free[s], Shape::kKeyWarps + (OUT ? 8 : 0) + 2 * VB);
+            ptx::mbar_init(&sm.o_free[s], 4);
         }
-        for (uint64_t* b : {&sm.scores, &sm.s_read, &sm.keys_read, &sm.added, &sm.o_full}) ptx::mbar_init(b, 1);
-        for (uint64_t* b : {&sm.p_ready, &sm.keys, &sm.o_free}) ptx::mbar_init(b, 4);
-        ptx::mbar_init(&sm.s_ready, 2 * VB);
+        for (uint64_t* b : {&sm.scores, &sm.keys_read, &sm.added, &sm.far, &sm.o_full}) ptx::mbar_init(b, 1);
+        for (uint64_t* b : {&sm.p_ready, &sm.far_ok}) ptx::mbar_init(b, 4);
+        ptx::mbar_init(&sm.keys, Shape::kKeyWarps);
+        for (uint64_t* b : {&sm.s_ready, &sm.added_read}) ptx::mbar_init(b, 2 * VB);
         ptx::fence_mbar_init();
         sm.fail = 0;
     }
@@ -160,52 +166,54 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             // ---------------------------------------------------------- MMAs
             constexpr uint32_t id_scores = idesc16<F16>(128, 128, 0, 0), id_far = idesc16<F16>(128, V, 0, 0),
                                id_near = idesc16<F16>(128, V, 0, 1), id_added = idesc16<F16>(128, K, 1, 1);
-            const uint64_t hi_mn = ptx::smem_desc(base + Shape::kHi, 16384, 1024);
-            const uint64_t s_k = ptx::smem_desc(base + Shape::kS, 16, 1024);
             for (int it = 0; it < chunks && !*fail; ++it) {
                 const int sx = it % NS;
                 const uint32_t ph = it & 1, px = (it / NS) & 1;
-                const uint64_t y_mn = ptx::smem_desc(base + Shape::kY + sx * Shape::kYBytes, 16384, 1024);
+                const uint32_t y_mn = desc_lo(base + Shape::kY + sx * Shape::kYBytes, 16384);
+                const uint32_t q_k = desc_lo(base + Shape::kQ + sx * Shape::kXBytes, 16);
                 if constexpr (OUT) {
-                    const uint64_t q_k = ptx::smem_desc(base + Shape::kQ + sx * Shape::kXBytes, 16, 1024);
-                    const uint64_t x_k = ptx::smem_desc(base + Shape::kX + sx * Shape::kXBytes, 16, 1024);
+                    const uint32_t x_k = desc_lo(base + Shape::kX + sx * Shape::kXBytes, 16);
                     wait(sm.x_full[sx], px);
                     wait(sm.q_full[sx], px);
                     ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int ks = 0; ks < 4 * KB; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        ptx::mma_bf16(tmem + Shape::kScores, q_k + off, x_k + off, id_scores, ks > 0);
+                    for (uint32_t ks = 0; ks < 4 * KB; ++ks) {
+                        const uint32_t off = (ks & 3) * 2 + (ks >> 2) * 1024;
+                        mma_lo(tmem + Shape::kScores, q_k + off, x_k + off, id_scores, ks);
                     }
                     ptx::mma_commit(&sm.scores);
                     ptx::mma_commit(&sm.x_empty[sx]);
+                }
+                if constexpr (OUT) {
+                    const uint32_t t_out = tmem + Shape::kOut + ph * 128, s_k = desc_lo(base + Shape::kS, 16);
                     wait(sm.s_ready, ph);
-                    if (it > 0) wait(sm.o_free, ph ^ 1);
+                    if (it >= 2) wait(sm.o_free[ph], ((it >> 1) - 1) & 1);
                     ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int ks = 0; ks < 4 * KB; ++ks)
-                        ptx::mma_bf16(tmem + Shape::kFar, q_k + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                                      s_k + (((ks >> 2) * V * 128 + (ks & 3) * 32) >> 4), id_far, ks > 0);
-                    ptx::mma_commit(&sm.s_read);
+                    for (uint32_t ks = 0; ks < 4 * KB; ++ks)
+                        mma_lo(t_out, q_k + (ks & 3) * 2 + (ks >> 2) * 1024, s_k + (ks & 3) * 2 + (ks >> 2) * (V * 8), id_far, ks);
+                    ptx::mma_commit(&sm.far);
                     ptx::mma_commit(&sm.q_empty[sx]);
-                } else {
-                    wait(sm.s_ready, ph);
                 }
+                if (it > 0) wait(sm.added_read, ph ^ 1);
                 wait(sm.y_full[sx], px);
                 wait(sm.keys, ph);
                 ptx::tc_fence_after();
+                const uint32_t hi_mn = desc_lo(base + Shape::kHi, 16384);
 #pragma unroll 1
-                for (int ks = 0; ks < 16; ++ks)  // hi, then lo
-                    ptx::mma_bf16(tmem + Shape::kAdded, y_mn + (ks & 7) * 128,
-                                  hi_mn + (ks & 7) * 128 + (ks >> 3) * (Shape::kXBytes >> 4), id_added, ks > 0);
+                for (uint32_t ks = 0; ks < 16; ++ks)  // hi, then lo
+                    mma_lo(tmem + Shape::kAdded, y_mn + (ks & 7) * 128, hi_mn + (ks & 7) * 128 + (ks >> 3) * (Shape::kXBytes >> 4),
+                           id_added, ks);
                 ptx::mma_commit(&sm.added);
                 ptx::mma_commit(&sm.keys_read);
                 if constexpr (OUT) {
+                    const uint32_t t_out = tmem + Shape::kOut + ph * 128;
                     wait(sm.p_ready, ph);
+                    wait(sm.far_ok, ph);
                     ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem + Shape::kNear, tmem + Shape::kScores + ks * 8, y_mn + ks * 128, id_near, ks > 0);
+                    for (uint32_t ks = 0; ks < 8; ++ks)
+                        mma_ts_lo(t_out, tmem + Shape::kScores + ks * 8, y_mn + ks * 128, id_near);
                     ptx::mma_commit(&sm.o_full);
                 }
                 ptx::mma_commit(&sm.y_empty[sx]);
@@ -228,11 +236,13 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 arrive(sm.g_ready[st]);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < Shape::kFirstState) {
         if constexpr (OUT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
         // ---------------------------------------------------------- keys: scaled, in two parts
-        const int j = quarter * 32 + lane;  // the token whose row this thread has
+        // the token whose row this thread has, and 16-byte pieces from c_first on (all of it, or half)
+        constexpr int kPieces = K / 8 / (Shape::kKeyWarps / 4);
+        const int j = quarter * 32 + lane, c_first = ((warp - 4) >> 2) * kPieces;
         const uint32_t to = swizzled_row(base + Shape::kHi, j);
         for (int it = 0; it < chunks; ++it) {
             const int st = it & 1, sx = it % NS;
@@ -244,12 +254,13 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             arrive(sm.g_free[st]);
             wait(sm.x_full[sx], (it / NS) & 1);
             const uint32_t row = swizzled_row(base + Shape::kX + sx * Shape::kXBytes, j);
+            float up = 1.f;
             if constexpr (F16) {
                 // The scaled keys may be far below fp16's normal range, where a part keeps no relative precision: a
                 // power of two for all of the chunk's brings the largest near the top of it.
                 __half2 most = __half2half2(__ushort_as_half(0));
 #pragma unroll 4
-                for (int c = 0; c < K / 8; ++c) {
+                for (int c = c_first; c < c_first + kPieces; ++c) {
                     const uint4 x = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -257,48 +268,48 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 }
                 const float m = live ? fmaxf(__low2float(most), __high2float(most)) * fabsf(w) : 0.f;
                 const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(m));
-                if (lane == 0) sm.key_top[quarter] = top;
-                named_sync(4, 128);
-                const float up = scale_to_f16(max(max(sm.key_top[0], sm.key_top[1]), max(sm.key_top[2], sm.key_top[3])));
+                if (lane == 0) sm.key_top[st][warp - 4] = top;
+                named_sync(4, 32 * Shape::kKeyWarps);
+                uint32_t all = sm.key_top[st][0];
+#pragma unroll
+                for (int i = 1; i < Shape::kKeyWarps; ++i) all = max(all, sm.key_top[st][i]);
+                up = scale_to_f16(all);
                 w *= up;
-                if (j == 0) sm.key_unscale[st] = 1.f / up;
             }
-            if (it > 0) wait(sm.keys_read, st ^ 1);
-            const uint64_t w2 = pair_of(w, w), minus = pair_of(-1.f, -1.f);
-            // (A loop of few instructions: five warps with code of their own share what a scheduler keeps of it.)
-#pragma unroll 1
-            for (int c0 = 0; c0 < K / 8; c0 += 4) {
-                const uint32_t block = (uint32_t)(c0 >> 3) * 16384u;
-                uint4 x[4];
+            uint4 x[kPieces];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = lds128((row ^ (((c0 + i) & 7) << 4)) + block);
-                    if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 f = from_b16x2<F16>(in[e]);
-                        const uint64_t p = mul2(pair_of(f.x, f.y), w2);
-                        f = floats_of(p);
-                        hi[e] = pack_b16x2(f.x, f.y, F16);
-                        f = from_b16x2<F16>(hi[e]);
-                        f = floats_of(fma2(pair_of(f.x, f.y), minus, p));
-                        lo[e] = pack_b16x2(f.x, f.y, F16);
-                    }
-                    const uint32_t p = (to ^ (((c0 + i) & 7) << 4)) + block;
-                    sts128(p, hi[0], hi[1], hi[2], hi[3]);
-                    sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
-                }
+            for (int i = 0; i < kPieces; ++i) {
+                const int c = c_first + i;
+                x[i] = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
             }
             arrive(sm.x_empty[sx]);
+            if (it > 0) wait(sm.keys_read, st ^ 1);
+            if (F16 && j == 0 && c_first == 0) sm.key_unscale[st] = 1.f / up;
+            const uint64_t w2 = pair_of(w, w), minus = pair_of(-1.f, -1.f);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int c = c_first + i;
+                if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 f = from_b16x2<F16>(in[e]);
+                    const uint64_t p = mul2(pair_of(f.x, f.y), w2);
+                    f = floats_of(p);
+                    hi[e] = pack_b16x2(f.x, f.y, F16);
+                    f = from_b16x2<F16>(hi[e]);
+                    f = floats_of(fma2(pair_of(f.x, f.y), minus, p));
+                    lo[e] = pack_b16x2(f.x, f.y, F16);
+                }
+                const uint32_t p = (to ^ ((c & 7) << 4)) + (c >> 3) * 16384;
+                sts128(p, hi[0], hi[1], hi[2], hi[3]);
+                sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
+            }
             if (at.len - chunk_at(it) * kDecayChunk < kDecayChunk) {
                 // rows behind the sequence are another's, or nobody's: a zero weight would not hold back a NaN
                 wait(sm.y_full[sx], (it / NS) & 1);
-                if (!live) {
+                if (!live && c_first == 0) {
                     const uint32_t y = base + Shape::kY + sx * Shape::kYBytes + j * 128;
 #pragma unroll 1
                     for (int c = 0; c < V / 8; ++c) sts128(y + (c >> 3) * 16384 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
@@ -307,7 +318,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             ptx::fence_proxy_async_smem();
             arrive(sm.keys);
         }
-    } else if (warp < 12) {
+    } else if (warp < Shape::kFirstState + 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kStateRegs));
         // ---------------------------------------------------------- the state, transposed: column v of S
         const int v = quarter * 32 + lane;
@@ -319,12 +330,15 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             const uint16_t* start16 = static_cast<const uint16_t*>(dir.start.p) + seq * K * V + v;
             const float* start = first ? static_cast<const float*>(dir.start.p) + seq * K * V + v : piece;
             const bool none = a.totals_only || (first && !dir.start.p), b16 = first && dir.start.b16;
+            if (none) {
 #pragma unroll
-            for (int k0 = 0; k0 < K; k0 += 16) {  // (16 loads in flight)
+                for (int k = 0; k < K; ++k) S[k] = 0.f;
+            } else if (!b16) {  // (all loads in flight: one after the other in sixteens they took 6 us)
 #pragma unroll
-                for (int k = k0; k < k0 + 16; ++k)
-                    S[k] = none ? 0.f : b16 ? from_b16<false>(start16[k * V]) : start[k * V];
-                asm volatile("" ::: "memory");
+                for (int k = 0; k < K; ++k) S[k] = __ldg(start + k * V);
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k) S[k] = from_b16<false>(__ldg(start16 + k * V));
             }
             const bool keep = !OUT && dir.kept;
             float decay = 1.f;
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 const int st = it & 1, ph = it & 1;
                 if (OUT || keep) {
                     // S as 16 bits (and, kept, what that lost), in rows of 128 bytes as the MMAs read them
-                    if (OUT && it > 0) wait(sm.s_read, ph ^ 1);
+                    if (OUT && it > 0) wait(sm.far, ph ^ 1);  // (the far products have read the last one)
                     if (!OUT && it > 0) {
                         if (v == 0) ptx::bulk_wait_read0();  // the last chunk's copy has left
                         named_sync(1, kThreads);
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                         }
                     }
                 }
-                arrive(sm.s_ready);  // also: the last chunk's products have been read
+                if (OUT) arrive(sm.s_ready);
                 wait(sm.g_ready[st], (it >> 1) & 1);
                 const float whole = sm.whole[st];
                 arrive(sm.g_free[st]);
@@ -402,6 +416,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     }
                 }
                 ptx::tc_fence_before();
+                arrive(sm.added_read);
             }
             if (a.totals_only) {
 #pragma unroll
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             }
             if (keep && v == 0) ptx::bulk_wait0();
         }
-    } else if (warp < 16) {
+    } else if (warp < Shape::kFirstState + 8) {
         if constexpr (OUT) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kScoreRegs));
             // ------------------------------------------------------ P: row i of the scores
@@ -440,46 +455,45 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 // the end of its 32 and from there to i, both at most one: one multiplication each
                 // instead of an exponential per pair.
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < quarter; ++b) {
+                    const int end = 32 * b + 31;
+                    const float r = a.scale * exp2_fast((hi - d.hi[end]) + (lo - d.lo[end]));
+                    const uint64_t r2 = pair_of(r, r);
+                    float s[32];
                     uint32_t p[16];
-                    if (b <= quarter) {
-                        float s[32];
-                        ptx::tmem_ld16(t_row + 32 * b, s);
-                        ptx::tmem_ld16(t_row + 32 * b + 16, s + 16);
-                        if (b < quarter) {
-                            const int end = 32 * b + 31;
-                            const float r = a.scale * exp2_fast((hi - d.hi[end]) + (lo - d.lo[end]));
-                            ptx::tmem_ld_wait();
+                    ptx::tmem_ld16(t_row + 32 * b, s);
+                    ptx::tmem_ld16(t_row + 32 * b + 16, s + 16);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 c = *reinterpret_cast<const float4*>(&sm.column[32 * b + 4 * e]);
-                                float* x = s + 4 * e;
-                                const uint64_t r2 = pair_of(r, r);
-                                const float2 u = floats_of(mul2(pair_of(x[0], x[1]), mul2(r2, pair_of(c.x, c.y))));
-                                const float2 v = floats_of(mul2(pair_of(x[2], x[3]), mul2(r2, pair_of(c.z, c.w))));
-                                x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
-                            }
-                        } else {
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 h4 = *reinterpret_cast<const float4*>(&d.hi[32 * b + 4 * e]);
-                                const float4 l4 = *reinterpret_cast<const float4*>(&d.lo[32 * b + 4 * e]);
-                                const float hj[4] = {h4.x, h4.y, h4.z, h4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                                for (int f = 0; f < 4; ++f) {
-                                    const float w = a.scale * exp2_fast((hi - hj[f]) + (lo - lj[f]));
-                                    s[4 * e + f] = 4 * e + f <= lane ? s[4 * e + f] * w : 0.f;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] = pack_b16x2(s[2 * e], s[2 * e + 1], F16);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] = 0u;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float4 c = *reinterpret_cast<const float4*>(&sm.column[32 * b + 2 * e]);
+                        const float2 u = floats_of(mul2(pair_of(s[2 * e], s[2 * e + 1]), mul2(r2, pair_of(c.x, c.y))));
+                        const float2 v = floats_of(mul2(pair_of(s[2 * e + 2], s[2 * e + 3]), mul2(r2, pair_of(c.z, c.w))));
+                        p[e] = pack_b16x2(u.x, u.y, F16);
+                        p[e + 1] = pack_b16x2(v.x, v.y, F16);
                     }
                     tmem_st16(t_row + 16 * b, p);  // (over scores that have been read)
+                }
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {  // the diagonal's block
+                    float s[16];
+                    uint32_t p[8];
+                    ptx::tmem_ld16(t_row + 32 * quarter + c, s);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 h2 = *reinterpret_cast<const float2*>(&d.hi[32 * quarter + c + e]);
+                        const float2 l2 = *reinterpret_cast<const float2*>(&d.lo[32 * quarter + c + e]);
+                        const float u = s[e] * (a.scale * exp2_fast((hi - h2.x) + (lo - l2.x)));
+                        const float v = s[e + 1] * (a.scale * exp2_fast((hi - h2.y) + (lo - l2.y)));
+                        p[e >> 1] = pack_b16x2(c + e <= lane ? u : 0.f, c + e + 1 <= lane ? v : 0.f, F16);
+                    }
+                    tmem_st8(t_row + 16 * quarter + (c >> 1), p);
+                }
+#pragma unroll 1
+                for (int c = 16 * quarter + 16; c < 64; c += 8) {
+                    const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                    tmem_st8(t_row + c, none);
                 }
                 tmem_st_wait();
                 ptx::tc_fence_before();
@@ -499,39 +513,54 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             for (int it = 0; it < chunks; ++it) {
                 const int st = it & 1, tok = chunk_at(it) * kDecayChunk + i;
                 const bool whole = tok - lane + 32 <= at.len;
+                const uint32_t t_out = t_row + Shape::kOut + st * 128;
                 wait(sm.g_ready[st], (it >> 1) & 1);
                 float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]);
                 arrive(sm.g_free[st]);
+                // the far part, scaled by rows: the near products add to it
+                wait(sm.far, st);
+                ptx::tc_fence_after();
+                if (F16) f *= sm.unscale[st];
+#pragma unroll 1
+                for (int c = 0; c < V; c += 32) {
+                    float u[32];
+                    ptx::tmem_ld16(t_out + c, u);
+                    ptx::tmem_ld16(t_out + c + 16, u + 16);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 r = floats_of(mul2(pair_of(f, f), pair_of(u[e], u[e + 1])));
+                        u[e] = r.x, u[e + 1] = r.y;
+                    }
+                    tmem_st16(t_out + c, reinterpret_cast<const uint32_t*>(u));
+                    tmem_st16(t_out + c + 16, reinterpret_cast<const uint32_t*>(u + 16));
+                }
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                arrive(sm.far_ok);
                 if (lane == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
-                wait(sm.o_full, it & 1);
+                wait(sm.o_full, st);
                 ptx::tc_fence_after();
                 __syncwarp();
-                if (F16) f *= sm.unscale[st];
                 uint16_t* o = a.o + (((int64_t)at.bos + tok) * a.H + h) * V;
 #pragma unroll 1
-                for (int c = 0; c < V / 32; ++c) {
-                    float far[32], near[32];
-                    ptx::tmem_ld16(t_row + Shape::kFar + 32 * c, far);
-                    ptx::tmem_ld16(t_row + Shape::kNear + 32 * c, near);
-                    ptx::tmem_ld16(t_row + Shape::kFar + 32 * c + 16, far + 16);
-                    ptx::tmem_ld16(t_row + Shape::kNear + 32 * c + 16, near + 16);
+                for (int c = 0; c < V; c += 32) {
+                    float u[32];
+                    ptx::tmem_ld16(t_out + c, u);
+                    ptx::tmem_ld16(t_out + c + 16, u + 16);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int n = 8 * g + 2 * e;
-                            const float2 r = floats_of(fma2(pair_of(f, f), pair_of(far[n], far[n + 1]), pair_of(near[n], near[n + 1])));
-                            y[e] = pack_b16x2(r.x, r.y, F16);
-                        }
-                        if (whole) sts128((to ^ ((((c & 1) << 2) + g) << 4)) + (c >> 1) * 16384, y[0], y[1], y[2], y[3]);
-                        else if (tok < at.len) *reinterpret_cast<uint4*>(o + 32 * c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int e = 0; e < 4; ++e) y[e] = pack_b16x2(u[8 * g + 2 * e], u[8 * g + 2 * e + 1], F16);
+                        if (whole) sts128((to ^ (((c & 63) << 1) + g * 16)) + (c >> 6) * 16384, y[0], y[1], y[2], y[3]);
+                        else if (tok < at.len) *reinterpret_cast<uint4*>(o + c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
                 ptx::tc_fence_before();
                 ptx::fence_proxy_async_smem();
-                arrive(sm.o_free);
+                arrive(sm.o_free[st]);
                 if (whole && lane == 0) {
 #pragma unroll
                     for (int b = 0; b < VB; ++b)

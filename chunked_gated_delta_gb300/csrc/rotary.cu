@@ -30,6 +30,7 @@ struct RotaryArgs {
     const double* freqs;
     int64_t tokens, q_stride, k_stride, q_out_stride, k_out_stride;  // in elements
     int32_t q_heads, k_heads, dim, pairs, positions64, inverse;
+    uint32_t magic;  // e / per_head is the upper half of e * magic (0: divide)
     float amplitude;
 };
 
@@ -63,10 +64,10 @@ struct alignas(sizeof(T) * C) Piece {
 // C: elements of a load. A row of a head is items: those of pairs (two loads: in the half layout the
 // x and the y of C pairs, else 2 C elements of C pairs), then those that are copied (one load each, two in an item).
 template <int IO, int C, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotaryThreads) kda_rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kRotaryThreads, C > 1 ? 6 : 8) kda_rotary_kernel(const RotaryArgs a) {
     using T = typename Io<IO>::T;
     using P = Piece<T, C>;
-    __shared__ float2 s_turn[2][kMostPairs];  // cos, sin
+    __shared__ __align__(16) float2 s_turn[2][kMostPairs];  // cos, sin
     const int tid = threadIdx.x;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kRotaryThreads) kda_rotary_kernel(const Rotary
         int first, second, pair, count;  // offsets of the two loads; first pair (-1: copied), loads of an item
     };
     auto item_at = [&](int64_t tok, int e) {
-        const int head = e / per_head, i = e - head * per_head;
+        const int head = a.magic ? (int)__umulhi((uint32_t)e, a.magic) : e / per_head, i = e - head * per_head;
         At r;
         if (head < a.q_heads) {
             r.in = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * a.dim;
@@ -149,20 +150,41 @@ __global__ void __launch_bounds__(kRotaryThreads) kda_rotary_kernel(const Rotary
                 if (e >= items) break;
                 const At at = item_at(tok, e);
                 if (at.pair >= 0) {
+                    if constexpr (C == 8) {  // 16 bits: words of two elements
+                        const float4* turns = reinterpret_cast<const float4*>(&s_turn[buf][at.pair]);  // two pairs' each
+                        uint32_t* u = reinterpret_cast<uint32_t*>(&x[i]);
+                        uint32_t* w = reinterpret_cast<uint32_t*>(&y[i]);
+                        constexpr bool kF16 = IO == KDA_DTYPE_F16;
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const float2 t = s_turn[buf][at.pair + c];
-                        T *u, *w;
-                        if constexpr (INTERLEAVED) {
-                            u = 2 * c < C ? &x[i].x[2 * c % C] : &y[i].x[2 * c % C];
-                            w = 2 * c + 1 < C ? &x[i].x[(2 * c + 1) % C] : &y[i].x[(2 * c + 1) % C];
-                        } else {
-                            u = &x[i].x[c];
-                            w = &y[i].x[c];
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 t = turns[c];
+                            if constexpr (INTERLEAVED) {
+                                uint32_t* v = c < 2 ? u + 2 * c : w + 2 * c - 4;
+                                const float2 m = from_b16x2<kF16>(v[0]), n = from_b16x2<kF16>(v[1]);
+                                v[0] = pack_b16x2(m.x * t.x - m.y * t.y, m.x * t.y + m.y * t.x, kF16);
+                                v[1] = pack_b16x2(n.x * t.z - n.y * t.w, n.x * t.w + n.y * t.z, kF16);
+                            } else {
+                                const float2 m = from_b16x2<kF16>(u[c]), n = from_b16x2<kF16>(w[c]);
+                                u[c] = pack_b16x2(m.x * t.x - n.x * t.y, m.y * t.z - n.y * t.w, kF16);
+                                w[c] = pack_b16x2(m.x * t.y + n.x * t.x, m.y * t.w + n.y * t.z, kF16);
+                            }
                         }
-                        const float m = Io<IO>::get(*u), n = Io<IO>::get(*w);
-                        *u = Io<IO>::put(m * t.x - n * t.y);
-                        *w = Io<IO>::put(m * t.y + n * t.x);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            const float2 t = s_turn[buf][at.pair + c];
+                            T *u, *w;
+                            if constexpr (INTERLEAVED) {
+                                u = 2 * c < C ? &x[i].x[2 * c % C] : &y[i].x[2 * c % C];
+                                w = 2 * c + 1 < C ? &x[i].x[(2 * c + 1) % C] : &y[i].x[(2 * c + 1) % C];
+                            } else {
+                                u = &x[i].x[c];
+                                w = &y[i].x[c];
+                            }
+                            const float m = Io<IO>::get(*u), n = Io<IO>::get(*w);
+                            *u = Io<IO>::put(m * t.x - n * t.y);
+                            *w = Io<IO>::put(m * t.y + n * t.x);
+                        }
                     }
                 } else if (at.in == at.out) {
                     continue;
@@ -234,7 +256,11 @@ extern "C" kda_status kda_rotary(const void* q, const void* k, const void* posit
         for (const void* x : {k, static_cast<const void*>(k_out)}) wide = wide && is_aligned(x, 16);
         for (int64_t x : {a.k_stride, a.k_out_stride}) wide = wide && x % C == 0;
     }
-    const int64_t most = (int64_t)device_sm_count() * 12;
+    const int W = wide ? C : 1;
+    const uint32_t per_head = (uint32_t)(p.pairs / W + (dim - 2 * p.pairs + 2 * W - 1) / (2 * W));
+    // (floor(2^32 / d) + 1 divides e by d where e * d < 2^32)
+    if (per_head > 1 && (uint64_t)(q_heads + k_heads) * per_head * per_head < (1ull << 32)) a.magic = (uint32_t)((1ull << 32) / per_head) + 1;
+    const int64_t most = (int64_t)device_sm_count() * 6;
     const unsigned grid = (unsigned)(tokens < most ? tokens : most);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
