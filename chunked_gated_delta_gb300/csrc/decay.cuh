@@ -73,7 +73,7 @@ struct DecayJoinArgs {
 
 struct DecayGradArgs {
     CUtensorMap tm_q, tm_k, tm_v, tm_do;
-    CUtensorMap tm_dq, tm_dk, tm_dv;  // boxes of 64 x 32 rows (dq, dk: not grouped)
+    CUtensorMap tm_dq, tm_dk, tm_dv;  // boxes of 128 bytes x 32 rows (dq, dk: as they are written)
     DecaySeqs seqs;      // seg_chunks = 1
     const float* g;
     int64_t g_stride;

@@ -29,8 +29,8 @@ struct DecayPlan {
 DecayPlan decay_plan(const kda_dims& d, bool backward) {
     const bool packed = d.num_seqs > 0;
     const int64_t N = packed ? d.num_seqs : d.B, all = ceil_div(d.T, kDecayChunk);
-    // packed lengths are not known here: a few times their mean is planned for
-    const int64_t mean = (all + N - 1) / N, nc = !packed ? all : all < 4 * mean ? all : 4 * mean;
+    // packed lengths are not known here: the longest is taken for twice their mean
+    const int64_t mean = (all + N - 1) / N, nc = !packed ? all : all < 2 * mean ? all : 2 * mean;
     const int dirs = backward ? 2 : 1;
     const PassUs pass = backward ? kKeepUs : kOutUs;
     const int64_t units = N * d.H * dirs;
@@ -133,6 +133,15 @@ bool token_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t row
     return make_tensormap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// fp32 parts of a group's dq and dk [rows, H, K]: boxes of 32 x 32 rows
+bool group_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t rows) {
+    if (rows == 0) return true;
+    const uint64_t dims[3] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)rows};
+    const uint64_t strides[2] = {(uint64_t)dim * 4, (uint64_t)dim * 4 * heads};
+    const uint32_t box[3] = {32, 1, 32};
+    return make_tensormap(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 DecaySeqs seqs_of(const kda_dims& d, const int32_t* cu, int64_t pieces, int32_t seg_chunks, int32_t N) {
     return DecaySeqs{cu, N, d.T, seg_chunks, (int32_t)pieces, seg_chunks == kUncut};
 }
@@ -230,8 +239,10 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
     DecayGradArgs a{};
     if (!token_map(&a.tm_q, q, d.K, hq, rows, sd.q) || !token_map(&a.tm_k, k, d.K, hq, rows, sd.k) ||
         !token_map(&a.tm_v, v, d.V, d.H, rows, sd.v) || !token_map(&a.tm_do, d_o, d.V, d.H, rows, sd.d_o) ||
-        !token_map(&a.tm_dq, dq, d.K, hq, rows, (int64_t)hq * d.K, 32) ||
-        !token_map(&a.tm_dk, dk, d.K, hq, rows, (int64_t)hq * d.K, 32) || !token_map(&a.tm_dv, dv, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
+        (!grouped && (!token_map(&a.tm_dq, dq, d.K, hq, rows, (int64_t)hq * d.K, 32) ||
+                      !token_map(&a.tm_dk, dk, d.K, hq, rows, (int64_t)hq * d.K, 32))) ||
+        (grouped && (!group_map(&a.tm_dq, static_cast<uint8_t*>(workspace) + ws.dq32, d.K, d.H, rows) ||
+                     !group_map(&a.tm_dk, static_cast<uint8_t*>(workspace) + ws.dk32, d.K, d.H, rows))) || !token_map(&a.tm_dv, dv, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
         return KDA_ERR_CUDA;
     DecayScanArgs c{};
     const int32_t b16 = opts->state_dtype == KDA_STATE_BF16;

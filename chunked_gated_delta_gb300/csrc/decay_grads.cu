@@ -50,6 +50,7 @@ struct GradShape {
     static constexpr int kSmem = kSmall + (int)sizeof(Small);
     static_assert(sizeof(Small) >= sizeof(DecayScratch) && sizeof(Sums) <= 32768, "what shares memory fits");
     static_assert(kSmem <= 227 * 1024, "fits an SM");
+    static_assert(4 * kPart == 2 * kXBytes, "a group's fp32 dq and dk fit where q and k, and the states, were");
     // Where part `part` of 64 values of dS lies, the vb'th time.
     static __host__ __device__ constexpr int d_state(int vb, int part) {
         return vb == 0 ? kRing + (2 + part) * kPart : part == 0 ? kRing + 3 * kPart : kV;
@@ -398,8 +399,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         ptx::tc_fence_before();
         arrive(sm.dv_ok);
 
-        // Out: whole tiles by TMA, from where their inputs were (q, k and v have been read by then); rows of a
-        // sequence's last chunk, and fp32 parts of a group, by their threads.
+        // Out: whole tiles by TMA, from where inputs were that have been read by then; rows of a sequence's last chunk
+        // by their threads.
         const bool live = row < valid, staged = valid == kDecayChunk;
         const int64_t tok = (int64_t)row0 + row;
         auto store16 = [&](uint32_t t, int col, int count, uint32_t tile, uint16_t* to) {
@@ -422,16 +423,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 }
             }
         };
-        auto store32 = [&](uint32_t t, float* to) {
+        auto store32 = [&](uint32_t t, uint32_t tile, float* to) {
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 16) {
+            for (int c = part * kCols; c < (part + 1) * kCols; c += 16) {
                 float u[16];
                 ptx::tmem_ld16(t + c, u);
                 ptx::tmem_ld_wait();
-                if (live)
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+                const uint32_t p = swizzled_row(tile + (c >> 5) * 16384, row) ^ ((c & 31) << 2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<float4*>(to + c + 4 * e) = make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+                for (int e = 0; e < 4; ++e) {
+                    if (staged) sts128(p ^ (e << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    else if (live) *reinterpret_cast<float4*>(to + c + 4 * e) = make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+                }
             }
         };
         wait(sm.dqk, 0);
@@ -441,28 +445,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             store16(t_row + kTdq + part * kCols, part * kCols, kCols, base + Shape::kQ, static_cast<uint16_t*>(a.dq) + to);
             store16(t_row + kTdk + part * kCols, part * kCols, kCols, base + Shape::kK, static_cast<uint16_t*>(a.dk) + to);
         } else {
-            store32(t_row + kTdq + part * kCols, static_cast<float*>(a.dq) + to + part * kCols);
-            store32(t_row + kTdk + part * kCols, static_cast<float*>(a.dk) + to + part * kCols);
+            store32(t_row + kTdq, base + Shape::kQ, static_cast<float*>(a.dq) + to);
+            store32(t_row + kTdk, base + Shape::kRing, static_cast<float*>(a.dk) + to);
         }
         // (the four warps of these rows: one of them sends what all have written)
-        auto send = [&](bool what, auto store) {
+        auto send = [&](auto store) {
             ptx::fence_proxy_async_smem();
             named_sync(2 + quarter, 128);
-            if (staged && what && part == 0 && lane == 0) {
+            if (staged && part == 0 && lane == 0) {
                 store();
                 ptx::bulk_commit();
             }
         };
-        send(a.group == 1, [&] {
-            for (int b = 0; b < KB; ++b) {
-                ptx::tma_store_3d(&a.tm_dq, raw + Shape::kQ + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
-                ptx::tma_store_3d(&a.tm_dk, raw + Shape::kK + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
+        send([&] {
+            // (fp32: twice the columns of 128 bytes, dq's where q and k were, dk's where the states were)
+            const int blocks = a.group == 1 ? KB : 2 * KB, wide = 64 / (a.group == 1 ? 1 : 2);
+            const int from_dk = a.group == 1 ? Shape::kK : Shape::kRing;
+            for (int b = 0; b < blocks; ++b) {
+                const int at_box = b * 16384 + quarter * 4096;
+                ptx::tma_store_3d(&a.tm_dq, raw + Shape::kQ + at_box, b * wide, h, row0 + quarter * 32);
+                ptx::tma_store_3d(&a.tm_dk, raw + from_dk + at_box, b * wide, h, row0 + quarter * 32);
             }
         });
         wait(sm.dv, 0);
         ptx::tc_fence_after();
         store16(t_dv, part * kColsV, kColsV, base + Shape::kV, a.dv + (tok * a.H + h) * V);
-        send(true, [&] {
+        send([&] {
             for (int b = 0; b < VB; ++b)
                 ptx::tma_store_3d(&a.tm_dv, raw + Shape::kV + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
         });
