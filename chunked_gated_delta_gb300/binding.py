@@ -545,7 +545,7 @@ def decay_fwd(q, k, v, g, scale=None, h0=None, cu_seqlens=None, output_final_sta
     reads q/k head h // (H // Hqk)).  h0: [N,H,K,V] fp32 or bf16 or None; ht has
     its dtype, or ``state_dtype``, or fp32.  cu_seqlens: int32 [N+1] on the device
     (B must be 1) or None.  scale defaults to K**-0.5.  ``workspace``: a uint8 CUDA tensor of
-    decay_workspace_size bytes, on 1024 bytes, or None (then one is allocated per call).
+    decay_workspace_size bytes, or None (then one is allocated per call).
     ``status``: an int32 CUDA tensor that starts at zero and takes errors in
     cu_seqlens and waits that ran out (``binding.status`` reads it).  All tensors,
     and ``stream``, are of one GPU; outputs are allocated for ``stream``.

@@ -174,7 +174,7 @@ extern "C" kda_status kda_decay_fwd(const void* q, const void* k, const void* v,
     if (!is_aligned(g, 4) || !is_aligned(cu_seqlens, 4) || !is_aligned(status_word, 4)) return KDA_ERR_ALIGNMENT;
     const DecayPlan plan = decay_plan(d, false);
     const DecayWs ws = decay_ws(d, *opts, plan, false);
-    if (ws.total > 0 && (!workspace || !is_aligned(workspace, 1024) || workspace_bytes < ws.total)) return KDA_ERR_WORKSPACE;
+    if (ws.total > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < ws.total)) return KDA_ERR_WORKSPACE;
     if (rows == 0 && !ht) return KDA_OK;
     const int hq = opts->qk_heads > 0 ? opts->qk_heads : d.H;
     const bool f16 = opts->io_dtype == KDA_IO_F16;
@@ -233,7 +233,7 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
         return KDA_ERR_ALIGNMENT;
     const DecayPlan plan = decay_plan(d, true);
     const DecayWs ws = decay_ws(d, *opts, plan, true);
-    if (ws.total > 0 && (!workspace || !is_aligned(workspace, 1024) || workspace_bytes < ws.total)) return KDA_ERR_WORKSPACE;
+    if (ws.total > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < ws.total)) return KDA_ERR_WORKSPACE;
     const int hq = opts->qk_heads > 0 ? opts->qk_heads : d.H;
     const bool f16 = opts->io_dtype == KDA_IO_F16, grouped = hq != d.H;
     DecayGradArgs a{};

@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     auto& sm = *reinterpret_cast<typename Shape::Small*>(raw + Shape::kSmall);
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
 
-    ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int item = blockIdx.x / a.H, h = blockIdx.x - item * a.H, hq = h / a.group;
     DecayPiece at;
@@ -106,6 +105,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
+    // (not before: a dependent that shares this SM could take the TMEM that this block still needs)
+    ptx::grid_dep_launch();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;

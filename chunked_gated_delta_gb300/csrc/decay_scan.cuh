@@ -27,7 +27,7 @@ namespace {
 template <int KB, int VB, bool OUT>
 struct DecayScanShape {
     static constexpr int K = 64 * KB, V = 64 * VB;
-    static constexpr int kKeyWarps = OUT ? 8 : 4;  // (a thread has a token's row, or half of it)
+    static constexpr int kKeyWarps = 8;  // (a thread has half of a token's row)
     static constexpr int kFirstState = 4 + kKeyWarps;
     static constexpr int kThreads = 32 * (kFirstState + 4 + (OUT ? 8 : 0));
     static constexpr int kXBytes = KB * 16384, kYBytes = VB * 16384, kStateBytes = V * K * 2;
@@ -42,10 +42,10 @@ struct DecayScanShape {
     static constexpr int kO = kS + (OUT ? 1 : 2) * kStateBytes;
     static constexpr int kSmall = kO + (OUT ? kYBytes : 0);
     // registers: those that the block is launched with, handed out as control, keys, state, scores, output
-    static constexpr int kControlRegs = OUT ? 56 : 64, kKeyRegs = OUT ? 64 : 176, kStateRegs = OUT ? 168 : 240;
+    static constexpr int kControlRegs = OUT ? 56 : 64, kKeyRegs = OUT ? 64 : 96, kStateRegs = OUT ? 168 : 240;
     static constexpr int kScoreRegs = 64, kOutRegs = 64;
     static_assert(OUT ? kControlRegs + 2 * kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 6 * 80
-                      : kControlRegs + kKeyRegs + kStateRegs <= 3 * 160,
+                      : kControlRegs + 2 * kKeyRegs + kStateRegs <= 4 * 128,
                   "within what the block is launched with");
     struct Small {
         ChunkDecay decay[2];
@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     const DecayScanDir& dir = a.dir[blockIdx.y];
     const bool reverse = !OUT && dir.reverse;
 
-    ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int item = blockIdx.x / a.H, h = blockIdx.x - item * a.H;
     DecayPiece at;
@@ -118,6 +117,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
+    // (not before: a dependent that shares this SM could take the TMEM that this block still needs)
+    ptx::grid_dep_launch();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem, base = ptx::smem_u32(raw);
@@ -237,8 +238,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             }
         }
     } else if (warp < Shape::kFirstState) {
-        if constexpr (OUT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
         // ---------------------------------------------------------- keys: scaled, in two parts
         // the token whose row this thread has, and 16-byte pieces from c_first on (all of it, or half)
         constexpr int kPieces = K / 8 / (Shape::kKeyWarps / 4);

@@ -228,6 +228,7 @@ extern "C" kda_status kda_rotary(const void* q, const void* k, const void* posit
     if (tokens == 0) return KDA_OK;
     if (!q || !q_out || !positions || !freqs || (k_heads > 0 && (!k || !k_out))) return KDA_ERR_INVALID_ARG;
     // in place, rows as they lie, or apart
+    if (k_heads > 0 && (q_out == k_out || q_out == k || k_out == q)) return KDA_ERR_INVALID_ARG;
     if ((q == q_out && a.q_stride != a.q_out_stride) || (k_heads > 0 && k == k_out && a.k_stride != a.k_out_stride))
         return KDA_ERR_INVALID_ARG;
     const int es = dtype_bytes(p.io_dtype);

@@ -434,12 +434,8 @@ at::Tensor workspace_of(const DecayInputs& x, const at::Tensor* given, bool back
         *at_ = given->data_ptr();
     } else {
         *bytes = want == (size_t)-1 ? 0 : want;
-        if (*bytes) {  // (torch's blocks start on 512 bytes, the workspace on 1024)
-            made = empty({(int64_t)*bytes + 512}, at::kByte, x.q);
-            *at_ = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(made.data_ptr()) + 1023) & ~(uintptr_t)1023);
-        } else {
-            *at_ = nullptr;
-        }
+        if (*bytes) made = empty({(int64_t)*bytes}, at::kByte, x.q);
+        *at_ = *bytes ? made.data_ptr() : nullptr;
     }
     return made;
 }

@@ -505,7 +505,7 @@ kda_status kda_linear(const void* x, const void* w, const float* bias, const voi
  * Inputs are finite: a value that is not reaches the other tokens of its chunk.
  * Scores and states are rounded to io_dtype as operands of their products (states in
  * fp16 by a common power of two, so they keep fp32's range); the states themselves, and
- * what adds to them, keep 2^-17 of themselves or better. Results do not depend on timing (no atomics).
+ * what adds to them, keep 2^-17 of themselves (bf16) or 2^-22 (fp16). Results do not depend on timing (no atomics).
  */
 typedef struct kda_decay_opts {
     int32_t io_dtype;
@@ -523,7 +523,7 @@ typedef struct kda_decay_opts {
  * Long sequences of few heads are cut into pieces that run side by side: a pass over k and v
  * finds what each adds to the state, a join gives each its entry state. The backward keeps
  * the state before every chunk and its gradient: 8 K V bytes per 128 tokens and head.
- * Workspaces are 1024-byte aligned; calls that may run concurrently do not share one.
+ * Workspaces are 256-byte aligned; calls that may run concurrently do not share one.
  */
 size_t kda_decay_workspace_size(const kda_dims* dims, const kda_decay_opts* opts, int32_t backward);
 
@@ -562,7 +562,8 @@ kda_status kda_decay_step(const void* q, const void* k, const void* v, const flo
  * and the rest is copied. Pairs are (i, i + pairs), or with `interleaved` (2 i, 2 i + 1). With
  * `inverse` the angle is -a (the gradients of q and k from those of their turned values).
  *   q, q_out  [tokens, q_heads, dim], k, k_out [tokens, k_heads, dim] bf16, fp16 or fp32 (io_dtype);
- *             k_heads = 0: no k.  An output may be its input with the same stride.
+ *             k_heads = 0: no k.  An output may be its own input with the same stride; nothing else
+ *             of the four shares memory (KDA_ERR_INVALID_ARG where they begin alike)
  *   positions int32, or int64 with positions_i64, [tokens]: any value
  *   freqs     fp64 [pairs] radians per position; a is right to 2^-31 of a turn beside 2^-53 of position * freq
  *   *_stride  elements between tokens (0: contiguous); any alignment of the elements' own size is

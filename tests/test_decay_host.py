@@ -15,7 +15,7 @@ from chunked_gated_delta_gb300 import binding, layer
 from test_layer_host import Operators
 from test_ops_devices import Named
 
-FAKE = 1 << 20  # a 1024-byte-aligned non-null address; never dereferenced on these paths
+FAKE = 1 << 20  # an aligned non-null address; never dereferenced on these paths
 P = ctypes.c_void_p
 BF16, F32, F64, I32, I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
 
@@ -77,7 +77,7 @@ def test_forward_refusals(lib):
         assert call_fwd(lib, **kw) == 3, kw
     long = (1, 40000, 1, 128, 128, 0)                                 # cut into pieces: needs a workspace
     assert call_fwd(lib, dims=long, ws=0) == 4 and call_fwd(lib, dims=long, size=1000) == 4
-    assert call_fwd(lib, dims=long, ws=FAKE + 512) == 4
+    assert call_fwd(lib, dims=long, ws=FAKE + 128) == 4
     assert call_fwd(lib, dims=(2, 0, 4, 128, 128, 0), q=0, k=0, v=0, g=0, o=0) == 0  # nothing to do
 
 
@@ -86,7 +86,7 @@ def test_backward_refusals(lib):
     assert call_bwd(lib, h0=FAKE, dh0=FAKE) == 1 and call_bwd(lib, dht=FAKE, dh0=FAKE) == 1
     for kw in (dict(do=FAKE + 8), dict(dq=FAKE + 8), dict(dh0=FAKE + 4), dict(dg=FAKE + 1), dict(do_stride=516)):
         assert call_bwd(lib, **kw) == 3, kw
-    assert call_bwd(lib, ws=0) == 4 and call_bwd(lib, size=100) == 4 and call_bwd(lib, ws=FAKE + 256) == 4
+    assert call_bwd(lib, ws=0) == 4 and call_bwd(lib, size=100) == 4 and call_bwd(lib, ws=FAKE + 64) == 4
 
 
 def test_step_refusals(lib):
@@ -97,7 +97,7 @@ def test_step_refusals(lib):
 
 
 def test_rotary_refusals(lib):
-    def call(tokens=4, hq=2, hk=1, dim=64, q=FAKE, k=FAKE, pos=FAKE, freqs=FAKE, qo=FAKE * 2, ko=FAKE * 2, opts=None, **kw):
+    def call(tokens=4, hq=2, hk=1, dim=64, q=FAKE, k=FAKE * 3, pos=FAKE, freqs=FAKE, qo=FAKE * 2, ko=FAKE * 4, opts=None, **kw):
         o = binding.RotaryOpts(**{"pairs": 32, "amplitude": 1.0, **kw}) if opts is None else opts
         return lib.kda_rotary(P(q), P(k), P(pos), P(freqs), P(qo), P(ko), tokens, hq, hk, dim, ctypes.byref(o) if o else None, None)
 
@@ -105,7 +105,8 @@ def test_rotary_refusals(lib):
     for kw in (dict(tokens=-1), dict(hq=0), dict(hk=-1), dict(dim=0), dict(pairs=0), dict(pairs=33), dict(io_dtype=3),
                dict(positions_i64=2), dict(interleaved=2), dict(inverse=-1), dict(reserved=1), dict(q_stride=127),
                dict(k_out_stride=8), dict(q=0), dict(k=0), dict(pos=0), dict(freqs=0), dict(qo=0), dict(ko=0),
-               dict(qo=FAKE, q_stride=136), dict(ko=FAKE, k_out_stride=72)):
+               dict(qo=FAKE, q_stride=136), dict(ko=FAKE * 3, k_out_stride=72), dict(ko=FAKE * 2), dict(qo=FAKE * 3),
+               dict(ko=FAKE)):
         assert call(**kw) == 1, kw
     assert call(dim=2048, pairs=513) == 2
     for kw in (dict(q=FAKE + 1), dict(ko=FAKE + 1), dict(pos=FAKE + 2), dict(positions_i64=1, pos=FAKE + 4), dict(freqs=FAKE + 4)):
