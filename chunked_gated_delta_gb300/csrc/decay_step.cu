@@ -30,6 +30,7 @@ struct DecayStepArgs {
     int64_t q_stride, k_stride, v_stride, g_stride;
     float scale;
     int32_t N, T, H, V, group, num_slots;
+    int32_t vec;  // rows of q, k and v take loads of four elements
 };
 
 template <bool STATE16>
@@ -50,13 +51,24 @@ __device__ __forceinline__ void store_four(void* p, int64_t four, float4 s) {
         static_cast<float4*>(p)[four] = s;
 }
 
+// Four 16-bit elements; vec: together.
+template <bool F16>
+__device__ __forceinline__ float4 load_inputs(const uint16_t* p, bool vec) {
+    if (vec) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        const float2 x = from_b16x2<F16>(w.x), y = from_b16x2<F16>(w.y);
+        return make_float4(x.x, x.y, y.x, y.y);
+    }
+    return make_float4(from_b16<F16>(p[0]), from_b16<F16>(p[1]), from_b16<F16>(p[2]), from_b16<F16>(p[3]));
+}
+
 // One CTA has VT columns of one (sequence, head): THREADS threads, each kRows rows of four columns.
 template <int K, int VT, int THREADS, bool F16, bool STATE16, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const DecayStepArgs a) {
     constexpr int kColGroups = VT / 4, kRowLanes = THREADS / kColGroups, kRows = K / kRowLanes;
     constexpr int kWarps = THREADS / 32, kParts = kColGroups >= 32 ? kRowLanes : kWarps;
     static_assert(kRows >= 1 && kRows * kRowLanes == K, "the threads tile the K rows");
-    __shared__ float s_k[kStepTokens][K], s_q[kStepTokens][K];
+    __shared__ __align__(16) float s_k[kStepTokens][K], s_q[kStepTokens][K];
     __shared__ float4 s_v[kStepTokens][kColGroups];
     __shared__ float s_decay[kStepTokens];
     __shared__ float4 s_o[kStepTokens][kParts][kColGroups];
@@ -92,20 +104,25 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const D
         for (int i = 0; i < kRows; ++i) S[i] = load_four<STATE16>(a.state, at + i * row_step);
     }
     const int hq = h / a.group;
+    // Inputs of kStepTokens tokens, four elements a thread where rows allow it: one trip to memory.
     auto stage = [&](int t0) {
-        for (int e = tid; e < kStepTokens * K; e += THREADS) {
-            const int j = e / K, r = e % K;
-            if (t0 + j < len) {
+        constexpr int kEach = K / 4, kEachV = VT / 4;
+#pragma unroll
+        for (int e0 = 0; e0 < kStepTokens * kEach; e0 += THREADS) {
+            const int j = (e0 + tid) / kEach, r = (e0 + tid) % kEach * 4;
+            if (j < kStepTokens && t0 + j < len) {
                 const int64_t row = row0 + t0 + j;
-                s_k[j][r] = from_b16<F16>(a.k[row * a.k_stride + (int64_t)hq * K + r]);
-                s_q[j][r] = from_b16<F16>(a.q[row * a.q_stride + (int64_t)hq * K + r]);
+                const uint16_t* k = a.k + row * a.k_stride + (int64_t)hq * K + r;
+                const uint16_t* q = a.q + row * a.q_stride + (int64_t)hq * K + r;
+                *reinterpret_cast<float4*>(&s_k[j][r]) = load_inputs<F16>(k, a.vec);
+                *reinterpret_cast<float4*>(&s_q[j][r]) = load_inputs<F16>(q, a.vec);
             }
         }
-        for (int e = tid; e < kStepTokens * VT; e += THREADS) {
-            const int j = e / VT, c = e % VT;
-            if (t0 + j < len)
-                reinterpret_cast<float*>(s_v[j])[c] =
-                    from_b16<F16>(a.v[(row0 + t0 + j) * a.v_stride + (int64_t)h * a.V + tile * VT + c]);
+#pragma unroll
+        for (int e0 = 0; e0 < kStepTokens * kEachV; e0 += THREADS) {
+            const int j = (e0 + tid) / kEachV, c = (e0 + tid) % kEachV;
+            if (j < kStepTokens && t0 + j < len)
+                s_v[j][c] = load_inputs<F16>(a.v + (row0 + t0 + j) * a.v_stride + (int64_t)h * a.V + tile * VT + c * 4, a.vec);
         }
         if (tid < kStepTokens && t0 + tid < len) s_decay[tid] = expf(a.g[(row0 + t0 + tid) * a.g_stride + h]);
     };
@@ -240,6 +257,8 @@ extern "C" kda_status kda_decay_step(const void* q, const void* k, const void* v
     a.V = d.V;
     a.group = d.H / hq;
     a.num_slots = p.num_slots;
+    a.vec = is_aligned(q, 8) && is_aligned(k, 8) && is_aligned(v, 8) && a.q_stride % 4 == 0 && a.k_stride % 4 == 0 &&
+            a.v_stride % 4 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f16 = p.io_dtype == KDA_IO_F16, s16 = p.state_dtype == KDA_STATE_BF16;
     const cudaError_t e = d.K == 128 ? launch<128, 64, 256, 4>(a, f16, s16, s) : launch<64, 64, 256, 4>(a, f16, s16, s);
