@@ -25,6 +25,9 @@ namespace kda {
 namespace {
 
 constexpr int kWorkers = 512, kWorkerWarps = kWorkers / 32, kGradThreads = kWorkers + 32;
+// Of the 16 blocks of 32 x 32 scores six lie right of the diagonal: their warps have nothing to do while the others make
+// P and dP, and take <S, dS> meanwhile.
+constexpr int kDotWarps = 6;
 
 template <int KB, int VB>
 struct GradShape {
@@ -45,7 +48,7 @@ struct GradShape {
     // when everything else is done, in place of dP: the parts of dg
     struct Sums {
         float far_q[4][kDecayChunk], far_k[4][kDecayChunk], near_k[4][kDecayChunk], near_q[4][kDecayChunk];
-        float across[kWorkerWarps];
+        float across[kDotWarps], later[4], before[4];
     };
     static constexpr int kSmem = kSmall + (int)sizeof(Small);
     static_assert(sizeof(Small) >= sizeof(DecayScratch) && sizeof(Sums) <= 32768, "what shares memory fits");
@@ -96,7 +99,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     if (tid == 0) {
         for (uint64_t* b : {&sm.in_full, &sm.scores, &sm.s_full, &sm.ring_done, &sm.far, &sm.dv_far, &sm.dqk, &sm.dv})
             ptx::mbar_init(b, 1);
-        for (uint64_t* b : {&sm.clean, &sm.ring_read, &sm.far_ok, &sm.p_ok, &sm.dv_ok}) ptx::mbar_init(b, kWorkerWarps);
+        for (uint64_t* b : {&sm.clean, &sm.far_ok, &sm.p_ok, &sm.dv_ok}) ptx::mbar_init(b, kWorkerWarps);
+        ptx::mbar_init(&sm.ring_read, kDotWarps);
         ptx::fence_mbar_init();
         sm.fail = 0;
     }
@@ -263,12 +267,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         arrive(sm.clean);
 
         // <S, dS>, 64 values at a time: the same element of all four tiles, wherever it lies
+        const int dot_warp = part < quarter ? quarter * (quarter - 1) / 2 + part : -1;  // 0 .. 5
         auto dot_states = [&](int vb) {
             wait(sm.s_full, vb & 1);
-            const uint32_t s = base + Shape::kRing + tid * 16, ds = base + Shape::d_state(vb, 0) + tid * 16,
-                           dsl = base + Shape::d_state(vb, 1) + tid * 16;
+            const uint32_t s = base + Shape::kRing, ds = base + Shape::d_state(vb, 0), dsl = base + Shape::d_state(vb, 1);
 #pragma unroll 1
-            for (int c = 0; c < Shape::kPart; c += kWorkers * 16) {
+            for (int c = (dot_warp * 32 + lane) * 16; c < Shape::kPart; c += kDotWarps * 512) {
                 const uint4 w[4] = {lds128(s + c), lds128(s + c + Shape::kPart), lds128(ds + c), lds128(dsl + c)};
                 auto dot = [&](uint32_t s, uint32_t sl, uint32_t t, uint32_t tl) {
                     const float2 x = from_b16x2<F16>(s), xl = from_b16x2<F16>(sl), y = from_b16x2<F16>(t), yl = from_b16x2<F16>(tl);
@@ -282,16 +286,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             }
             arrive(sm.ring_read);
         };
-        dot_states(0);
         named_sync(1, kWorkers);  // column is there
 
         // P^T and dP^T: row j, 32 columns i
-        wait(sm.scores, 0);
-        ptx::tc_fence_after();
         {
             const int b = part;
             uint32_t p[16], dp[16];
             if (b >= quarter) {
+                wait(sm.scores, 0);
+                ptx::tc_fence_after();
                 float s[32], e[32];
                 ptx::tmem_ld16(t_row + kT0 + 32 * b, s);
                 ptx::tmem_ld16(t_row + kT0 + 32 * b + 16, s + 16);
@@ -329,6 +332,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 }
                 near_q = transposed_sum(s, lane);
             } else {
+                dot_states(0);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) p[c] = dp[c] = 0u;
             }
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         ptx::fence_proxy_async_smem();
         arrive(sm.p_ok);
 #pragma unroll 1
-        for (int vb = 1; vb < VB; ++vb) dot_states(vb);
+        for (int vb = 1; vb < VB; ++vb)
+            if (dot_warp >= 0) dot_states(vb);
         across *= up_q * up_k;
 
         // the far parts of dq and dk: scaled by rows, and their products with q and k
@@ -483,41 +488,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         sums.far_k[part][row] = far_k;
         sums.near_k[part][row] = near_k;
         sums.near_q[quarter][part * 32 + lane] = near_q;
-        if (lane == 0) sums.across[warp] = across;
+        if (lane == 0 && dot_warp >= 0) sums.across[dot_warp] = across;
         named_sync(1, kWorkers);
-        if (warp == 0 && !sm.fail) {
-            float later[4], before[4], all = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWorkerWarps; ++w) all += sums.across[w];
-            all *= sm.whole;
-            auto four = [](const float (&x)[4][kDecayChunk], int t) { return (x[0][t] + x[1][t]) + (x[2][t] + x[3][t]); };
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * lane + i;
-                later[i] = four(sums.far_q, t) + (four(sums.near_q, t) - four(sums.near_k, t));
-                before[i] = four(sums.far_k, t);
-            }
-            // later: sums from t on; before: sums up to t, t itself not among them
-#pragma unroll
-            for (int i = 2; i >= 0; --i) later[i] += later[i + 1];
-#pragma unroll
-            for (int i = 1; i < 4; ++i) before[i] += before[i - 1];
-            float right = later[0], left = before[3];
+        if (part == 0) {  // four warps, a token a thread
+            auto four = [&](const float (&x)[4][kDecayChunk]) { return (x[0][row] + x[1][row]) + (x[2][row] + x[3][row]); };
+            // later: sum from this token on; before: sum up to it, itself not among them
+            float later = four(sums.far_q) + (four(sums.near_q) - four(sums.near_k)), before = four(sums.far_k);
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const float r = __shfl_down_sync(~0u, right, off), l = __shfl_up_sync(~0u, left, off);
-                if (lane + off < 32) right += r;
-                if (lane >= off) left += l;
+                const float l = __shfl_down_sync(~0u, later, off), b = __shfl_up_sync(~0u, before, off);
+                if (lane + off < 32) later += l;
+                if (lane >= off) before += b;
             }
-            right = __shfl_down_sync(~0u, right, 1);
-            left = __shfl_up_sync(~0u, left, 1);
-            if (lane == 31) right = 0.f;
-            if (lane == 0) left = 0.f;
+            if (lane == 0) sums.later[quarter] = later;
+            if (lane == 31) sums.before[quarter] = before;
+            before = __shfl_up_sync(~0u, before, 1);
+            if (lane == 0) before = 0.f;
+            float all = 0.f;
+#pragma unroll
+            for (int i = 0; i < kDotWarps; ++i) all += sums.across[i];
+            named_sync(6, 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 4 * lane + i;
-                if (t < valid) a.dg[((int64_t)row0 + t) * a.H + h] = all + (later[i] + right) + (left + (i ? before[i - 1] : 0.f));
+                if (i > quarter) later += sums.later[i];
+                if (i < quarter) before += sums.before[i];
             }
+            if (live) a.dg[tok * a.H + h] = all * sm.whole + later + before;
         }
         if (part == 0 && lane == 0) ptx::bulk_wait_read0();
     }
