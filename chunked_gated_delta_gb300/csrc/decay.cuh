@@ -321,12 +321,14 @@ __device__ __forceinline__ uint32_t clock_lo() {
     asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
     return t;
 }
-__device__ __forceinline__ void wait_or_note(uint64_t* bar, uint32_t parity, volatile int32_t* fail) {
-    const uint32_t t0 = clock_lo();
+__device__ __forceinline__ void wait_or_note(uint64_t* bar, uint32_t parity, int32_t* fail) {
+    const uint32_t t0 = clock_lo(), at = ptx::smem_u32(fail);
 #pragma unroll 1
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (*fail) break;
-        if (clock_lo() - t0 > kDecayWaitCycles) *fail = 1;
+        int32_t failed;
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(failed) : "r"(at) : "memory");
+        if (failed) break;
+        if (clock_lo() - t0 > kDecayWaitCycles) asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(at), "r"(1) : "memory");
     }
 }
 

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     const uint32_t tmem = sm.tmem;
     volatile int32_t* fail = &sm.fail;
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-        wait_or_note(&bar, parity, fail);
+        wait_or_note(&bar, parity, &sm.fail);
         return !*fail;
     };
 

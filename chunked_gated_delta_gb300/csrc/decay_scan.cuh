@@ -42,7 +42,7 @@ struct DecayScanShape {
     static constexpr int kO = kS + (OUT ? 1 : 2) * kStateBytes;
     static constexpr int kSmall = kO + (OUT ? kYBytes : 0);
     // registers: those that the block is launched with, handed out as control, keys, state, scores, output
-    static constexpr int kControlRegs = OUT ? 56 : 64, kKeyRegs = OUT ? 64 : 96, kStateRegs = OUT ? 168 : 240;
+    static constexpr int kControlRegs = OUT ? 56 : 96, kKeyRegs = OUT ? 64 : 88, kStateRegs = OUT ? 168 : 240;
     static constexpr int kScoreRegs = 64, kOutRegs = 64;
     static_assert(OUT ? kControlRegs + 2 * kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 6 * 80
                       : kControlRegs + 2 * kKeyRegs + kStateRegs <= 4 * 128,
@@ -56,6 +56,9 @@ struct DecayScanShape {
         uint64_t scores, p_ready, s_ready, keys, keys_read, added, added_read, far, far_ok, o_full, o_free[2];
         uint32_t tmem;
         int32_t fail;
+        // The piece: first token row, tokens from there to the sequence's end, chunks, index of the first one, sequence,
+        // head, and whether it starts and ends its direction. (Here and not in registers, which the roles are short of.)
+        int32_t row, left, chunks, chunk, n, head, first, last;
     };
     static constexpr int kSmem = kSmall + (int)sizeof(Small);
     static_assert(sizeof(Small) >= sizeof(DecaySortScratch), "the search's scratch fits");
@@ -76,22 +79,29 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     const bool reverse = !OUT && dir.reverse;
 
     ptx::grid_dep_wait();
-    const int item = blockIdx.x / a.H, h = blockIdx.x - item * a.H;
-    DecayPiece at;
-    auto& scratch = *reinterpret_cast<DecaySortScratch*>(&sm);
-    if (!find_piece<Shape::kThreads>(a.seqs, item, false, true, scratch, at,
-                                     a.seqs.whole ? scratch.len : nullptr)) {
-        if (blockIdx.x == 0 && tid == 0 && a.status) atomicOr(a.status, kStatusBadSeqlens);
-        return;
+    {
+        const int item = blockIdx.x / a.H;
+        DecayPiece at;
+        auto& scratch = *reinterpret_cast<DecaySortScratch*>(&sm);
+        if (!find_piece<Shape::kThreads>(a.seqs, item, false, true, scratch, at, a.seqs.whole ? scratch.len : nullptr)) {
+            if (blockIdx.x == 0 && tid == 0 && a.status) atomicOr(a.status, kStatusBadSeqlens);
+            return;
+        }
+        const bool first = at.piece == 0, last = at.piece == at.pieces - 1;
+        if (at.n < 0 || (a.totals_only && (reverse ? first : last))) return;  // (nothing follows a direction's last piece)
+        __syncthreads();  // the search's scratch is free
+        if (tid == 0) {
+            const int c0 = at.piece * a.seqs.seg_chunks;
+            sm.row = at.bos + c0 * kDecayChunk;
+            sm.left = at.len - c0 * kDecayChunk;
+            sm.chunks = min(ceil_div(at.len, kDecayChunk) - c0, a.seqs.seg_chunks);
+            sm.chunk = at.chunk_base + c0;
+            sm.n = at.n;
+            sm.head = blockIdx.x - item * a.H;
+            sm.first = reverse ? last : first;
+            sm.last = reverse ? first : last;
+        }
     }
-    if (at.n < 0) return;
-    const bool first = reverse ? at.piece == at.pieces - 1 : at.piece == 0;
-    const bool last = reverse ? at.piece == 0 : at.piece == at.pieces - 1;
-    if (a.totals_only && last) return;  // nothing follows it
-    const int c0 = at.piece * a.seqs.seg_chunks;
-    const int chunks = min(ceil_div(at.len, kDecayChunk) - c0, a.seqs.seg_chunks);
-    auto chunk_at = [&](int it) { return c0 + (reverse ? chunks - 1 - it : it); };
-    __syncthreads();  // the search's scratch is free
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -122,8 +132,11 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem, base = ptx::smem_u32(raw);
+    const int chunks = sm.chunks;
+    // tokens of the piece before the it'th chunk that is taken
+    auto offset = [&](int it) { return (reverse ? chunks - 1 - it : it) * kDecayChunk; };
     volatile int32_t* fail = &sm.fail;
-    auto wait = [&](uint64_t& bar, uint32_t parity) { wait_or_note(&bar, parity, fail); };
+    auto wait = [&](uint64_t& bar, uint32_t parity) { wait_or_note(&bar, parity, &sm.fail); };
     auto arrive = [&](uint64_t& bar) {  // once per warp
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bar);
@@ -133,10 +146,10 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kControlRegs));
         if (warp == 0 && elect_one()) {
             // ---------------------------------------------------------- loads
-            const int hq = h / a.group;
+            const int h = sm.head, hq = h / a.group;
             int it = 0;
             for (; it < chunks; ++it) {
-                const int sx = it % NS, row = at.bos + chunk_at(it) * kDecayChunk;
+                const int sx = it % NS, row = sm.row + offset(it);
                 const uint32_t px = ((it / NS) & 1) ^ 1;  // of the stage's last use
                 if (it >= NS) wait(sm.x_empty[sx], px);
                 if (*fail) break;
@@ -222,8 +235,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         } else if (warp == 2) {
             // ---------------------------------------------------------- decays
             auto loaded = [&](int it) {
-                const int c = chunk_at(it);
-                return load_g(a.g, a.g_stride, h, (int64_t)at.bos + c * kDecayChunk, at.len - c * kDecayChunk, lane);
+                return load_g(a.g, a.g_stride, sm.head, (int64_t)sm.row + offset(it), sm.left - offset(it), lane);
             };
             LoadedG next;
             if (chunks > 0) next = loaded(0);
@@ -246,7 +258,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         const uint32_t to = swizzled_row(base + Shape::kHi, j);
         for (int it = 0; it < chunks; ++it) {
             const int st = it & 1, sx = it % NS;
-            const bool live = j < at.len - chunk_at(it) * kDecayChunk;
+            const bool live = j < sm.left - offset(it);
             wait(sm.g_ready[st], (it >> 1) & 1);
             const ChunkDecay& d = sm.decay[st];
             float w = dir.weight * exp2_fast(reverse ? d.hi[j] + d.lo[j]
@@ -276,37 +288,41 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 up = scale_to_f16(all);
                 w *= up;
             }
-            uint4 x[kPieces];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int c = c_first + i;
-                x[i] = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
-            }
-            arrive(sm.x_empty[sx]);
             if (it > 0) wait(sm.keys_read, st ^ 1);
             if (F16 && j == 0 && c_first == 0) sm.key_unscale[st] = 1.f / up;
             const uint64_t w2 = pair_of(w, w), minus = pair_of(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int c = c_first + i;
-                if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t hi[4], lo[4];
+            for (int half = 0; half < 2; ++half) {
+                constexpr int kHalf = kPieces / 2;
+                uint4 x[kHalf];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 f = from_b16x2<F16>(in[e]);
-                    const uint64_t p = mul2(pair_of(f.x, f.y), w2);
-                    f = floats_of(p);
-                    hi[e] = pack_b16x2(f.x, f.y, F16);
-                    f = from_b16x2<F16>(hi[e]);
-                    f = floats_of(fma2(pair_of(f.x, f.y), minus, p));
-                    lo[e] = pack_b16x2(f.x, f.y, F16);
+                for (int i = 0; i < kHalf; ++i) {
+                    const int c = c_first + half * kHalf + i;
+                    x[i] = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
                 }
-                const uint32_t p = (to ^ ((c & 7) << 4)) + (c >> 3) * 16384;
-                sts128(p, hi[0], hi[1], hi[2], hi[3]);
-                sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
+                if (half == 1) arrive(sm.x_empty[sx]);
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) {
+                    const int c = c_first + half * kHalf + i;
+                    if (!live) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = from_b16x2<F16>(in[e]);
+                        const uint64_t p = mul2(pair_of(f.x, f.y), w2);
+                        f = floats_of(p);
+                        hi[e] = pack_b16x2(f.x, f.y, F16);
+                        f = from_b16x2<F16>(hi[e]);
+                        f = floats_of(fma2(pair_of(f.x, f.y), minus, p));
+                        lo[e] = pack_b16x2(f.x, f.y, F16);
+                    }
+                    const uint32_t p = (to ^ ((c & 7) << 4)) + (c >> 3) * 16384;
+                    sts128(p, hi[0], hi[1], hi[2], hi[3]);
+                    sts128(p + Shape::kXBytes, lo[0], lo[1], lo[2], lo[3]);
+                }
             }
-            if (at.len - chunk_at(it) * kDecayChunk < kDecayChunk) {
+            if (sm.left - offset(it) < kDecayChunk) {
                 // rows behind the sequence are another's, or nobody's: a zero weight would not hold back a NaN
                 wait(sm.y_full[sx], (it / NS) & 1);
                 if (!live && c_first == 0) {
@@ -325,7 +341,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         constexpr int kThreads = 64 * VB;
         if (quarter < 2 * VB) {
             float S[K];
-            const int64_t unit = (int64_t)item * a.H + h, seq = (int64_t)at.n * a.H + h;
+            const bool first = sm.first;
+            const int64_t unit = blockIdx.x, seq = (int64_t)sm.n * a.H + sm.head;
             float* piece = dir.totals + unit * K * V + v;  // (null without pieces: not used then)
             const uint16_t* start16 = static_cast<const uint16_t*>(dir.start.p) + seq * K * V + v;
             const float* start = first ? static_cast<const float*>(dir.start.p) + seq * K * V + v : piece;
@@ -386,7 +403,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     } else {
                         named_sync(2, kThreads);
                         if (v == 0) {
-                            const int64_t chunk = (int64_t)(at.chunk_base + chunk_at(it)) * a.H + h;
+                            const int64_t chunk = (int64_t)(sm.chunk + offset(it) / kDecayChunk) * a.H + sm.head;
                             bulk_store_async(dir.kept + chunk * 2 * Shape::kStateBytes, raw + Shape::kS,
                                              2 * Shape::kStateBytes);
                             ptx::bulk_commit();
@@ -422,7 +439,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < K; ++k) piece[k * V] = S[k];
                 if (v == 0) dir.decays[unit] = decay;
-            } else if (last && dir.end.p) {
+            } else if (sm.last && dir.end.p) {
+                const int64_t seq = (int64_t)sm.n * a.H + sm.head;
                 if (dir.end.b16) {
                     uint16_t* p = static_cast<uint16_t*>(dir.end.p) + seq * K * V + v;
 #pragma unroll
@@ -511,8 +529,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16), box = base + Shape::kO + quarter * 4096;
             const uint32_t to = swizzled_row(box, lane);
             for (int it = 0; it < chunks; ++it) {
-                const int st = it & 1, tok = chunk_at(it) * kDecayChunk + i;
-                const bool whole = tok - lane + 32 <= at.len;
+                const int st = it & 1, tok = offset(it) + i;
+                const bool whole = tok - lane + 32 <= sm.left;
                 const uint32_t t_out = t_row + Shape::kOut + st * 128;
                 wait(sm.g_ready[st], (it >> 1) & 1);
                 float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]);
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 wait(sm.o_full, st);
                 ptx::tc_fence_after();
                 __syncwarp();
-                uint16_t* o = a.o + (((int64_t)at.bos + tok) * a.H + h) * V;
+                uint16_t* o = a.o + (((int64_t)sm.row + tok) * a.H + sm.head) * V;
 #pragma unroll 1
                 for (int c = 0; c < V; c += 32) {
                     float u[32];
@@ -555,7 +573,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = pack_b16x2(u[8 * g + 2 * e], u[8 * g + 2 * e + 1], F16);
                         if (whole) sts128((to ^ (((c & 63) << 1) + g * 16)) + (c >> 6) * 16384, y[0], y[1], y[2], y[3]);
-                        else if (tok < at.len) *reinterpret_cast<uint4*>(o + c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+                        else if (tok < sm.left) *reinterpret_cast<uint4*>(o + c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
                 ptx::tc_fence_before();
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 if (whole && lane == 0) {
 #pragma unroll
                     for (int b = 0; b < VB; ++b)
-                        ptx::tma_store_3d(&a.tm_o, raw + Shape::kO + quarter * 4096 + b * 16384, b * 64, h, at.bos + tok);
+                        ptx::tma_store_3d(&a.tm_o, raw + Shape::kO + quarter * 4096 + b * 16384, b * 64, sm.head, sm.row + tok);
                     ptx::bulk_commit();
                 }
             }
