@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         auto send = [&](auto store) {
             ptx::fence_proxy_async_smem();
             named_sync(2 + quarter, 128);
-            if (staged && part == 0 && lane == 0) {
+            if (staged && part == 0 && elect_one()) {
                 store();
                 ptx::bulk_commit();
             }
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             }
             if (live) a.dg[tok * a.H + h] = all * sm.whole + later + before;
         }
-        if (part == 0 && lane == 0) ptx::bulk_wait_read0();
+        if (part == 0 && elect_one()) ptx::bulk_wait_read0();
     }
     __syncwarp();
     ptx::tc_fence_before();

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     // S as 16 bits (and, kept, what that lost), in rows of 128 bytes as the MMAs read them
                     if (OUT && it > 0) wait(sm.far, ph ^ 1);  // (the far products have read the last one)
                     if (!OUT && it > 0) {
-                        if (v == 0) ptx::bulk_wait_read0();  // the last chunk's copy has left
+                        if (quarter == 0 && elect_one()) ptx::bulk_wait_read0();  // the last chunk's copy has left
                         named_sync(1, kThreads);
                     }
                     float up = 1.f;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                         if (v == 0) sm.unscale[st] = 1.f / up;
                     } else {
                         named_sync(2, kThreads);
-                        if (v == 0) {
+                        if (quarter == 0 && elect_one()) {
                             const int64_t chunk = (int64_t)(sm.chunk + offset(it) / kDecayChunk) * a.H + sm.head;
                             bulk_store_async(dir.kept + chunk * 2 * Shape::kStateBytes, raw + Shape::kS,
                                              2 * Shape::kStateBytes);
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     for (int k = 0; k < K; ++k) p[k * V] = S[k];
                 }
             }
-            if (keep && v == 0) ptx::bulk_wait0();
+            if (quarter == 0 && keep && elect_one()) ptx::bulk_wait0();
         }
     } else if (warp < Shape::kFirstState + 8) {
         if constexpr (OUT) {
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 tmem_st_wait();
                 ptx::tc_fence_before();
                 arrive(sm.far_ok);
-                if (lane == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
+                if (elect_one()) ptx::bulk_wait_read0();  // the last chunk's rows have left
                 wait(sm.o_full, st);
                 ptx::tc_fence_after();
                 __syncwarp();
@@ -579,14 +579,14 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 ptx::tc_fence_before();
                 ptx::fence_proxy_async_smem();
                 arrive(sm.o_free[st]);
-                if (whole && lane == 0) {
+                if (elect_one() && whole) {
 #pragma unroll
                     for (int b = 0; b < VB; ++b)
                         ptx::tma_store_3d(&a.tm_o, raw + Shape::kO + quarter * 4096 + b * 16384, b * 64, sm.head, sm.row + tok);
                     ptx::bulk_commit();
                 }
             }
-            if (lane == 0) ptx::bulk_wait0();
+            if (elect_one()) ptx::bulk_wait0();
         }
     }
     __syncwarp();
