@@ -16,9 +16,17 @@
 // sequence takes it as a difference of ever longer sums. For the same reason S and dS are kept in
 // two parts of 16 bits each, both multiplied for the far parts of dq and dk.
 //
-// All products are tcgen05 MMAs of 128 tokens. Their scores are computed transposed (lane j, column
+// All products are tcgen05 MMAs of 128 tokens. The scores are computed transposed (lane j, column
 // i), so that P^T and dP^T are operands out of TMEM for dv and dk; dP for dq goes through
-// shared memory. The far parts are scaled by rows in registers and put back, and the near products add to them.
+// shared memory. The far parts are scaled by rows in registers and put back, and the near products add
+// to them. S and dS come 64 values at a time; outputs leave by TMA from where their inputs were.
+//
+// Bound: the chain of a tile's phases (one CTA of 226 KB per SM): loads 2.3 thousand cycles, scores 1.9, P and
+// dP 3.1, the second half of the states until 8.9, far parts 1.7, near products and stores 6 (1.9 GHz; tensor cores
+// 23% busy, issue 33%, `profiles/kda_decay.md`). 352 KB a tile: 4 x 8192 tokens x 32 heads of 128 x 128
+// 610 us, 4.7 TB/s; the states' scan before it 370 us, 5.7 TB/s; both together 980. First as 8 warps
+// with stores by threads 888 us for this kernel. A persistent form that loads the next tile's do and states early
+// measured the same (1012 for both).
 #include "decay.cuh"
 
 namespace kda {
