@@ -312,16 +312,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 if (b > quarter) {
                     const int end = 32 * b - 1;
                     const float r = a.scale * exp2_fast((d.hi[end] - hi) + (d.lo[end] - lo));
+                    const uint64_t r2 = pair_of(r, r);
+                    uint64_t sum = 0;  // (two zeros)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float2 f = *reinterpret_cast<const float2*>(&sm.column[32 * b + 2 * c]);
-                        const float f0 = r * f.x, f1 = r * f.y;
-                        p[c] = pack_b16x2(s[2 * c] * f0, s[2 * c + 1] * f1, F16);
-                        e[2 * c] *= f0, e[2 * c + 1] *= f1;
-                        dp[c] = pack_b16x2(e[2 * c], e[2 * c + 1], F16);
-                        s[2 * c] *= e[2 * c], s[2 * c + 1] *= e[2 * c + 1];
-                        near_k += s[2 * c] + s[2 * c + 1];
+                        const float2 column = *reinterpret_cast<const float2*>(&sm.column[32 * b + 2 * c]);
+                        const uint64_t f = mul2(r2, pair_of(column.x, column.y)), x = pair_of(s[2 * c], s[2 * c + 1]);
+                        const float2 scaled = floats_of(mul2(x, f));
+                        p[c] = pack_b16x2(scaled.x, scaled.y, F16);
+                        const uint64_t y = mul2(pair_of(e[2 * c], e[2 * c + 1]), f), m = mul2(x, y);
+                        const float2 dscaled = floats_of(y), pair = floats_of(m);
+                        dp[c] = pack_b16x2(dscaled.x, dscaled.y, F16);
+                        s[2 * c] = pair.x, s[2 * c + 1] = pair.y;
+                        sum = add2(sum, m);
                     }
+                    const float2 both = floats_of(sum);
+                    near_k = both.x + both.y;
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
@@ -368,7 +374,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         wait(sm.far, 0);
         ptx::tc_fence_after();
         auto scaled = [&](uint32_t column, float f, uint32_t x) {
-            float sum = 0.f;
+            uint64_t sum = 0;  // (two zeros)
+            const uint64_t f2 = pair_of(f, f);
 #pragma unroll 1
             for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 16) {
                 float u[16];
@@ -382,14 +389,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 y = from_b16x2<F16>(in[e]);
-                        u[8 * g + 2 * e] *= f, u[8 * g + 2 * e + 1] *= f;
-                        sum = fmaf(u[8 * g + 2 * e], y.x, sum);
-                        sum = fmaf(u[8 * g + 2 * e + 1], y.y, sum);
+                        const uint64_t x = mul2(pair_of(u[8 * g + 2 * e], u[8 * g + 2 * e + 1]), f2);
+                        sum = fma2(x, pair_of(y.x, y.y), sum);
+                        const float2 now = floats_of(x);
+                        u[8 * g + 2 * e] = now.x, u[8 * g + 2 * e + 1] = now.y;
                     }
                 }
                 tmem_st16(t_row + column + c0, reinterpret_cast<const uint32_t*>(u));
             }
-            return sum;
+            const float2 both = floats_of(sum);
+            return both.x + both.y;
         };
         far_q = scaled(kTdq, a.scale * seen * up_q, base + Shape::kQ);
         far_k = scaled(kTdk, kept * up_k, base + Shape::kK);
