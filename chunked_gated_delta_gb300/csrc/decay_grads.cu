@@ -23,8 +23,8 @@
 //
 // Bound: the chain of a tile's phases (one CTA of 226 KB per SM): loads 2.3 thousand cycles, scores 1.9, P and
 // dP 3.1, the second half of the states until 8.9, far parts 1.7, near products and stores 6 (1.9 GHz; tensor cores
-// 23% busy, issue 33%, `profiles/kda_decay.md`). 352 KB a tile: 4 x 8192 tokens x 32 heads of 128 x 128
-// 610 us, 4.7 TB/s; the states' scan before it 370 us, 5.7 TB/s; both together 980. First as 8 warps
+// 23% busy, issue 33%). 352 KB a tile: 4 x 8192 tokens x 32 heads of 128 x 128
+// 595 us, 4.8 TB/s; the states' scan before it 370 us, 5.7 TB/s; both together 967. First as 8 warps
 // with stores by threads 888 us for this kernel. A persistent form that loads the next tile's do and states early
 // measured the same (1012 for both).
 #include "decay.cuh"
