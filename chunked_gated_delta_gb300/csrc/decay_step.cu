@@ -8,10 +8,12 @@
 //
 // Bound: each state is read and written once per call, 2 K V 4 bytes (128 KB at
 // K = V = 128 in fp32) against 5 K V flops a token: HBM, or for a handful of states the
-// launch and one trip to memory. Four CTAs of 64 columns an SM, in different
-// stages of load, sums and store, keep it busy without a ring: 512 requests x 32 heads
-// of 128 x 128 in fp32 315 us (6.8 TB/s, what a copy reaches); with registers for two or
-// three an SM 458 and 363, columns by 32 in 128 threads, eight an SM 314.
+// launch and one trip to memory. Few threads with many columns each spend the least on a token's
+// shared loads and sums over rows, so five CTAs (K = 64: eight) of 128 threads an SM, in different stages of
+// load, sums and store, keep HBM busy without a ring, and sums are taken two floats at a time: 512 requests x
+// 32 heads of 128 x 128 in fp32 307 us (7 TB/s, what a copy reaches), 96 x 3 tokens x 32 heads of 128 x 64 in
+// bf16 25.6, of 64 x 64 15.5. One float at a time in 256 threads, four an SM, 315, 32.9 and 20.4;
+// columns by 32 in 128 threads, eight an SM, 310, 28.5 and 18 to 20; 128 columns 388.
 #include "decay.cuh"
 
 namespace kda {
@@ -33,22 +35,28 @@ struct DecayStepArgs {
     int32_t vec;  // rows of q, k and v take loads of four elements
 };
 
+// Four columns of a state as two pairs of floats.
 template <bool STATE16>
-__device__ __forceinline__ float4 load_four(const void* p, int64_t four) {
+__device__ __forceinline__ void load_four(const void* p, int64_t four, uint64_t (&s)[2]) {
     if constexpr (STATE16) {
         const uint2 w = static_cast<const uint2*>(p)[four];
         const float2 a = from_b16x2<false>(w.x), b = from_b16x2<false>(w.y);
-        return make_float4(a.x, a.y, b.x, b.y);
+        s[0] = pair_of(a.x, a.y);
+        s[1] = pair_of(b.x, b.y);
     } else {
-        return static_cast<const float4*>(p)[four];
+        const ulonglong2 w = static_cast<const ulonglong2*>(p)[four];
+        s[0] = w.x;
+        s[1] = w.y;
     }
 }
 template <bool STATE16>
-__device__ __forceinline__ void store_four(void* p, int64_t four, float4 s) {
-    if constexpr (STATE16)
-        static_cast<uint2*>(p)[four] = make_uint2(pack_b16x2(s.x, s.y, false), pack_b16x2(s.z, s.w, false));
-    else
-        static_cast<float4*>(p)[four] = s;
+__device__ __forceinline__ void store_four(void* p, int64_t four, const uint64_t (&s)[2]) {
+    if constexpr (STATE16) {
+        const float2 a = floats_of(s[0]), b = floats_of(s[1]);
+        static_cast<uint2*>(p)[four] = make_uint2(pack_b16x2(a.x, a.y, false), pack_b16x2(b.x, b.y, false));
+    } else {
+        static_cast<ulonglong2*>(p)[four] = make_ulonglong2(s[0], s[1]);
+    }
 }
 
 // Four 16-bit elements; vec: together.
@@ -82,6 +90,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const D
 
     int64_t row0 = (int64_t)n * a.T;
     int len = a.T;
+    const int slot = a.slots ? a.slots[n] : n;  // (asked for together with the bounds)
     if (a.cu) {
         const int bos = a.cu[n], eos = a.cu[n + 1];
         if (bos < 0 || eos < bos || eos > a.T || (n == 0 && bos != 0) || (n == a.N - 1 && eos != a.T)) {
@@ -92,16 +101,15 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const D
         len = eos - bos;
     }
     if (len == 0) return;
-    const int slot = a.slots ? a.slots[n] : n;
     const bool in_cache = slot >= 0 && slot < a.num_slots;
 
     const int cg = tid % kColGroups, rl = tid / kColGroups;
     const int64_t at = in_cache ? ((((int64_t)slot * a.H + h) * K + rl) * a.V + tile * VT) / 4 + cg : 0;
     const int64_t row_step = (int64_t)kRowLanes * a.V / 4;
-    float4 S[kRows];
+    uint64_t S[kRows][2];  // two floats each
     if (in_cache) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) S[i] = load_four<STATE16>(a.state, at + i * row_step);
+        for (int i = 0; i < kRows; ++i) load_four<STATE16>(a.state, at + i * row_step, S[i]);
     }
     const int hq = h / a.group;
     // Inputs of kStepTokens tokens, four elements a thread where rows allow it: one trip to memory.
@@ -148,16 +156,21 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_decay_step_kernel(const D
         }
         const int count = min(kStepTokens, len - t0);
         for (int j = 0; j < count; ++j) {
-            const float d = s_decay[j];
+            const uint64_t d = pair_of(s_decay[j], s_decay[j]);
             const float4 v = s_v[j][cg];
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint64_t v01 = pair_of(v.x, v.y), v23 = pair_of(v.z, v.w);
+            uint64_t y01 = 0, y23 = 0;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const float k = s_k[j][rl + i * kRowLanes], q = s_q[j][rl + i * kRowLanes];
-                S[i] = make_float4(fmaf(d, S[i].x, k * v.x), fmaf(d, S[i].y, k * v.y), fmaf(d, S[i].z, k * v.z),
-                                   fmaf(d, S[i].w, k * v.w));
-                y = make_float4(fmaf(q, S[i].x, y.x), fmaf(q, S[i].y, y.y), fmaf(q, S[i].z, y.z), fmaf(q, S[i].w, y.w));
+                const uint64_t k = pair_of(s_k[j][rl + i * kRowLanes], s_k[j][rl + i * kRowLanes]);
+                const uint64_t q = pair_of(s_q[j][rl + i * kRowLanes], s_q[j][rl + i * kRowLanes]);
+                S[i][0] = fma2(d, S[i][0], mul2(k, v01));
+                S[i][1] = fma2(d, S[i][1], mul2(k, v23));
+                y01 = fma2(q, S[i][0], y01);
+                y23 = fma2(q, S[i][1], y23);
             }
+            const float2 ya = floats_of(y01), yb = floats_of(y23);
+            float4 y = make_float4(ya.x, ya.y, yb.x, yb.y);
 #pragma unroll
             for (int off = kColGroups; off < 32; off <<= 1) {  // row lanes of the same columns in this warp
                 y.x += __shfl_xor_sync(~0u, y.x, off);
@@ -261,6 +274,6 @@ extern "C" kda_status kda_decay_step(const void* q, const void* k, const void* v
             a.v_stride % 4 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f16 = p.io_dtype == KDA_IO_F16, s16 = p.state_dtype == KDA_STATE_BF16;
-    const cudaError_t e = d.K == 128 ? launch<128, 64, 256, 4>(a, f16, s16, s) : launch<64, 64, 256, 4>(a, f16, s16, s);
+    const cudaError_t e = d.K == 128 ? launch<128, 64, 128, 5>(a, f16, s16, s) : launch<64, 64, 128, 8>(a, f16, s16, s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
