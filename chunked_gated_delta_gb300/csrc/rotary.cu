@@ -9,10 +9,12 @@
 // lost to its size (beside the frequency's own 53 bits), without any 64-bit float
 // arithmetic per token.
 //
-// Bound: q and k read and written once. A CTA goes through tokens; its threads
-// make a token's cosines and sines once for all heads, in shared memory, while
-// the rows of that token are on their way, 16 bytes a load. 32768 tokens x 64 heads of 128 in bf16 190 us (5.7 TB/s,
-// 85% of a copy; 303 with one element a conversion and 118 registers); 59 tokens x 40 heads 5 us, the call.
+// Bound: q and k read and written once. A CTA goes through groups of tokens (one, or as many as its loads hold);
+// its threads make their cosines and sines once for all heads, in shared memory, while
+// the rows are on their way, 16 bytes a load, from places that a thread works out once. 32768 tokens x 64 heads of
+// 128 in bf16 164 us (6.5 TB/s, 98% of a copy) in both layouts; 59 tokens x 40 heads 5 us, the call. Two loads side by
+// side for the interleaved layout 190, and places worked out for every token 114 instead of 110 us for
+// 40 heads of which half is turned.
 #include "internal.h"
 #include "layer_ops.cuh"
 #include "ptx.cuh"
@@ -31,6 +33,7 @@ struct RotaryArgs {
     const double* freqs;
     int64_t tokens, q_stride, k_stride, q_out_stride, k_out_stride;  // in elements
     int32_t q_heads, k_heads, dim, pairs, positions64, inverse;
+    int32_t group;   // consecutive tokens that a CTA takes together
     uint32_t magic;  // e / per_head is the upper half of e * magic (0: divide)
     float amplitude;
 };
@@ -62,103 +65,118 @@ struct alignas(sizeof(T) * C) Piece {
     T x[C];
 };
 
-// C: elements of a load. A row of a head is items: those of pairs (two loads: in the half layout the
-// x and the y of C pairs, else 2 C elements of C pairs), then those that are copied (one load each, two in an item).
+// C: elements of a load. A row of a head is items: those of pairs (two loads of C elements: in the half layout the
+// x and the y of C pairs, else C / 2 pairs in the first half of the turned elements and C / 2 in the second, so that
+// a warp's loads and stores are of whole lines in both; C = 1 is a pair either way), then those that are copied (two
+// loads of C elements next to each other).
 template <int IO, int C, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads, C > 1 ? 6 : 8) kda_rotary_kernel(const RotaryArgs a) {
     using T = typename Io<IO>::T;
     using P = Piece<T, C>;
     __shared__ __align__(16) float2 s_turn[2][kMostPairs];  // cos, sin
+    __shared__ uint64_t s_share[kMostPairs];  // one position's share of a turn, times 2^64
+    __shared__ int16_t s_of[kMostPairs];      // which of the tokens taken together
     const int tid = threadIdx.x;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    constexpr int kOwn = kMostPairs / kRotaryThreads;
-    uint64_t turn[kOwn];  // of the pairs that this thread looks after: one position's share of a turn, times 2^64
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const int p = tid + i * kRotaryThreads;
-        double t = p < a.pairs ? a.freqs[p] * 0.15915494309189535 : 0.0;
+    const int own = a.group * a.pairs;
+    for (int p = tid; p < own; p += kRotaryThreads) {  // (each read by the thread that wrote it)
+        const int of = p / a.pairs;
+        double t = a.freqs[p - of * a.pairs] * 0.15915494309189535;
         t -= floor(t);
-        turn[i] = __double2ull_rn(t * 18446744073709551616.0);
+        s_share[p] = __double2ull_rn(t * 18446744073709551616.0);
+        s_of[p] = (int16_t)of;
     }
     const int turned = a.pairs / C;                               // items of pairs in a head
     const int copied = (a.dim - 2 * a.pairs + 2 * C - 1) / (2 * C);
     const int per_head = turned + copied, heads = a.q_heads + a.k_heads, items = heads * per_head;
 
-    auto angles = [&](int64_t tok, float2* to) {
-        const uint64_t pos = a.positions64 ? static_cast<const uint64_t*>(a.positions)[tok]
-                                           : (uint64_t)(int64_t)static_cast<const int32_t*>(a.positions)[tok];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int p = tid + i * kRotaryThreads;
-            if (p >= a.pairs) break;
+    auto angles = [&](int64_t tok, int count, float2* to) {
+        for (int p = tid; p < count * a.pairs; p += kRotaryThreads) {
+            const int64_t at = tok + s_of[p];
+            const uint64_t pos = a.positions64 ? static_cast<const uint64_t*>(a.positions)[at]
+                                               : (uint64_t)(int64_t)static_cast<const int32_t*>(a.positions)[at];
             // (the leading 32 bits of the fraction, as half turns in -1 .. 1)
-            const float half_turns = (float)(int32_t)(uint32_t)((pos * turn[i]) >> 32) * 0x1p-31f;
+            const float half_turns = (float)(int32_t)(uint32_t)((pos * s_share[p]) >> 32) * 0x1p-31f;
             float s, c;
             sincospif(half_turns, &s, &c);
             to[p] = make_float2(a.amplitude * c, a.inverse ? -a.amplitude * s : a.amplitude * s);
         }
     };
-    struct At {
+    constexpr int kOneLoad = -1, kTwoLoads = -2;  // of an item that is copied
+    struct Item {
         const T* in;
         T* out;
-        int first, second, pair, count;  // offsets of the two loads; first pair (-1: copied), loads of an item
+        int pair;   // the turn of its first pair, or how it is copied
+        bool of_q;
     };
     auto item_at = [&](int64_t tok, int e) {
+        const int t = a.group == 1 ? 0 : e / items;
+        e -= t * items;
+        tok += t;
         const int head = a.magic ? (int)__umulhi((uint32_t)e, a.magic) : e / per_head, i = e - head * per_head;
-        At r;
-        if (head < a.q_heads) {
-            r.in = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * a.dim;
-            r.out = static_cast<T*>(a.q_out) + tok * a.q_out_stride + (int64_t)head * a.dim;
-        } else {
-            r.in = static_cast<const T*>(a.k) + tok * a.k_stride + (int64_t)(head - a.q_heads) * a.dim;
-            r.out = static_cast<T*>(a.k_out) + tok * a.k_out_stride + (int64_t)(head - a.q_heads) * a.dim;
-        }
-        r.count = 2;
+        Item r;
+        r.of_q = head < a.q_heads;
+        int first;
         if (i < turned) {
-            r.pair = i * C;
-            r.first = INTERLEAVED ? 2 * r.pair : r.pair;
-            r.second = INTERLEAVED ? r.first + C : r.pair + a.pairs;
+            r.pair = t * a.pairs + (INTERLEAVED && C > 1 ? i * (C / 2) : i * C);
+            first = INTERLEAVED && C == 1 ? 2 * i : i * C;
         } else {
-            r.pair = -1;
-            r.first = 2 * a.pairs + (i - turned) * 2 * C;
-            r.second = r.first + C;
-            if (r.second >= a.dim) r.count = 1;
+            first = 2 * a.pairs + (i - turned) * 2 * C;
+            r.pair = first + C < a.dim ? kTwoLoads : kOneLoad;
+        }
+        if (r.of_q) {
+            r.in = static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)head * a.dim + first;
+            r.out = static_cast<T*>(a.q_out) + tok * a.q_out_stride + (int64_t)head * a.dim + first;
+        } else {
+            r.in = static_cast<const T*>(a.k) + tok * a.k_stride + (int64_t)(head - a.q_heads) * a.dim + first;
+            r.out = static_cast<T*>(a.k_out) + tok * a.k_out_stride + (int64_t)(head - a.q_heads) * a.dim + first;
         }
         return r;
     };
+    const int apart = INTERLEAVED && C == 1 ? 1 : a.pairs;  // the two loads of a turned item
 
+    const int64_t first_token = (int64_t)blockIdx.x * a.group, ahead = (int64_t)gridDim.x * a.group;
+    const bool once = a.group * items <= kItems * kRotaryThreads;  // then a thread has the same items of every token
+    Item item[kItems];
+    if (once) {
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) item[i] = item_at(first_token, tid + i * kRotaryThreads);
+    }
     int buf = 0;
-    for (int64_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x, buf ^= 1) {
-        for (int e0 = tid; e0 - tid < items; e0 += kItems * kRotaryThreads) {
+    for (int64_t tok = first_token; tok < a.tokens; tok += ahead, buf ^= 1) {
+        const int count = a.tokens - tok < a.group ? (int)(a.tokens - tok) : a.group, all = count * items;
+        for (int e0 = tid; e0 - tid < all; e0 += kItems * kRotaryThreads) {
             P x[kItems], y[kItems];
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 const int e = e0 + i * kRotaryThreads;
-                if (e < items) {
-                    const At at = item_at(tok, e);
-                    x[i] = *reinterpret_cast<const P*>(at.in + at.first);
-                    if (at.count == 2) y[i] = *reinterpret_cast<const P*>(at.in + at.second);
+                if (e < all) {
+                    if (!once) item[i] = item_at(tok, e);
+                    const Item at = item[i];
+                    x[i] = *reinterpret_cast<const P*>(at.in);
+                    if (at.pair != kOneLoad) y[i] = *reinterpret_cast<const P*>(at.in + (at.pair >= 0 ? apart : C));
                 }
             }
-            if (e0 == tid) {  // (one barrier per token: the buffer before last has been read by all)
-                angles(tok, s_turn[buf]);
+            if (e0 == tid) {  // (one barrier per group: the buffer before last has been read by all)
+                angles(tok, count, s_turn[buf]);
                 __syncthreads();
             }
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
                 const int e = e0 + i * kRotaryThreads;
-                if (e >= items) break;
-                const At at = item_at(tok, e);
+                if (e >= all) break;
+                const Item at = item[i];
                 if (at.pair >= 0) {
                     if constexpr (C == 8) {  // 16 bits: words of two elements
                         const float4* turns = reinterpret_cast<const float4*>(&s_turn[buf][at.pair]);  // two pairs' each
+                        const int half = a.pairs >> 2;  // between the turns of an item's two loads
                         uint32_t* u = reinterpret_cast<uint32_t*>(&x[i]);
                         uint32_t* w = reinterpret_cast<uint32_t*>(&y[i]);
                         constexpr bool kF16 = IO == KDA_DTYPE_F16;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float4 t = turns[c];
+                            const float4 t = turns[INTERLEAVED && c >= 2 ? half + c - 2 : c];
                             if constexpr (INTERLEAVED) {
                                 uint32_t* v = c < 2 ? u + 2 * c : w + 2 * c - 4;
                                 const float2 m = from_b16x2<kF16>(v[0]), n = from_b16x2<kF16>(v[1]);
@@ -173,7 +191,8 @@ __global__ void __launch_bounds__(kRotaryThreads, C > 1 ? 6 : 8) kda_rotary_kern
                     } else {
 #pragma unroll
                         for (int c = 0; c < C; ++c) {
-                            const float2 t = s_turn[buf][at.pair + c];
+                            const int late = INTERLEAVED && C > 1 && 2 * c >= C ? (a.pairs - C) / 2 : 0;
+                            const float2 t = s_turn[buf][at.pair + c + late];
                             T *u, *w;
                             if constexpr (INTERLEAVED) {
                                 u = 2 * c < C ? &x[i].x[2 * c % C] : &y[i].x[2 * c % C];
@@ -190,8 +209,15 @@ __global__ void __launch_bounds__(kRotaryThreads, C > 1 ? 6 : 8) kda_rotary_kern
                 } else if (at.in == at.out) {
                     continue;
                 }
-                *reinterpret_cast<P*>(at.out + at.first) = x[i];
-                if (at.count == 2) *reinterpret_cast<P*>(at.out + at.second) = y[i];
+                *reinterpret_cast<P*>(at.out) = x[i];
+                if (at.pair != kOneLoad) *reinterpret_cast<P*>(at.out + (at.pair >= 0 ? apart : C)) = y[i];
+            }
+        }
+        if (once) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                item[i].in += ahead * (item[i].of_q ? a.q_stride : a.k_stride);
+                item[i].out += ahead * (item[i].of_q ? a.q_out_stride : a.k_out_stride);
             }
         }
     }
@@ -262,8 +288,17 @@ extern "C" kda_status kda_rotary(const void* q, const void* k, const void* posit
     const uint32_t per_head = (uint32_t)(p.pairs / W + (dim - 2 * p.pairs + 2 * W - 1) / (2 * W));
     // (floor(2^32 / d) + 1 divides e by d where e * d < 2^32)
     if (per_head > 1 && (uint64_t)(q_heads + k_heads) * per_head * per_head < (1ull << 32)) a.magic = (uint32_t)((1ull << 32) / per_head) + 1;
-    const int64_t most = (int64_t)device_sm_count() * 6;
-    const unsigned grid = (unsigned)(tokens < most ? tokens : most);
+    // Tokens of few heads are taken together, as far as their loads and turns fit, and every CTA has some.
+    const int64_t most = (int64_t)device_sm_count() * 6, items = (int64_t)(q_heads + k_heads) * per_head;
+    int64_t group = kItems * kRotaryThreads / items;
+    if (group > kMostPairs / p.pairs) group = kMostPairs / p.pairs;
+    if (group > tokens / most) group = tokens / most;
+    a.group = group > 1 ? (int32_t)group : 1;
+    const int64_t groups = (tokens + a.group - 1) / a.group;
+    // Four times the CTAs that fit balance the end of a long call (64 heads of 128, 32768 tokens, pairs side by side:
+    // 164 us, else 183), where each has four groups for its start (9 heads of 256, 16384 tokens: 39 us with more, 35).
+    const int64_t ctas = groups >= 16 * most ? 4 * most : most;
+    const unsigned grid = (unsigned)(groups < ctas ? groups : ctas);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (p.io_dtype == KDA_DTYPE_F32)

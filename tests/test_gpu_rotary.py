@@ -155,3 +155,17 @@ def test_no_tokens_and_refusals():
     wide.copy_(q)
     with pytest.raises(kda.KdaError):  # the same memory with another stride
         kda.rotary(wide, None, pos, freqs, q_out=wide.as_strided((2, 3, 2, 64), (3 * 128, 128, 64, 1)))
+
+
+@pytest.mark.parametrize("T,H,Hk,D,R", [(1823, 1, 0, 16, 16), (1825, 1, 0, 16, 16), (30011, 1, 0, 16, 8), (20011, 1, 1, 24, 16), (40000, 1, 0, 2, 2),
+                                        (9001, 8, 1, 256, 256), (4001, 2, 1, 7, 6), (5555, 32, 8, 128, 64), (3001, 2, 0, 1024, 1024)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_tokens_taken_together(T, H, Hk, D, R, interleaved):
+    """Tokens of few heads share a CTA's pass: every size of such a group, a last one that is cut short, in place."""
+    freqs, _ = kda.rotary_freqs(R)
+    pos = torch.randperm(T, generator=torch.Generator().manual_seed(T)).cuda()[None]
+    for dtype in (torch.bfloat16, torch.float32):
+        q, k = randn(1, T, H, D, dtype=dtype), randn(1, T, Hk, D, dtype=dtype) if Hk else None
+        a, b = check(q, k, pos, freqs, interleaved=interleaved)
+        kda.rotary(q, k, pos, freqs, interleaved=interleaved, q_out=q, k_out=k)
+        assert torch.equal(q, a) and (b is None or torch.equal(k, b))
