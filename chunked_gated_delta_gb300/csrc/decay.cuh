@@ -79,12 +79,13 @@ struct DecayGradArgs {
     int64_t g_stride;
     const uint8_t *kept, *dkept;
     const float *kept_scale, *dkept_scale;
-    void *dq, *dk;       // [rows, Hqk, K] 16 bits, or (grouped) fp32 [rows, H, K]
+    void *dq, *dk;       // [rows, Hqk, K] 16 bits, or (groups of three and more) fp32 [rows, H, K]
     uint16_t* dv;        // [rows, H, V]
     float* dg;           // fp32 [rows, H]
     int32_t* status;
     float scale;
     int32_t H, group, sms;
+    int32_t paired;      // groups of two: their value heads are a cluster and add dq and dk up themselves
 };
 
 cudaError_t launch_decay_out(const DecayScanArgs& a, int K, int V, bool f16, cudaStream_t s);

@@ -79,7 +79,7 @@ DecayWs decay_ws(const kda_dims& d, const kda_decay_opts& o, const DecayPlan& p,
             w.kept_scale[i] = take((size_t)p.chunks * H * 4);
         }
     }
-    if (backward && o.qk_heads > 0 && o.qk_heads != d.H) {
+    if (backward && o.qk_heads > 0 && d.H > 2 * o.qk_heads) {
         w.dq32 = take(rows * H * d.K * 4);
         w.dk32 = take(rows * H * d.K * 4);
     }
@@ -235,14 +235,15 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
     const DecayWs ws = decay_ws(d, *opts, plan, true);
     if (ws.total > 0 && (!workspace || !is_aligned(workspace, 256) || workspace_bytes < ws.total)) return KDA_ERR_WORKSPACE;
     const int hq = opts->qk_heads > 0 ? opts->qk_heads : d.H;
-    const bool f16 = opts->io_dtype == KDA_IO_F16, grouped = hq != d.H;
+    const bool f16 = opts->io_dtype == KDA_IO_F16, paired = d.H == 2 * hq, parts = d.H > 2 * hq;
     DecayGradArgs a{};
     if (!token_map(&a.tm_q, q, d.K, hq, rows, sd.q) || !token_map(&a.tm_k, k, d.K, hq, rows, sd.k) ||
         !token_map(&a.tm_v, v, d.V, d.H, rows, sd.v) || !token_map(&a.tm_do, d_o, d.V, d.H, rows, sd.d_o) ||
-        (!grouped && (!token_map(&a.tm_dq, dq, d.K, hq, rows, (int64_t)hq * d.K, 32) ||
-                      !token_map(&a.tm_dk, dk, d.K, hq, rows, (int64_t)hq * d.K, 32))) ||
-        (grouped && (!group_map(&a.tm_dq, static_cast<uint8_t*>(workspace) + ws.dq32, d.K, d.H, rows) ||
-                     !group_map(&a.tm_dk, static_cast<uint8_t*>(workspace) + ws.dk32, d.K, d.H, rows))) || !token_map(&a.tm_dv, dv, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
+        (!parts && (!token_map(&a.tm_dq, dq, d.K, hq, rows, (int64_t)hq * d.K, 32) ||
+                    !token_map(&a.tm_dk, dk, d.K, hq, rows, (int64_t)hq * d.K, 32))) ||
+        (parts && (!group_map(&a.tm_dq, static_cast<uint8_t*>(workspace) + ws.dq32, d.K, d.H, rows) ||
+                   !group_map(&a.tm_dk, static_cast<uint8_t*>(workspace) + ws.dk32, d.K, d.H, rows))) ||
+        !token_map(&a.tm_dv, dv, d.V, d.H, rows, (int64_t)d.H * d.V, 32))
         return KDA_ERR_CUDA;
     DecayScanArgs c{};
     const int32_t b16 = opts->state_dtype == KDA_STATE_BF16;
@@ -288,8 +289,8 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
         a.dkept = c.dir[1].kept;
         a.kept_scale = c.dir[0].kept_scale;
         a.dkept_scale = c.dir[1].kept_scale;
-        a.dq = grouped ? static_cast<void*>(w + ws.dq32) : dq;
-        a.dk = grouped ? static_cast<void*>(w + ws.dk32) : dk;
+        a.dq = parts ? static_cast<void*>(w + ws.dq32) : dq;
+        a.dk = parts ? static_cast<void*>(w + ws.dk32) : dk;
         a.dv = static_cast<uint16_t*>(dv);
         a.dg = opts->head_gate ? reinterpret_cast<float*>(w + ws.dg) : dg;
         a.status = status_word;
@@ -297,8 +298,9 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
         a.H = d.H;
         a.group = d.H / hq;
         a.sms = device_sm_count();
+        a.paired = paired;
         if (e == cudaSuccess) e = launch_decay_grads(a, d.K, d.V, f16, s);
-        if (e == cudaSuccess && grouped)
+        if (e == cudaSuccess && parts)
             e = launch_decay_group(static_cast<const float*>(a.dq), static_cast<const float*>(a.dk), dq, dk, rows, hq, d.K,
                                    a.group, f16, device_sm_count(), s);
     }

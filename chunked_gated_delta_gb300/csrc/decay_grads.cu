@@ -21,6 +21,12 @@
 // shared memory. The far parts are scaled by rows in registers and put back, and the near products add
 // to them. S and dS come 64 values at a time; outputs leave by TMA from where their inputs were.
 //
+// Value heads that share q and k: two of them are a cluster of two CTAs; each gives the other its fp32 dq and
+// dk of half of the rows, straight into the other's shared memory, while dv and dg are made, and adds up
+// the half that it keeps (4 x 4096 x 32 heads in pairs 550 us, against 635 with fp32 parts in HBM and a kernel that adds
+// them up). More heads leave such parts: pairs that add up two of four or eight took 625 and 617 us against 618 and 609,
+// clusters of four and eight that read one another's tiles 629 and 785.
+//
 // Bound: the chain of a tile's phases (one CTA of 226 KB per SM): loads 2.3 thousand cycles, scores 1.9, P and
 // dP 3.1, the second half of the states until 8.9, far parts 1.7, near products and stores 6 (1.9 GHz; tensor cores
 // 23% busy, issue 33%). 352 KB a tile: 4 x 8192 tokens x 32 heads of 128 x 128
@@ -51,6 +57,7 @@ struct GradShape {
         float whole;
         uint32_t tmem;
         int32_t fail;
+        uint64_t may_give, given;  // of a pair: the other's rows may be given to it, it has given this one's
         uint64_t in_full, clean, scores, s_full, ring_read, ring_done, far, far_ok, p_ok, dv_far, dv_ok, dqk, dv;
     };
     // when everything else is done, in place of dP: the parts of dg
@@ -69,6 +76,25 @@ struct GradShape {
 };
 // TMEM columns: the scores, and when all of them have been read P^T, dP^T and dv in their place; dq and dk.
 constexpr uint32_t kT0 = 0, kT1 = 128, kTp = kT0, kTdp = kT0 + 64, kTdv = kT1, kTdq = 256, kTdk = 384;
+
+// A barrier of all threads of a cluster, in two halves: writes before the one are seen after the other.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Where the other CTA of a pair has what lies at this one's shared address `at`.
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, int rank) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+    return there;
+}
+__device__ __forceinline__ void arrive_there(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// bytes of this CTA's shared memory into another's, whose barrier counts them
+__device__ __forceinline__ void bulk_push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "r"(from), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // x[0 .. 31] of each lane: lane l gets the sum over the lanes of x[l].
 __device__ __forceinline__ float transposed_sum(float (&x)[32], int lane) {
@@ -109,7 +135,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             ptx::mbar_init(b, 1);
         for (uint64_t* b : {&sm.clean, &sm.far_ok, &sm.p_ok, &sm.dv_ok}) ptx::mbar_init(b, kWorkerWarps);
         ptx::mbar_init(&sm.ring_read, kDotWarps);
+        ptx::mbar_init(&sm.may_give, 1);
+        ptx::mbar_init(&sm.given, 1);
         ptx::fence_mbar_init();
+        if (a.paired) ptx::mbar_arrive_expect_tx(&sm.given, 2 * 64 * K * 4);
         sm.fail = 0;
     }
     if (warp == kWorkerWarps) {
@@ -122,6 +151,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    if (a.paired) cluster_arrive();  // this CTA's barriers are there
     volatile int32_t* fail = &sm.fail;
     auto wait = [&](uint64_t& bar, uint32_t parity) {
         wait_or_note(&bar, parity, &sm.fail);
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 const uint32_t p = swizzled_row(tile + (c >> 5) * 16384, row) ^ ((c & 31) << 2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (staged) sts128(p ^ (e << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    if (staged || a.paired) sts128(p ^ (e << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                     else if (live) *reinterpret_cast<float4*>(to + c + 4 * e) = make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
                 }
             }
@@ -464,7 +494,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         wait(sm.dqk, 0);
         ptx::tc_fence_after();
         const int64_t to = (tok * a.H + h) * K;
-        if (a.group == 1) {
+        const bool mine = (quarter >> 1) == (h & 1);  // (of a pair each head has half of the rows)
+        if (a.paired) {
+            // The other head's rows go to where that has them, which is free once its products are done.
+            cluster_wait();  // its barriers are there
+            const int peer = 1 - (h & 1);
+            if (warp == 0 && elect_one()) arrive_there(in_cta(ptx::smem_u32(&sm.may_give), peer));
+            if (!mine) {
+                store32(t_row + kTdq, base + Shape::kQ, nullptr);
+                store32(t_row + kTdk, base + Shape::kRing, nullptr);
+                ptx::fence_proxy_async_smem();
+                named_sync(7, 256);
+                if (warp == 2 * peer && elect_one() && wait(sm.may_give, 0)) {
+                    const uint32_t bar = in_cta(ptx::smem_u32(&sm.given), peer);
+                    for (int b = 0; b < 2 * KB; ++b) {
+                        const uint32_t at_rows = b * 16384 + peer * 8192;
+                        bulk_push(in_cta(base + Shape::kQ + at_rows, peer), base + Shape::kQ + at_rows, 8192, bar);
+                        bulk_push(in_cta(base + Shape::kRing + at_rows, peer), base + Shape::kRing + at_rows, 8192, bar);
+                    }
+                }
+            }
+        } else if (a.group == 1) {
             store16(t_row + kTdq + part * kCols, part * kCols, kCols, base + Shape::kQ, static_cast<uint16_t*>(a.dq) + to);
             store16(t_row + kTdk + part * kCols, part * kCols, kCols, base + Shape::kK, static_cast<uint16_t*>(a.dk) + to);
         } else {
@@ -480,7 +530,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 ptx::bulk_commit();
             }
         };
-        send([&] {
+        if (!a.paired) send([&] {
             // (fp32: twice the columns of 128 bytes, dq's where q and k were, dk's where the states were)
             const int blocks = a.group == 1 ? KB : 2 * KB, wide = 64 / (a.group == 1 ? 1 : 2);
             const int from_dk = a.group == 1 ? Shape::kK : Shape::kRing;
@@ -532,9 +582,52 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             }
             if (live) a.dg[tok * a.H + h] = all * sm.whole + later + before;
         }
+        if (a.paired && mine) {  // what the other head had for these rows has landed where it had it itself
+            wait(sm.given, 0);
+            auto add = [&](uint32_t column, uint32_t tile, void* to) {
+                uint32_t w[kCols / 2];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    const int col = part * kCols + c;
+                    float u[16];
+                    ptx::tmem_ld16(t_row + column + col, u);
+                    const uint32_t p = swizzled_row(tile + (col >> 5) * 16384, row) ^ ((col & 31) << 2);
+                    const uint4 x[4] = {lds128(p), lds128(p ^ 16), lds128(p ^ 32), lds128(p ^ 48)};
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[c / 2 + 2 * e] = pack_b16x2(u[4 * e] + __uint_as_float(x[e].x), u[4 * e + 1] + __uint_as_float(x[e].y), F16);
+                        w[c / 2 + 2 * e + 1] = pack_b16x2(u[4 * e + 2] + __uint_as_float(x[e].z), u[4 * e + 3] + __uint_as_float(x[e].w), F16);
+                    }
+                }
+                named_sync(2 + quarter, 128);  // the sums of these rows have been read
+                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(to) + (tok * (a.H / 2) + hq) * K + part * kCols);
+#pragma unroll
+                for (int c = 0; c < kCols; c += 8) {
+                    const int col = part * kCols + c;
+                    const uint32_t p = swizzled_row(tile + (col >> 6) * 16384, row) ^ ((col & 63) << 1);
+                    if (staged) sts128(p, w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+                    else if (live) out[c / 8] = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+                }
+            };
+            add(kTdq, base + Shape::kQ, a.dq);
+            add(kTdk, base + Shape::kRing, a.dk);
+            send([&] {
+                for (int b = 0; b < KB; ++b) {
+                    const int at_box = b * 16384 + quarter * 4096;
+                    ptx::tma_store_3d(&a.tm_dq, raw + Shape::kQ + at_box, b * 64, hq, row0 + quarter * 32);
+                    ptx::tma_store_3d(&a.tm_dk, raw + Shape::kRing + at_box, b * 64, hq, row0 + quarter * 32);
+                }
+            });
+        }
         if (part == 0 && elect_one()) ptx::bulk_wait_read0();
     }
     __syncwarp();
+    if (a.paired) {  // what either has given has landed before one of them leaves
+        if (warp == kWorkerWarps) cluster_wait();  // (the workers have been there)
+        cluster_arrive();
+        cluster_wait();
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -548,7 +641,20 @@ cudaError_t launch_shape(const DecayGradArgs& a, cudaStream_t s) {
     auto kern = kda_decay_grads_kernel<KB, VB, F16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3((unsigned)(a.seqs.pieces * a.H)), dim3(kGradThreads), (size_t)Shape::kSmem, s, a);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.seqs.pieces * a.H));
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.dynamicSmemBytes = Shape::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.paired ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // The gradients of q and k, summed over the value heads that share them: in fp32 [rows, Hqk, group, K] each.

@@ -58,6 +58,19 @@ def test_heads(H, hq, gate):
     compare(run(x), x, rows(2, 200))
 
 
+@pytest.mark.parametrize("H,hq", [(2, 1), (6, 3), (12, 3), (16, 2), (16, 1), (7, 1)])
+@pytest.mark.parametrize("K,V,io", [(128, 128, torch.bfloat16), (64, 128, torch.float16), (128, 64, torch.float16)])
+def test_groups(H, hq, K, V, io):
+    """Value heads that share q and k, by twos, fours, eights and others: their gradients are summed, rows behind a
+    sequence's end left out, with the same bits each time."""
+    lens = [1, 0, 129, 300, 127]
+    x = make(1, sum(lens), H, K, V, hq=hq, io=io, N=len(lens), seed=H + hq)
+    a, b = run(x, cu=offsets(lens)), run(x, cu=offsets(lens))
+    compare(a, x, spans(lens))
+    for name in ("dq", "dk", "dv", "dg", "dh0"):
+        assert torch.equal(a[name], b[name])
+
+
 @pytest.mark.parametrize("lens", [[5], [0, 7, 0, 130, 128, 1, 0], [300, 1, 2, 299], [0, 0]])
 @pytest.mark.parametrize("K,V,io", [(128, 128, torch.bfloat16), (64, 64, torch.float16)])
 def test_packed(lens, K, V, io):
