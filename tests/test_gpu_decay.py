@@ -260,6 +260,18 @@ def test_bad_offsets_are_reported():
     run(x, cu=offsets([100, 100, 100]))
 
 
+def test_bad_offsets_of_pairs_are_reported():
+    """A pair's two CTAs leave together, and what comes after is as always."""
+    x = make(1, 300, 4, 64, 64, hq=2, N=3)
+    for cu in ([0, 100, 50, 300], [0, 100, 200, 299], [0, 100, 400, 300]):
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        kda.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], h0=x["h0"], dht=x["dht"], cu_seqlens=bad, status=word)
+        torch.cuda.synchronize()
+        assert word.item() != 0
+    compare(run(x, cu=offsets([100, 150, 50])), x, spans([100, 150, 50]))
+
+
 def test_no_tokens():
     for shape in ((2, 0), (1, 0)):
         x = make(*shape, 2, 64, 64)
