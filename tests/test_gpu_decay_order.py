@@ -77,6 +77,20 @@ def test_two_streams_at_once():
                 assert torch.equal(t, u)
 
 
+def test_pairs_on_two_streams_at_once():
+    """Clusters of two calls on the same SMs, with more of them than fit at once."""
+    xs = [make(2, 2100, 16, 128, 64, hq=8, seed=i) for i in range(2)]
+    want = [[t.clone() for t in both(x)] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [both(x, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for t, u in zip(a, b):
+                assert torch.equal(t, u)
+
+
 def test_outputs_belong_to_the_stream():
     """What a call on another stream allocates is that stream's: memory freed there with work pending is not handed
     to this one (the workspace is freed as the call returns)."""
