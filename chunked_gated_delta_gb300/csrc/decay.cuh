@@ -92,11 +92,12 @@ cudaError_t launch_decay_out(const DecayScanArgs& a, int K, int V, bool f16, cud
 cudaError_t launch_decay_states(const DecayScanArgs& a, int K, int V, bool f16, int dirs, cudaStream_t s);
 cudaError_t launch_decay_join(const DecayJoinArgs& a, int dirs, cudaStream_t s);
 cudaError_t launch_decay_grads(const DecayGradArgs& a, int K, int V, bool f16, cudaStream_t s);
-// dq, dk [rows, heads, K] in 16 bits from fp32 [rows, heads, group, K]
-cudaError_t launch_decay_group(const float* dq32, const float* dk32, void* dq, void* dk, int64_t rows, int heads, int K,
-                               int group, bool f16, int sms, cudaStream_t s);
-// out [H]: dg [rows, H] summed over the rows; part: fp32 [(rows + 255) / 256, H]
-cudaError_t launch_decay_gate(const float* dg, float* part, float* out, int64_t rows, int H, cudaStream_t s);
+// dq, dk [rows, heads, K] in 16 bits from fp32 [rows, heads, group, K] (nothing if the offsets of seqs are out of order)
+cudaError_t launch_decay_group(const float* dq32, const float* dk32, void* dq, void* dk, const DecaySeqs& seqs, int64_t rows,
+                               int heads, int K, int group, bool f16, int sms, cudaStream_t s);
+// out [H]: dg [rows, H] summed over the rows (likewise); part: fp32 [(rows + 255) / 256, H]
+cudaError_t launch_decay_gate(const float* dg, float* part, float* out, const DecaySeqs& seqs, int64_t rows, int H,
+                              cudaStream_t s);
 
 namespace {
 
@@ -117,6 +118,19 @@ struct DecayScratch {
 struct DecaySortScratch : DecayScratch {
     int32_t len[kMostSorted];
 };
+
+// cu[n] and cu[n + 1] are no sequence's bounds.
+__device__ __forceinline__ bool out_of_order(int bos, int eos, int n, int N, int T) {
+    return bos < 0 || eos < bos || eos > T || (n == 0 && bos != 0) || (n == N - 1 && eos != T);
+}
+// cu is 0 = c0 <= c1 <= ... <= cN = T. Called by all THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ bool in_order(const DecaySeqs& s) {
+    if (!s.cu) return true;
+    bool bad = false;
+    for (int n = threadIdx.x; n < s.N; n += THREADS) bad |= out_of_order(s.cu[n], s.cu[n + 1], n, s.N, s.T);
+    return !__syncthreads_or(bad);
+}
 
 // The piece with this index, or the first of sequence `by_seq` (index then a sequence).  Called by
 // all THREADS threads.  A sequence without tokens has one piece where `empty` says so.  Returns
@@ -159,7 +173,7 @@ __device__ __forceinline__ bool find_piece(const DecaySeqs& s, int index, bool b
     bool bad = false;
     for (int n = first; n < last; ++n) {
         const int bos = s.cu[n], eos = s.cu[n + 1];
-        bad |= bos < 0 || eos < bos || eos > s.T || (n == 0 && bos != 0) || (n == s.N - 1 && eos != s.T);
+        bad |= out_of_order(bos, eos, n, s.N, s.T);
         const int nc = ceil_div(max(eos - bos, 0), kDecayChunk);
         chunks += nc;
         pieces += max(ceil_div(nc, s.seg_chunks), empty ? 1 : 0);

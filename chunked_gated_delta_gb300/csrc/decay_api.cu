@@ -301,10 +301,10 @@ extern "C" kda_status kda_decay_bwd(const void* q, const void* k, const void* v,
         a.paired = paired;
         if (e == cudaSuccess) e = launch_decay_grads(a, d.K, d.V, f16, s);
         if (e == cudaSuccess && parts)
-            e = launch_decay_group(static_cast<const float*>(a.dq), static_cast<const float*>(a.dk), dq, dk, rows, hq, d.K,
-                                   a.group, f16, device_sm_count(), s);
+            e = launch_decay_group(static_cast<const float*>(a.dq), static_cast<const float*>(a.dk), dq, dk, c.seqs, rows, hq,
+                                   d.K, a.group, f16, device_sm_count(), s);
     }
     if (e == cudaSuccess && opts->head_gate)
-        e = launch_decay_gate(a.dg, reinterpret_cast<float*>(w + ws.dg_part), dg, rows, d.H, s);
+        e = launch_decay_gate(a.dg, reinterpret_cast<float*>(w + ws.dg_part), dg, c.seqs, rows, d.H, s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -657,11 +657,13 @@ cudaError_t launch_shape(const DecayGradArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-// The gradients of q and k, summed over the value heads that share them: in fp32 [rows, Hqk, group, K] each.
+// The gradients of q and k, summed over the value heads that share them: in fp32 [rows, Hqk, group, K] each. (Where the
+// offsets are out of order the kernels before have written none, and this one must not write what it would find.)
 __global__ void __launch_bounds__(256) kda_decay_group_kernel(const float* dq32, const float* dk32, void* dq, void* dk,
-                                                              int64_t fours, int K4, int group, int f16) {
+                                                              DecaySeqs seqs, int64_t fours, int K4, int group, int f16) {
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if (!in_order<256>(seqs)) return;
     const float* in = blockIdx.y ? dk32 : dq32;
     uint2* out = static_cast<uint2*>(blockIdx.y ? dk : dq);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < fours; i += (int64_t)gridDim.x * 256) {
@@ -688,10 +690,12 @@ __global__ void __launch_bounds__(256) kda_decay_gate_rows_kernel(const float* d
     for (int64_t r = r0; r < r1; ++r) s += (double)dg[r * H + h];
     part[(int64_t)blockIdx.x * H + h] = (float)s;
 }
-__global__ void __launch_bounds__(256) kda_decay_gate_kernel(const float* part, float* dg, int64_t parts, int H) {
+__global__ void __launch_bounds__(256) kda_decay_gate_kernel(const float* part, float* dg, DecaySeqs seqs, int64_t parts,
+                                                             int H) {
     __shared__ double sums[256];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
+    if (!in_order<256>(seqs)) return;
     const int h = blockIdx.x;
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < parts; i += 256) s += (double)part[i * H + h];
@@ -714,21 +718,22 @@ cudaError_t launch_decay_grads(const DecayGradArgs& a, int K, int V, bool f16, c
     return f16 ? launch_shape<1, 1, true>(a, s) : launch_shape<1, 1, false>(a, s);
 }
 
-cudaError_t launch_decay_group(const float* dq32, const float* dk32, void* dq, void* dk, int64_t rows, int heads, int K,
-                               int group, bool f16, int sms, cudaStream_t s) {
+cudaError_t launch_decay_group(const float* dq32, const float* dk32, void* dq, void* dk, const DecaySeqs& seqs, int64_t rows,
+                               int heads, int K, int group, bool f16, int sms, cudaStream_t s) {
     const int64_t fours = rows * heads * (K / 4), blocks = (fours + 255) / 256;
     return launch_dependent(kda_decay_group_kernel, dim3((unsigned)(blocks < 16 * sms ? blocks : 16 * sms), 2), dim3(256),
-                            (size_t)0, s, dq32, dk32, dq, dk, fours, K / 4, group, (int)f16);
+                            (size_t)0, s, dq32, dk32, dq, dk, seqs, fours, K / 4, group, (int)f16);
 }
 
-cudaError_t launch_decay_gate(const float* dg, float* part, float* out, int64_t rows, int H, cudaStream_t s) {
+cudaError_t launch_decay_gate(const float* dg, float* part, float* out, const DecaySeqs& seqs, int64_t rows, int H,
+                              cudaStream_t s) {
     const int64_t parts = (rows + kGateRows - 1) / kGateRows;
     if (parts > 0) {
         const cudaError_t e = launch_dependent(kda_decay_gate_rows_kernel, dim3((unsigned)parts, (unsigned)((H + 255) / 256)),
                                                dim3(256), (size_t)0, s, dg, part, rows, H);
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(kda_decay_gate_kernel, dim3((unsigned)H), dim3(256), (size_t)0, s, part, out, parts, H);
+    return launch_dependent(kda_decay_gate_kernel, dim3((unsigned)H), dim3(256), (size_t)0, s, part, out, seqs, parts, H);
 }
 
 }  // namespace kda
