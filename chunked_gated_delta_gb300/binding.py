@@ -569,7 +569,8 @@ def decay_bwd(q, k, v, g, do, scale=None, h0=None, dht=None, cu_seqlens=None, wa
 def decay_step(q, k, v, g, state, slots=None, scale=None, cu_seqlens=None, out=None, status=None, stream=None):
     """decay_fwd's recurrence for the few new tokens of each sequence (kda_decay_step), on a
     cache of states [num_slots,H,K,V] updated in place.  Returns o [B,T,H,V].  g as in
-    decay_fwd; state, slots, cu_seqlens, status and stream as in step."""
+    decay_fwd; state, slots, cu_seqlens, status and stream as in step, but that with any
+    cu_seqlens out of order no sequence is taken."""
     return (_calls or _layer_calls()).decay_step(q, k, v, g, state, slots, scale, cu_seqlens, out, status, stream)
 
 

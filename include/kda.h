@@ -552,7 +552,8 @@ kda_status kda_decay_bwd(const void* q, const void* k, const void* v, const floa
 
 /*
  * Decode step, token by token in fp32 on chip: state [num_slots, H, K, V], slots, cu_seqlens, padding
- * and errors as in kda_step. q, k and v are aligned to their elements.
+ * and errors as in kda_step, but that with any cu_seqlens out of order no sequence is taken. q, k and v are
+ * aligned to their elements.
  */
 kda_status kda_decay_step(const void* q, const void* k, const void* v, const float* g, float scale, void* state,
                           const int32_t* slots, const int32_t* cu_seqlens, void* o, const kda_dims* dims,

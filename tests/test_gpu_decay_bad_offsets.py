@@ -1,5 +1,5 @@
-"""cu_seqlens out of order, beyond the rows or short of them: decay_bwd reports it and writes nothing, whichever kernels
-a head layout and a form of the decay bring in."""
+"""cu_seqlens out of order, beyond the rows or short of them: decay_bwd and decay_step report it and write nothing,
+whichever kernels a head layout and a form of the decay bring in."""
 from __future__ import annotations
 
 import ctypes
@@ -64,3 +64,63 @@ def test_no_gradient_of_many_sequences_is_written():
         bad[i] = sum(lens) + 1
         for n, t in backward(x, bad.cuda(), None).items():
             assert bool((t == 7.0).all()), (n, i)
+
+
+def step(x, state, cu, slots, word):
+    out = torch.full_like(x["v"], 7.0)
+    kda.decay_step(x["q"], x["k"], x["v"], x["g"], state, slots=slots, cu_seqlens=cu, out=out, status=word)
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("with_slots", [True, False])
+@pytest.mark.parametrize("K,V,st", [(128, 128, torch.float32), (64, 64, torch.bfloat16), (64, 128, torch.float32)])
+def test_no_state_and_no_output_is_written(K, V, st, with_slots):
+    """0, 3, 1, 4 among them: by their own bounds alone the first and the last sequence would both have rows 1 and 2."""
+    x = make(1, 4, 4, K, V, hq=2, h0=False, do=False)
+    start = torch.randn((5, 4, K, V), generator=torch.Generator(device="cuda").manual_seed(K), device="cuda").to(st)
+    slots = torch.tensor([4, 1, 2], dtype=torch.int32, device="cuda") if with_slots else None
+    for cu in ([0, 3, 1, 4], [0, 1, 2, 3], [1, 2, 3, 4], [0, 1, 2, 5], [0, -1, 2, 4], [0, 0, 5, 4], [0, 4, 4, 3]):
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        state, bad = start.clone(), torch.tensor(cu, dtype=torch.int32, device="cuda")
+        out = step(x, state, bad, slots, word)
+        assert binding.status(word) == 7, cu
+        assert torch.equal(state, start) and bool((out == 7.0).all()), cu
+        assert bool((step(x, state, bad, slots, None) == 7.0).all()) and torch.equal(state, start)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    state, good = start.clone(), torch.tensor([0, 1, 3, 4], dtype=torch.int32, device="cuda")
+    out = step(x, state, good, slots, word)
+    assert binding.status(word) == 0 and bool((out != 7.0).any()) and not torch.equal(state, start)
+
+
+def test_one_of_many_sequences_is_out_of_order():
+    """More sequences than a block has threads; a slot given twice and one outside the cache do not hide it."""
+    N = 300
+    x = make(1, 2 * N, 2, 64, 64, h0=False, do=False)
+    start = torch.randn((N + 1, 2, 64, 64), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    slots = torch.arange(N, dtype=torch.int32, device="cuda")
+    slots[7], slots[9] = 6, N + 5
+    cu = torch.arange(0, 2 * N + 1, 2, dtype=torch.int32)
+    for i in (1, 2, 3, 4, 150, N - 3, N - 2, N - 1):
+        bad = cu.clone()
+        bad[i] = 2 * N + 1
+        state, word = start.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = step(x, state, bad.cuda(), slots, word)
+        assert word.item() != 0 and torch.equal(state, start) and bool((out == 7.0).all()), i
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 127, 128, 129, 515])
+def test_each_of_so_many_sequences_out_of_order(N):
+    """The offset that is wrong: any of them, the first and the last among them; and none."""
+    x = make(1, 3 * N, 1, 64, 64, h0=False, do=False)
+    start = torch.zeros((N, 1, 64, 64), device="cuda")
+    cu = torch.arange(0, 3 * N + 1, 3, dtype=torch.int32, device="cuda")
+    for i in sorted({*range(min(N, 9) + 1), N // 2, N - 1, N}):
+        bad = cu.clone()
+        bad[i] = 2 if i == 0 else int(cu[i - 1]) - 1 if i < N else 3 * N - 1
+        state, word = start.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = step(x, state, bad, None, word)
+        assert binding.status(word) == 7 and bool((state == 0.0).all()) and bool((out == 7.0).all()), i
+    state, word = start.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    step(x, state, cu, None, word)
+    assert binding.status(word) == 0 and bool((state != 0.0).any(-1).any(-1).all())
