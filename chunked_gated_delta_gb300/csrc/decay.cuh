@@ -271,6 +271,15 @@ __device__ __forceinline__ Pair sum_decay(const LoadedG& g, ChunkDecay& out, int
     }
     return {__shfl_sync(~0u, s.hi, 31), __shfl_sync(~0u, s.lo, 31)};
 }
+// n for a chunk whose decays between two tokens are at most 2^n: 0 unless some g are above zero.
+__device__ __forceinline__ int rise_of(const LoadedG& g) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += fmaxf(g.v[i], 0.f);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(~0u, s, off);
+    return (int)fminf(ceilf(s * 1.44269504f), 126.f);
+}
 // exp of a chunk's whole decay, to less than its last bit: a state of thousands of chunks is multiplied by
 // one after the other, so their errors add up. 2^n times the power series of exp(x), |x| <= ln(2) / 2, to its
 // ninth term (what is left is below 2^-33); only the last addition rounds at the size of the result.
@@ -418,6 +427,15 @@ __device__ __forceinline__ float scale_to_f16(uint32_t top_bits) {
     if (top_bits == 0 || e == 128) return 1.f;
     const int n = min(max(13 - e, -126), 126);
     return __uint_as_float((uint32_t)(n + 127) << 23);
+}
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+// n for scores in fp16: times 2^n the largest, `top`, is 2^13 .. 2^14 after decays of at most 2^rise, so that those down to
+// 2^-27 of it are in fp16's normal range. At most 40: scores below 2^-54 add less than half of fp16's smallest number
+// to any output, and what the state adds to the same sum is multiplied by 2^n too.
+__device__ __forceinline__ int score_power(float top, int rise) {
+    const uint32_t bits = __float_as_uint(top);
+    const int e = (int)(bits >> 23) - 127;
+    return bits == 0 || e == 128 ? 0 : min(max(13 - e - rise, -126), 40);
 }
 
 }  // namespace

@@ -53,18 +53,17 @@ struct DecayScanShape {
     static constexpr int kHi = OUT ? kQ + kStages * kXBytes : kQ, kLo = kHi + kXBytes, kS = kLo + kXBytes;
     static constexpr int kO = kS + (OUT ? 1 : 2) * kStateBytes;
     static constexpr int kSmall = kO + (OUT ? kYBytes : 0);
-    // registers: those that the block is launched with, handed out as control, keys, state, scores, output
-    static constexpr int kControlRegs = OUT ? 56 : 96, kKeyRegs = OUT ? 64 : 88, kStateRegs = OUT ? 168 : 240;
-    static constexpr int kScoreRegs = 64, kOutRegs = 64;
-    static_assert(OUT ? kControlRegs + 2 * kKeyRegs + kStateRegs + kScoreRegs + kOutRegs <= 6 * 80
-                      : kControlRegs + 2 * kKeyRegs + kStateRegs <= 4 * 128,
-                  "within what the block is launched with");
     struct Small {
         ChunkDecay decay[2];
         float column[OUT ? kDecayChunk : 1];  // exp of the decay from a column to the end of its 32
         float whole[2], unscale[2], key_unscale[2];
         uint32_t top[4], key_top[2][8];
+        // fp16: see rise_of; the largest of the keys as they are; what 32 rows' scores are multiplied by, as a power of two
+        int32_t rise[2];
+        uint32_t plain_top[2][8];
+        int8_t score_powers[2][4];
         uint64_t x_full[2], x_empty[2], q_full[2], q_empty[2], y_full[2], y_empty[2], g_ready[2], g_free[2];
+        uint64_t plain[2], scaled[2];  // plain_top and score_powers are there
         uint64_t scores, p_ready, s_ready, keys, keys_read, added, added_read, far, far_ok, o_full, o_free[2];
         uint32_t tmem;
         int32_t fail;
@@ -79,10 +78,39 @@ struct DecayScanShape {
     static constexpr uint32_t kTmem = OUT ? 512 : 128;
 };
 
+// Registers: those that the block is launched with, handed out as control, keys, state, scores, output. (fp16 with its
+// output: its scores' and outputs' powers of two spill with bf16's split: 237 instead of 231 us, K = 64 23.9 instead of 20.6.)
+template <bool F16, bool OUT>
+struct DecayScanRegs {
+    static constexpr bool kPowers = F16 && OUT;
+    static constexpr int kControl = kPowers ? 40 : OUT ? 56 : 96, kKeys = kPowers ? 56 : OUT ? 64 : 88;
+    static constexpr int kState = kPowers ? 176 : OUT ? 168 : 240, kScores = kPowers ? 80 : 64, kOut = kPowers ? 72 : 64;
+    static_assert(OUT ? kControl + 2 * kKeys + kState + kScores + kOut <= 6 * 80 : kControl + 2 * kKeys + kState <= 4 * 128,
+                  "within what the block is launched with");
+};
+
+// The largest in size of PIECES 16-byte pieces of fp16 in a swizzled row, from piece c0 on (NaN counts as nothing).
+template <int PIECES>
+__device__ __forceinline__ float largest_half(uint32_t row, int c0) {
+    __half2 most[4];  // (one would be a chain of as many steps as there are words)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most[e] = __half2half2(__ushort_as_half(0));
+#pragma unroll 2
+    for (int c = c0; c < c0 + PIECES; ++c) {
+        const uint4 x = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most[e] = __hmax2(most[e], __habs2(*reinterpret_cast<const __half2*>(&in[e])));
+    }
+    const __half2 all = __hmax2(__hmax2(most[0], most[1]), __hmax2(most[2], most[3]));
+    return fmaxf(__low2float(all), __high2float(all));
+}
+
 template <int KB, int VB, bool F16, bool OUT>
 __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     kda_decay_scan_kernel(const __grid_constant__ DecayScanArgs a) {
     using Shape = DecayScanShape<KB, VB, OUT>;
+    using Regs = DecayScanRegs<F16, OUT>;
     constexpr int K = Shape::K, V = Shape::V, NS = Shape::kStages;
     extern __shared__ __align__(1024) uint8_t raw[];
     auto& sm = *reinterpret_cast<typename Shape::Small*>(raw + Shape::kSmall);
@@ -118,9 +146,11 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&sm.x_full[s], 1);
-            ptx::mbar_init(&sm.x_empty[s], Shape::kKeyWarps + (OUT ? 1 : 0));
+            ptx::mbar_init(&sm.x_empty[s], Shape::kKeyWarps + (OUT ? 1 : 0) + (OUT && F16 ? 4 : 0));
             ptx::mbar_init(&sm.q_full[s], 1);
-            ptx::mbar_init(&sm.q_empty[s], 1);
+            ptx::mbar_init(&sm.q_empty[s], F16 ? 5 : 1);
+            ptx::mbar_init(&sm.plain[s], 1);
+            ptx::mbar_init(&sm.scaled[s], 4);
             ptx::mbar_init(&sm.y_full[s], 1);
             ptx::mbar_init(&sm.y_empty[s], 1);
             ptx::mbar_init(&sm.g_ready[s], 1);
@@ -155,7 +185,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kControlRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kControl));
         if (warp == 0 && elect_one()) {
             // ---------------------------------------------------------- loads
             const int h = sm.head, hq = h / a.group;
@@ -257,12 +287,13 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 if (it + 1 < chunks) next = loaded(it + 1);
                 if (it >= 2) wait(sm.g_free[st], ((it >> 1) - 1) & 1);
                 const Pair all = sum_decay(now, sm.decay[st], lane);
-                if (lane == 0) sm.whole[st] = whole_decay(all);
+                const int rise = OUT && F16 ? rise_of(now) : 0;
+                if (lane == 0) sm.whole[st] = whole_decay(all), sm.rise[st] = rise;
                 arrive(sm.g_ready[st]);
             }
         }
     } else if (warp < Shape::kFirstState) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kKeyRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kKeys));
         // ---------------------------------------------------------- keys: scaled, in two parts
         // the token whose row this thread has, and 16-byte pieces from c_first on (all of it, or half)
         constexpr int kPieces = K / 8 / (Shape::kKeyWarps / 4);
@@ -282,18 +313,12 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             if constexpr (F16) {
                 // The scaled keys may be far below fp16's normal range, where a part keeps no relative precision: a
                 // power of two for all of the chunk's brings the largest near the top of it.
-                __half2 most = __half2half2(__ushort_as_half(0));
-#pragma unroll 4
-                for (int c = c_first; c < c_first + kPieces; ++c) {
-                    const uint4 x = lds128((row ^ ((c & 7) << 4)) + (c >> 3) * 16384);
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&in[e])));
-                }
-                const float m = live ? fmaxf(__low2float(most), __high2float(most)) * fabsf(w) : 0.f;
+                const float plain = live ? largest_half<kPieces>(row, c_first) : 0.f, m = plain * fabsf(w);
                 const uint32_t top = __reduce_max_sync(~0u, __float_as_uint(m));
-                if (lane == 0) sm.key_top[st][warp - 4] = top;
+                const uint32_t plain_top = OUT ? __reduce_max_sync(~0u, __float_as_uint(plain)) : 0u;
+                if (lane == 0) sm.key_top[st][warp - 4] = top, sm.plain_top[st][warp - 4] = plain_top;
                 named_sync(4, 32 * Shape::kKeyWarps);
+                if (OUT && j == 0 && c_first == 0) ptx::mbar_arrive(&sm.plain[st]);
                 uint32_t all = sm.key_top[st][0];
 #pragma unroll
                 for (int i = 1; i < Shape::kKeyWarps; ++i) all = max(all, sm.key_top[st][i]);
@@ -347,7 +372,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
             arrive(sm.keys);
         }
     } else if (warp < Shape::kFirstState + 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kStateRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs::kState));
         // ---------------------------------------------------------- the state, transposed: column v of S
         const int v = quarter * 32 + lane;
         constexpr int kThreads = 64 * VB;
@@ -467,18 +492,39 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         }
     } else if (warp < Shape::kFirstState + 8) {
         if constexpr (OUT) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kScoreRegs));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kScores));  // (or none: 80)
             // ------------------------------------------------------ P: row i of the scores
             const int i = quarter * 32 + lane;
             const uint32_t t_row = tmem + Shape::kScores + ((uint32_t)(quarter * 32) << 16);
             for (int it = 0; it < chunks; ++it) {
-                const int st = it & 1;
+                const int st = it & 1, sx = it % NS;
+                float scale = a.scale;
                 wait(sm.g_ready[st], (it >> 1) & 1);
                 const ChunkDecay& d = sm.decay[st];
                 const float hi = d.hi[i], lo = d.lo[i];
                 named_sync(3, 128);  // the last chunk's factors have been read
                 sm.column[i] = exp2_fast(gap(d, quarter * 32 + 31, hi, lo));
                 named_sync(3, 128);
+                if constexpr (F16) {
+                    // Scores as fp16 have to be near the top of its range, or small ones lose their bits and large ones
+                    // overflow: a power of two for each 32 rows, which their far parts are multiplied by and o divided. It
+                    // is found before the scores are there, from what they can be at most, K max |q| max |k| (of random
+                    // rows 2^5 times their largest). 4 x 8192 tokens x 32 heads of 128 x 128 take 231 us, without any power
+                    // 219; found from the scores themselves, which it has to wait for, 255 where this was 243, by the two
+                    // warps with the least to do 268.
+                    wait(sm.q_full[sx], (it / NS) & 1);
+                    const float mine = largest_half<K / 8>(swizzled_row(base + Shape::kQ + sx * Shape::kXBytes, i), 0);
+                    const uint32_t q_top = __reduce_max_sync(~0u, i < sm.left - offset(it) ? __float_as_uint(mine) : 0u);
+                    arrive(sm.q_empty[sx]);
+                    wait(sm.plain[st], (it >> 1) & 1);
+                    const uint32_t k_top = __reduce_max_sync(~0u, sm.plain_top[st][lane & 7]);
+                    arrive(sm.x_empty[sx]);  // (plain_top has been read: the keys after the next may come)
+                    const float most = (float)K * fabsf(scale) * __uint_as_float(q_top) * __uint_as_float(k_top);
+                    const int n = score_power(most, sm.rise[st]);
+                    if (lane == 0) sm.score_powers[st][quarter] = (int8_t)n;
+                    scale *= power_of_two(n);
+                    arrive(sm.scaled[st]);
+                }
                 wait(sm.scores, it & 1);
                 ptx::tc_fence_after();
                 // Left of the diagonal's 32 x 32 block a pair's decay is taken in two steps, from the token to
@@ -487,7 +533,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
 #pragma unroll 1
                 for (int b = 0; b < quarter; ++b) {
                     const int end = 32 * b + 31;
-                    const float r = a.scale * exp2_fast((hi - d.hi[end]) + (lo - d.lo[end]));
+                    const float r = scale * exp2_fast((hi - d.hi[end]) + (lo - d.lo[end]));
                     const uint64_t r2 = pair_of(r, r);
                     float s[32];
                     uint32_t p[16];
@@ -514,8 +560,8 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     for (int e = 0; e < 16; e += 2) {
                         const float2 h2 = *reinterpret_cast<const float2*>(&d.hi[32 * quarter + c + e]);
                         const float2 l2 = *reinterpret_cast<const float2*>(&d.lo[32 * quarter + c + e]);
-                        const float u = s[e] * (a.scale * exp2_fast((hi - h2.x) + (lo - l2.x)));
-                        const float v = s[e + 1] * (a.scale * exp2_fast((hi - h2.y) + (lo - l2.y)));
+                        const float u = s[e] * (scale * exp2_fast((hi - h2.x) + (lo - l2.x)));
+                        const float v = s[e + 1] * (scale * exp2_fast((hi - h2.y) + (lo - l2.y)));
                         p[e >> 1] = pack_b16x2(c + e <= lane ? u : 0.f, c + e + 1 <= lane ? v : 0.f, F16);
                     }
                     tmem_st8(t_row + 16 * quarter + (c >> 1), p);
@@ -533,7 +579,7 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         }
     } else {
         if constexpr (OUT) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kOutRegs));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kOut));
             // ------------------------------------------------------ o: row i
             // A warp's 32 rows leave by TMA out of a swizzled copy (rows stored by their threads are 32 lines a store);
             // where the sequence ends among them, by their threads.
@@ -545,8 +591,14 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 const bool whole = tok - lane + 32 <= sm.left;
                 const uint32_t t_out = t_row + Shape::kOut + st * 128;
                 wait(sm.g_ready[st], (it >> 1) & 1);
-                float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]);
+                float f = a.scale * exp2_fast(sm.decay[st].hi[i] + sm.decay[st].lo[i]), down = 1.f;
                 arrive(sm.g_free[st]);
+                if constexpr (F16) {
+                    wait(sm.scaled[st], (it >> 1) & 1);
+                    const int n = sm.score_powers[st][quarter];
+                    f *= power_of_two(n);
+                    down = power_of_two(-n);
+                }
                 // the far part, scaled by rows: the near products add to it
                 wait(sm.far, st);
                 ptx::tc_fence_after();
@@ -583,7 +635,11 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                     for (int g = 0; g < 4; ++g) {
                         uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = pack_b16x2(u[8 * g + 2 * e], u[8 * g + 2 * e + 1], F16);
+                        for (int e = 0; e < 4; ++e) {
+                            float2 x = make_float2(u[8 * g + 2 * e], u[8 * g + 2 * e + 1]);
+                            if constexpr (F16) x = floats_of(mul2(pair_of(x.x, x.y), pair_of(down, down)));
+                            y[e] = pack_b16x2(x.x, x.y, F16);
+                        }
                         if (whole) sts128((to ^ (((c & 63) << 1) + g * 16)) + (c >> 6) * 16384, y[0], y[1], y[2], y[3]);
                         else if (tok < sm.left) *reinterpret_cast<uint4*>(o + c + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
