@@ -55,6 +55,8 @@ struct GradShape {
         ChunkDecay decay;
         float column[kDecayChunk];  // exp of the decay from the end of the 32 tokens before to a column
         float whole;
+        int32_t rise;                     // fp16: see rise_of
+        uint32_t top[2][kWorkerWarps];    // fp16: the largest of a warp's scores, and of do v^T
         uint32_t tmem;
         int32_t fail;
         uint64_t may_give, given;  // of a pair: the other's rows may be given to it, it has given this one's
@@ -284,9 +286,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         };
         float far_q = 0.f, far_k = 0.f, near_k = 0.f, near_q = 0.f, across = 0.f;
         if (warp == 0) {
-            const Pair all = sum_decay(load_g(a.g, a.g_stride, h, row0, valid, lane), sm.decay, lane);
-            if (lane == 0) sm.whole = whole_decay(all);
+            const LoadedG g = load_g(a.g, a.g_stride, h, row0, valid, lane);
+            const Pair all = sum_decay(g, sm.decay, lane);
+            const int rise = F16 ? rise_of(g) : 0;
+            if (lane == 0) sm.whole = whole_decay(all), sm.rise = rise;
         }
+        if (F16 && lane == 0) sm.top[0][warp] = sm.top[1][warp] = 0u;  // (warps right of the diagonal have no scores)
         float up_q = 1.f, up_k = 1.f;
         if (F16) up_q = a.kept_scale[unit], up_k = a.dkept_scale[unit];
         named_sync(1, kWorkers);
@@ -326,6 +331,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         };
         named_sync(1, kWorkers);  // column is there
 
+        // P and dP as fp16 have to be near the top of its range, or small ones lose their bits and large ones overflow: a
+        // power of two for the chunk's P and one for its dP, which the far parts of dv, and of dq and dk, are multiplied by and
+        // the outputs divided (4 x 8192 tokens x 32 heads of 128 x 128, with the scan: 1039 us, without any 1004).
+        auto power = [&](int which) {
+            const uint32_t top = __reduce_max_sync(~0u, sm.top[which][lane & (kWorkerWarps - 1)]);
+            return score_power(__uint_as_float(top) * fabsf(a.scale), sm.rise);
+        };
         // P^T and dP^T: row j, 32 columns i
         {
             const int b = part;
@@ -339,6 +351,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 ptx::tmem_ld16(t_row + kT1 + 32 * b, e);
                 ptx::tmem_ld16(t_row + kT1 + 32 * b + 16, e + 16);
                 ptx::tmem_ld_wait();
+                float up_p = 1.f, up_d = 1.f;
+                if constexpr (F16) {
+                    float most_s = 0.f, most_e = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const bool pair = b > quarter || c >= lane;
+                        most_s = fmaxf(most_s, pair ? fabsf(s[c]) : 0.f);
+                        most_e = fmaxf(most_e, pair ? fabsf(e[c]) : 0.f);
+                    }
+                    const uint32_t top_s = __reduce_max_sync(~0u, __float_as_uint(most_s));
+                    const uint32_t top_e = __reduce_max_sync(~0u, __float_as_uint(most_e));
+                    if (lane == 0) sm.top[0][warp] = top_s, sm.top[1][warp] = top_e;
+                    named_sync(8, 32 * (kWorkerWarps - kDotWarps));
+                    up_p = power_of_two(power(0)), up_d = power_of_two(power(1));
+                }
                 if (b > quarter) {
                     const int end = 32 * b - 1;
                     const float r = a.scale * exp2_fast((d.hi[end] - hi) + (d.lo[end] - lo));
@@ -348,10 +375,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                     for (int c = 0; c < 16; ++c) {
                         const float2 column = *reinterpret_cast<const float2*>(&sm.column[32 * b + 2 * c]);
                         const uint64_t f = mul2(r2, pair_of(column.x, column.y)), x = pair_of(s[2 * c], s[2 * c + 1]);
-                        const float2 scaled = floats_of(mul2(x, f));
+                        const float2 scaled = floats_of(F16 ? mul2(mul2(x, f), pair_of(up_p, up_p)) : mul2(x, f));
                         p[c] = pack_b16x2(scaled.x, scaled.y, F16);
                         const uint64_t y = mul2(pair_of(e[2 * c], e[2 * c + 1]), f), m = mul2(x, y);
-                        const float2 dscaled = floats_of(y), pair = floats_of(m);
+                        const float2 dscaled = floats_of(F16 ? mul2(y, pair_of(up_d, up_d)) : y), pair = floats_of(m);
                         dp[c] = pack_b16x2(dscaled.x, dscaled.y, F16);
                         s[2 * c] = pair.x, s[2 * c + 1] = pair.y;
                         sum = add2(sum, m);
@@ -362,13 +389,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         const float f = a.scale * exp2_fast((d.hi[32 * b + c] - hi) + (d.lo[32 * b + c] - lo));
-                        const float x = c >= lane ? s[c] * f : 0.f;
+                        const float x = c >= lane ? (F16 ? up_p * (s[c] * f) : s[c] * f) : 0.f;
                         e[c] = c >= lane ? e[c] * f : 0.f;
                         s[c] = c > lane ? s[c] * e[c] : 0.f;  // (a token's pair with itself has no decay)
                         near_k += s[c];
                         if (c & 1) {
                             p[c >> 1] = pack_b16x2(__uint_as_float(p[c >> 1]), x, F16);
-                            dp[c >> 1] = pack_b16x2(e[c - 1], e[c], F16);
+                            dp[c >> 1] = F16 ? pack_b16x2(up_d * e[c - 1], up_d * e[c], F16) : pack_b16x2(e[c - 1], e[c], F16);
                         } else {
                             p[c >> 1] = __float_as_uint(x);
                         }
@@ -398,6 +425,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         for (int vb = 1; vb < VB; ++vb)
             if (dot_warp >= 0) dot_states(vb);
         across *= up_q * up_k;
+        float p_up = 1.f, p_down = 1.f, d_up = 1.f, d_down = 1.f;
+        if constexpr (F16) {
+            const int p = power(0), d = power(1);
+            p_up = power_of_two(p), p_down = power_of_two(-p), d_up = power_of_two(d), d_down = power_of_two(-d);
+        }
 
         // the far parts of dq and dk: scaled by rows, and their products with q and k
         const float seen = exp2_fast(hi + lo), kept = exp2_fast(gap(d, kDecayChunk - 1, hi, lo));
@@ -430,8 +462,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             const float2 both = floats_of(sum);
             return both.x + both.y;
         };
-        far_q = scaled(kTdq, a.scale * seen * up_q, base + Shape::kQ);
-        far_k = scaled(kTdk, kept * up_k, base + Shape::kK);
+        far_q = scaled(kTdq, a.scale * seen * up_q * d_up, base + Shape::kQ) * d_down;
+        far_k = scaled(kTdk, kept * up_k * d_up, base + Shape::kK) * d_down;
         tmem_st_wait();
         ptx::tc_fence_before();
         arrive(sm.far_ok);
@@ -445,7 +477,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             ptx::tmem_ld16(t_dv + c, u);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] *= kept * up_k;
+            for (int e = 0; e < 16; ++e) u[e] *= kept * up_k * p_up;
             tmem_st16(t_dv + c, reinterpret_cast<const uint32_t*>(u));
         }
         tmem_st_wait();
@@ -456,7 +488,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         // by their threads.
         const bool live = row < valid, staged = valid == kDecayChunk;
         const int64_t tok = (int64_t)row0 + row;
-        auto store16 = [&](uint32_t t, int col, int count, uint32_t tile, uint16_t* to) {
+        auto store16 = [&](uint32_t t, int col, int count, uint32_t tile, uint16_t* to, float down) {
 #pragma unroll 1
             for (int c = 0; c < count; c += 16) {
                 float u[16];
@@ -464,7 +496,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 ptx::tmem_ld_wait();
                 uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = pack_b16x2(u[2 * e], u[2 * e + 1], F16);
+                for (int e = 0; e < 8; ++e)
+                    w[e] = F16 ? pack_b16x2(down * u[2 * e], down * u[2 * e + 1], F16) : pack_b16x2(u[2 * e], u[2 * e + 1], F16);
                 const int at_col = col + c;
                 if (staged) {
                     const uint32_t p = swizzled_row(tile + (at_col >> 6) * 16384, row);
@@ -482,6 +515,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 float u[16];
                 ptx::tmem_ld16(t + c, u);
                 ptx::tmem_ld_wait();
+                if constexpr (F16) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] *= d_down;
+                }
                 const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
                 const uint32_t p = swizzled_row(tile + (c >> 5) * 16384, row) ^ ((c & 31) << 2);
 #pragma unroll
@@ -515,8 +552,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 }
             }
         } else if (a.group == 1) {
-            store16(t_row + kTdq + part * kCols, part * kCols, kCols, base + Shape::kQ, static_cast<uint16_t*>(a.dq) + to);
-            store16(t_row + kTdk + part * kCols, part * kCols, kCols, base + Shape::kK, static_cast<uint16_t*>(a.dk) + to);
+            store16(t_row + kTdq + part * kCols, part * kCols, kCols, base + Shape::kQ, static_cast<uint16_t*>(a.dq) + to, d_down);
+            store16(t_row + kTdk + part * kCols, part * kCols, kCols, base + Shape::kK, static_cast<uint16_t*>(a.dk) + to, d_down);
         } else {
             store32(t_row + kTdq, base + Shape::kQ, static_cast<float*>(a.dq) + to);
             store32(t_row + kTdk, base + Shape::kRing, static_cast<float*>(a.dk) + to);
@@ -542,7 +579,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         });
         wait(sm.dv, 0);
         ptx::tc_fence_after();
-        store16(t_dv, part * kColsV, kColsV, base + Shape::kV, a.dv + (tok * a.H + h) * V);
+        store16(t_dv, part * kColsV, kColsV, base + Shape::kV, a.dv + (tok * a.H + h) * V, p_down);
         send([&] {
             for (int b = 0; b < VB; ++b)
                 ptx::tma_store_3d(&a.tm_dv, raw + Shape::kV + b * 16384 + quarter * 4096, b * 64, h, row0 + quarter * 32);
@@ -594,6 +631,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                     const uint32_t p = swizzled_row(tile + (col >> 5) * 16384, row) ^ ((col & 31) << 2);
                     const uint4 x[4] = {lds128(p), lds128(p ^ 16), lds128(p ^ 32), lds128(p ^ 48)};
                     ptx::tmem_ld_wait();
+                    if constexpr (F16) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) u[e] *= d_down;
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         w[c / 2 + 2 * e] = pack_b16x2(u[4 * e] + __uint_as_float(x[e].x), u[4 * e + 1] + __uint_as_float(x[e].y), F16);

@@ -502,12 +502,11 @@ kda_status kda_linear(const void* x, const void* w, const float* bias, const voi
  *             is written) and slots, and waits that ran out (results are then incomplete), as in kda_step
  * q, k, v and d_o of fwd and bwd are 16-byte aligned with strides of a multiple of 8
  * elements; o, states and gradients are contiguous and 16-byte aligned (KDA_ERR_ALIGNMENT).
- * Inputs are finite: a value that is not reaches the other tokens of its chunk. In fp16, kda_decay_bwd takes
- * scale (q_i . k_j) and scale (d_o_i . v_j) of tokens of a chunk that are below 65504. Outputs share
+ * Inputs are finite: a value that is not reaches the other tokens of its chunk. Outputs share
  * no memory with inputs or with one another.
  * Scores and states are rounded to io_dtype as operands of their products (in fp16 by powers of
- * two, so they keep fp32's range: of a state, and for the forward of 32 tokens' scores, which keep 2^-11 of themselves
- * or 2^-38 of the largest that they can be, K scale max |q| max |k|, or 2^-65); the states themselves, and
+ * two, so they keep fp32's range: of a state, and of the scores of a chunk, for the forward of 32 tokens, which keep
+ * 2^-11 of themselves or 2^-38 of the largest that they can be, K scale max |q| max |k|, or 2^-65); the states themselves, and
  * what adds to them, keep 2^-17 of themselves (bf16) or 2^-22 (fp16). Results do not depend on timing (no atomics).
  */
 typedef struct kda_decay_opts {

@@ -1,5 +1,5 @@
-"""decay_fwd in fp16 with scores far below and above fp16's range: scale (q_i . k_j) is an operand of products,
-and keeps its bits whatever its size.
+"""decay_fwd and decay_bwd in fp16 with scores far below and above fp16's range: scale (q_i . k_j) and
+scale (do_i . v_j) are operands of products, and keep their bits whatever their size.
 
 Bounds, u = 2^-11: o, dq, dk, dv are held to u |ref| (the output's rounding; 2^-25 below fp16's normal range) and
 (u + 2^-15) W, W the same sum over absolute values, as in decay_util. A score is rounded next to a power of two that
@@ -41,8 +41,9 @@ def compare(got, x, bounds):
                 most *= x["v"].shape[2] // x["q"].shape[2]
             assert_close(y, r, U * 1.01, (U + 2.0 ** -15) * w + 2.0 ** -31 * most + TINY[F16], name)
             normal = r.abs() >= 2.0 ** -13  # (below, the output's own steps are wider than 2^-11)
+            assert normal.double().mean() > 0.25  # (of the reference: enough of it is looked at)
             off = ((y.double() - r)[normal].norm() / r[normal].norm()).item()
-            assert normal.float().mean() > 0.5 and off <= 2 * U, (name, off)
+            assert off <= 2 * U, (name, off)
         elif name == "dg":
             pairs = (x["q"].double().abs().flatten(0, 1) * W["dq"]).sum(-1)
             pairs = pairs.repeat_interleave(x["v"].shape[2] // pairs.shape[1], 1)
@@ -113,3 +114,29 @@ def test_forward_that_grows():
     x = make(1, 128, 2, 64, 64, io=F16, h0=False, do=False)
     x["g"] = torch.rand(x["g"].shape, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda") * 0.12
     compare(run(x, grads=False), x, spans([128]))
+
+
+SMALL, LARGE = dict(q=-7, k=-7, v=8, do=8, dht=-8), dict(q=8, k=8, v=-9, do=-9, h0=-9)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("powers", [SMALL, LARGE], ids=["small scores", "small gradients of scores"])
+@pytest.mark.parametrize("H,hq", [(2, 2), (4, 2), (4, 1)])
+def test_gradients(K, V, powers, H, hq):
+    x = sized(make(1, 300, H, K, V, hq=hq, io=F16, mean=3.0, seed=K + V), **powers)
+    compare(run(x), x, spans([300]))
+
+
+@pytest.mark.parametrize("hq", [2, 1])
+def test_gradients_of_scores_above_fp16s_range(hq):
+    x = sized(make(2, 200, 2, 64, 64, hq=hq, io=F16, mean=3.0), q=11, k=11, v=-12, do=-9, h0=-12)
+    q, k = (t.double().transpose(1, 2) for t in (x["q"], x["k"]))
+    assert 64 ** -0.5 * (q @ k.transpose(-1, -2)).tril().abs().max().item() > 2 * 65504
+    compare(run(x), x, spans([200, 200]))
+
+
+@pytest.mark.parametrize("gate", ["token", "head"])
+def test_gradients_packed(gate):
+    lens = [1, 0, 129, 300, 127]
+    x = sized(make(1, sum(lens), 4, 64, 128, hq=2, io=F16, gate=gate, N=len(lens), mean=3.0), **SMALL)
+    compare({n: t for n, t in run(x, offsets(lens)).items() if gate == "token" or n != "dg"}, x, spans(lens))
