@@ -148,10 +148,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    // (not before: a dependent that shares this SM could take the TMEM that this block still needs)
-    ptx::grid_dep_launch();
     __syncthreads();
     ptx::tc_fence_after();
+    // (not before: it counts from a block's first thread that runs it, and a dependent that shares this SM could take the
+    // TMEM that this block still needs)
+    ptx::grid_dep_launch();
     const uint32_t tmem = sm.tmem;
     if (a.paired) cluster_arrive();  // this CTA's barriers are there
     volatile int32_t* fail = &sm.fail;

@@ -169,10 +169,11 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    // (not before: a dependent that shares this SM could take the TMEM that this block still needs)
-    ptx::grid_dep_launch();
     __syncthreads();
     ptx::tc_fence_after();
+    // (not before: it counts from a block's first thread that runs it, and a dependent that shares this SM could take the
+    // TMEM that this block still needs)
+    ptx::grid_dep_launch();
     const uint32_t tmem = sm.tmem, base = ptx::smem_u32(raw);
     const int chunks = sm.chunks;
     // tokens of the piece before the it'th chunk that is taken

@@ -1,0 +1,29 @@
+"""Orders in the kernels of linear attention with a decay per head that no run would show to be wrong, read in their
+sources on the CPU."""
+from __future__ import annotations
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "chunked_gated_delta_gb300", "csrc")
+
+
+def source(name):
+    """Without comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name", ["decay_scan.cuh", "decay_grads.cu"])
+def test_dependents_are_let_in_when_tmem_is_had(name):
+    """The launch of dependents counts for a block as soon as one of its threads has asked for it. It is asked for behind a
+    barrier of the whole block that the allocating warp reaches with its TMEM: a dependent on the same SM that took it first
+    would wait for this grid, and this grid for the TMEM."""
+    text = source(name)
+    alloc = text.index("ptx::tmem_alloc(")
+    sync = text.index("__syncthreads();", alloc)
+    launch = text.index("ptx::grid_dep_launch();", alloc)
+    assert sync < launch
+    assert "grid_dep_launch" not in text[text.rindex("__global__", 0, alloc):alloc]
