@@ -350,10 +350,12 @@ __device__ __forceinline__ uint32_t clock_lo() {
     asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
     return t;
 }
+// CLUSTER: the arrivals come from the other CTA of a pair.
+template <bool CLUSTER = false>
 __device__ __forceinline__ void wait_or_note(uint64_t* bar, uint32_t parity, int32_t* fail) {
     const uint32_t t0 = clock_lo(), at = ptx::smem_u32(fail);
 #pragma unroll 1
-    while (!ptx::mbar_try_wait(bar, parity)) {
+    while (!try_wait<CLUSTER>(bar, parity)) {
         int32_t failed;
         asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(failed) : "r"(at) : "memory");
         if (failed) break;

@@ -160,6 +160,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
         wait_or_note(&bar, parity, &sm.fail);
         return !*fail;
     };
+    auto wait_cluster = [&](uint64_t& bar, uint32_t parity) {
+        wait_or_note<true>(&bar, parity, &sm.fail);
+        return !*fail;
+    };
 
     if (warp == kWorkerWarps) {
         if (elect_one()) {
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
                 store32(t_row + kTdk, base + Shape::kRing, nullptr);
                 ptx::fence_proxy_async_smem();
                 named_sync(7, 256);
-                if (warp == 2 * peer && elect_one() && wait(sm.may_give, 0)) {
+                if (warp == 2 * peer && elect_one() && wait_cluster(sm.may_give, 0)) {
                     const uint32_t bar = in_cta(ptx::smem_u32(&sm.given), peer);
                     for (int b = 0; b < 2 * KB; ++b) {
                         const uint32_t at_rows = b * 16384 + peer * 8192;
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_decay_grads_kernel(const 
             if (live) a.dg[tok * a.H + h] = all * sm.whole + later + before;
         }
         if (a.paired && mine) {  // what the other head had for these rows has landed where it had it itself
-            wait(sm.given, 0);
+            wait_cluster(sm.given, 0);
             auto add = [&](uint32_t column, uint32_t tile, void* to) {
                 uint32_t w[kCols / 2];
 #pragma unroll

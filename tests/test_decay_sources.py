@@ -27,3 +27,18 @@ def test_dependents_are_let_in_when_tmem_is_had(name):
     launch = text.index("ptx::grid_dep_launch();", alloc)
     assert sync < launch
     assert "grid_dep_launch" not in text[text.rindex("__global__", 0, alloc):alloc]
+
+
+def test_barriers_of_a_pair_are_waited_for_in_the_clusters_scope():
+    """The other CTA arrives on may_give, and its copies complete given: an acquire at the CTA's own scope would not order
+    what it did before them."""
+    text = source("decay_grads.cu")
+    for bar in ("may_give", "given"):
+        waits = re.findall(r"(\w+)\(sm\.%s, " % bar, text)
+        assert waits and all(w == "wait_cluster" for w in waits), (bar, waits)
+    assert re.search(r"auto wait_cluster = [^;]*;\s*wait_or_note<true>\(", text) or \
+        re.search(r"auto wait_cluster = \[&\][^{]*\{\s*wait_or_note<true>\(", text)
+    wait = source("decay.cuh")
+    wait = wait[wait.index("template <bool CLUSTER = false>"):]
+    assert "try_wait<CLUSTER>(bar, parity)" in wait[:wait.index("\n}")]
+    assert "mbarrier.try_wait.parity.acquire.cluster" in source("waits.cuh")
