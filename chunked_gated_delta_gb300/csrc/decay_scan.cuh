@@ -390,10 +390,10 @@ __global__ void __launch_bounds__(DecayScanShape<KB, VB, OUT>::kThreads, 1)
                 for (int k = 0; k < K; ++k) S[k] = 0.f;
             } else if (!b16) {  // (all loads in flight: one after the other in sixteens they took 6 us)
 #pragma unroll
-                for (int k = 0; k < K; ++k) S[k] = __ldg(start + k * V);
+                for (int k = 0; k < K; ++k) S[k] = __ldcg(start + k * V);
             } else {
 #pragma unroll
-                for (int k = 0; k < K; ++k) S[k] = from_b16<false>(__ldg(start16 + k * V));
+                for (int k = 0; k < K; ++k) S[k] = from_b16<false>(__ldcg(start16 + k * V));
             }
             const bool keep = !OUT && dir.kept;
             float decay = 1.f;

@@ -42,3 +42,10 @@ def test_barriers_of_a_pair_are_waited_for_in_the_clusters_scope():
     wait = wait[wait.index("template <bool CLUSTER = false>"):]
     assert "try_wait<CLUSTER>(bar, parity)" in wait[:wait.index("\n}")]
     assert "mbarrier.try_wait.parity.acquire.cluster" in source("waits.cuh")
+
+
+@pytest.mark.parametrize("name", sorted(n for n in os.listdir(CSRC) if n.startswith(("decay", "rotary"))))
+def test_nothing_is_loaded_past_the_coherent_caches(name):
+    """These kernels may be resident before the one in front of them has written (the states of a cache, the totals that a
+    join rewrites in place): its memory is not read-only for their lifetime, as non-coherent loads require."""
+    assert not re.search(r"__ldg\(|ld\.global\.nc|__restrict__", source(name))
