@@ -5,9 +5,9 @@
 //
 // The angle of a far position is hundreds of thousands of radians, of which fp32 would
 // keep a few hundredths. It is taken in turns, as a fraction of 64 bits: position times
-// that fraction, as integers, wraps around where the angle does, so nothing is
-// lost to its size (beside the frequency's own 53 bits), without any 64-bit float
-// arithmetic per token.
+// that fraction, as integers, wraps around where the angle does, so little is lost to its size (2^-65 of a turn
+// for each position, beside the frequency's own 53 bits), without any 64-bit float arithmetic per token. Of the product's
+// leading 32 bits an fp32 number has 24; the other eight turn its sine and cosine by what they are worth.
 //
 // Bound: q and k read and written once. A CTA goes through groups of tokens (one, or as many as its loads hold);
 // its threads make their cosines and sines once for all heads, in shared memory, while
@@ -96,10 +96,14 @@ __global__ void __launch_bounds__(kRotaryThreads, C > 1 ? 6 : 8) kda_rotary_kern
             const int64_t at = tok + s_of[p];
             const uint64_t pos = a.positions64 ? static_cast<const uint64_t*>(a.positions)[at]
                                                : (uint64_t)(int64_t)static_cast<const int32_t*>(a.positions)[at];
-            // (the leading 32 bits of the fraction, as half turns in -1 .. 1)
-            const float half_turns = (float)(int32_t)(uint32_t)((pos * s_share[p]) >> 32) * 0x1p-31f;
+            // (the leading 32 bits of the fraction, as half turns in -1 .. 1: 24 of them, and the angle that the rest is)
+            const uint32_t turn = (uint32_t)((pos * s_share[p]) >> 32);
+            const float half_turns = (float)(int32_t)(turn & ~0xffu) * 0x1p-31f, rest = (float)(turn & 0xffu) * (3.14159265f * 0x1p-31f);
             float s, c;
             sincospif(half_turns, &s, &c);
+            const float s0 = s;
+            s = fmaf(c, rest, s);
+            c = fmaf(-s0, rest, c);
             to[p] = make_float2(a.amplitude * c, a.inverse ? -a.amplitude * s : a.amplitude * s);
         }
     };

@@ -568,7 +568,8 @@ kda_status kda_decay_step(const void* q, const void* k, const void* v, const flo
  *             k_heads = 0: no k.  An output may be its own input with the same stride; nothing else
  *             of the four shares memory (KDA_ERR_INVALID_ARG where they begin alike)
  *   positions int32, or int64 with positions_i64, [tokens]: any value
- *   freqs     fp64 [pairs] radians per position; a is right to 2^-31 of a turn beside 2^-53 of position * freq
+ *   freqs     fp64 [pairs] radians per position; a is right to 2^-31 of a turn, beside 2^-52 of position * freq and
+ *             2^-65 of a turn for each position
  *   *_stride  elements between tokens (0: contiguous); any alignment of the elements' own size is
  *             taken, rows on 16 bytes with dim and pairs of whole 16-byte pieces in 16-byte loads
  * pairs in 1 .. 512 (KDA_ERR_UNSUPPORTED above), at most dim / 2.  Asynchronous on `stream`.
