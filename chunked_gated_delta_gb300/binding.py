@@ -607,7 +607,7 @@ def rotary_freqs(dim, base=10000.0, scaling=None, factor=1.0, original_length=40
     base * factor^(dim / (dim - 2)), which divides the slowest by factor and keeps the
     fastest.  "yarn": pairs that turn more than ``fast`` times over original_length
     positions are kept, those that turn less than ``slow`` times divided by factor, in
-    between a mixture linear in the pair's index; amplitude 0.1 ln(factor) + 1.
+    between a mixture linear in the pair's index; amplitude 0.1 ln(factor) + 1 (1 for factors below 1).
     """
     import math
     import torch
@@ -627,7 +627,7 @@ def rotary_freqs(dim, base=10000.0, scaling=None, factor=1.0, original_length=40
             low, high = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), dim - 1)
             divided = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
             freqs = freqs * (1.0 - divided) + freqs / factor * divided
-            amplitude = 0.1 * math.log(factor) + 1.0
+            amplitude = max(0.1 * math.log(factor) + 1.0, 1.0)
         elif scaling is not None:
             raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     return freqs.to(device), amplitude
