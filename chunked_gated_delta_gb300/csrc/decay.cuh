@@ -1,5 +1,5 @@
 // decay.cuh -- what the kernels of linear attention with a decay per head share
-// (decay_scan.cu: states and output; decay_grads.cu: gradients; decay_api.cu:
+// (decay_scan.cuh: states and output; decay_grads.cu: gradients; decay_api.cu:
 // the C entries).
 //
 // With S the K x V state of one (sequence, head) and g_t <= 0 its log decay,
@@ -231,8 +231,8 @@ __device__ __forceinline__ Pair log2_decay(float g) {
 }
 
 // The decays of one chunk up to each of its tokens, in powers of two: differences of these sums are
-// right to 2^-24 of themselves however large the sums have grown, since what the leading parts lost
-// is kept in the second ones.
+// right to 2^-24 of themselves and 2^-43 of the sums (up to 15 additions of pairs, 2^-47 each), since what the
+// leading parts lost is kept in the second ones.
 struct ChunkDecay {
     float hi[kDecayChunk], lo[kDecayChunk];
 };

@@ -29,7 +29,8 @@ struct DecayPlan {
 DecayPlan decay_plan(const kda_dims& d, bool backward) {
     const bool packed = d.num_seqs > 0;
     const int64_t N = packed ? d.num_seqs : d.B, all = ceil_div(d.T, kDecayChunk);
-    // packed lengths are not known here: the longest is taken for twice their mean
+    // packed lengths are not known here: the longest is taken for twice their mean (as evenly spread ones have it). One that
+    // is far longer is walked alone at the end: of 65536 tokens x 32 heads in 16 sequences, one of 64000 makes 361 us 1493.
     const int64_t mean = (all + N - 1) / N, nc = !packed ? all : all < 2 * mean ? all : 2 * mean;
     const int dirs = backward ? 2 : 1;
     const PassUs pass = backward ? kKeepUs : kOutUs;

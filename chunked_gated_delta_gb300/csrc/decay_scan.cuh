@@ -24,8 +24,8 @@
 //
 // Bound: HBM and, close behind it, shared memory. A chunk's 96 KB in and 32 KB out take
 // 4800 cycles of an SM's share of HBM (128 CTAs), and the 576 KB that its loads, products and
-// operands move through shared memory 4500. 4 x 8192 tokens x 32 heads of 128 x 128 in bf16: 195 to
-// 207 us, 5.2 to 5.5 TB/s (78 to 82% of what a copy reaches). Steps on the way (us): k scaled in
+// operands move through shared memory 4500. 4 x 8192 tokens x 32 heads of 128 x 128 in bf16: 205 to
+// 208 us, 5.3 TB/s (79 to 80% of what a copy reaches); in fp16 231. Steps on the way (us): k scaled in
 // place, hi after lo, o by its threads' stores 345; registers spilled beside what is left of L1, each a
 // trip to L2, brought down 311; loops instead of unrolled code (five roles' code has to fit the instruction
 // cache together) 277; o by TMA and k, v, q in single buffers 212; waits of a few instructions, far

@@ -11,7 +11,7 @@
 // launch and one trip to memory. Few threads with many columns each spend the least on a token's
 // shared loads and sums over rows, so five CTAs (K = 64: eight) of 128 threads an SM, in different stages of
 // load, sums and store, keep HBM busy without a ring, and sums are taken two floats at a time: 512 requests x
-// 32 heads of 128 x 128 in fp32 307 us (7 TB/s, what a copy reaches), 96 x 3 tokens x 32 heads of 128 x 64 in
+// 32 heads of 128 x 128 in fp32 307 us (7 TB/s; a copy reaches 6.7), 96 x 3 tokens x 32 heads of 128 x 64 in
 // bf16 25.6, of 64 x 64 15.5. One float at a time in 256 threads, four an SM, 315, 32.9 and 20.4;
 // columns by 32 in 128 threads, eight an SM, 310, 28.5 and 18 to 20; 128 columns 388.
 #include "decay.cuh"
